@@ -411,6 +411,99 @@ int sf_op_attn_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
                    int32_t S, int32_t Hq, int32_t Hkv, int32_t hd, const float* table,
                    int32_t deterministic, void* stream);
 
+/* Attention with a sliding window and sinks, forward: as sf_op_attn_fwd, but
+ * query q sees key k when k <= q and (q - k < window or k < sinks): its own
+ * and the window - 1 keys before it, and the first `sinks` tokens of its
+ * sequence.  window >= 1 (window >= S: plain causal attention), sinks >= 0;
+ * both may exceed S.  Key blocks that no query of a tile sees are not read; in
+ * the blocks that are read, a value row has to be finite even where it is
+ * masked (its weight is 0, and 0 * inf is NaN). */
+int sf_op_attn_window_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int32_t B, int32_t S,
+                          int32_t Hq, int32_t Hkv, int32_t hd, int32_t window, int32_t sinks,
+                          void* stream);
+
+/* Backward of sf_op_attn_window_fwd: arguments as sf_op_attn_bwd with the
+ * window and sinks of the forward.  dq_acc: fp32 of
+ * sf_op_attn_window_dq_scratch(...) elements (16-byte aligned).  With
+ * deterministic != 0 the scratch has a slot for each key block that a query
+ * block can see (about window / 128 + sinks / 128 + 2, not S / 128), summed in
+ * key order.  The scratch size is -1 for bad sizes. */
+int sf_op_attn_window_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
+                          const float* lse, float* delta, float* dq_acc, uint16_t* dqkv,
+                          int32_t B, int32_t S, int32_t Hq, int32_t Hkv, int32_t hd,
+                          int32_t window, int32_t sinks, const float* table,
+                          int32_t deterministic, void* stream);
+int64_t sf_op_attn_window_dq_scratch(int32_t B, int32_t S, int32_t Hq, int32_t hd, int32_t window,
+                                     int32_t sinks, int32_t deterministic);
+
+/* Norms of queries and keys for each head, with the rotary embedding in the
+ * same pass.  x bf16 [tokens, ldx] holds rows of Hq query, Hkv key and Hkv
+ * value heads of head_dim columns (the Q/K/V projection's output, not
+ * rotated).  For a query or key head h with gain g (gq or gk, bf16
+ * [head_dim]): z = g * h / sqrt(mean(h^2) + eps), y = z rotated as sf_op_rope
+ * does, computed in fp32 and rounded once.  The position of token t is pos[t]
+ * (int32 [tokens], device) or, when pos == NULL, t % seq; table: device copy
+ * of sf_rope_table (seq rows, 16-byte aligned).  pos lives on the device, so
+ * this call cannot check it: a position outside [0, seq) sets the device error
+ * word to 5 and its token is not rotated.  y may be x (with ldy == ldx): the
+ * value heads then stay; else they are copied.  Columns beyond the heads are
+ * left alone.  head_dim a multiple of 16 in [16, 256]; ldx and ldy multiples of
+ * 8, x, y, gq, gk 16-byte aligned; tokens may be 0. */
+int sf_op_qknorm_rope_fwd(const uint16_t* x, int64_t ldx, uint16_t* y, int64_t ldy,
+                          int64_t tokens, int32_t seq, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                          const uint16_t* gq, const uint16_t* gk, float eps, const float* table,
+                          const int32_t* pos, void* stream);
+
+/* Backward of sf_op_qknorm_rope_fwd from its x (not y) and dy (bf16 [tokens,
+ * lddy], the gradient of y: sf_op_attn_bwd's or sf_op_attn_window_bwd's dqkv
+ * with table == NULL): dx gets the gradient of x, its value columns dy's.
+ * dx may be dy (with lddx == lddy), not x.  dgq, dgk bf16 [head_dim]: the
+ * gains' gradients, summed over all tokens and heads in a fixed order
+ * (bit-reproducible).  scratch: fp32 of
+ * sf_op_qknorm_rope_bwd_scratch(tokens, Hq, Hkv, head_dim) elements (16-byte
+ * aligned; the size is -1 for bad sizes).  tokens >= 1. */
+int sf_op_qknorm_rope_bwd(const uint16_t* x, int64_t ldx, const uint16_t* dy, int64_t lddy,
+                          uint16_t* dx, int64_t lddx, int64_t tokens, int32_t seq, int32_t Hq,
+                          int32_t Hkv, int32_t head_dim, const uint16_t* gq, const uint16_t* gk,
+                          float eps, const float* table, const int32_t* pos, float* scratch,
+                          uint16_t* dgq, uint16_t* dgk, void* stream);
+int64_t sf_op_qknorm_rope_bwd_scratch(int64_t tokens, int32_t Hq, int32_t Hkv, int32_t head_dim);
+
+/* 8-bit activation checkpoints.  A row of d fp32 values is kept as d one-byte
+ * codes (q [rows, d]) and one fp32 scale for each block of 128 columns (the
+ * last may be shorter): scale [rows, ceil(d/128)], sf_op_ckpt8_scales floats.
+ * With a the largest magnitude of a block and T = 127 (SF_CKPT_INT8, two's
+ * complement codes) or 448 (SF_CKPT_E4M3): scale = a / T, code = round(x *
+ * (T / a)), value = code * scale, each operation in fp32 rounded to nearest
+ * even.  A block with a < 2^-100 is stored as zeros (scale 0); a block that
+ * holds an infinity or a NaN gets a NaN scale, so its values load as NaN.
+ * d a multiple of 8 in [8, 16384], buffers 16-byte aligned, rows < 2^31. */
+#define SF_CKPT_INT8 0
+#define SF_CKPT_E4M3 1
+int64_t sf_op_ckpt8_scales(int64_t rows, int32_t d);
+/* Codes and scales of x, and the values of codes and scales. */
+int sf_op_ckpt8_save(const float* x, uint8_t* q, float* scale, int32_t fmt, int64_t rows,
+                     int32_t d, void* stream);
+int sf_op_ckpt8_load(const uint8_t* q, const float* scale, float* x, int32_t fmt, int64_t rows,
+                     int32_t d, void* stream);
+/* sf_op_rmsnorm_fwd of x (y and rstd from x itself, not from its codes) that
+ * also saves x, reading x once: the forward of a checkpointed layer. */
+int sf_op_rmsnorm_fwd_save8(const float* x, const uint16_t* g, uint16_t* y, float* rstd,
+                            uint8_t* q, float* scale, int32_t fmt, int64_t rows, int32_t d,
+                            float eps, void* stream);
+/* sf_op_rmsnorm_fwd of the values of codes and scales: the recompute before a
+ * layer's backward.  x fp32 [rows, d] gets the values unless it is NULL (the
+ * residual that the recomputed layer adds to). */
+int sf_op_rmsnorm_fwd_load8(const uint8_t* q, const float* scale, const uint16_t* g, uint16_t* y,
+                            float* rstd, float* x, int32_t fmt, int64_t rows, int32_t d, float eps,
+                            void* stream);
+/* sf_op_rmsnorm_bwd at the values of codes and scales (rstd: theirs, from
+ * sf_op_rmsnorm_fwd_load8).  scratch as sf_op_rmsnorm_bwd. */
+int sf_op_rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const uint16_t* g,
+                            const float* rstd, const float* dy, const float* dres, float* dx,
+                            uint16_t* dxb, uint16_t* dg, float* scratch, int32_t fmt, int64_t rows,
+                            int32_t d, void* stream);
+
 /* m = silu(a) * b with ab = [a | b] bf16 [rows, 2*ffn]; m bf16 [rows, ffn]. */
 int sf_op_swiglu_fwd(const uint16_t* ab, uint16_t* m, int64_t rows, int32_t ffn, void* stream);
 /* dab = [dm * b * s(1 + a(1-s)) | dm * silu(a)], s = sigmoid(a). */
@@ -500,7 +593,8 @@ int sf_op_rmsnorm_bwd_noalloc(const float* x, const uint16_t* g, const float* rs
 /* Read and clear the device error word of the kernel API on the current
  * device.  0: no error; 1, 2, 3: a bounded wait ran out in a GEMM, an
  * attention or a cross-entropy kernel; 4: sf_op_lce met a label at or beyond
- * the vocabulary.  The first code a launch writes stays.  Synchronises the
+ * the vocabulary; 5: sf_op_qknorm_rope_fwd or _bwd met a position outside the
+ * rotation table.  The first code a launch writes stays.  Synchronises the
  * device. */
 int sf_op_device_error(int32_t* out);
 

@@ -27,6 +27,8 @@ STATUS_NAMES = {0: "SF_OK", -1: "SF_EINVAL", -2: "SF_ENOMEM", -3: "SF_ECUDA",
 # GEMM layouts and epilogues of sf_op_gemm
 NT, NN, TN = 0, 1, 2
 EPI_BF16, EPI_F32, EPI_F32_ADD, EPI_F32_ACC = 0, 1, 2, 3
+# formats of an 8-bit checkpoint
+CKPT_INT8, CKPT_E4M3 = 0, 1
 
 
 class SfError(RuntimeError):
@@ -120,6 +122,20 @@ _SIGS = {
     "sf_op_attn_fwd": (ctypes.c_int, [_VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _VP]),
     "sf_op_attn_bwd": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32,
                                       _I32, _VP, _I32, _VP]),
+    "sf_op_attn_window_fwd": (ctypes.c_int, [_VP, _VP, _VP] + [_I32] * 7 + [_VP]),
+    "sf_op_attn_window_bwd": (ctypes.c_int, [_VP] * 7 + [_I32] * 7 + [_VP, _I32, _VP]),
+    "sf_op_attn_window_dq_scratch": (_I64, [_I32] * 7),
+    "sf_op_qknorm_rope_fwd": (ctypes.c_int, [_VP, _I64, _VP, _I64, _I64, _I32, _I32, _I32, _I32, _VP,
+                                             _VP, _F32, _VP, _VP, _VP]),
+    "sf_op_qknorm_rope_bwd": (ctypes.c_int, [_VP, _I64, _VP, _I64, _VP, _I64, _I64, _I32, _I32, _I32,
+                                             _I32, _VP, _VP, _F32, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "sf_op_qknorm_rope_bwd_scratch": (_I64, [_I64, _I32, _I32, _I32]),
+    "sf_op_ckpt8_scales": (_I64, [_I64, _I32]),
+    "sf_op_ckpt8_save": (ctypes.c_int, [_VP, _VP, _VP, _I32, _I64, _I32, _VP]),
+    "sf_op_ckpt8_load": (ctypes.c_int, [_VP, _VP, _VP, _I32, _I64, _I32, _VP]),
+    "sf_op_rmsnorm_fwd_save8": (ctypes.c_int, [_VP] * 6 + [_I32, _I64, _I32, _F32, _VP]),
+    "sf_op_rmsnorm_fwd_load8": (ctypes.c_int, [_VP] * 6 + [_I32, _I64, _I32, _F32, _VP]),
+    "sf_op_rmsnorm_bwd_load8": (ctypes.c_int, [_VP] * 10 + [_I32, _I64, _I32, _VP]),
     "sf_op_swiglu_fwd": (ctypes.c_int, [_VP, _VP, _I64, _I32, _VP]),
     "sf_op_swiglu_bwd": (ctypes.c_int, [_VP, _VP, _VP, _I64, _I32, _VP]),
     "sf_op_lce": (ctypes.c_int, [_VP, _VP, _VP, _I64, _I32, _I32, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
@@ -418,6 +434,67 @@ def op_attn_bwd(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, hd, table
 def attn_dq_scratch_floats(B, S, Hq, hd, deterministic=0) -> int:
     """Floats of the dq_acc scratch sf_op_attn_bwd needs."""
     return (((S + 127) // 128) if deterministic else 1) * B * S * Hq * hd
+
+
+def op_attn_window_fwd(qkv, o, lse, B, S, Hq, Hkv, hd, window, sinks=0, stream=0) -> int:
+    """Causal attention where query q sees keys q - window + 1 .. q and the first `sinks`."""
+    return lib().sf_op_attn_window_fwd(qkv, o, lse, B, S, Hq, Hkv, hd, window, sinks, _s(stream))
+
+
+def op_attn_window_bwd(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, hd, window, sinks=0,
+                       table=0, stream=0, deterministic=0) -> int:
+    return lib().sf_op_attn_window_bwd(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, hd,
+                                       window, sinks, table or None, deterministic, _s(stream))
+
+
+def attn_window_dq_scratch_floats(B, S, Hq, hd, window, sinks=0, deterministic=0) -> int:
+    """Floats of the dq_acc scratch op_attn_window_bwd needs."""
+    return int(lib().sf_op_attn_window_dq_scratch(B, S, Hq, hd, window, sinks, deterministic))
+
+
+def op_qknorm_rope_fwd(x, ldx, y, ldy, tokens, seq, Hq, Hkv, head_dim, gq, gk, eps, table, pos=0,
+                       stream=0) -> int:
+    """Norms of query and key heads with the rotation; y may be x (value heads stay)."""
+    return lib().sf_op_qknorm_rope_fwd(x, ldx, y, ldy, tokens, seq, Hq, Hkv, head_dim, gq, gk, eps,
+                                       table, pos or None, _s(stream))
+
+
+def op_qknorm_rope_bwd(x, ldx, dy, lddy, dx, lddx, tokens, seq, Hq, Hkv, head_dim, gq, gk, eps,
+                       table, pos, scratch, dgq, dgk, stream=0) -> int:
+    return lib().sf_op_qknorm_rope_bwd(x, ldx, dy, lddy, dx, lddx, tokens, seq, Hq, Hkv, head_dim,
+                                       gq, gk, eps, table, pos or None, scratch, dgq, dgk, _s(stream))
+
+
+def qknorm_rope_bwd_scratch(tokens, Hq, Hkv, head_dim) -> int:
+    return int(lib().sf_op_qknorm_rope_bwd_scratch(tokens, Hq, Hkv, head_dim))
+
+
+def ckpt8_scales(rows, d) -> int:
+    """Floats of an 8-bit checkpoint's scales."""
+    return int(lib().sf_op_ckpt8_scales(rows, d))
+
+
+def op_ckpt8_save(x, q, scale, fmt, rows, d, stream=0) -> int:
+    return lib().sf_op_ckpt8_save(x, q, scale, fmt, rows, d, _s(stream))
+
+
+def op_ckpt8_load(q, scale, x, fmt, rows, d, stream=0) -> int:
+    return lib().sf_op_ckpt8_load(q, scale, x, fmt, rows, d, _s(stream))
+
+
+def op_rmsnorm_fwd_save8(x, g, y, rstd, q, scale, fmt, rows, d, eps, stream=0) -> int:
+    """RMSNorm of x that also saves x as an 8-bit checkpoint."""
+    return lib().sf_op_rmsnorm_fwd_save8(x, g, y, rstd, q, scale, fmt, rows, d, eps, _s(stream))
+
+
+def op_rmsnorm_fwd_load8(q, scale, g, y, rstd, x, fmt, rows, d, eps, stream=0) -> int:
+    """RMSNorm of a checkpoint's values; x (0: none) gets the values."""
+    return lib().sf_op_rmsnorm_fwd_load8(q, scale, g, y, rstd, x or None, fmt, rows, d, eps, _s(stream))
+
+
+def op_rmsnorm_bwd_load8(q, scale, g, rstd, dy, dres, dx, dxb, dg, scratch, fmt, rows, d, stream=0) -> int:
+    return lib().sf_op_rmsnorm_bwd_load8(q, scale, g, rstd, dy, dres or None, dx, dxb, dg, scratch, fmt,
+                                         rows, d, _s(stream))
 
 
 def op_swiglu_fwd(ab, m, rows, ffn, stream=0) -> int:

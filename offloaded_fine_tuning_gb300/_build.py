@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsfslide.so")
-SOURCES = ["gemm.cu", "attention.cu", "elementwise.cu", "engine.cpp", "ops.cpp", "noalloc.cu", "attention_tc.cu"]
+SOURCES = ["gemm.cu", "attention.cu", "elementwise.cu", "engine.cpp", "ops.cpp", "noalloc.cu", "attention_tc.cu", "qknorm.cu",
+           "ckpt8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

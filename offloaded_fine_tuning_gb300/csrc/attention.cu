@@ -65,9 +65,12 @@ __global__ void attn_delta_kernel(const bf16* __restrict__ o, const bf16* __rest
 // columns of dqkv (8 pairs per thread).  slots == 0: one accumulated buffer
 // [T, Hq*hd]; else slot j [T, Hq*hd] holds key block j's part, written for
 // positions s >= 128 j, and the parts are added in the order j = 0, 1, ...
+// With a window (> 0) only the sinks' key blocks and those from the start of
+// the window of s's query block (64 queries at head dim 128, else 128) have
+// parts, the latter in slots that blocks take in turn.
 __global__ void attn_dq_kernel(const float* __restrict__ dq_acc, bf16* __restrict__ dqkv,
                                int64_t tokens, int S, int Hq, int Hkv, int hd, float scale,
-                               const float2* __restrict__ cs, int slots) {
+                               const float2* __restrict__ cs, int slots, int window, int sinks) {
   const int half = hd / 2, groups = half / 8;
   const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= tokens * Hq * groups) return;
@@ -77,7 +80,15 @@ __global__ void attn_dq_kernel(const float* __restrict__ dq_acc, bf16* __restric
   const int64_t t = th / Hq;
   const int s = (int)(t % S);
   const int64_t ld = (int64_t)Hq * hd;
-  const float* src = dq_acc + t * ld + (int64_t)h * hd + gr * 8;
+  const int qb = hd == 128 ? 64 : 128;  // queries of a backward block
+  const int ns = window > 0 ? (sinks + 127) / 128 : 0;
+  const int wb = window > 0 ? max(0, s / qb * qb - window + 1) / 128 : 0;
+  auto slot_of = [&](int j) -> int64_t {
+    return window > 0 && j >= ns ? ns + (j - ns) % attn_window_slots(window) : j;
+  };
+  const int first = slots > 0 && ns == 0 ? wb : 0;
+  const float* base = dq_acc + t * ld + (int64_t)h * hd + gr * 8;
+  const float* src = base + (slots > 0 ? slot_of(first) : 0) * tokens * ld;
   bf16* dst = dqkv + t * (int64_t)(Hq + 2 * Hkv) * hd + (int64_t)h * hd + gr * 8;
   float x1[8], x2[8];
 #pragma unroll
@@ -88,8 +99,9 @@ __global__ void attn_dq_kernel(const float* __restrict__ dq_acc, bf16* __restric
     x2[i] = c.x; x2[i + 1] = c.y; x2[i + 2] = c.z; x2[i + 3] = c.w;
   }
   const int last = slots > 0 ? s / 128 : 0;
-  for (int j = 1; j <= last; ++j) {
-    const float* p = src + (int64_t)j * tokens * ld;
+  for (int j = first + 1; j <= last; ++j) {
+    if (j >= ns && j < wb) continue;
+    const float* p = base + slot_of(j) * tokens * ld;
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
       float4 a = *reinterpret_cast<const float4*>(p + i);
@@ -127,11 +139,12 @@ void attn_delta(const bf16* o, const bf16* dout, float* delta, int B, int S, int
 }
 
 void attn_dq_finalize(const float* dq_acc, bf16* dqkv, int B, int S, int Hq, int Hkv, int hd,
-                      float scale, const float2* cs, int slots, cudaStream_t st) {
+                      float scale, const float2* cs, int slots, int window, int sinks,
+                      cudaStream_t st) {
   const int64_t T = (int64_t)B * S;
   const int64_t n = T * Hq * (hd / 16);
   attn_dq_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(dq_acc, dqkv, T, S, Hq, Hkv, hd, scale,
-                                                               cs, slots);
+                                                               cs, slots, window, sinks);
 }
 
 }  // namespace sf

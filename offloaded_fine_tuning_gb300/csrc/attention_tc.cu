@@ -120,6 +120,12 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// A sliding window with sinks (the kernels' WIN variants): query q sees key k
+// when k <= q and (q - k < size or k < sinks).  The host clips both to S.
+struct AttWindow {
+  int size, sinks;
+};
+
 }  // namespace
 
 // ------------------------------------------------------------------ forward, two query tiles per CTA
@@ -165,11 +171,11 @@ struct AttFwd2Cfg {
 static_assert(AttFwd2Cfg<128>::SMEM <= 232448, "forward shared memory");
 }  // namespace
 
-template <int HD>
+template <int HD, bool WIN>
 __global__ void __launch_bounds__(kAttFwd2Threads, 1)
     attn_fwd_pp_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_o,
                        float* __restrict__ lse, int S, int Hq, int Hkv, int B, float scale_log2,
-                       int pair_heads, int* err) {
+                       int pair_heads, AttWindow win, int* err) {
   using C = AttFwd2Cfg<HD>;
   constexpr int NB = HD / 64;  // 64-column boxes per tile
   constexpr uint32_t ID_S = umma_idesc_bf16(128, 128, false, false);
@@ -209,7 +215,9 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
   const int npb = pair_heads ? nqb : (nqb + 1) / 2;  // query positions of an item
   const int per_rank = pair_heads ? (Hq / 2) * B : Hq * B;
   const int num_items = npb * per_rank;
-  struct Item { int h0, h1, qb0, qb1, b, g, nkv; };
+  // The key blocks of an item: 0 .. nkv - 1, or, with a window, its first ns
+  // (the sinks') and then those from ns + skip on (the window's).
+  struct Item { int h0, h1, qb0, qb1, b, g, nkv, ns, skip; };
   auto item_of = [&](int t) -> Item {
     const int rank = t / per_rank, rem = t - rank * per_rank;
     Item x;
@@ -227,8 +235,17 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
     }
     x.g = x.h0 / grp;
     x.nkv = x.qb1 + 1 < nqb ? x.qb1 + 1 : nqb;
+    x.ns = x.skip = 0;
+    if (WIN) {
+      const int lo = x.qb0 * 128 - win.size + 1;  // the first tile's first key
+      const int wb = lo > 0 ? lo / 128 : 0, sb = (win.sinks + 127) / 128;
+      x.ns = sb < wb ? sb : wb;
+      x.skip = wb - x.ns;
+      x.nkv -= x.skip;
+    }
     return x;
   };
+  auto key_block = [&](const Item& x, int j) { return WIN && j >= x.ns ? j + x.skip : j; };
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -291,9 +308,10 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
       const Item x = item_of(t);
       const int colK = (Hq + x.g) * HD, colV = (Hq + Hkv + x.g) * HD;
       for (int j = 0; j < x.nkv; ++j) {
-        if (!entry(true, colK, j * 128, x.b)) { ok = false; break; }
+        const int krow = key_block(x, j) * 128;
+        if (!entry(true, colK, krow, x.b)) { ok = false; break; }
         pv_col = colV;
-        pv_row = j * 128;
+        pv_row = krow;
         pv_b = x.b;
         if (j == 0) {
           for (int tt = 0; tt < 2; ++tt) {
@@ -443,9 +461,10 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
       // it only moves when a block's max exceeds it by more than 8, so O in
       // TMEM is rarely rescaled (O / l does not depend on the choice of m).
       float m = -INFINITY, l = 0.f;
-      // One key block: S from TMEM, P back over it.  Compiled twice, with the
-      // causal mask (the diagonal block and any block past it) and without.
-      auto block = [&](int j, long G, auto diag) -> bool {
+      // One key block (the item's j-th, block kb): S from TMEM, P back over it.
+      // Compiled twice, with the mask (the diagonal block and any block past
+      // it, and blocks that the window's start cuts) and without.
+      auto block = [&](int j, int kb, long G, auto diag) -> bool {
         constexpr bool DIAG = decltype(diag)::value;
         if (!__all_sync(0xffffffffu, mbar_wait(s_full(tt), (uint32_t)(G & 1), abort_flag))) return false;
         tc_fence_after();
@@ -461,10 +480,17 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
             for (int i = 0; i < 32; ++i) s[32 * c + i] = __uint_as_float(r[c][i]);
         }
         if (DIAG) {  // keys after the query are masked (every key of a block past the diagonal)
-          const int lim = q - j * 128;
+          const int lim = q - kb * 128;
+          if (WIN) {  // and keys before the window that are no sinks
+            const int lo = lim - win.size, sk = win.sinks - kb * 128;
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i > lim) s[i] = -INFINITY;
+            for (int i = 0; i < 128; ++i)
+              if (i > lim || (i <= lo && i >= sk)) s[i] = -INFINITY;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i > lim) s[i] = -INFINITY;
+          }
         }
         // row max: eight chains of three-input maxima over columns 16..127
         float mx8[8];
@@ -477,7 +503,12 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
         float mx = max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
         mx *= scale_log2;  // the scale is positive: the max commutes with it
         const bool grow = mx > m + 8.f;
-        const float m_new = grow ? mx : m;
+        float m_new = grow ? mx : m;
+        // A window can start inside or after this block for some rows: until a
+        // row has seen a key its m is -inf, and exponents are taken against 0
+        // (-inf - -inf would be NaN); every p of such a row is 0.
+        const bool none = WIN && DIAG && m_new == -INFINITY;
+        if (none) m_new = 0.f;
         const float corr = ex2_approx(m - m_new);  // 1 without growth, 0 on the first block
         // p = 2^(s * scale - m): the arguments and the partial row sums as
         // paired fp32 operations, the exponentials on the special-function unit
@@ -491,7 +522,7 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
         }
         const float ps = ((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) + ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7]));
         l = l * corr + ps;
-        m = m_new;
+        m = none ? -INFINITY : m_new;
         // the row of P, bf16 pairs, over the first 64 columns of S
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -519,7 +550,10 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
         return true;
       };
       for (int j = 0; j < x.nkv; ++j, ++G) {
-        ok = j >= qb ? block(j, G, std::true_type{}) : block(j, G, std::false_type{});
+        const int kb = key_block(x, j);
+        bool masked = kb >= qb;
+        if (WIN) masked = masked || (qb * 128 + 127 - kb * 128 >= win.size && kb * 128 + 127 >= win.sinks);
+        ok = masked ? block(j, kb, G, std::true_type{}) : block(j, kb, G, std::false_type{});
         if (!ok) break;
       }
       if (!ok) break;
@@ -571,6 +605,21 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
 }
 
 // ------------------------------------------------------------------ backward
+namespace {
+// With a window: the last query that sees a key of the 128-key block at k0.
+__device__ __forceinline__ int last_query(const AttWindow& win, int k0, int S) {
+  const int q = k0 + 127 + win.size - 1;
+  return k0 < win.sinks || q > S - 1 ? S - 1 : q;
+}
+// The deterministic variant's dQ slot of key block j: the sinks' blocks have
+// their own, the others take attn_window_slots of them in turn (attn_dq_kernel
+// sums the slots of a query's blocks in key order).
+__device__ __forceinline__ int dq_slot(const AttWindow& win, int j) {
+  const int ns = (win.sinks + 127) / 128;
+  return j < ns ? j : ns + (j - ns) % attn_window_slots(win.size);
+}
+}  // namespace
+
 // One CTA per (128-key block j, kv head g, batch b).  It walks every query
 // head of the group and every 128-query block i >= j.  Per (head, block):
 //   MMA:     S^T = K Q^T -> TMEM[0,128),  dP^T = V dO^T -> TMEM[128,256)
@@ -599,13 +648,13 @@ struct AttBwdCfg {
 };
 }  // namespace
 
-template <int HD, bool DET>
+template <int HD, bool DET, bool WIN>
 __global__ void __launch_bounds__(kAttThreads, 1)
     attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv,
                        const __grid_constant__ CUtensorMap tm_do, const float* __restrict__ lse,
                        const float* __restrict__ delta, float* __restrict__ dq_acc,
                        __nv_bfloat16* __restrict__ dqkv, const float2* __restrict__ cs, int S,
-                       int Hq, int Hkv, float scale, float scale_log2, int* err) {
+                       int Hq, int Hkv, float scale, float scale_log2, AttWindow win, int* err) {
   using C = AttBwdCfg<HD>;
   constexpr int NB = HD / 64;
   constexpr uint32_t ID_SQ = umma_idesc_bf16(128, 128, false, false);  // S^T, dP^T
@@ -636,7 +685,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   const int grp = Hq / Hkv;
   const int k0 = j * 128;
   const int nqb = (S + 127) / 128;
-  const int n_it = grp * (nqb - j);  // (head, query block) pairs
+  // query blocks j .. j + per_head - 1 can see these keys
+  const int per_head = (WIN ? last_query(win, k0, S) / 128 + 1 : nqb) - j;
+  const int n_it = grp * per_head;  // (head, query block) pairs
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -675,8 +726,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     bool ok = true;
     int issued = 0;
     for (int it = 0; it < n_it; ++it) {
-      const int h = g * grp + it / (nqb - j);
-      const int q0 = (j + it % (nqb - j)) * 128;
+      const int h = g * grp + it / per_head;
+      const int q0 = (j + it % per_head) * 128;
       if (!mbar_wait(qdo_empty, (it & 1) ^ 1, abort_flag)) { ok = false; break; }
       mbar_arrive_expect_tx(qdo_full, 2 * C::TILE);
 #pragma unroll
@@ -744,6 +795,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const int key = k0 + r;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const int tid = threadIdx.x - 64;  // 0..127
+    // the last query that sees this thread's key (before the key: no one does)
+    const int q_end = WIN ? (key < win.sinks || key > S - win.size ? S - 1 : key + win.size - 1) : 0;
     const int64_t ldo = (int64_t)Hq * HD;
     bool ok = true;
     // lse (log2 units) and D of the query block, one value per thread, loaded
@@ -752,8 +805,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       lv = 0.f;
       dv = 0.f;
       if (it_ >= n_it) return;
-      const int h_ = g * grp + it_ / (nqb - j);
-      const int q_ = (j + it_ % (nqb - j)) * 128 + tid;
+      const int h_ = g * grp + it_ / per_head;
+      const int q_ = (j + it_ % per_head) * 128 + tid;
       if (q_ < S) {
         const int64_t o = ((int64_t)b * Hq + h_) * S + q_;
         lv = lse[o] * 1.4426950408889634f;
@@ -763,8 +816,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     float next_l, next_d;
     fetch(0, next_l, next_d);
     for (int it = 0; it < n_it; ++it) {
-      const int h = g * grp + it / (nqb - j);
-      const int q0 = (j + it % (nqb - j)) * 128;
+      const int h = g * grp + it / per_head;
+      const int q0 = (j + it % per_head) * 128;
       const uint32_t ph = it & 1;
       float* bL = sLD + (it & 1) * 256;
       float* bD = bL + 128;
@@ -792,7 +845,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           const int qq = 32 * c + e;
           const int q = q0 + qq;
           float pv = 0.f;
-          if (q < S && key <= q) pv = ex2_approx(fmaf(__uint_as_float(sr[e]), scale_log2, -bL[qq]));
+          if (WIN ? key <= q && q <= q_end : q < S && key <= q)
+            pv = ex2_approx(fmaf(__uint_as_float(sr[e]), scale_log2, -bL[qq]));
           p[e] = pv;
           ds[e] = pv * (__uint_as_float(dr[e]) - bD[qq]);
         }
@@ -820,7 +874,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       tc_fence_after();
       const int q = q0 + r;
       // deterministic: this key block's own slot, plain stores
-      const int64_t row = DET ? ((int64_t)j * gridDim.z + b) * S + q : (int64_t)b * S + q;
+      const int64_t slot = WIN ? dq_slot(win, j) : j;
+      const int64_t row = DET ? (slot * gridDim.z + b) * S + q : (int64_t)b * S + q;
       float* dst = dq_acc + row * ldo + (int64_t)h * HD;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
@@ -942,7 +997,7 @@ struct AttBwd2Cfg {
 };
 }  // namespace
 
-template <bool DET>
+template <bool DET, bool WIN>
 __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     attn_bwd_tc2_kernel(const __grid_constant__ CUtensorMap tm_kv,
                         const __grid_constant__ CUtensorMap tm_q,
@@ -950,7 +1005,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
                         const __grid_constant__ CUtensorMap tm_dq,
                         const __grid_constant__ CUtensorMap tm_dkv, const float* __restrict__ lse,
                         const float* __restrict__ delta, const float2* __restrict__ cs, int S,
-                        int Hq, int Hkv, float scale, float scale_log2, int* err) {
+                        int Hq, int Hkv, float scale, float scale_log2, AttWindow win, int* err) {
   using C = AttBwd2Cfg;
   constexpr int HD = 128;
   constexpr uint32_t ID_SP = umma_idesc_bf16(128, 64, false, false);  // S^T, dP^T
@@ -986,7 +1041,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
   const int k0 = j * 128;
   const int nqb = (S + 63) / 64;
   const int first = 2 * j;  // first 64-query block that can see these keys
-  const int per_head = nqb - first;
+  const int per_head = (WIN ? last_query(win, k0, S) / 64 + 1 : nqb) - first;
   const int n_it = grp * per_head;
 
   if (threadIdx.x == 0) {
@@ -1119,6 +1174,8 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     const int key = k0 + r;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const int tid = threadIdx.x - 64;
+    // the last query that sees this thread's key (before the key: no one does)
+    const int q_end = WIN ? (key < win.sinks || key > S - win.size ? S - 1 : key + win.size - 1) : 0;
     bool ok = true;
     auto fetch = [&](int it_, float& lv, float& dv) {
       lv = 0.f;
@@ -1151,7 +1208,8 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
         const int h_ = g * grp + it_ / per_head;
         const int qb_ = (first + it_ % per_head) * 64 + 32 * half;
         if (DET)  // this key block's own slot of the dQ buffer
-          tma_store_3d(&tm_dq, stage, h_ * HD + 32 * quarter, qb_, j * (int)gridDim.z + b);
+          tma_store_3d(&tm_dq, stage, h_ * HD + 32 * quarter, qb_,
+                       (WIN ? dq_slot(win, j) : j) * (int)gridDim.z + b);
         else
           tma_reduce_add_3d(&tm_dq, stage, h_ * HD + 32 * quarter, qb_, b);
         bulk_commit_group();
@@ -1205,6 +1263,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       const float4* L4 = reinterpret_cast<const float4*>(bL + 32 * half);
       const float4* D4 = reinterpret_cast<const float4*>(bD + 32 * half);
       uint32_t pp[16], dd[16];
+      const int e_lo = key - qb, e_hi = q_end - qb;  // this thread's visible columns (WIN)
       auto grad_tile = [&](auto mask_tag) {
         constexpr bool kMask = decltype(mask_tag)::value;
 #pragma unroll
@@ -1221,8 +1280,13 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
             fma2(x0, x1, scale_log2, -lv[i], -lv[i + 1]);
             x0 = ex2_approx(x0);
             x1 = ex2_approx(x1);
-            if (kMask && !(qb + e < S && key <= qb + e)) x0 = 0.f;
-            if (kMask && !(qb + e + 1 < S && key <= qb + e + 1)) x1 = 0.f;
+            if (WIN) {
+              if (kMask && (e < e_lo || e > e_hi)) x0 = 0.f;
+              if (kMask && (e + 1 < e_lo || e + 1 > e_hi)) x1 = 0.f;
+            } else {
+              if (kMask && !(qb + e < S && key <= qb + e)) x0 = 0.f;
+              if (kMask && !(qb + e + 1 < S && key <= qb + e + 1)) x1 = 0.f;
+            }
             pv[i] = x0;
             pv[i + 1] = x1;
             // dS = P (dP - D): a paired subtract and a paired multiply
@@ -1238,8 +1302,10 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
           dd[2 * k + 1] = pack2_bf16(sv[2], sv[3]);
         }
       };
-      // Only blocks that touch the diagonal or the sequence end need the mask.
-      if (qb < k0 + 128 || qb + 32 > S)
+      // Only blocks that touch the diagonal, the sequence end or the window's
+      // start need the mask.
+      const bool cut = WIN && qb + 31 - k0 >= win.size && k0 + 127 >= win.sinks;
+      if (qb < k0 + 128 || qb + 32 > S || cut)
         grad_tile(std::true_type{});
       else
         grad_tile(std::false_type{});
@@ -1387,9 +1453,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn_att() {
   return fn;
 }
 
-template <int HD>
+template <int HD, bool WIN>
 int fwd_pp(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int S, int Hq, int Hkv,
-           int* err, cudaStream_t st) {
+           AttWindow win, int* err, cudaStream_t st) {
   using C = AttFwd2Cfg<HD>;
   auto fn = encode_fn_att();
   if (!fn) return -3;
@@ -1408,22 +1474,22 @@ int fwd_pp(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int S,
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return -3;
-  if (!smem_attr_set(reinterpret_cast<const void*>(attn_fwd_pp_kernel<HD>), C::SMEM)) return -3;
+  if (!smem_attr_set(reinterpret_cast<const void*>(attn_fwd_pp_kernel<HD, WIN>), C::SMEM)) return -3;
   // two query heads of a group per item when the group size is even, else
   // two consecutive query blocks of one head
   const int pair_heads = (Hq / Hkv) % 2 == 0 ? 1 : 0;
   const int nqb = (S + 127) / 128;
   const int items = pair_heads ? nqb * (Hq / 2) * B : ((nqb + 1) / 2) * Hq * B;
   const int grid = items < num_sms() ? items : num_sms();
-  attn_fwd_pp_kernel<HD><<<grid, kAttFwd2Threads, C::SMEM, st>>>(
-      tm, tm_o, lse, S, Hq, Hkv, B, 1.4426950408889634f / sqrtf((float)HD), pair_heads, err);
+  attn_fwd_pp_kernel<HD, WIN><<<grid, kAttFwd2Threads, C::SMEM, st>>>(
+      tm, tm_o, lse, S, Hq, Hkv, B, 1.4426950408889634f / sqrtf((float)HD), pair_heads, win, err);
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
-template <int HD, bool DET>
+template <int HD, bool DET, bool WIN>
 int bwd_tc(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
            const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq,
-           int Hkv, const float2* cs, int* err, cudaStream_t st) {
+           int Hkv, const float2* cs, AttWindow win, int* err, cudaStream_t st) {
   using C = AttBwdCfg<HD>;
   auto fn = encode_fn_att();
   if (!fn) return -3;
@@ -1442,23 +1508,24 @@ int bwd_tc(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16
          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return -3;
-  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc_kernel<HD, DET>), C::SMEM)) return -3;
+  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc_kernel<HD, DET, WIN>), C::SMEM)) return -3;
   const int64_t T = (int64_t)B * S;
   if (!DET && cudaMemsetAsync(dq_acc, 0, (size_t)T * WO * sizeof(float), st) != cudaSuccess)
     return -3;
   attn_delta(o, dout, delta, B, S, Hq, HD, st);
   const float scale = 1.f / sqrtf((float)HD);
   dim3 grid((S + 127) / 128, Hkv, B);
-  attn_bwd_tc_kernel<HD, DET><<<grid, kAttThreads, C::SMEM, st>>>(
-      tq, td, lse, delta, dq_acc, dqkv, cs, S, Hq, Hkv, scale, scale * 1.4426950408889634f, err);
-  attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? (S + 127) / 128 : 0, st);
+  attn_bwd_tc_kernel<HD, DET, WIN><<<grid, kAttThreads, C::SMEM, st>>>(
+      tq, td, lse, delta, dq_acc, dqkv, cs, S, Hq, Hkv, scale, scale * 1.4426950408889634f, win, err);
+  attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? (S + 127) / 128 : 0,
+                   WIN ? win.size : 0, win.sinks, st);
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
-template <bool DET>
+template <bool DET, bool WIN>
 int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
             const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq,
-            int Hkv, const float2* cs, int* err, cudaStream_t st) {
+            int Hkv, const float2* cs, AttWindow win, int* err, cudaStream_t st) {
   using C = AttBwd2Cfg;
   constexpr int HD = 128;
   auto fn = encode_fn_att();
@@ -1479,26 +1546,45 @@ int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat1
   };
   cuuint64_t sdq[2] = {(cuuint64_t)(WO * 4), (cuuint64_t)(S * WO * 4)};
   const int nkb = (S + 127) / 128;
-  cuuint64_t ddq[3] = {(cuuint64_t)WO, (cuuint64_t)S, (cuuint64_t)(DET ? B * nkb : B)};
+  const int slots = WIN ? attn_window_dq_slots(S, win.size, win.sinks) : nkb;
+  cuuint64_t ddq[3] = {(cuuint64_t)WO, (cuuint64_t)S, (cuuint64_t)(DET ? (int64_t)B * slots : B)};
   if (!enc(&tkv, qkv, dq, sq, box_kv) || !enc(&tq, qkv, dq, sq, box_q) ||
       !enc(&td, dout, dd, sd, box_q) || !enc(&tdkv, dqkv, dq, sq, box_kv) ||
       fn(&tdq, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, dq_acc, ddq, sdq, box_dq, estr,
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return -3;
-  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc2_kernel<DET>), C::SMEM)) return -3;
+  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc2_kernel<DET, WIN>), C::SMEM)) return -3;
   const int64_t T = (int64_t)B * S;
   if (!DET && cudaMemsetAsync(dq_acc, 0, (size_t)T * WO * sizeof(float), st) != cudaSuccess)
     return -3;
   attn_delta(o, dout, delta, B, S, Hq, HD, st);
   const float scale = 1.f / sqrtf((float)HD);
   dim3 grid((S + 127) / 128, Hkv, B);
-  attn_bwd_tc2_kernel<DET><<<grid, kAttBwd2Threads, C::SMEM, st>>>(
-      tkv, tq, td, tdq, tdkv, lse, delta, cs, S, Hq, Hkv, scale, scale * 1.4426950408889634f, err);
-  attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? nkb : 0, st);
+  attn_bwd_tc2_kernel<DET, WIN><<<grid, kAttBwd2Threads, C::SMEM, st>>>(
+      tkv, tq, td, tdq, tdkv, lse, delta, cs, S, Hq, Hkv, scale, scale * 1.4426950408889634f, win,
+      err);
+  attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? nkb : 0, WIN ? win.size : 0,
+                   win.sinks, st);
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
+}  // namespace
+
+namespace {
+template <bool DET, bool WIN>
+int bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
+        const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq,
+        int Hkv, int hd, const float2* cs, AttWindow win, int* err, cudaStream_t st) {
+  if (hd == 64)
+    return bwd_tc<64, DET, WIN>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, win, err, st);
+  if (hd == 128)
+    return bwd_tc2<DET, WIN>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, win, err, st);
+  return -1;
+}
+AttWindow clip(int window, int sinks, int S) {
+  return {window < S ? window : S, sinks < S ? sinks : S};
+}
 }  // namespace
 
 int attn_bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
@@ -1507,15 +1593,24 @@ int attn_bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat
              cudaStream_t st) {
   if (B <= 0 || S <= 0) return 0;
   if (Hkv <= 0 || Hq % Hkv) return -1;
-  if (hd == 64)
-    return deterministic
-               ? bwd_tc<64, true>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, err, st)
-               : bwd_tc<64, false>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, err, st);
-  if (hd == 128)
-    return deterministic
-               ? bwd_tc2<true>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, err, st)
-               : bwd_tc2<false>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, err, st);
-  return -1;
+  const AttWindow all{S, 0};
+  return deterministic ? bwd<true, false>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv,
+                                          hd, cs, all, err, st)
+                       : bwd<false, false>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv,
+                                           hd, cs, all, err, st);
+}
+
+int attn_window_bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
+                    const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B,
+                    int S, int Hq, int Hkv, int hd, int window, int sinks, const float2* cs,
+                    bool deterministic, int* err, cudaStream_t st) {
+  if (B <= 0 || S <= 0) return 0;
+  if (Hkv <= 0 || Hq % Hkv || window < 1 || sinks < 0) return -1;
+  const AttWindow win = clip(window, sinks, S);
+  return deterministic ? bwd<true, true>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv,
+                                         hd, cs, win, err, st)
+                       : bwd<false, true>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv,
+                                          hd, cs, win, err, st);
 }
 
 int attn_fwd(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int S, int Hq, int Hkv,
@@ -1523,8 +1618,19 @@ int attn_fwd(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int 
   if (B <= 0 || S <= 0) return 0;
   if (Hkv <= 0 || Hq % Hkv) return -1;
   if ((reinterpret_cast<uintptr_t>(qkv) & 15) != 0) return -1;
-  if (hd == 64) return fwd_pp<64>(qkv, o, lse, B, S, Hq, Hkv, err, st);
-  if (hd == 128) return fwd_pp<128>(qkv, o, lse, B, S, Hq, Hkv, err, st);
+  const AttWindow all{S, 0};
+  if (hd == 64) return fwd_pp<64, false>(qkv, o, lse, B, S, Hq, Hkv, all, err, st);
+  if (hd == 128) return fwd_pp<128, false>(qkv, o, lse, B, S, Hq, Hkv, all, err, st);
+  return -1;
+}
+
+int attn_window_fwd(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int S, int Hq,
+                    int Hkv, int hd, int window, int sinks, int* err, cudaStream_t st) {
+  if (B <= 0 || S <= 0) return 0;
+  if (Hkv <= 0 || Hq % Hkv || window < 1 || sinks < 0) return -1;
+  const AttWindow win = clip(window, sinks, S);
+  if (hd == 64) return fwd_pp<64, true>(qkv, o, lse, B, S, Hq, Hkv, win, err, st);
+  if (hd == 128) return fwd_pp<128, true>(qkv, o, lse, B, S, Hq, Hkv, win, err, st);
   return -1;
 }
 

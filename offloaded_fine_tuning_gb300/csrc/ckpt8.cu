@@ -1,0 +1,382 @@
+// 8-bit activation checkpoints: a layer's input (fp32 [rows, d]) kept as one
+// byte an element with one fp32 scale for each block of 128 columns of a row,
+// and RMSNorm computed on the way in (forward, saving) and on the way out
+// (recompute and backward, from the codes).
+//
+// With a the largest magnitude of a block and T = 127 (int8) or 448 (e4m3):
+//   scale = a / T,  code = round(x * (T / a)),  value = code * scale,
+// all in fp32, round to nearest even.  int8 keeps 1/254 of the block's largest
+// magnitude at worst; e4m3 keeps every value to 2^-4 of itself above a 2^-6
+// of 448ths.  A block whose a is below 2^-100 (T / a would overflow) is stored
+// as zeros; a block that holds an infinity or a NaN has a NaN scale, so it
+// comes back as NaN and a step that diverged is not hidden.
+//
+// Every kernel here streams its rows once and is bound by memory traffic.  A
+// lane holds four columns (a float4, or four codes), so a warp holds a block:
+// its largest magnitude is one integer warp reduction of |x|'s bits, which
+// order like the values, with infinities and NaNs on top.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sf.h"
+#include "sf_internal.h"
+
+namespace sf {
+
+namespace {
+
+typedef __nv_bfloat16 bf16;
+
+constexpr int kBlock = 128;   // columns that share a scale
+constexpr int kThreads = 256;
+
+template <int FMT>
+constexpr float kTop = FMT == SF_CKPT_INT8 ? 127.f : 448.f;
+
+// The block's scale and the factor to its codes (0: every code is 0), from the
+// bits of its largest magnitude.
+template <int FMT>
+__device__ __forceinline__ void block_scale(uint32_t bits, float& scale, float& inv) {
+  const float a = __uint_as_float(bits);
+  inv = scale = 0.f;
+  if (bits >= 0x7f800000u) {
+    scale = __uint_as_float(0x7fc00000u);
+  } else if (a >= 7.888609052210118e-31f) {  // 2^-100
+    inv = __fdiv_rn(kTop<FMT>, a);
+    scale = __fdiv_rn(a, kTop<FMT>);
+  }
+}
+
+__device__ __forceinline__ uint32_t max_bits(const float4& v) {
+  const uint32_t m = 0x7fffffffu;
+  return max(max(__float_as_uint(v.x) & m, __float_as_uint(v.y) & m),
+             max(__float_as_uint(v.z) & m, __float_as_uint(v.w) & m));
+}
+
+// Four codes, the lowest column in the lowest byte.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode(const float4& v, float inv) {
+  if (inv == 0.f) return 0u;  // a zero or a non-finite block
+  if (FMT == SF_CKPT_INT8) {
+    const uint32_t a = (uint32_t)__float2int_rn(v.x * inv), b = (uint32_t)__float2int_rn(v.y * inv);
+    const uint32_t c = (uint32_t)__float2int_rn(v.z * inv), d = (uint32_t)__float2int_rn(v.w * inv);
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  }
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v.x * inv, v.y * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v.z * inv, v.w * inv), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+template <int FMT>
+__device__ __forceinline__ float4 decode(uint32_t q, float scale) {
+  float4 v;
+  if (FMT == SF_CKPT_INT8) {
+    // code + 128 in the low mantissa byte of 2^23: exact, and no conversions
+    const uint32_t u = q ^ 0x80808080u;
+    v.x = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)) - 8388736.f;
+    v.y = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)) - 8388736.f;
+    v.z = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)) - 8388736.f;
+    v.w = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - 8388736.f;
+  } else {
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q & 0xffffu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q >> 16), __NV_E4M3);
+    const float2 f = __half22float2(__half2(a)), g = __half22float2(__half2(b));
+    v = make_float4(f.x, f.y, g.x, g.y);
+  }
+  return make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Block-wide sum; every thread gets the result.  `sh` holds >= 32 floats.
+__device__ __forceinline__ float block_sum(float v, float* sh) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  v = warp_sum(v);
+  __syncthreads();
+  if (lane == 0) sh[w] = v;
+  __syncthreads();
+  return warp_sum(lane < nw ? sh[lane] : 0.f);
+}
+
+__device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+__device__ __forceinline__ float4 unpack4(uint2 u) {
+  const float2 a = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// ------------------------------------------------------------------ save and load alone
+constexpr int kCopyBlocks = 4;  // blocks a warp has in flight
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads)
+    save_kernel(const float* __restrict__ x, uint8_t* __restrict__ q, float* __restrict__ scale,
+                int64_t blocks, int nb, int d) {
+  const int lane = threadIdx.x & 31;
+  const int64_t first = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kCopyBlocks;
+  float4 v[kCopyBlocks];
+  int64_t at[kCopyBlocks];
+#pragma unroll
+  for (int u = 0; u < kCopyBlocks; ++u) {
+    const int64_t b = first + u, row = b / nb;
+    const int col = (int)(b - row * nb) * kBlock + 4 * lane;
+    at[u] = b < blocks && col < d ? row * d + col : -1;
+    v[u] = at[u] >= 0 ? *reinterpret_cast<const float4*>(x + at[u]) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int u = 0; u < kCopyBlocks; ++u) {
+    float s, inv;
+    block_scale<FMT>(__reduce_max_sync(0xffffffffu, max_bits(v[u])), s, inv);
+    if (at[u] >= 0) *reinterpret_cast<uint32_t*>(q + at[u]) = encode<FMT>(v[u], inv);
+    if (lane == 0 && first + u < blocks) scale[first + u] = s;
+  }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads)
+    load_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scale,
+                float* __restrict__ x, int64_t blocks, int nb, int d) {
+  const int lane = threadIdx.x & 31;
+  const int64_t first = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kCopyBlocks;
+  uint32_t c[kCopyBlocks];
+  float s[kCopyBlocks];
+  int64_t at[kCopyBlocks];
+#pragma unroll
+  for (int u = 0; u < kCopyBlocks; ++u) {
+    const int64_t b = first + u, row = b / nb;
+    const int col = (int)(b - row * nb) * kBlock + 4 * lane;
+    at[u] = b < blocks && col < d ? row * d + col : -1;
+    c[u] = at[u] >= 0 ? *reinterpret_cast<const uint32_t*>(q + at[u]) : 0u;
+    s[u] = at[u] >= 0 ? scale[b] : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kCopyBlocks; ++u)
+    if (at[u] >= 0) *reinterpret_cast<float4*>(x + at[u]) = decode<FMT>(c[u], s[u]);
+}
+
+// ------------------------------------------------------------------ RMSNorm forward
+// One CTA per row; thread t holds the four columns t, t + 256, ... (CH of
+// them), so each warp holds whole blocks.  LOAD: the row comes from the codes
+// (and is written to xout unless that is null); else from x, and is saved.
+template <int CH, int FMT, bool LOAD>
+__global__ void __launch_bounds__(kThreads)
+    norm_fwd8_kernel(const float* __restrict__ x, const bf16* __restrict__ g,
+                     bf16* __restrict__ y, float* __restrict__ rstd_out, uint8_t* q, float* scale,
+                     float* __restrict__ xout, int nb, int d, float eps) {
+  __shared__ float sh[32];
+  const int64_t row = blockIdx.x;
+  const int n4 = d >> 2, lane = threadIdx.x & 31;
+  uint32_t* qr = reinterpret_cast<uint32_t*>(q + row * d);
+  float* sr = scale + row * nb;
+  float4 v[CH];
+  float ss = 0.f;
+  if (LOAD) {
+    uint32_t c[CH];
+    float s[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      c[k] = i < n4 ? qr[i] : 0u;
+      s[k] = i < n4 ? sr[i >> 5] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < CH; ++k) v[k] = decode<FMT>(c[k], s[k]);
+  } else {
+    const float4* xr = reinterpret_cast<const float4*>(x + row * d);
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      v[k] = i < n4 ? xr[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+    ss += v[k].x * v[k].x + v[k].y * v[k].y + v[k].z * v[k].z + v[k].w * v[k].w;
+  if (!LOAD) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      float s, inv;
+      block_scale<FMT>(__reduce_max_sync(0xffffffffu, max_bits(v[k])), s, inv);
+      if (i < n4) {
+        qr[i] = encode<FMT>(v[k], inv);
+        if (lane == 0) sr[i >> 5] = s;
+      }
+    }
+  } else if (xout) {
+    float4* xo = reinterpret_cast<float4*>(xout + row * d);
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      if (i < n4) xo[i] = v[k];
+    }
+  }
+  ss = block_sum(ss, sh);
+  const float rstd = rsqrtf(ss / d + eps);
+  if (threadIdx.x == 0) rstd_out[row] = rstd;
+  const uint2* gr = reinterpret_cast<const uint2*>(g);
+  uint2* yr = reinterpret_cast<uint2*>(y + row * d);
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int i = threadIdx.x + k * kThreads;
+    if (i < n4) {
+      const float4 gg = unpack4(gr[i]);
+      yr[i] = pack4(v[k].x * rstd * gg.x, v[k].y * rstd * gg.y, v[k].z * rstd * gg.z, v[k].w * rstd * gg.w);
+    }
+  }
+}
+
+template <int FMT, bool LOAD>
+void norm_fwd8(const float* x, const bf16* g, bf16* y, float* rstd, uint8_t* q, float* scale,
+               float* xout, int64_t rows, int d, float eps, cudaStream_t st) {
+  const int nb = (d + kBlock - 1) / kBlock;
+  const int ch = (d / 4 + kThreads - 1) / kThreads;  // d <= 16384: at most 16
+#define SF_NORM8(CH)                                                                             \
+  norm_fwd8_kernel<CH, FMT, LOAD><<<(unsigned)rows, kThreads, 0, st>>>(x, g, y, rstd, q, scale, xout, \
+                                                                       nb, d, eps)
+  if (ch <= 1) SF_NORM8(1);
+  else if (ch <= 2) SF_NORM8(2);
+  else if (ch <= 4) SF_NORM8(4);
+  else if (ch <= 8) SF_NORM8(8);
+  else if (ch <= 12) SF_NORM8(12);
+  else SF_NORM8(16);
+#undef SF_NORM8
+}
+
+// ------------------------------------------------------------------ RMSNorm backward
+// CTAs stride over rows; a thread owns the same columns of every row, so the
+// gain gradient of the CTA's rows stays in registers.
+template <int CH, int FMT>
+__global__ void __launch_bounds__(512)
+    norm_bwd8_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scale,
+                     const bf16* __restrict__ g, const float* __restrict__ rstd,
+                     const float* __restrict__ dy, const float* __restrict__ dres,
+                     float* __restrict__ dx, bf16* __restrict__ dxb, float* __restrict__ dg_part,
+                     int64_t rows, int nb, int d) {
+  __shared__ float sh[32];
+  const int n4 = d >> 2;
+  const float inv_d = 1.f / d;
+  float4 gacc[CH];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) gacc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const float r = rstd[row];
+    float4 dv[CH], xh[CH];
+    float dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int i = threadIdx.x + k * 512;
+      dv[k] = xh[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n4) {
+        dv[k] = reinterpret_cast<const float4*>(dy + row * d)[i];
+        xh[k] = decode<FMT>(reinterpret_cast<const uint32_t*>(q + row * d)[i],
+                            scale[row * nb + (i >> 5)]);
+        const float4 gg = unpack4(reinterpret_cast<const uint2*>(g)[i]);
+        xh[k] = make_float4(xh[k].x * r, xh[k].y * r, xh[k].z * r, xh[k].w * r);
+        gacc[k].x += dv[k].x * xh[k].x; gacc[k].y += dv[k].y * xh[k].y;
+        gacc[k].z += dv[k].z * xh[k].z; gacc[k].w += dv[k].w * xh[k].w;
+        dv[k] = make_float4(dv[k].x * gg.x, dv[k].y * gg.y, dv[k].z * gg.z, dv[k].w * gg.w);
+        dot += dv[k].x * xh[k].x + dv[k].y * xh[k].y + dv[k].z * xh[k].z + dv[k].w * xh[k].w;
+      }
+    }
+    dot = block_sum(dot, sh) * inv_d;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int i = threadIdx.x + k * 512;
+      if (i < n4) {
+        float4 o = dres ? reinterpret_cast<const float4*>(dres + row * d)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+        o.x += r * (dv[k].x - xh[k].x * dot);
+        o.y += r * (dv[k].y - xh[k].y * dot);
+        o.z += r * (dv[k].z - xh[k].z * dot);
+        o.w += r * (dv[k].w - xh[k].w * dot);
+        reinterpret_cast<float4*>(dx + row * d)[i] = o;
+        reinterpret_cast<uint2*>(dxb + row * d)[i] = pack4(o.x, o.y, o.z, o.w);
+      }
+    }
+  }
+  float4* part = reinterpret_cast<float4*>(dg_part + (int64_t)blockIdx.x * d);
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int i = threadIdx.x + k * 512;
+    if (i < n4) part[i] = gacc[k];
+  }
+}
+
+template <int FMT>
+void norm_bwd8(const uint8_t* q, const float* scale, const bf16* g, const float* rstd,
+               const float* dy, const float* dres, float* dx, bf16* dxb, float* dg_part, int parts,
+               int64_t rows, int d, cudaStream_t st) {
+  const int nb = (d + kBlock - 1) / kBlock;
+#define SF_NORM8(CH)                                                                                 \
+  norm_bwd8_kernel<CH, FMT><<<parts, 512, 0, st>>>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, rows, \
+                                                   nb, d)
+  const int ch = (d / 4 + 511) / 512;
+  if (ch <= 1) SF_NORM8(1);
+  else if (ch <= 2) SF_NORM8(2);
+  else if (ch <= 4) SF_NORM8(4);
+  else SF_NORM8(8);
+#undef SF_NORM8
+}
+
+}  // namespace
+
+void ckpt8_save(const float* x, uint8_t* q, float* scale, int fmt, int64_t rows, int d,
+                cudaStream_t st) {
+  const int nb = (d + kBlock - 1) / kBlock, per = kThreads / 32 * kCopyBlocks;
+  const int64_t blocks = rows * nb;
+  const unsigned grid = (unsigned)((blocks + per - 1) / per);
+  if (fmt == SF_CKPT_INT8)
+    save_kernel<SF_CKPT_INT8><<<grid, kThreads, 0, st>>>(x, q, scale, blocks, nb, d);
+  else
+    save_kernel<SF_CKPT_E4M3><<<grid, kThreads, 0, st>>>(x, q, scale, blocks, nb, d);
+}
+
+void ckpt8_load(const uint8_t* q, const float* scale, float* x, int fmt, int64_t rows, int d,
+                cudaStream_t st) {
+  const int nb = (d + kBlock - 1) / kBlock, per = kThreads / 32 * kCopyBlocks;
+  const int64_t blocks = rows * nb;
+  const unsigned grid = (unsigned)((blocks + per - 1) / per);
+  if (fmt == SF_CKPT_INT8)
+    load_kernel<SF_CKPT_INT8><<<grid, kThreads, 0, st>>>(q, scale, x, blocks, nb, d);
+  else
+    load_kernel<SF_CKPT_E4M3><<<grid, kThreads, 0, st>>>(q, scale, x, blocks, nb, d);
+}
+
+void rmsnorm_fwd_save8(const float* x, const bf16* g, bf16* y, float* rstd, uint8_t* q,
+                       float* scale, int fmt, int64_t rows, int d, float eps, cudaStream_t st) {
+  if (fmt == SF_CKPT_INT8)
+    norm_fwd8<SF_CKPT_INT8, false>(x, g, y, rstd, q, scale, nullptr, rows, d, eps, st);
+  else
+    norm_fwd8<SF_CKPT_E4M3, false>(x, g, y, rstd, q, scale, nullptr, rows, d, eps, st);
+}
+
+void rmsnorm_fwd_load8(const uint8_t* q, const float* scale, const bf16* g, bf16* y, float* rstd,
+                       float* xout, int fmt, int64_t rows, int d, float eps, cudaStream_t st) {
+  uint8_t* qq = const_cast<uint8_t*>(q);
+  float* ss = const_cast<float*>(scale);
+  if (fmt == SF_CKPT_INT8)
+    norm_fwd8<SF_CKPT_INT8, true>(nullptr, g, y, rstd, qq, ss, xout, rows, d, eps, st);
+  else
+    norm_fwd8<SF_CKPT_E4M3, true>(nullptr, g, y, rstd, qq, ss, xout, rows, d, eps, st);
+}
+
+void rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const bf16* g, const float* rstd,
+                       const float* dy, const float* dres, float* dx, bf16* dxb, float* dg_part,
+                       int parts, int fmt, int64_t rows, int d, cudaStream_t st) {
+  if (fmt == SF_CKPT_INT8)
+    norm_bwd8<SF_CKPT_INT8>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, parts, rows, d, st);
+  else
+    norm_bwd8<SF_CKPT_E4M3>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, parts, rows, d, st);
+}
+
+}  // namespace sf

@@ -185,6 +185,188 @@ int sf_op_attn_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
   return SF_OK;
 }
 
+int sf_op_attn_window_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int32_t B, int32_t S_,
+                          int32_t Hq, int32_t Hkv, int32_t hd, int32_t window, int32_t sinks,
+                          void* stream) {
+  if (B < 0 || S_ < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (hd != 64 && hd != 128)) return SF_EINVAL;
+  if (window < 1 || sinks < 0) return SF_EINVAL;
+  if (B == 0 || S_ == 0) return SF_OK;
+  if (!qkv || !o || !lse || !al16(qkv) || !al16(o)) return SF_EINVAL;
+  int* err = dev_err_word();
+  if (!err) return SF_ECUDA;
+  if (sf::attn_window_fwd(reinterpret_cast<const bf16*>(qkv), reinterpret_cast<bf16*>(o), lse, B,
+                          S_, Hq, Hkv, hd, window, sinks, err, S(stream)) != 0)
+    return SF_ECUDA;
+  return SF_OK;
+}
+
+int64_t sf_op_attn_window_dq_scratch(int32_t B, int32_t S_, int32_t Hq, int32_t hd, int32_t window,
+                                     int32_t sinks, int32_t deterministic) {
+  if (B < 0 || S_ < 0 || Hq < 1 || (hd != 64 && hd != 128) || window < 1 || sinks < 0) return -1;
+  const int64_t slots = deterministic ? sf::attn_window_dq_slots(S_, window, sinks) : 1;
+  return slots * B * S_ * Hq * hd;
+}
+
+int sf_op_attn_window_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
+                          const float* lse, float* delta, float* dq_acc, uint16_t* dqkv,
+                          int32_t B, int32_t S_, int32_t Hq, int32_t Hkv, int32_t hd,
+                          int32_t window, int32_t sinks, const float* table,
+                          int32_t deterministic, void* stream) {
+  if (B < 0 || S_ < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (hd != 64 && hd != 128)) return SF_EINVAL;
+  if (window < 1 || sinks < 0) return SF_EINVAL;
+  if (B == 0 || S_ == 0) return SF_OK;
+  if (!qkv || !o || !dout || !lse || !delta || !dq_acc || !dqkv) return SF_EINVAL;
+  if (!al16(qkv) || !al16(o) || !al16(dout) || !al16(dq_acc) || !al16(dqkv)) return SF_EINVAL;
+  if (reinterpret_cast<uintptr_t>(table) & 7) return SF_EINVAL;
+  int* err = dev_err_word();
+  if (!err) return SF_ECUDA;
+  if (sf::attn_window_bwd(reinterpret_cast<const bf16*>(qkv), reinterpret_cast<const bf16*>(o),
+                          reinterpret_cast<const bf16*>(dout), lse, delta, dq_acc,
+                          reinterpret_cast<bf16*>(dqkv), B, S_, Hq, Hkv, hd, window, sinks,
+                          reinterpret_cast<const float2*>(table), deterministic != 0, err,
+                          S(stream)) != 0)
+    return SF_ECUDA;
+  return SF_OK;
+}
+
+// The sizes both directions of the query/key norm take.
+static bool qknorm_sizes(int64_t tokens, int32_t Hq, int32_t Hkv, int32_t hd) {
+  if (tokens < 0 || Hq < 1 || Hkv < 1 || hd < 16 || hd > 256 || hd % 16) return false;
+  // bounds the launch grids (and no device holds such a tensor)
+  const int64_t heads = (int64_t)Hq + 2 * (int64_t)Hkv;
+  return heads <= 65536 && tokens <= ((int64_t)1 << 34) / heads;
+}
+
+static bool qknorm_check(int64_t tokens, int32_t seq, int32_t Hq, int32_t Hkv, int32_t hd,
+                         const uint16_t* gq, const uint16_t* gk, float eps, const float* table,
+                         const int32_t* pos, sf::QkNormArgs* a) {
+  if (seq < 1 || !(eps > 0.f) || !gq || !gk || !table || !al16(gq) || !al16(gk) || !al16(table) ||
+      (reinterpret_cast<uintptr_t>(pos) & 3))
+    return false;
+  a->tokens = tokens; a->seq = seq; a->Hq = Hq; a->Hkv = Hkv; a->hd = hd;
+  a->gq = reinterpret_cast<const bf16*>(gq);
+  a->gk = reinterpret_cast<const bf16*>(gk);
+  a->eps = eps;
+  a->cs = reinterpret_cast<const float2*>(table);
+  a->pos = pos;
+  return true;
+}
+
+int sf_op_qknorm_rope_fwd(const uint16_t* x, int64_t ldx, uint16_t* y, int64_t ldy,
+                          int64_t tokens, int32_t seq, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                          const uint16_t* gq, const uint16_t* gk, float eps, const float* table,
+                          const int32_t* pos, void* stream) {
+  if (!qknorm_sizes(tokens, Hq, Hkv, head_dim)) return SF_EINVAL;
+  const int64_t width = ((int64_t)Hq + 2 * (int64_t)Hkv) * head_dim;
+  if (ldx % 8 || ldy % 8 || ldx < width || ldy < width || (x == y && ldx != ldy)) return SF_EINVAL;
+  sf::QkNormArgs a;
+  if (!qknorm_check(tokens, seq, Hq, Hkv, head_dim, gq, gk, eps, table, pos, &a)) return SF_EINVAL;
+  if (tokens == 0) return SF_OK;
+  if (!x || !y || !al16(x) || !al16(y)) return SF_EINVAL;
+  int* err = dev_err_word();
+  if (!err) return SF_ECUDA;
+  sf::qknorm_rope_fwd(a, reinterpret_cast<const bf16*>(x), ldx, reinterpret_cast<bf16*>(y), ldy,
+                      err, S(stream));
+  return launched();
+}
+
+int64_t sf_op_qknorm_rope_bwd_scratch(int64_t tokens, int32_t Hq, int32_t Hkv, int32_t head_dim) {
+  if (!qknorm_sizes(tokens, Hq, Hkv, head_dim)) return -1;
+  return (int64_t)sf::qknorm_parts(tokens, Hq, Hkv, head_dim) * 2 * head_dim;
+}
+
+int sf_op_qknorm_rope_bwd(const uint16_t* x, int64_t ldx, const uint16_t* dy, int64_t lddy,
+                          uint16_t* dx, int64_t lddx, int64_t tokens, int32_t seq, int32_t Hq,
+                          int32_t Hkv, int32_t head_dim, const uint16_t* gq, const uint16_t* gk,
+                          float eps, const float* table, const int32_t* pos, float* scratch,
+                          uint16_t* dgq, uint16_t* dgk, void* stream) {
+  if (tokens < 1 || !qknorm_sizes(tokens, Hq, Hkv, head_dim)) return SF_EINVAL;
+  const int64_t width = ((int64_t)Hq + 2 * (int64_t)Hkv) * head_dim;
+  if (ldx % 8 || lddy % 8 || lddx % 8 || ldx < width || lddy < width || lddx < width) return SF_EINVAL;
+  if (x == dx || (dx == dy && lddx != lddy)) return SF_EINVAL;
+  sf::QkNormArgs a;
+  if (!qknorm_check(tokens, seq, Hq, Hkv, head_dim, gq, gk, eps, table, pos, &a)) return SF_EINVAL;
+  if (!x || !dy || !dx || !scratch || !dgq || !dgk) return SF_EINVAL;
+  if (!al16(x) || !al16(dy) || !al16(dx) || !al16(scratch) ||
+      ((reinterpret_cast<uintptr_t>(dgq) | reinterpret_cast<uintptr_t>(dgk)) & 1))
+    return SF_EINVAL;
+  int* err = dev_err_word();
+  if (!err) return SF_ECUDA;
+  sf::qknorm_rope_bwd(a, reinterpret_cast<const bf16*>(x), ldx, reinterpret_cast<const bf16*>(dy),
+                      lddy, reinterpret_cast<bf16*>(dx), lddx, scratch,
+                      reinterpret_cast<bf16*>(dgq), reinterpret_cast<bf16*>(dgk), err, S(stream));
+  return launched();
+}
+
+// Sizes and format of an 8-bit checkpoint.
+static bool ckpt8_sizes(int32_t fmt, int64_t rows, int32_t d) {
+  return (fmt == SF_CKPT_INT8 || fmt == SF_CKPT_E4M3) && rows >= 0 && rows <= INT32_MAX && d >= 8 &&
+         d % 8 == 0 && d <= 16384;
+}
+
+int64_t sf_op_ckpt8_scales(int64_t rows, int32_t d) {
+  if (!ckpt8_sizes(SF_CKPT_INT8, rows, d)) return -1;
+  return rows * ((d + 127) / 128);
+}
+
+int sf_op_ckpt8_save(const float* x, uint8_t* q, float* scale, int32_t fmt, int64_t rows,
+                     int32_t d, void* stream) {
+  if (!ckpt8_sizes(fmt, rows, d)) return SF_EINVAL;
+  if (rows == 0) return SF_OK;
+  if (!x || !q || !scale || !al16(x) || !al16(q) || !al16(scale)) return SF_EINVAL;
+  sf::ckpt8_save(x, q, scale, fmt, rows, d, S(stream));
+  return launched();
+}
+
+int sf_op_ckpt8_load(const uint8_t* q, const float* scale, float* x, int32_t fmt, int64_t rows,
+                     int32_t d, void* stream) {
+  if (!ckpt8_sizes(fmt, rows, d)) return SF_EINVAL;
+  if (rows == 0) return SF_OK;
+  if (!x || !q || !scale || !al16(x) || !al16(q) || !al16(scale)) return SF_EINVAL;
+  sf::ckpt8_load(q, scale, x, fmt, rows, d, S(stream));
+  return launched();
+}
+
+int sf_op_rmsnorm_fwd_save8(const float* x, const uint16_t* g, uint16_t* y, float* rstd,
+                            uint8_t* q, float* scale, int32_t fmt, int64_t rows, int32_t d,
+                            float eps, void* stream) {
+  if (!ckpt8_sizes(fmt, rows, d) || !(eps > 0.f)) return SF_EINVAL;
+  if (rows == 0) return SF_OK;
+  if (!x || !g || !y || !rstd || !q || !scale) return SF_EINVAL;
+  if (!al16(x) || !al16(y) || !al16(q) || !al16(scale) || !al16(g)) return SF_EINVAL;
+  sf::rmsnorm_fwd_save8(x, reinterpret_cast<const bf16*>(g), reinterpret_cast<bf16*>(y), rstd, q,
+                        scale, fmt, rows, d, eps, S(stream));
+  return launched();
+}
+
+int sf_op_rmsnorm_fwd_load8(const uint8_t* q, const float* scale, const uint16_t* g, uint16_t* y,
+                            float* rstd, float* x, int32_t fmt, int64_t rows, int32_t d, float eps,
+                            void* stream) {
+  if (!ckpt8_sizes(fmt, rows, d) || !(eps > 0.f)) return SF_EINVAL;
+  if (rows == 0) return SF_OK;
+  if (!q || !scale || !g || !y || !rstd) return SF_EINVAL;
+  if (!al16(q) || !al16(scale) || !al16(g) || !al16(y) || !al16(x)) return SF_EINVAL;
+  sf::rmsnorm_fwd_load8(q, scale, reinterpret_cast<const bf16*>(g), reinterpret_cast<bf16*>(y),
+                        rstd, x, fmt, rows, d, eps, S(stream));
+  return launched();
+}
+
+int sf_op_rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const uint16_t* g,
+                            const float* rstd, const float* dy, const float* dres, float* dx,
+                            uint16_t* dxb, uint16_t* dg, float* scratch, int32_t fmt, int64_t rows,
+                            int32_t d, void* stream) {
+  if (!ckpt8_sizes(fmt, rows, d) || rows < 1) return SF_EINVAL;
+  if (!q || !scale || !g || !rstd || !dy || !dx || !dxb || !dg || !scratch) return SF_EINVAL;
+  if (!al16(q) || !al16(scale) || !al16(g) || !al16(dy) || !al16(dres) || !al16(dx) ||
+      !al16(dxb) || !al16(scratch))
+    return SF_EINVAL;
+  const int parts = sf::rmsnorm_bwd_parts(rows, d);
+  sf::rmsnorm_bwd_load8(q, scale, reinterpret_cast<const bf16*>(g), rstd, dy, dres, dx,
+                        reinterpret_cast<bf16*>(dxb), scratch, parts, fmt, rows, d, S(stream));
+  sf::reduce_parts_bf16(scratch, parts, d, reinterpret_cast<bf16*>(dg), S(stream));
+  return launched();
+}
+
 int sf_op_swiglu_fwd(const uint16_t* ab, uint16_t* m, int64_t rows, int32_t ffn, void* stream) {
   if (rows < 0 || ffn < 8 || ffn % 8) return SF_EINVAL;
   if (rows == 0) return SF_OK;

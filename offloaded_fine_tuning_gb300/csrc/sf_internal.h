@@ -14,6 +14,7 @@ enum DevErr : int {
   kDevAttnTimeout = 2,
   kDevCeTimeout = 3,
   kDevCeBadLabel = 4,  // a label at or beyond the vocabulary (the row is ignored)
+  kDevBadPosition = 5,  // a position outside the rotation table (the token is not rotated)
 };
 
 // Operand layouts of C[M,N] = A * B (all matrices row-major in memory):
@@ -139,7 +140,70 @@ void attn_delta(const __nv_bfloat16* o, const __nv_bfloat16* dout, float* delta,
 // dQ = scale * (accumulated or slot-summed dq_acc), inverse RoPE, into the
 // query columns of dqkv (attention.cu); slots = 0 for one accumulated buffer.
 void attn_dq_finalize(const float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq, int Hkv,
-                      int hd, float scale, const float2* cs, int slots, cudaStream_t st);
+                      int hd, float scale, const float2* cs, int slots, int window, int sinks,
+                      cudaStream_t st);
+// The same attention with a sliding window and sinks: query q sees key k when
+// k <= q and (q - k < window or k < sinks).  window >= 1, sinks >= 0; both are
+// clipped to S.  dq_acc when deterministic: attn_window_dq_slots slots.
+int attn_window_fwd(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int S, int Hq,
+                    int Hkv, int hd, int window, int sinks, int* err, cudaStream_t st);
+int attn_window_bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
+                    const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B,
+                    int S, int Hq, int Hkv, int hd, int window, int sinks, const float2* cs,
+                    bool deterministic, int* err, cudaStream_t st);
+// Key blocks of 128 that the windows of a query block (64 or 128 queries,
+// aligned) can reach: its own and those of the window - 1 keys before it.
+__host__ __device__ constexpr int attn_window_slots(int window) { return (window + 126) / 128 + 1; }
+// dQ slots of the deterministic backward: one for each of the sinks' key
+// blocks, and attn_window_slots that the other key blocks take in turn.
+__host__ __device__ constexpr int attn_window_dq_slots(int S, int window, int sinks) {
+  const int w = window < S ? window : S, k = sinks < S ? sinks : S;
+  const int ns = (k + 127) / 128, rest = (S + 127) / 128 - ns, turn = attn_window_slots(w);
+  return ns + (rest < turn ? rest : turn);
+}
+
+// ---- norms of queries and keys with the rotation (qknorm.cu)
+// Rows of Hq query, Hkv key and Hkv value heads of hd columns (hd % 16 == 0,
+// 16 to 256; row strides multiples of 8).  The position of token t is pos[t],
+// or t % seq when pos is null; cs [seq, hd/2].
+struct QkNormArgs {
+  int64_t tokens = 0;
+  int seq = 0, Hq = 0, Hkv = 0, hd = 0;
+  const __nv_bfloat16 *gq = nullptr, *gk = nullptr;
+  float eps = 0.f;
+  const float2* cs = nullptr;
+  const int32_t* pos = nullptr;
+};
+// y = rotated norms of x's query and key heads; value heads copied unless y == x.
+void qknorm_rope_fwd(const QkNormArgs& a, const __nv_bfloat16* x, int64_t ldx, __nv_bfloat16* y,
+                     int64_t ldy, int* err, cudaStream_t st);
+// dx (may be dy) from dy and the raw x; the gains' gradients from fp32
+// partials in part [qknorm_parts, 2 * hd], summed in a fixed order.
+void qknorm_rope_bwd(const QkNormArgs& a, const __nv_bfloat16* x, int64_t ldx,
+                     const __nv_bfloat16* dy, int64_t lddy, __nv_bfloat16* dx, int64_t lddx,
+                     float* part, __nv_bfloat16* dgq, __nv_bfloat16* dgk, int* err,
+                     cudaStream_t st);
+int qknorm_parts(int64_t tokens, int Hq, int Hkv, int hd);
+
+// ---- 8-bit checkpoints (ckpt8.cu): codes [rows, d], fp32 scales
+// [rows, ceil(d / 128)], one for each block of 128 columns (sf.h has the rule).
+void ckpt8_save(const float* x, uint8_t* q, float* scale, int fmt, int64_t rows, int d,
+                cudaStream_t st);
+void ckpt8_load(const uint8_t* q, const float* scale, float* x, int fmt, int64_t rows, int d,
+                cudaStream_t st);
+// rmsnorm_fwd that also saves x.
+void rmsnorm_fwd_save8(const float* x, const __nv_bfloat16* g, __nv_bfloat16* y, float* rstd,
+                       uint8_t* q, float* scale, int fmt, int64_t rows, int d, float eps,
+                       cudaStream_t st);
+// rmsnorm_fwd of the saved values; xout (null: none) gets them too.
+void rmsnorm_fwd_load8(const uint8_t* q, const float* scale, const __nv_bfloat16* g,
+                       __nv_bfloat16* y, float* rstd, float* xout, int fmt, int64_t rows, int d,
+                       float eps, cudaStream_t st);
+// rmsnorm_bwd at the saved values; dg_part [rmsnorm_bwd_parts, d].
+void rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const __nv_bfloat16* g,
+                       const float* rstd, const float* dy, const float* dres, float* dx,
+                       __nv_bfloat16* dxb, float* dg_part, int parts, int fmt, int64_t rows, int d,
+                       cudaStream_t st);
 
 int num_sms();
 
