@@ -272,7 +272,7 @@ int sf_op_qknorm_rope_fwd(const uint16_t* x, int64_t ldx, uint16_t* y, int64_t l
 
 int64_t sf_op_qknorm_rope_bwd_scratch(int64_t tokens, int32_t Hq, int32_t Hkv, int32_t head_dim) {
   if (!qknorm_sizes(tokens, Hq, Hkv, head_dim)) return -1;
-  return (int64_t)sf::qknorm_parts(tokens, Hq, Hkv, head_dim) * 2 * head_dim;
+  return (int64_t)sf::qknorm_parts(tokens, Hq, head_dim) * 2 * head_dim;
 }
 
 int sf_op_qknorm_rope_bwd(const uint16_t* x, int64_t ldx, const uint16_t* dy, int64_t lddy,

@@ -27,10 +27,11 @@ namespace {
 
 typedef __nv_bfloat16 bf16;
 
-constexpr int kQkThreads = 256;
+constexpr int kQkThreads = 128;
 constexpr int kQkWarps = kQkThreads / 32;
-constexpr int kQkFwdSteps = 4;  // head groups a warp has in flight, forward
-constexpr int kQkBwdSteps = 2;  // and backward (x and dy)
+constexpr int kQkCtas = 4;       // resident CTAs an SM is given
+constexpr int kQkFwdStages = 8;  // steps a lane has in flight, forward (x)
+constexpr int kQkBwdStages = 5;  // and backward (x and dy)
 
 __device__ __forceinline__ void unpack(const uint4& u, float* f) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
@@ -81,199 +82,258 @@ __device__ __forceinline__ void rotation(const QkNormArgs& a, int64_t t, int sub
   }
 }
 
-// One warp per token and chunk of kQkFwdSteps groups of 32 / TPH heads; the
-// heads from Hq + Hkv on (the values) are copied.
-template <int TPH>
-__global__ void __launch_bounds__(kQkThreads)
-    qknorm_fwd_kernel(const QkNormArgs a, const bf16* x, int64_t ldx, bf16* y,
-                      int64_t ldy, int heads, int chunks, int* err) {
-  constexpr int G = 32 / TPH;
-  const int lane = threadIdx.x & 31, sub = lane % TPH, slot = lane / TPH;
-  const int64_t unit = (int64_t)blockIdx.x * kQkWarps + (threadIdx.x >> 5);
-  const int64_t t = unit / chunks;
-  const int h0 = (int)(unit - t * chunks) * (kQkFwdSteps * G) + slot;
-  if (t >= a.tokens) return;
-  const int half = a.hd / 2;
-  const bool in = 8 * sub < half;
-  uint4 lo[kQkFwdSteps], hi[kQkFwdSteps];
-#pragma unroll
-  for (int u = 0; u < kQkFwdSteps; ++u) {
-    const int h = h0 + u * G;
-    lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-    if (in && h < heads) {
-      const bf16* p = x + t * ldx + (int64_t)h * a.hd + 8 * sub;
-      lo[u] = *reinterpret_cast<const uint4*>(p);
-      hi[u] = *reinterpret_cast<const uint4*>(p + half);
-    }
-  }
-  float co[8], si[8];
-  uint4 g[2][2] = {};
-  if (in) {
-    rotation(a, t, sub, co, si, err);
-    g[0][0] = *reinterpret_cast<const uint4*>(a.gq + 8 * sub);
-    g[0][1] = *reinterpret_cast<const uint4*>(a.gq + half + 8 * sub);
-    g[1][0] = *reinterpret_cast<const uint4*>(a.gk + 8 * sub);
-    g[1][1] = *reinterpret_cast<const uint4*>(a.gk + half + 8 * sub);
-  }
-#pragma unroll
-  for (int u = 0; u < kQkFwdSteps; ++u) {
-    const int h = h0 + u * G;
-    float x1[8], x2[8], ss = 0.f;
-    unpack(lo[u], x1);
-    unpack(hi[u], x2);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x1[i] * x1[i] + x2[i] * x2[i];
-    ss = head_sum<TPH>(ss);
-    if (!in || h >= heads) continue;
-    if (h < a.Hq + a.Hkv) {
-      const float r = rsqrtf(ss / a.hd + a.eps);
-      float g1[8], g2[8], y1[8], y2[8];
-      unpack(h < a.Hq ? g[0][0] : g[1][0], g1);
-      unpack(h < a.Hq ? g[0][1] : g[1][1], g2);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float z1 = x1[i] * r * g1[i], z2 = x2[i] * r * g2[i];
-        y1[i] = z1 * co[i] - z2 * si[i];
-        y2[i] = z2 * co[i] + z1 * si[i];
-      }
-      lo[u] = pack(y1);
-      hi[u] = pack(y2);
-    }
-    bf16* p = y + t * ldy + (int64_t)h * a.hd + 8 * sub;
-    *reinterpret_cast<uint4*>(p) = lo[u];
-    *reinterpret_cast<uint4*>(p + half) = hi[u];
-  }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src)
+               : "memory");
+  return v;
 }
 
-// The heads [first, first + count) of every token with gain g: writes dx and
-// adds dz * xh of the lane's columns into acc (eight of each half).
-template <int TPH>
-__device__ __forceinline__ void bwd_heads(const QkNormArgs& a, const bf16* __restrict__ x,
-                                          int64_t ldx, const bf16* dy, int64_t lddy, bf16* dx,
-                                          int64_t lddx, int first, int count, const bf16* g,
-                                          float (&acc)[16], int* err) {
+// Head ranges that a token's steps go through: steps of 32 / TPH heads, first
+// the query heads, then the key heads, then (vals) the value heads.
+struct Steps {
+  int q, k, v;
+  __device__ __forceinline__ int all() const { return q + k + v; }
+};
+
+// All steps of all tokens in token order, of which each warp takes an equal
+// contiguous range.  A lane copies its 16-byte pieces of the steps ahead (NS
+// of them a step: both halves of x, and of dy) into its own places of a ring
+// in shared memory, STAGES - 1 steps before it reads them back, so no barrier
+// is needed and the bytes in flight do not depend on registers.
+// body(t, kind, h, live, piece[NS]) gets the token, the kind of head (0 query,
+// 1 key, 2 value), the lane's head and whether the lane holds a piece of it.
+template <int TPH, int NS, int STAGES, class Body>
+__device__ __forceinline__ void each_step(const QkNormArgs& a, const Steps& ss, uint32_t ring,
+                                          const bf16* x, int64_t ldx, const bf16* dy, int64_t lddy,
+                                          Body&& body) {
   constexpr int G = 32 / TPH;
   const int lane = threadIdx.x & 31, sub = lane % TPH, slot = lane / TPH;
-  const int half = a.hd / 2;
+  const int steps = ss.all(), hd = a.hd, half = hd / 2;
   const bool in = 8 * sub < half;
-  const int chunks = (count + kQkBwdSteps * G - 1) / (kQkBwdSteps * G);
-  const int64_t units = a.tokens * chunks;
-  const float inv_hd = 1.f / a.hd;
-  float g1[8], g2[8];
-  {
-    uint4 a1 = make_uint4(0, 0, 0, 0), a2 = a1;
-    if (in) {
-      a1 = *reinterpret_cast<const uint4*>(g + 8 * sub);
-      a2 = *reinterpret_cast<const uint4*>(g + half + 8 * sub);
+  const int64_t n = a.tokens * steps;
+  // kind and head of the lane at step i; false where it has none
+  auto head = [&](int i, int& kind, int& h) -> bool {
+    kind = i < ss.q ? 0 : i < ss.q + ss.k ? 1 : 2;
+    h = (i - (kind == 0 ? 0 : kind == 1 ? ss.q : ss.q + ss.k)) * G + slot;
+    const bool live = in && h < (kind == 0 ? a.Hq : a.Hkv);
+    h += kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + a.Hkv;
+    return live;
+  };
+  const int64_t warps = (int64_t)gridDim.x * kQkWarps;
+  const int64_t w = (int64_t)blockIdx.x * kQkWarps + (threadIdx.x >> 5);
+  // warp w's range: n / warps steps, the first n % warps warps one more
+  const int64_t each = n / warps, more = n - each * warps;
+  const int64_t begin = w * each + (w < more ? w : more);
+  const int left0 = (int)(each + (w < more ? 1 : 0));
+  struct Cursor {
+    int64_t t;
+    int i, left;
+  };
+  Cursor pf{begin / steps, (int)(begin % steps), left0}, cur = pf;
+  auto advance = [&](Cursor& c) {
+    --c.left;
+    if (++c.i == steps) {
+      c.i = 0;
+      ++c.t;
     }
-    unpack(a1, g1);
-    unpack(a2, g2);
+  };
+  int put = 0;
+  auto issue = [&]() {
+    if (pf.left > 0) {
+      int kind, h;
+      if (head(pf.i, kind, h)) {
+        const int64_t c = (int64_t)h * hd + 8 * sub;
+        const uint32_t at = ring + (uint32_t)(put * NS * kQkThreads) * 16u;
+        copy16(at, x + pf.t * ldx + c);
+        copy16(at + kQkThreads * 16, x + pf.t * ldx + c + half);
+        if (NS == 4) {
+          copy16(at + 2 * kQkThreads * 16, dy + pf.t * lddy + c);
+          copy16(at + 3 * kQkThreads * 16, dy + pf.t * lddy + c + half);
+        }
+      }
+      advance(pf);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    put = put + 1 == STAGES ? 0 : put + 1;
+  };
+#pragma unroll 1
+  for (int k = 0; k < STAGES - 1; ++k) issue();
+  int get = 0;
+#pragma unroll 1
+  while (cur.left > 0) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    int kind, h;
+    const bool live = head(cur.i, kind, h);
+    uint4 piece[NS];
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      piece[k] = make_uint4(0, 0, 0, 0);
+      if (live) piece[k] = lds16(ring + (uint32_t)((get * NS + k) * kQkThreads) * 16u);
+    }
+    body(cur.t, kind, h, live, piece);
+    // into the place that the step before this one was read from
+    issue();
+    advance(cur);
+    get = get + 1 == STAGES ? 0 : get + 1;
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int64_t unit = (int64_t)blockIdx.x * kQkWarps + (threadIdx.x >> 5); unit < units;
-       unit += (int64_t)gridDim.x * kQkWarps) {
-    const int64_t t = unit / chunks;
-    const int h0 = (int)(unit - t * chunks) * (kQkBwdSteps * G) + slot;
-    uint4 xl[kQkBwdSteps], xh[kQkBwdSteps], dl[kQkBwdSteps], dh[kQkBwdSteps];
-#pragma unroll
-    for (int u = 0; u < kQkBwdSteps; ++u) {
-      const int h = h0 + u * G;
-      xl[u] = xh[u] = dl[u] = dh[u] = make_uint4(0, 0, 0, 0);
-      if (in && h < count) {
-        const int64_t c = (int64_t)(first + h) * a.hd + 8 * sub;
-        xl[u] = *reinterpret_cast<const uint4*>(x + t * ldx + c);
-        xh[u] = *reinterpret_cast<const uint4*>(x + t * ldx + c + half);
-        dl[u] = *reinterpret_cast<const uint4*>(dy + t * lddy + c);
-        dh[u] = *reinterpret_cast<const uint4*>(dy + t * lddy + c + half);
-      }
-    }
-    float co[8], si[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) co[i] = si[i] = 0.f;
-    if (in) rotation(a, t, sub, co, si, err);
-#pragma unroll
-    for (int u = 0; u < kQkBwdSteps; ++u) {
-      const int h = h0 + u * G;
-      float x1[8], x2[8], d1[8], d2[8], ss = 0.f, dot = 0.f;
-      unpack(xl[u], x1);
-      unpack(xh[u], x2);
-      unpack(dl[u], d1);
-      unpack(dh[u], d2);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss += x1[i] * x1[i] + x2[i] * x2[i];
-        const float z1 = d1[i] * co[i] + d2[i] * si[i], z2 = d2[i] * co[i] - d1[i] * si[i];
-        d1[i] = z1;
-        d2[i] = z2;
-        dot += g1[i] * z1 * x1[i] + g2[i] * z2 * x2[i];
-      }
-      ss = head_sum<TPH>(ss);
-      dot = head_sum<TPH>(dot);
-      const float r = rsqrtf(ss * inv_hd + a.eps);
-      const float m = r * dot * inv_hd * r;  // mean(g dz xh) * r, to multiply x by
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[i] += d1[i] * (x1[i] * r);
-        acc[8 + i] += d2[i] * (x2[i] * r);
-        d1[i] = r * (g1[i] * d1[i] - m * x1[i]);
-        d2[i] = r * (g2[i] * d2[i] - m * x2[i]);
-      }
-      if (in && h < count) {
-        bf16* p = dx + t * lddx + (int64_t)(first + h) * a.hd + 8 * sub;
-        *reinterpret_cast<uint4*>(p) = pack(d1);
-        *reinterpret_cast<uint4*>(p + half) = pack(d2);
-      }
-    }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <int TPH>
+__device__ __forceinline__ Steps steps_of(const QkNormArgs& a, bool q, bool k, bool v) {
+  constexpr int G = 32 / TPH;
+  const int kv = (a.Hkv + G - 1) / G;
+  return {q ? (a.Hq + G - 1) / G : 0, k ? kv : 0, v ? kv : 0};
+}
+
+// Persistent CTAs; the value heads are copied unless the call is in place.
+template <int TPH>
+__global__ void __launch_bounds__(kQkThreads, kQkCtas)
+    qknorm_fwd_kernel(const QkNormArgs a, const bf16* x, int64_t ldx, bf16* y, int64_t ldy, int* err) {
+  __shared__ __align__(16) uint8_t buf[2 * kQkFwdStages * kQkThreads * 16];
+  const uint32_t ring = smem_u32(buf) + threadIdx.x * 16;
+  const int sub = (threadIdx.x & 31) % TPH, half = a.hd / 2;
+  const bool in = 8 * sub < half;
+  uint4 gq1 = {}, gq2 = {}, gk1 = {}, gk2 = {};
+  if (in) {
+    gq1 = *reinterpret_cast<const uint4*>(a.gq + 8 * sub);
+    gq2 = *reinterpret_cast<const uint4*>(a.gq + half + 8 * sub);
+    gk1 = *reinterpret_cast<const uint4*>(a.gk + 8 * sub);
+    gk2 = *reinterpret_cast<const uint4*>(a.gk + half + 8 * sub);
   }
-  // the head groups of the warp hold the same columns
+  float co[8], si[8];
+  int64_t at = -1;  // the token whose rotation is in co, si
+  each_step<TPH, 2, kQkFwdStages>(
+      a, steps_of<TPH>(a, true, true, x != y), ring, x, ldx, nullptr, 0,
+      [&](int64_t t, int kind, int h, bool live, uint4 (&piece)[2]) {
+        if (kind < 2) {
+          if (t != at) {
+            if (in) rotation(a, t, sub, co, si, err);
+            at = t;
+          }
+          float x1[8], x2[8], g1[8], g2[8], ss = 0.f;
+          unpack(piece[0], x1);
+          unpack(piece[1], x2);
+          unpack(kind ? gk1 : gq1, g1);
+          unpack(kind ? gk2 : gq2, g2);
 #pragma unroll
-  for (int o = 16; o >= TPH; o >>= 1)
+          for (int i = 0; i < 8; ++i) ss += x1[i] * x1[i] + x2[i] * x2[i];
+          ss = head_sum<TPH>(ss);
+          const float r = rsqrtf(ss / a.hd + a.eps);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+          for (int i = 0; i < 8; ++i) {
+            const float z1 = x1[i] * r * g1[i], z2 = x2[i] * r * g2[i];
+            x1[i] = z1 * co[i] - z2 * si[i];
+            x2[i] = z2 * co[i] + z1 * si[i];
+          }
+          piece[0] = pack(x1);
+          piece[1] = pack(x2);
+        }
+        if (!live) return;
+        bf16* p = y + t * ldy + (int64_t)h * a.hd + 8 * sub;
+        *reinterpret_cast<uint4*>(p) = piece[0];
+        *reinterpret_cast<uint4*>(p + half) = piece[1];
+      });
 }
 
 // Persistent CTAs: all query heads, then all key heads (so one gain and one
-// set of sums is in registers at a time), then the value columns are copied.
+// set of sums is in registers at a time), then the value heads are copied.
 // Every CTA writes the sums of its heads to its row of part [gridDim, 2 hd].
 template <int TPH>
-__global__ void __launch_bounds__(kQkThreads, 2)
+__global__ void __launch_bounds__(kQkThreads, kQkCtas)
     qknorm_bwd_kernel(const QkNormArgs a, const bf16* __restrict__ x, int64_t ldx, const bf16* dy,
                       int64_t lddy, bf16* dx, int64_t lddx, float* __restrict__ part, int* err) {
-  __shared__ float sums[kQkWarps][2][16 * TPH];
+  __shared__ __align__(16) uint8_t buf[4 * kQkBwdStages * kQkThreads * 16];
+  const uint32_t ring = smem_u32(buf) + threadIdx.x * 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int half = a.hd / 2;
-  float acc[16];
-#pragma unroll
+  const int sub = lane % TPH, half = a.hd / 2;
+  const bool in = 8 * sub < half;
+  const float inv_hd = 1.f / a.hd;
+#pragma unroll 1
   for (int k = 0; k < 2; ++k) {
-    bwd_heads<TPH>(a, x, ldx, dy, lddy, dx, lddx, k ? a.Hq : 0, k ? a.Hkv : a.Hq, k ? a.gk : a.gq,
-                   acc, err);
+    float g1[8] = {}, g2[8] = {}, co[8] = {}, si[8] = {}, acc[16] = {};
+    if (in) {
+      const bf16* g = (k ? a.gk : a.gq) + 8 * sub;
+      unpack(*reinterpret_cast<const uint4*>(g), g1);
+      unpack(*reinterpret_cast<const uint4*>(g + half), g2);
+    }
+    int64_t at = -1;  // the token whose rotation is in co, si
+    each_step<TPH, 4, kQkBwdStages>(
+        a, steps_of<TPH>(a, k == 0, k == 1, false), ring, x, ldx, dy, lddy,
+        [&](int64_t t, int, int h, bool live, const uint4 (&piece)[4]) {
+          if (t != at) {
+            if (in) rotation(a, t, sub, co, si, err);
+            at = t;
+          }
+          float x1[8], x2[8], d1[8], d2[8], ss = 0.f, dot = 0.f;
+          unpack(piece[0], x1);
+          unpack(piece[1], x2);
+          unpack(piece[2], d1);
+          unpack(piece[3], d2);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            ss += x1[i] * x1[i] + x2[i] * x2[i];
+            const float z1 = d1[i] * co[i] + d2[i] * si[i], z2 = d2[i] * co[i] - d1[i] * si[i];
+            d1[i] = z1;
+            d2[i] = z2;
+            dot += g1[i] * z1 * x1[i] + g2[i] * z2 * x2[i];
+          }
+          ss = head_sum<TPH>(ss);
+          dot = head_sum<TPH>(dot);
+          const float r = rsqrtf(ss * inv_hd + a.eps);
+          const float m = r * dot * inv_hd * r;  // mean(g dz xh) * r, to multiply x by
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[i] += d1[i] * (x1[i] * r);
+            acc[8 + i] += d2[i] * (x2[i] * r);
+            d1[i] = r * (g1[i] * d1[i] - m * x1[i]);
+            d2[i] = r * (g2[i] * d2[i] - m * x2[i]);
+          }
+          if (!live) return;
+          bf16* p = dx + t * lddx + (int64_t)h * a.hd + 8 * sub;
+          *reinterpret_cast<uint4*>(p) = pack(d1);
+          *reinterpret_cast<uint4*>(p + half) = pack(d2);
+        });
+    // the head groups of the warp hold the same columns
+#pragma unroll
+    for (int o = 16; o >= TPH; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    // the warps' sums meet in the ring, which every lane has emptied
+    float* sums = reinterpret_cast<float*>(buf);
+    __syncthreads();
     if (lane < TPH) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sums[warp][k][8 * lane + i] = acc[i];
-        sums[warp][k][8 * TPH + 8 * lane + i] = acc[8 + i];
+        sums[warp * 16 * TPH + 8 * lane + i] = acc[i];
+        sums[warp * 16 * TPH + 8 * TPH + 8 * lane + i] = acc[8 + i];
       }
     }
-  }
-  if (dx != dy) {
-    const int n = a.Hkv * a.hd / 8;  // 16-byte pieces of a token's values
-    const int64_t c0 = (int64_t)(a.Hq + a.Hkv) * a.hd;
-    for (int64_t i = (int64_t)blockIdx.x * kQkThreads + threadIdx.x; i < a.tokens * n;
-         i += (int64_t)gridDim.x * kQkThreads) {
-      const int64_t t = i / n, c = c0 + (i - t * n) * 8;
-      *reinterpret_cast<uint4*>(dx + t * lddx + c) = *reinterpret_cast<const uint4*>(dy + t * lddy + c);
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * a.hd; i += kQkThreads) {
-    const int k = i / a.hd, j = i - k * a.hd;
-    const int at = j < half ? j : 8 * TPH + j - half;
-    float s = 0.f;
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.hd; j += kQkThreads) {
+      const int c = j < half ? j : 8 * TPH + j - half;
+      float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kQkWarps; ++w) s += sums[w][k][at];
-    part[(int64_t)blockIdx.x * 2 * a.hd + i] = s;
+      for (int w = 0; w < kQkWarps; ++w) s += sums[w * 16 * TPH + c];
+      part[((int64_t)blockIdx.x * 2 + k) * a.hd + j] = s;
+    }
+    __syncthreads();
   }
+  if (dx != dy)
+    each_step<TPH, 2, kQkFwdStages>(
+        a, steps_of<TPH>(a, false, false, true), ring, dy, lddy, nullptr, 0,
+        [&](int64_t t, int, int h, bool live, const uint4 (&piece)[2]) {
+          if (!live) return;
+          bf16* p = dx + t * lddx + (int64_t)h * a.hd + 8 * sub;
+          *reinterpret_cast<uint4*>(p) = piece[0];
+          *reinterpret_cast<uint4*>(p + half) = piece[1];
+        });
 }
 
 // dgq[j] and dgk[j]: column sums of the partials, in a fixed order.  A CTA
@@ -307,42 +367,41 @@ int lanes_per_head(int hd) {
   return n;
 }
 
-template <int TPH>
-void fwd(const QkNormArgs& a, const bf16* x, int64_t ldx, bf16* y, int64_t ldy, int* err,
-         cudaStream_t st) {
-  const int heads = a.Hq + (x == y ? 1 : 2) * a.Hkv;
-  const int per = kQkFwdSteps * (32 / TPH);
-  const int chunks = (heads + per - 1) / per;
-  const int64_t grid = (a.tokens * chunks + kQkWarps - 1) / kQkWarps;
-  qknorm_fwd_kernel<TPH><<<(unsigned)grid, kQkThreads, 0, st>>>(a, x, ldx, y, ldy, heads, chunks, err);
+// CTAs for n steps (each a group of 32 / TPH heads of a token): as many as the
+// steps fill, at most what the SMs hold at once.
+int qk_ctas(int64_t n) {
+  const int64_t need = (n + kQkWarps - 1) / kQkWarps;
+  const int most = kQkCtas * num_sms();
+  return need < most ? (int)(need > 0 ? need : 1) : most;
+}
+
+int64_t head_steps(int heads, int hd) {
+  const int per = 32 / lanes_per_head(hd);
+  return (heads + per - 1) / per;
 }
 
 }  // namespace
 
-int qknorm_parts(int64_t tokens, int Hq, int Hkv, int hd) {
-  // as many CTAs as the query heads fill, at most what the SMs hold at once
-  const int per = kQkBwdSteps * (32 / lanes_per_head(hd));
-  const int64_t need = (tokens * ((Hq + per - 1) / per) + kQkWarps - 1) / kQkWarps;
-  const int most = 2 * num_sms();
-  (void)Hkv;
-  return need < most ? (int)(need > 0 ? need : 1) : most;
-}
+int qknorm_parts(int64_t tokens, int Hq, int hd) { return qk_ctas(tokens * head_steps(Hq, hd)); }
 
 void qknorm_rope_fwd(const QkNormArgs& a, const bf16* x, int64_t ldx, bf16* y, int64_t ldy,
                      int* err, cudaStream_t st) {
+  const int grid = qk_ctas(a.tokens * (head_steps(a.Hq, a.hd) + (x == y ? 1 : 2) * head_steps(a.Hkv, a.hd)));
+#define SF_QK_FWD(T) qknorm_fwd_kernel<T><<<grid, kQkThreads, 0, st>>>(a, x, ldx, y, ldy, err)
   switch (lanes_per_head(a.hd)) {
-    case 1: return fwd<1>(a, x, ldx, y, ldy, err, st);
-    case 2: return fwd<2>(a, x, ldx, y, ldy, err, st);
-    case 4: return fwd<4>(a, x, ldx, y, ldy, err, st);
-    case 8: return fwd<8>(a, x, ldx, y, ldy, err, st);
-    default: return fwd<16>(a, x, ldx, y, ldy, err, st);
+    case 1: SF_QK_FWD(1); break;
+    case 2: SF_QK_FWD(2); break;
+    case 4: SF_QK_FWD(4); break;
+    case 8: SF_QK_FWD(8); break;
+    default: SF_QK_FWD(16);
   }
+#undef SF_QK_FWD
 }
 
 void qknorm_rope_bwd(const QkNormArgs& a, const bf16* x, int64_t ldx, const bf16* dy, int64_t lddy,
                      bf16* dx, int64_t lddx, float* part, bf16* dgq, bf16* dgk, int* err,
                      cudaStream_t st) {
-  const int parts = qknorm_parts(a.tokens, a.Hq, a.Hkv, a.hd);
+  const int parts = qknorm_parts(a.tokens, a.Hq, a.hd);
 #define SF_QK_BWD(T) \
   qknorm_bwd_kernel<T><<<parts, kQkThreads, 0, st>>>(a, x, ldx, dy, lddy, dx, lddx, part, err)
   switch (lanes_per_head(a.hd)) {

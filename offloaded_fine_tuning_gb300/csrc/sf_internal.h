@@ -183,7 +183,7 @@ void qknorm_rope_bwd(const QkNormArgs& a, const __nv_bfloat16* x, int64_t ldx,
                      const __nv_bfloat16* dy, int64_t lddy, __nv_bfloat16* dx, int64_t lddx,
                      float* part, __nv_bfloat16* dgq, __nv_bfloat16* dgk, int* err,
                      cudaStream_t st);
-int qknorm_parts(int64_t tokens, int Hq, int Hkv, int hd);
+int qknorm_parts(int64_t tokens, int Hq, int hd);
 
 // ---- 8-bit checkpoints (ckpt8.cu): codes [rows, d], fp32 scales
 // [rows, ceil(d / 128)], one for each block of 128 columns (sf.h has the rule).
