@@ -21,6 +21,9 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
+#include <utility>
+#include <vector>
 
 #include "sf.h"
 #include "sf_internal.h"
@@ -254,78 +257,216 @@ void norm_fwd8(const float* x, const bf16* g, bf16* y, float* rstd, uint8_t* q, 
 }
 
 // ------------------------------------------------------------------ RMSNorm backward
-// CTAs stride over rows; a thread owns the same columns of every row, so the
-// gain gradient of the CTA's rows stays in registers.
+// One CTA of 512 threads per SM, in groups of `lanes` threads (a power of two,
+// 32 to 512) that take a row each, so a thread holds at most CH quads of four
+// columns: 4 up to d = 8192 (narrower rows run several at a time), then 6 and
+// 8.  A thread copies its quads of the rows ahead (dy, dres and the codes, 36
+// bytes a quad; a warp's scales and the row's rstd with them) into its own
+// places of a ring in shared memory with cp.async and reads them back itself:
+// 74 KB (CH 4, three rows deep) to 110 KB (CH 6, two) are in flight per SM
+// whatever the registers hold, no barrier but the row's sum stands between
+// rows, and d % 16 == 8 needs no special case, as a bulk copy would.  At CH 8
+// the ring holds dy and the codes, and dres is only brought into L2 ahead.
+// The gain gradient of a thread's columns stays in registers over all rows.
+constexpr int kBwdThreads = 512;
+
+template <int CH>
+struct BwdRing {
+  static constexpr bool RES = CH <= 6;  // dres is in the ring
+  static constexpr int STAGES = CH <= 4 ? 3 : 2;
+  static constexpr int DY = 0, DRES = CH * kBwdThreads * 16;
+  static constexpr int CODES = DRES + (RES ? CH * kBwdThreads * 16 : 0);
+  static constexpr int SCALES = CODES + CH * kBwdThreads * 4;  // [16 warps][12]: CH scales, rstd at 8
+  static constexpr int STAGE = SCALES + kBwdThreads / 32 * 48;
+};
+static_assert(BwdRing<4>::STAGES * BwdRing<4>::STAGE <= 230000, "ring of 4 quads");
+static_assert(BwdRing<6>::STAGES * BwdRing<6>::STAGE <= 230000, "ring of 6 quads");
+static_assert(BwdRing<8>::STAGES * BwdRing<8>::STAGE <= 230000, "ring of 8 quads");
+
+__device__ __forceinline__ void async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <int CH, int FMT>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     norm_bwd8_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scale,
                      const bf16* __restrict__ g, const float* __restrict__ rstd,
                      const float* __restrict__ dy, const float* __restrict__ dres,
                      float* __restrict__ dx, bf16* __restrict__ dxb, float* __restrict__ dg_part,
-                     int64_t rows, int nb, int d) {
-  __shared__ float sh[32];
+                     int64_t rows, int nb, int d, int lanes) {
+  using R = BwdRing<CH>;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float sums[2][kBwdThreads / 32];  // the warps' sums of a row, of two rows in turn
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = threadIdx.x / lanes, t = threadIdx.x % lanes, groups = kBwdThreads / lanes;
   const int n4 = d >> 2;
   const float inv_d = 1.f / d;
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  uint2 gg[CH];
   float4 gacc[CH];
 #pragma unroll
-  for (int k = 0; k < CH; ++k) gacc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const float r = rstd[row];
-    float4 dv[CH], xh[CH];
+  for (int k = 0; k < CH; ++k) {
+    const int i = t + k * lanes;
+    gacc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    gg[k] = i < n4 ? reinterpret_cast<const uint2*>(g)[i] : make_uint2(0u, 0u);
+  }
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  int put = 0;
+  auto issue = [&](int64_t row) {
+    if (row < rows) {
+      const uint32_t st = base + (uint32_t)put * R::STAGE;
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int i = t + k * lanes;
+        if (i < n4) {
+          const uint32_t at = (uint32_t)(k * kBwdThreads + threadIdx.x);
+          async16(st + R::DY + at * 16, dy + row * d + 4 * i);
+          if (dres) {
+            if (R::RES) async16(st + R::DRES + at * 16, dres + row * d + 4 * i);
+            else asm volatile("prefetch.global.L2 [%0];" ::"l"(dres + row * d + 4 * i));
+          }
+          async4(st + R::CODES + at * 4, q + row * d + 4 * i);
+        }
+      }
+      // lane k < CH copies the scale of the warp's k-th block
+      const int i0 = (t & ~31) + lane * lanes;
+      if (lane < CH && i0 < n4)
+        async4(st + R::SCALES + (uint32_t)(warp * 12 + lane) * 4, scale + row * nb + (i0 >> 5));
+      if (lane == 8) async4(st + R::SCALES + (uint32_t)(warp * 12 + 8) * 4, rstd + row);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    put = put + 1 == R::STAGES ? 0 : put + 1;
+  };
+  const int64_t row0 = (int64_t)blockIdx.x * groups + group;
+  for (int k = 0; k < R::STAGES - 1; ++k) issue(row0 + k * stride);
+  int get = 0, par = 0;
+#pragma unroll 1
+  for (int64_t row = row0; row < rows; row += stride) {
+    issue(row + (R::STAGES - 1) * stride);
+    asm volatile("cp.async.wait_group %0;" ::"n"(R::STAGES - 1) : "memory");
+    __syncwarp();
+    const uint8_t* st = ring + get * R::STAGE;
+    const float4* sdy = reinterpret_cast<const float4*>(st + R::DY);
+    const float4* sdr = reinterpret_cast<const float4*>(st + R::DRES);
+    const uint32_t* sq = reinterpret_cast<const uint32_t*>(st + R::CODES);
+    const float* ss = reinterpret_cast<const float*>(st + R::SCALES) + warp * 12;
+    const float r = ss[8];
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int i = threadIdx.x + k * 512;
-      dv[k] = xh[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < n4) {
-        dv[k] = reinterpret_cast<const float4*>(dy + row * d)[i];
-        xh[k] = decode<FMT>(reinterpret_cast<const uint32_t*>(q + row * d)[i],
-                            scale[row * nb + (i >> 5)]);
-        const float4 gg = unpack4(reinterpret_cast<const uint2*>(g)[i]);
-        xh[k] = make_float4(xh[k].x * r, xh[k].y * r, xh[k].z * r, xh[k].w * r);
-        gacc[k].x += dv[k].x * xh[k].x; gacc[k].y += dv[k].y * xh[k].y;
-        gacc[k].z += dv[k].z * xh[k].z; gacc[k].w += dv[k].w * xh[k].w;
-        dv[k] = make_float4(dv[k].x * gg.x, dv[k].y * gg.y, dv[k].z * gg.z, dv[k].w * gg.w);
-        dot += dv[k].x * xh[k].x + dv[k].y * xh[k].y + dv[k].z * xh[k].z + dv[k].w * xh[k].w;
+      const int at = k * kBwdThreads + threadIdx.x;
+      if (t + k * lanes < n4) {
+        const float4 dv = sdy[at], w = unpack4(gg[k]);
+        float4 xh = decode<FMT>(sq[at], ss[k]);
+        xh = make_float4(xh.x * r, xh.y * r, xh.z * r, xh.w * r);
+        const float4 p = make_float4(dv.x * xh.x, dv.y * xh.y, dv.z * xh.z, dv.w * xh.w);
+        gacc[k].x += p.x; gacc[k].y += p.y; gacc[k].z += p.z; gacc[k].w += p.w;
+        dot += w.x * p.x + w.y * p.y + w.z * p.z + w.w * p.w;
       }
     }
-    dot = block_sum(dot, sh) * inv_d;
+    dot = warp_sum(dot);
+    if (lanes > 32) {
+      if (lane == 0) sums[par][warp] = dot;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
+      const int first = group * (lanes >> 5), n = lanes >> 5;
+      dot = warp_sum(lane < n ? sums[par][first + lane] : 0.f);
+      par ^= 1;
+    }
+    dot *= inv_d;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int i = threadIdx.x + k * 512;
+      const int at = k * kBwdThreads + threadIdx.x, i = t + k * lanes;
       if (i < n4) {
-        float4 o = dres ? reinterpret_cast<const float4*>(dres + row * d)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-        o.x += r * (dv[k].x - xh[k].x * dot);
-        o.y += r * (dv[k].y - xh[k].y * dot);
-        o.z += r * (dv[k].z - xh[k].z * dot);
-        o.w += r * (dv[k].w - xh[k].w * dot);
+        const float4 dv = sdy[at], w = unpack4(gg[k]);
+        float4 xh = decode<FMT>(sq[at], ss[k]);
+        xh = make_float4(xh.x * r, xh.y * r, xh.z * r, xh.w * r);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (dres) o = R::RES ? sdr[at] : reinterpret_cast<const float4*>(dres + row * d)[i];
+        o.x += r * (w.x * dv.x - xh.x * dot);
+        o.y += r * (w.y * dv.y - xh.y * dot);
+        o.z += r * (w.z * dv.z - xh.z * dot);
+        o.w += r * (w.w * dv.w - xh.w * dot);
         reinterpret_cast<float4*>(dx + row * d)[i] = o;
         reinterpret_cast<uint2*>(dxb + row * d)[i] = pack4(o.x, o.y, o.z, o.w);
       }
     }
+    __syncwarp();  // the warp's scales have been read: the next copies may replace them
+    get = get + 1 == R::STAGES ? 0 : get + 1;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   float4* part = reinterpret_cast<float4*>(dg_part + (int64_t)blockIdx.x * d);
+  if (groups == 1) {
 #pragma unroll
-  for (int k = 0; k < CH; ++k) {
-    const int i = threadIdx.x + k * 512;
-    if (i < n4) part[i] = gacc[k];
+    for (int k = 0; k < CH; ++k)
+      if (t + k * lanes < n4) part[t + k * lanes] = gacc[k];
+    return;
+  }
+  // the groups hold the same columns: joined in their order
+  __syncthreads();
+  float4* join = reinterpret_cast<float4*>(ring);  // [groups][CH * lanes]
+#pragma unroll
+  for (int k = 0; k < CH; ++k) join[(group * CH + k) * lanes + t] = gacc[k];
+  __syncthreads();
+  for (int i = threadIdx.x; i < n4; i += kBwdThreads) {
+    float4 s = join[i];
+    for (int u = 1; u < groups; ++u) {
+      const float4 v = join[u * CH * lanes + i];
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    part[i] = s;
   }
 }
 
-template <int FMT>
-void norm_bwd8(const uint8_t* q, const float* scale, const bf16* g, const float* rstd,
+// Threads of a row: enough for four quads each, 32 to 512.
+int bwd_lanes(int d) {
+  int n = 32;
+  while (n < kBwdThreads && n * 16 < d) n *= 2;
+  return n;
+}
+
+// Reserve a kernel's dynamic shared memory on the current device, once.
+bool reserve_smem(const void* kern, int bytes) {
+  static std::mutex mu;
+  static std::vector<std::pair<const void*, int>> done;  // (kernel, device)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> l(mu);
+  for (const auto& e : done)
+    if (e.first == kern && e.second == dev) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return false;
+  done.emplace_back(kern, dev);
+  return true;
+}
+
+template <int CH, int FMT>
+bool norm_bwd8(const uint8_t* q, const float* scale, const bf16* g, const float* rstd,
                const float* dy, const float* dres, float* dx, bf16* dxb, float* dg_part, int parts,
                int64_t rows, int d, cudaStream_t st) {
-  const int nb = (d + kBlock - 1) / kBlock;
-#define SF_NORM8(CH)                                                                                 \
-  norm_bwd8_kernel<CH, FMT><<<parts, 512, 0, st>>>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, rows, \
-                                                   nb, d)
-  const int ch = (d / 4 + 511) / 512;
-  if (ch <= 1) SF_NORM8(1);
-  else if (ch <= 2) SF_NORM8(2);
-  else if (ch <= 4) SF_NORM8(4);
-  else SF_NORM8(8);
-#undef SF_NORM8
+  using R = BwdRing<CH>;
+  const auto kern = norm_bwd8_kernel<CH, FMT>;
+  if (!reserve_smem(reinterpret_cast<const void*>(kern), R::STAGES * R::STAGE)) return false;
+  const int lanes = bwd_lanes(d);
+  const int64_t per = (rows + (int64_t)parts * (kBwdThreads / lanes) - 1) / ((int64_t)parts * (kBwdThreads / lanes));
+  // few rows a group: no more of the ring than they use
+  const int smem = (int)(per < R::STAGES ? per : R::STAGES) * R::STAGE;
+  kern<<<parts, kBwdThreads, smem, st>>>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, rows,
+                                         (d + kBlock - 1) / kBlock, d, lanes);
+  return true;
+}
+
+template <int FMT>
+bool norm_bwd8_any(const uint8_t* q, const float* scale, const bf16* g, const float* rstd,
+                   const float* dy, const float* dres, float* dx, bf16* dxb, float* dg_part,
+                   int parts, int64_t rows, int d, cudaStream_t st) {
+  if (d <= 4 * 4 * kBwdThreads)
+    return norm_bwd8<4, FMT>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, parts, rows, d, st);
+  if (d <= 6 * 4 * kBwdThreads)
+    return norm_bwd8<6, FMT>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, parts, rows, d, st);
+  return norm_bwd8<8, FMT>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, parts, rows, d, st);
 }
 
 }  // namespace
@@ -370,13 +511,19 @@ void rmsnorm_fwd_load8(const uint8_t* q, const float* scale, const bf16* g, bf16
     norm_fwd8<SF_CKPT_E4M3, true>(nullptr, g, y, rstd, qq, ss, xout, rows, d, eps, st);
 }
 
-void rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const bf16* g, const float* rstd,
+int rmsnorm_bwd_load8_parts(int64_t rows, int d) {
+  const int groups = kBwdThreads / bwd_lanes(d), sms = num_sms();
+  const int64_t need = (rows + groups - 1) / groups;
+  return need < sms ? (int)(need > 0 ? need : 1) : sms;
+}
+
+bool rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const bf16* g, const float* rstd,
                        const float* dy, const float* dres, float* dx, bf16* dxb, float* dg_part,
                        int parts, int fmt, int64_t rows, int d, cudaStream_t st) {
-  if (fmt == SF_CKPT_INT8)
-    norm_bwd8<SF_CKPT_INT8>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, parts, rows, d, st);
-  else
-    norm_bwd8<SF_CKPT_E4M3>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, parts, rows, d, st);
+  return fmt == SF_CKPT_INT8 ? norm_bwd8_any<SF_CKPT_INT8>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part,
+                                                           parts, rows, d, st)
+                             : norm_bwd8_any<SF_CKPT_E4M3>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part,
+                                                           parts, rows, d, st);
 }
 
 }  // namespace sf

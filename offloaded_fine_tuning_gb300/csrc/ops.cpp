@@ -360,9 +360,12 @@ int sf_op_rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const uint16_t
   if (!al16(q) || !al16(scale) || !al16(g) || !al16(dy) || !al16(dres) || !al16(dx) ||
       !al16(dxb) || !al16(scratch))
     return SF_EINVAL;
-  const int parts = sf::rmsnorm_bwd_parts(rows, d);
-  sf::rmsnorm_bwd_load8(q, scale, reinterpret_cast<const bf16*>(g), rstd, dy, dres, dx,
-                        reinterpret_cast<bf16*>(dxb), scratch, parts, fmt, rows, d, S(stream));
+  const int parts = sf::rmsnorm_bwd_load8_parts(rows, d);
+  if (!sf::rmsnorm_bwd_load8(q, scale, reinterpret_cast<const bf16*>(g), rstd, dy, dres, dx,
+                             reinterpret_cast<bf16*>(dxb), scratch, parts, fmt, rows, d, S(stream))) {
+    cudaGetLastError();
+    return SF_ECUDA;
+  }
   sf::reduce_parts_bf16(scratch, parts, d, reinterpret_cast<bf16*>(dg), S(stream));
   return launched();
 }

@@ -199,8 +199,10 @@ void rmsnorm_fwd_save8(const float* x, const __nv_bfloat16* g, __nv_bfloat16* y,
 void rmsnorm_fwd_load8(const uint8_t* q, const float* scale, const __nv_bfloat16* g,
                        __nv_bfloat16* y, float* rstd, float* xout, int fmt, int64_t rows, int d,
                        float eps, cudaStream_t st);
-// rmsnorm_bwd at the saved values; dg_part [rmsnorm_bwd_parts, d].
-void rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const __nv_bfloat16* g,
+// rmsnorm_bwd at the saved values; dg_part [parts, d] with parts =
+// rmsnorm_bwd_load8_parts (at most rmsnorm_bwd_parts).  False: no launch.
+int rmsnorm_bwd_load8_parts(int64_t rows, int d);
+bool rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const __nv_bfloat16* g,
                        const float* rstd, const float* dy, const float* dres, float* dx,
                        __nv_bfloat16* dxb, float* dg_part, int parts, int fmt, int64_t rows, int d,
                        cudaStream_t st);
