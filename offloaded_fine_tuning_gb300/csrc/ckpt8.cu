@@ -25,6 +25,7 @@
 #include <utility>
 #include <vector>
 
+#include "ptx.cuh"
 #include "sf.h"
 #include "sf_internal.h"
 
@@ -98,16 +99,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// Block-wide sum; every thread gets the result.  `sh` holds >= 32 floats.
-__device__ __forceinline__ float block_sum(float v, float* sh) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  v = warp_sum(v);
-  __syncthreads();
-  if (lane == 0) sh[w] = v;
-  __syncthreads();
-  return warp_sum(lane < nw ? sh[lane] : 0.f);
-}
-
 __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
   const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
@@ -168,17 +159,20 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------------------------ RMSNorm forward
-// One CTA per row; thread t holds the four columns t, t + 256, ... (CH of
-// them), so each warp holds whole blocks.  LOAD: the row comes from the codes
-// (and is written to xout unless that is null); else from x, and is saved.
-template <int CH, int FMT, bool LOAD>
+// Groups of LANES threads (a power of two, 32 to 256) take a row each, so
+// that narrow rows fill a CTA too (65536 x 512: save 88.7 us with a CTA per
+// row); thread t of a group holds the quads t, t + LANES, ... (CH of them), so
+// each warp holds whole blocks.  LOAD: the row comes from the codes (and is
+// written to xout unless that is null); else from x, and is saved.
+template <int LANES, int CH, int FMT, bool LOAD>
 __global__ void __launch_bounds__(kThreads)
     norm_fwd8_kernel(const float* __restrict__ x, const bf16* __restrict__ g,
                      bf16* __restrict__ y, float* __restrict__ rstd_out, uint8_t* q, float* scale,
-                     float* __restrict__ xout, int nb, int d, float eps) {
-  __shared__ float sh[32];
-  const int64_t row = blockIdx.x;
-  const int n4 = d >> 2, lane = threadIdx.x & 31;
+                     float* __restrict__ xout, int64_t rows, int nb, int d, float eps) {
+  __shared__ float sh[kThreads / 32];
+  const int group = threadIdx.x / LANES, t = threadIdx.x % LANES;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + group;
+  const int n4 = LANES == kThreads || row < rows ? d >> 2 : 0, lane = threadIdx.x & 31;
   uint32_t* qr = reinterpret_cast<uint32_t*>(q + row * d);
   float* sr = scale + row * nb;
   float4 v[CH];
@@ -188,7 +182,7 @@ __global__ void __launch_bounds__(kThreads)
     float s[CH];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int i = threadIdx.x + k * kThreads;
+      const int i = t + k * LANES;
       c[k] = i < n4 ? qr[i] : 0u;
       s[k] = i < n4 ? sr[i >> 5] : 0.f;
     }
@@ -198,7 +192,7 @@ __global__ void __launch_bounds__(kThreads)
     const float4* xr = reinterpret_cast<const float4*>(x + row * d);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int i = threadIdx.x + k * kThreads;
+      const int i = t + k * LANES;
       v[k] = i < n4 ? xr[i] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
@@ -208,7 +202,7 @@ __global__ void __launch_bounds__(kThreads)
   if (!LOAD) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int i = threadIdx.x + k * kThreads;
+      const int i = t + k * LANES;
       float s, inv;
       block_scale<FMT>(__reduce_max_sync(0xffffffffu, max_bits(v[k])), s, inv);
       if (i < n4) {
@@ -220,18 +214,25 @@ __global__ void __launch_bounds__(kThreads)
     float4* xo = reinterpret_cast<float4*>(xout + row * d);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int i = threadIdx.x + k * kThreads;
+      const int i = t + k * LANES;
       if (i < n4) xo[i] = v[k];
     }
   }
-  ss = block_sum(ss, sh);
+  ss = warp_sum(ss);
+  if (LANES > 32) {
+    if (lane == 0) sh[threadIdx.x >> 5] = ss;
+    __syncthreads();
+    const int n = LANES >> 5;
+    ss = warp_sum(lane < n ? sh[group * n + lane] : 0.f);
+  }
+  if (n4 == 0) return;
   const float rstd = rsqrtf(ss / d + eps);
-  if (threadIdx.x == 0) rstd_out[row] = rstd;
+  if (t == 0) rstd_out[row] = rstd;
   const uint2* gr = reinterpret_cast<const uint2*>(g);
   uint2* yr = reinterpret_cast<uint2*>(y + row * d);
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int i = threadIdx.x + k * kThreads;
+    const int i = t + k * LANES;
     if (i < n4) {
       const float4 gg = unpack4(gr[i]);
       yr[i] = pack4(v[k].x * rstd * gg.x, v[k].y * rstd * gg.y, v[k].z * rstd * gg.z, v[k].w * rstd * gg.w);
@@ -243,16 +244,19 @@ template <int FMT, bool LOAD>
 void norm_fwd8(const float* x, const bf16* g, bf16* y, float* rstd, uint8_t* q, float* scale,
                float* xout, int64_t rows, int d, float eps, cudaStream_t st) {
   const int nb = (d + kBlock - 1) / kBlock;
-  const int ch = (d / 4 + kThreads - 1) / kThreads;  // d <= 16384: at most 16
-#define SF_NORM8(CH)                                                                             \
-  norm_fwd8_kernel<CH, FMT, LOAD><<<(unsigned)rows, kThreads, 0, st>>>(x, g, y, rstd, q, scale, xout, \
-                                                                       nb, d, eps)
-  if (ch <= 1) SF_NORM8(1);
-  else if (ch <= 2) SF_NORM8(2);
-  else if (ch <= 4) SF_NORM8(4);
-  else if (ch <= 8) SF_NORM8(8);
-  else if (ch <= 12) SF_NORM8(12);
-  else SF_NORM8(16);
+#define SF_NORM8(LANES, CH)                                                                           \
+  do {                                                                                                \
+    const int per = kThreads / LANES;                                                                 \
+    norm_fwd8_kernel<LANES, CH, FMT, LOAD><<<(unsigned)((rows + per - 1) / per), kThreads, 0, st>>>(  \
+        x, g, y, rstd, q, scale, xout, rows, nb, d, eps);                                             \
+  } while (0)
+  if (d <= 512) SF_NORM8(32, 4);
+  else if (d <= 1024) SF_NORM8(64, 4);
+  else if (d <= 2048) SF_NORM8(128, 4);
+  else if (d <= 4096) SF_NORM8(256, 4);
+  else if (d <= 8192) SF_NORM8(256, 8);
+  else if (d <= 12288) SF_NORM8(256, 12);
+  else SF_NORM8(256, 16);  // d <= 16384
 #undef SF_NORM8
 }
 
@@ -397,6 +401,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     get = get + 1 == R::STAGES ? 0 : get + 1;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  allow_dependents();
   float4* part = reinterpret_cast<float4*>(dg_part + (int64_t)blockIdx.x * d);
   if (groups == 1) {
 #pragma unroll

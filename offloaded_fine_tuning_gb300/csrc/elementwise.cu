@@ -351,6 +351,48 @@ void reduce_parts_f16(const float* part, int parts, int d, uint16_t* out, float 
       part, parts, d, reinterpret_cast<__half*>(out), scale);
 }
 
+// out1[j] (j < n1) and out2[j - n1]: the sums over p of part[p, j], in a fixed
+// order.  A CTA takes 32 columns with 32 warps: warp w adds the partials w,
+// w + 32, ... of its lane's column, then a fixed tree adds the
+// warps' sums.  Launched as the dependent of the kernel that writes the partials, so
+// that only its reads (a few hundred rows from L2) follow that kernel's end.
+__global__ void __launch_bounds__(1024)
+    gain_sums_kernel(const float* __restrict__ part, int parts, int n1, __nv_bfloat16* __restrict__ out1,
+                     int n2, __nv_bfloat16* __restrict__ out2) {
+  __shared__ float sh[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n = n1 + n2;
+  const int j = blockIdx.x * 32 + lane;
+  wait_primary();
+  float s = 0.f;
+  if (j < n) {
+#pragma unroll 8
+    for (int p = w; p < parts; p += 32) s += __ldcg(part + (int64_t)p * n + j);
+  }
+  sh[w][lane] = s;
+  __syncthreads();
+  // warp w joins column w: one value per lane, added pairwise in a fixed tree
+  const float t = warp_sum(sh[lane][w]);
+  const int c = blockIdx.x * 32 + w;
+  if (lane == 0 && c < n) {
+    if (c < n1) out1[c] = __float2bfloat16_rn(t);
+    else out2[c - n1] = __float2bfloat16_rn(t);
+  }
+}
+
+void gain_sums(const float* part, int parts, int n1, __nv_bfloat16* out1, int n2,
+               __nv_bfloat16* out2, cudaStream_t st) {
+  cudaLaunchAttribute after[1];
+  after[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  after[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((n1 + n2 + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cfg.attrs = after;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, gain_sums_kernel, part, parts, n1, out1, n2, out2);
+}
+
 // Column sums of x [rows, cols] bf16 (row stride ld) as fp32 partials:
 // part[p][c] sums the rows [rows*p/parts, rows*(p+1)/parts).  Two columns per
 // thread, so a warp reads 128 contiguous bytes of a row.

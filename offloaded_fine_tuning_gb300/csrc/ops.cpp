@@ -366,7 +366,7 @@ int sf_op_rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const uint16_t
     cudaGetLastError();
     return SF_ECUDA;
   }
-  sf::reduce_parts_bf16(scratch, parts, d, reinterpret_cast<bf16*>(dg), S(stream));
+  sf::gain_sums(scratch, parts, d, reinterpret_cast<bf16*>(dg), 0, nullptr, S(stream));
   return launched();
 }
 

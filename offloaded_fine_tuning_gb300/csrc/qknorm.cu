@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas)
     }
     __syncthreads();
   }
+  allow_dependents();
   if (dx != dy)
     each_step<TPH, 2, kQkFwdStages>(
         a, steps_of<TPH>(a, false, false, true), ring, dy, lddy, nullptr, 0,
@@ -334,31 +335,6 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas)
           *reinterpret_cast<uint4*>(p) = piece[0];
           *reinterpret_cast<uint4*>(p + half) = piece[1];
         });
-}
-
-// dgq[j] and dgk[j]: column sums of the partials, in a fixed order.  A CTA
-// takes 32 columns; warp w adds the partials w, w + 32, ... of its lane's
-// column, then the 32 sums are added in warp order.
-__global__ void __launch_bounds__(1024)
-    qknorm_gain_kernel(const float* __restrict__ part, int parts, int hd, bf16* __restrict__ dgq,
-                       bf16* __restrict__ dgk) {
-  __shared__ float sh[32][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int j = blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (j < 2 * hd) {
-#pragma unroll 8
-    for (int p = w; p < parts; p += 32) s += part[(int64_t)p * 2 * hd + j];
-  }
-  sh[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && j < 2 * hd) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) t += sh[i][lane];
-    if (j < hd) dgq[j] = __float2bfloat16_rn(t);
-    else dgk[j - hd] = __float2bfloat16_rn(t);
-  }
 }
 
 int lanes_per_head(int hd) {
@@ -412,7 +388,7 @@ void qknorm_rope_bwd(const QkNormArgs& a, const bf16* x, int64_t ldx, const bf16
     default: SF_QK_BWD(16);
   }
 #undef SF_QK_BWD
-  qknorm_gain_kernel<<<(2 * a.hd + 31) / 32, 1024, 0, st>>>(part, parts, a.hd, dgq, dgk);
+  gain_sums(part, parts, a.hd, dgq, a.hd, dgk, st);
 }
 
 }  // namespace sf

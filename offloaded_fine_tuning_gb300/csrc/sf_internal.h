@@ -89,6 +89,10 @@ void reduce_parts_bf16(const float* part, int parts, int d, __nv_bfloat16* out, 
 // The same sum as fp16 after multiplying by scale (a scaled fp16 gradient).
 void reduce_parts_f16(const float* part, int parts, int d, uint16_t* out, float scale,
                       cudaStream_t st);
+// out1 = bf16 sums of the first n1 columns of part [parts, n1 + n2], out2 of the
+// others, in a fixed order.  Call it right after the launch that writes part.
+void gain_sums(const float* part, int parts, int n1, __nv_bfloat16* out1, int n2,
+               __nv_bfloat16* out2, cudaStream_t st);
 // out[c] = bf16(sum over rows of x[r, c]) for x bf16 [rows, cols] (cols even, row
 // stride ld, 4-byte aligned rows); part: fp32 scratch [parts, cols]
 void bias_grad(const __nv_bfloat16* x, int64_t ld, int64_t rows, int cols, float* part, int parts,
