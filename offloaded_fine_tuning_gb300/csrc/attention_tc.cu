@@ -115,6 +115,11 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
       : "f"(a), "f"(b));
 }
 
+// The n lowest bits set (n < 0: none, n > 31: all).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -246,6 +251,12 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
     return x;
   };
   auto key_block = [&](const Item& x, int j) { return WIN && j >= x.ns ? j + x.skip : j; };
+  // Keys of an item's j-th block that the tensor core takes: a block before the
+  // window has only its sinks (rounded up to the MMAs' 16).
+  auto block_keys = [&](const Item& x, int j) {
+    const int n = (win.sinks - j * 128 + 15) & ~15;
+    return WIN && j < x.ns && n < 128 ? n : 128;
+  };
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -346,13 +357,14 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
     const uint64_t dQ = smem_desc_sw128(sQ, 16, 1024), dK = smem_desc_sw128(sK, 16, 1024);
     const uint64_t dV = smem_desc_sw128(sV, 16384, 1024);
     // S_t = Q_t K(G)^T into the S columns of tile t
-    auto issue_s = [&](int tt, long G) {
+    auto issue_s = [&](int tt, long G, int keys) {
+      const uint32_t id = WIN ? umma_idesc_bf16(128, keys, false, false) : ID_S;
       const uint32_t ks = (uint32_t)(G % C::NE);
       const uint64_t a0 = dQ + (uint32_t)(tt * C::TILE / 16), b0 = dK + ks * (uint32_t)(C::TILE / 16);
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk) {
         const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;
-        umma_bf16(tmem_base + tt * 128, a0 + off, b0 + off, ID_S, kk > 0 ? 1u : 0u);
+        umma_bf16(tmem_base + tt * 128, a0 + off, b0 + off, id, kk > 0 ? 1u : 0u);
       }
       umma_commit(s_full(tt));
     };
@@ -367,7 +379,7 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
           break;
         }
         tc_fence_after();
-        issue_s(tt, 0);
+        issue_s(tt, 0, block_keys(x, 0));
         if (x.nkv == 1) umma_commit(q_empty(tt));
       }
       if (ok) umma_commit(kv_empty(0));  // entry 0: K(0) alone
@@ -375,13 +387,15 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
     for (; ok && t < num_items; t += gridDim.x, ++it) {
       const Item x = item_of(t);
       const bool has_next_item = t + (int)gridDim.x < num_items;
-      const int nkv_next = has_next_item ? item_of(t + gridDim.x).nkv : 0;
+      const Item nx = has_next_item ? item_of(t + gridDim.x) : x;
+      const int nkv_next = has_next_item ? nx.nkv : 0;
       for (int j = 0; ok && j < x.nkv; ++j, ++G) {
         const bool last = j + 1 == x.nkv;
         const bool has_next = !last || has_next_item;
         const long Gn = G + 1;
         // the next block's S: the last of its item releases that item's Q tile
         const bool next_is_last = last ? nkv_next == 1 : j + 2 == x.nkv;
+        const int keys = block_keys(x, j), keys_next = last ? block_keys(nx, 0) : block_keys(x, j + 1);
         const int vs = (int)(G % C::NE);
         const int es = (int)(Gn % C::NE);  // entry G + 1: V(G) and K(G + 1)
         if (!mbar_wait(kv_full(es), (uint32_t)((Gn / C::NE) & 1), abort_flag)) {
@@ -397,7 +411,7 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
           const uint64_t bv = dV + (uint32_t)vs * (uint32_t)(C::TILE / 16);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // O_t += P_t V: P as the tensor-memory A operand
-            umma_bf16_ts(tmem_base + O_COL + tt * HD, tmem_base + tt * 128 + kk * 8, bv + kk * (2048 / 16),
+            if (!WIN || kk * 16 < keys) umma_bf16_ts(tmem_base + O_COL + tt * HD, tmem_base + tt * 128 + kk * 8, bv + kk * (2048 / 16),
                          ID_O, (j > 0 || kk > 0) ? 1u : 0u);
           if (last) umma_commit(o_done(tt));
           if (has_next) {
@@ -406,7 +420,7 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
               break;
             }
             tc_fence_after();
-            issue_s(tt, Gn);
+            issue_s(tt, Gn, keys_next);
             if (next_is_last) umma_commit(q_empty(tt));
           }
         }
@@ -463,13 +477,52 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
       float m = -INFINITY, l = 0.f;
       // One key block (the item's j-th, block kb): S from TMEM, P back over it.
       // Compiled twice, with the mask (the diagonal block and any block past
-      // it, and blocks that the window's start cuts) and without.
+      // it, and blocks that the window's start cuts) and without.  With a
+      // window, up to a third of the blocks are cut, so the masked code works
+      // by groups of 32 columns, read from TMEM once for the row max and once
+      // for P: a group that none of the warp's rows sees is not read (its P is
+      // 0), one that all see is not masked, and the others take one mask word
+      // per row (2 x 8192 tokens, window 1024: 390 us with the mask as
+      // comparisons on 128 columns).
       auto block = [&](int j, int kb, long G, auto diag) -> bool {
         constexpr bool DIAG = decltype(diag)::value;
         if (!__all_sync(0xffffffffu, mbar_wait(s_full(tt), (uint32_t)(G & 1), abort_flag))) return false;
         tc_fence_after();
-        float s[128];
-        {
+        constexpr bool CUT = WIN && DIAG;
+        float s[CUT ? 32 : 128];
+        float mx = -INFINITY;
+        // CUT: group c of 32 columns into s; false when no row of the warp sees it
+        auto load_group = [&](int c) -> bool {
+          const int q0 = qb * 128 + quarter * 32, kc = kb * 128 + 32 * c;
+          if (kc > q0 + 31 || (kc >= win.sinks && q0 - (kc + 31) >= win.size)) return false;
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(lane_base + s_col + 32 * c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r[i]);
+          if (kc + 31 > q0 || (kc + 31 >= win.sinks && q0 + 31 - kc >= win.size)) {
+            const uint32_t seen = low_bits(q - kc + 1) &
+                                  (~low_bits(q - win.size + 1 - kc) | low_bits(win.sinks - kc));
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(seen & (1u << i))) s[i] = -INFINITY;
+          }
+          return true;
+        };
+        if constexpr (CUT) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            if (!load_group(c)) continue;
+            float mx4[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) mx4[a] = max3f(mx, s[a], s[4 + a]);
+#pragma unroll
+            for (int i = 8; i < 32; i += 8)
+#pragma unroll
+              for (int a = 0; a < 4; ++a) mx4[a] = max3f(mx4[a], s[i + a], s[i + 4 + a]);
+            mx = fmaxf(max3f(mx4[0], mx4[1], mx4[2]), mx4[3]);
+          }
+        } else {
           uint32_t r[4][32];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(lane_base + s_col + 32 * c, r[c]);
@@ -478,59 +531,73 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i) s[32 * c + i] = __uint_as_float(r[c][i]);
-        }
-        if (DIAG) {  // keys after the query are masked (every key of a block past the diagonal)
-          const int lim = q - kb * 128;
-          if (WIN) {  // and keys before the window that are no sinks
-            const int lo = lim - win.size, sk = win.sinks - kb * 128;
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i > lim || (i <= lo && i >= sk)) s[i] = -INFINITY;
-          } else {
+          if (DIAG) {  // keys after the query are masked (every key of a block past the diagonal)
+            const int lim = q - kb * 128;
 #pragma unroll
             for (int i = 0; i < 128; ++i)
               if (i > lim) s[i] = -INFINITY;
           }
+          // row max: eight chains of three-input maxima over columns 16..127
+          float mx8[8];
+#pragma unroll
+          for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(s[a], s[a + 8]);
+#pragma unroll
+          for (int i = 16; i < 128; i += 16)
+#pragma unroll
+            for (int a = 0; a < 8; ++a) mx8[a] = max3f(mx8[a], s[i + a], s[i + 8 + a]);
+          mx = max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
         }
-        // row max: eight chains of three-input maxima over columns 16..127
-        float mx8[8];
-#pragma unroll
-        for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(s[a], s[a + 8]);
-#pragma unroll
-        for (int i = 16; i < 128; i += 16)
-#pragma unroll
-          for (int a = 0; a < 8; ++a) mx8[a] = max3f(mx8[a], s[i + a], s[i + 8 + a]);
-        float mx = max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
         mx *= scale_log2;  // the scale is positive: the max commutes with it
         const bool grow = mx > m + 8.f;
         float m_new = grow ? mx : m;
         // A window can start inside or after this block for some rows: until a
         // row has seen a key its m is -inf, and exponents are taken against 0
         // (-inf - -inf would be NaN); every p of such a row is 0.
-        const bool none = WIN && DIAG && m_new == -INFINITY;
+        const bool none = CUT && m_new == -INFINITY;
         if (none) m_new = 0.f;
         const float corr = ex2_approx(m - m_new);  // 1 without growth, 0 on the first block
         // p = 2^(s * scale - m): the arguments and the partial row sums as
         // paired fp32 operations, the exponentials on the special-function unit
         float ps8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        auto exps = [&](float* v, int n) {
 #pragma unroll
-        for (int i = 0; i < 128; i += 2) {
-          fma2_scalar(s[i], s[i + 1], scale_log2, -m_new);
-          s[i] = ex2_approx(s[i]);
-          s[i + 1] = ex2_approx(s[i + 1]);
-          add2(ps8[i & 7], ps8[(i & 7) + 1], s[i], s[i + 1]);
+          for (int i = 0; i < n; i += 2) {
+            fma2_scalar(v[i], v[i + 1], scale_log2, -m_new);
+            v[i] = ex2_approx(v[i]);
+            v[i + 1] = ex2_approx(v[i + 1]);
+            add2(ps8[i & 7], ps8[(i & 7) + 1], v[i], v[i + 1]);
+          }
+        };
+        if constexpr (CUT) {
+          // P of group c takes columns 16 c to 16 c + 15, where the S of groups
+          // up to c / 2 was, which has been read for the last time
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+            if (load_group(c)) {
+              exps(s, 32);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[i] = pack2_bf16(s[2 * i], s[2 * i + 1]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[i] = 0u;
+            }
+            tmem_st_32x32b_x16(lane_base + s_col + 16 * c, pk);
+          }
+        } else {
+          exps(s, 128);
+          // the row of P, bf16 pairs, over the first 64 columns of S
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) pk[i] = pack2_bf16(s[64 * hh + 2 * i], s[64 * hh + 2 * i + 1]);
+            tmem_st_32x32b_x32(lane_base + s_col + 32 * hh, pk);
+          }
         }
         const float ps = ((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) + ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7]));
         l = l * corr + ps;
         m = none ? -INFINITY : m_new;
-        // the row of P, bf16 pairs, over the first 64 columns of S
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) pk[i] = pack2_bf16(s[64 * hh + 2 * i], s[64 * hh + 2 * i + 1]);
-          tmem_st_32x32b_x32(lane_base + s_col + 32 * hh, pk);
-        }
         if (j > 0 && __any_sync(0xffffffffu, grow)) {
           // every P V of this tile so far has completed (the S commit covers
           // them), and the next waits for this thread's P arrival below
