@@ -42,7 +42,6 @@ namespace sf {
 
 namespace {
 
-constexpr int kAttThreads = 192;
 // Grid position in longest-first order: the CTAs are dispatched roughly in
 // linear block order, so every CTA of rank 0 (the most work) is placed before
 // any CTA of rank 1, and so on, whatever the other two coordinates.
@@ -687,62 +686,80 @@ __device__ __forceinline__ int dq_slot(const AttWindow& win, int j) {
 }
 }  // namespace
 
-// One CTA per (128-key block j, kv head g, batch b).  It walks every query
-// head of the group and every 128-query block i >= j.  Per (head, block):
+// Backward for head_dim 64.  One CTA per (128-key block j, kv head g, batch b)
+// walks every query head of the group and every 128-query block that sees its
+// keys.  Per (head, block):
 //   MMA:     S^T = K Q^T -> TMEM[0,128),  dP^T = V dO^T -> TMEM[128,256)
-//   threads: one per key row: P^T = exp2(S^T*scale*log2e - lse*log2e) (causal),
-//            dS^T = P^T * (dP^T - D), both to shared memory (bf16, swizzled)
-//   MMA:     dV += P^T dO, dK += dS^T Q (TMEM, kept over the whole walk);
-//            dQ = dS K -> TMEM[0,hd) (the S^T columns, already consumed)
-//   threads: one per query row: dQ added into the fp32 dq_acc (vector atomics)
-// dS^T is stored once and read both as the K-major A of dK and as the
-// MN-major A (dS) of dQ.  At the end the threads write dK (scaled, inverse
-// RoPE) and dV of their key rows.
+//   threads: one per key row and half of the queries: P^T = exp2(S^T*scale*
+//            log2e - lse*log2e) (masked), dS^T = P^T * (dP^T - D), both to
+//            shared memory (bf16, swizzled)
+//   MMA:     dV += P^T dO, dK += dS^T Q (TMEM[384,512), kept over the walk);
+//            dQ = dS K -> TMEM, two buffers [256,384)
+//   threads: one per query row and half of the columns: dQ through shared
+//            memory into the fp32 dq_acc by TMA reduce-add (or, deterministic,
+//            a TMA store into the key block's own slot)
+// dS^T is stored once and read both as the K-major A of dK and as the MN-major
+// A (dS) of dQ.  The threads release the S^T and dP^T columns once they hold
+// them in registers, so the next block's are formed while they work, and dV,
+// dK and dQ run behind.  One thread issues every MMA at 55 to 77 cycles each,
+// which bounds a block (32 MMAs, 24 of them 64 wide, 32 cycles of work): hence
+// blocks of 128 queries.  With 64-query blocks and two CTAs sharing an SM the
+// 24 MMAs per 64 queries ran 121 us against the unpipelined 128-query kernel's
+// 155 (8 x 1001 tokens, 16 heads, window 250) but 650 against 570 us where
+// walks are long (2 x 4096, 16 heads in groups of 4).
 namespace {
-template <int HD>
+constexpr int kAttBwdThreads = 320;  // TMA warp, MMA warp, 8 softmax-gradient warps
 struct AttBwdCfg {
-  static constexpr int TILE = HD / 64 * 16384;
+  static constexpr int HD = 64;
+  static constexpr int TILE = 16384;  // 128 rows x 64 hd
+  static constexpr int NQ = 2;        // Q / dO stages
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = TILE;
   static constexpr int OFF_Q = 2 * TILE;
-  static constexpr int OFF_DO = 3 * TILE;
-  static constexpr int OFF_PT = 4 * TILE;
+  static constexpr int OFF_DO = OFF_Q + NQ * TILE;
+  static constexpr int OFF_PT = OFF_DO + NQ * TILE;  // 128 keys x 128 queries, two boxes of 64
   static constexpr int OFF_DST = OFF_PT + 32768;
-  static constexpr int OFF_LD = OFF_DST + 32768;  // lse*log2e and D, 2 buffers x 128 each
-  static constexpr int OFF_BAR = OFF_LD + 4 * 128 * 4;
-  static constexpr int NBAR = 11;
+  static constexpr int OFF_DQS = OFF_DST + 32768;    // dQ staging: 8 warps x [32 q][32 d] fp32
+  static constexpr int OFF_LD = OFF_DQS + 8 * 4096;  // [2][lse 128 | D 128]
+  static constexpr int OFF_BAR = OFF_LD + 2 * 256 * 4;
+  static constexpr int NBAR = 17;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
 };
+static_assert(AttBwdCfg::SMEM <= 232448, "backward shared memory");
 }  // namespace
 
-template <int HD, bool DET, bool WIN>
-__global__ void __launch_bounds__(kAttThreads, 1)
+template <bool DET, bool WIN>
+__global__ void __launch_bounds__(kAttBwdThreads, 1)
     attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv,
-                       const __grid_constant__ CUtensorMap tm_do, const float* __restrict__ lse,
-                       const float* __restrict__ delta, float* __restrict__ dq_acc,
-                       __nv_bfloat16* __restrict__ dqkv, const float2* __restrict__ cs, int S,
+                       const __grid_constant__ CUtensorMap tm_do,
+                       const __grid_constant__ CUtensorMap tm_dq,
+                       const __grid_constant__ CUtensorMap tm_dkv, const float* __restrict__ lse,
+                       const float* __restrict__ delta, const float2* __restrict__ cs, int S,
                        int Hq, int Hkv, float scale, float scale_log2, AttWindow win, int* err) {
-  using C = AttBwdCfg<HD>;
-  constexpr int NB = HD / 64;
-  constexpr uint32_t ID_SQ = umma_idesc_bf16(128, 128, false, false);  // S^T, dP^T
+  using C = AttBwdCfg;
+  constexpr int HD = C::HD;
+  constexpr uint32_t ID_SP = umma_idesc_bf16(128, 128, false, false);  // S^T, dP^T
   constexpr uint32_t ID_KV = umma_idesc_bf16(128, HD, false, true);    // dV, dK
   constexpr uint32_t ID_Q = umma_idesc_bf16(128, HD, true, true);      // dQ
   constexpr uint32_t TMEM_COLS = 512;
-  constexpr uint32_t COL_DP = 128, COL_DV = 256, COL_DK = 256 + HD;
+  constexpr uint32_t COL_DP = 128, COL_DQ = 256, COL_DV = 384, COL_DK = 448;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t s0 = smem_u32(smem);
   const uint32_t sK = s0 + C::OFF_K, sV = s0 + C::OFF_V, sQ = s0 + C::OFF_Q, sDO = s0 + C::OFF_DO;
-  const uint32_t sPt = s0 + C::OFF_PT, sDSt = s0 + C::OFF_DST;
-  float* sLD = reinterpret_cast<float*>(smem + C::OFF_LD);  // [2][lse 128 | D 128]
+  const uint32_t sPt = s0 + C::OFF_PT, sDSt = s0 + C::OFF_DST, sDQS = s0 + C::OFF_DQS;
+  float* sLD = reinterpret_cast<float*>(smem + C::OFF_LD);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   const uint32_t b0 = smem_u32(bars);
-  const uint32_t kv_full = b0, qdo_full = b0 + 8, qdo_empty = b0 + 16, sp_full = b0 + 24,
-                 ps_full = b0 + 32, dq_full = b0 + 40, dq_free = b0 + 48, acc_done = b0 + 56,
-                 drain = b0 + 64;
-  auto ld_full = [&](int i) { return b0 + 72u + 8u * i; };
+  const uint32_t kv_full = b0, sp_full = b0 + 8, s_free = b0 + 16, ps_full = b0 + 24,
+                 pds_free = b0 + 32, acc_done = b0 + 40, drain = b0 + 48;
+  auto qdo_full = [&](int i) { return b0 + 56u + 8u * i; };
+  auto qdo_empty = [&](int i) { return b0 + 72u + 8u * i; };
+  auto dq_full = [&](int i) { return b0 + 88u + 8u * i; };
+  auto dq_free = [&](int i) { return b0 + 104u + 8u * i; };
+  auto ld_full = [&](int i) { return b0 + 120u + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -751,27 +768,31 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   grid_rank_first(j, g, b);  // key block 0 sees the most query blocks
   const int grp = Hq / Hkv;
   const int k0 = j * 128;
-  const int nqb = (S + 127) / 128;
   // query blocks j .. j + per_head - 1 can see these keys
-  const int per_head = (WIN ? last_query(win, k0, S) / 128 + 1 : nqb) - j;
+  const int per_head = (WIN ? last_query(win, k0, S) / 128 + 1 : (S + 127) / 128) - j;
   const int n_it = grp * per_head;  // (head, query block) pairs
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    mbar_init(qdo_full, 1);
-    mbar_init(qdo_empty, 1);
     mbar_init(sp_full, 1);
-    mbar_init(ps_full, 128);
-    mbar_init(dq_full, 1);
-    mbar_init(dq_free, 128);
+    mbar_init(s_free, 256);
+    mbar_init(ps_full, 256);
+    mbar_init(pds_free, 1);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
-    mbar_init(ld_full(0), 128);
-    mbar_init(ld_full(1), 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(qdo_full(i), 1);
+      mbar_init(qdo_empty(i), 1);
+      mbar_init(dq_full(i), 1);
+      mbar_init(dq_free(i), 256);
+      mbar_init(ld_full(i), 128);
+    }
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_qkv);
     tma_prefetch_desc(&tm_do);
+    tma_prefetch_desc(&tm_dq);
+    tma_prefetch_desc(&tm_dkv);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
@@ -785,67 +806,70 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
     mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
-#pragma unroll
-    for (int c = 0; c < NB; ++c) {
-      tma_load_3d(sK + c * 16384, &tm_qkv, kv_full, (Hq + g) * HD + 64 * c, k0, b);
-      tma_load_3d(sV + c * 16384, &tm_qkv, kv_full, (Hq + Hkv + g) * HD + 64 * c, k0, b);
-    }
+    tma_load_3d(sK, &tm_qkv, kv_full, (Hq + g) * HD, k0, b);
+    tma_load_3d(sV, &tm_qkv, kv_full, (Hq + Hkv + g) * HD, k0, b);
     bool ok = true;
     int issued = 0;
     for (int it = 0; it < n_it; ++it) {
+      const int bq = it % C::NQ;
       const int h = g * grp + it / per_head;
       const int q0 = (j + it % per_head) * 128;
-      if (!mbar_wait(qdo_empty, (it & 1) ^ 1, abort_flag)) { ok = false; break; }
-      mbar_arrive_expect_tx(qdo_full, 2 * C::TILE);
-#pragma unroll
-      for (int c = 0; c < NB; ++c) {
-        tma_load_3d(sQ + c * 16384, &tm_qkv, qdo_full, h * HD + 64 * c, q0, b);
-        tma_load_3d(sDO + c * 16384, &tm_do, qdo_full, h * HD + 64 * c, q0, b);
-      }
+      if (!mbar_wait(qdo_empty(bq), ((it / C::NQ) & 1) ^ 1, abort_flag)) { ok = false; break; }
+      mbar_arrive_expect_tx(qdo_full(bq), 2 * C::TILE);
+      tma_load_3d(sQ + bq * C::TILE, &tm_qkv, qdo_full(bq), h * HD, q0, b);
+      tma_load_3d(sDO + bq * C::TILE, &tm_do, qdo_full(bq), h * HD, q0, b);
       issued = it + 1;
     }
     if (!ok) {
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
       mbar_wait(kv_full, 0, nullptr);
-      if (issued > 0) mbar_wait(qdo_full, (issued - 1) & 1, nullptr);
+      for (int it = issued - 1; it >= 0 && it >= issued - C::NQ; --it)
+        mbar_wait(qdo_full(it % C::NQ), (it / C::NQ) & 1, nullptr);
     }
   } else if (warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
     bool ok = mbar_wait(kv_full, 0, abort_flag);
-    for (int it = 0; ok && it < n_it; ++it) {
-      const uint32_t ph = it & 1;
-      if (!mbar_wait(qdo_full, ph, abort_flag) || !mbar_wait(dq_free, ph ^ 1u, abort_flag)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
+    // base descriptors; an operand at byte offset o is the base plus o / 16
+    const uint64_t dK = smem_desc_sw128(sK, 16, 1024), dV = smem_desc_sw128(sV, 16, 1024);
+    const uint64_t dQk = smem_desc_sw128(sQ, 16, 1024), dDOk = smem_desc_sw128(sDO, 16, 1024);
+    const uint64_t dPt = smem_desc_sw128(sPt, 16, 1024), dDSt = smem_desc_sw128(sDSt, 16, 1024);
+    const uint64_t dQm = smem_desc_sw128(sQ, 16384, 1024), dDOm = smem_desc_sw128(sDO, 16384, 1024);
+    const uint64_t dKm = smem_desc_sw128(sK, 16384, 1024), dDStm = smem_desc_sw128(sDSt, 16384, 1024);
+    for (int it = 0; ok && it <= n_it; ++it) {
+      if (it < n_it) {  // S^T and dP^T of block it, once the threads hold block it - 1's
+        const int bq = it % C::NQ;
+        if (!mbar_wait(qdo_full(bq), (it / C::NQ) & 1, abort_flag)) { ok = false; break; }
+        if (it >= 1 && !mbar_wait(s_free, (it - 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t qo = (uint32_t)bq * (uint32_t)(C::TILE / 16);
 #pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-        umma_bf16(tmem_base, smem_desc_sw128(sK + off, 16, 1024), smem_desc_sw128(sQ + off, 16, 1024),
-                  ID_SQ, kk > 0 ? 1u : 0u);
-        umma_bf16(tmem_base + COL_DP, smem_desc_sw128(sV + off, 16, 1024),
-                  smem_desc_sw128(sDO + off, 16, 1024), ID_SQ, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          umma_bf16(tmem_base, dK + kk * 2, dQk + qo + kk * 2, ID_SP, kk > 0 ? 1u : 0u);
+          umma_bf16(tmem_base + COL_DP, dV + kk * 2, dDOk + qo + kk * 2, ID_SP, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(sp_full);
       }
-      umma_commit(sp_full);
-      if (!mbar_wait(ps_full, ph, abort_flag)) { ok = false; break; }
-      tc_fence_after();
+      if (it >= 1) {  // dV, dK, dQ of block it - 1, once its P^T and dS^T are in shared memory
+        const int ip = it - 1, bq = ip % C::NQ, bd = ip & 1;
+        if (!mbar_wait(ps_full, ip & 1, abort_flag)) { ok = false; break; }
+        if (ip >= 2 && !mbar_wait(dq_free(bd), ((ip >> 1) - 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t qo = (uint32_t)bq * (uint32_t)(C::TILE / 16);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {  // contraction over the 128 queries
-        const uint32_t a_off = (kk >> 2) * 16384 + (kk & 3) * 32;
-        const uint32_t acc = (it > 0 || kk > 0) ? 1u : 0u;
-        umma_bf16(tmem_base + COL_DV, smem_desc_sw128(sPt + a_off, 16, 1024),
-                  smem_desc_sw128(sDO + kk * 2048, 16384, 1024), ID_KV, acc);
-        umma_bf16(tmem_base + COL_DK, smem_desc_sw128(sDSt + a_off, 16, 1024),
-                  smem_desc_sw128(sQ + kk * 2048, 16384, 1024), ID_KV, acc);
+        for (int kk = 0; kk < 8; ++kk) {  // over the 128 queries
+          const uint32_t acc = (ip > 0 || kk > 0) ? 1u : 0u;
+          const uint32_t ao = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;
+          umma_bf16(tmem_base + COL_DV, dPt + ao, dDOm + qo + kk * 128, ID_KV, acc);
+          umma_bf16(tmem_base + COL_DK, dDSt + ao, dQm + qo + kk * 128, ID_KV, acc);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // over the 128 keys
+          umma_bf16(tmem_base + COL_DQ + 64 * bd, dDStm + kk * 128, dKm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
+        umma_commit(dq_full(bd));
+        umma_commit(qdo_empty(bq));
+        umma_commit(pds_free);
       }
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)  // contraction over the 128 keys
-        umma_bf16(tmem_base, smem_desc_sw128(sDSt + kk * 2048, 16384, 1024),
-                  smem_desc_sw128(sK + kk * 2048, 16384, 1024), ID_Q, kk > 0 ? 1u : 0u);
-      umma_commit(dq_full);
-      umma_commit(qdo_empty);
     }
     if (ok) {
       umma_commit(acc_done);
@@ -856,22 +880,23 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       mbar_wait(drain, 0, nullptr);
     }
   } else if (warp >= 2) {
-    // ---------------------------------------------------------------- softmax-gradient threads
-    const int quarter = warp & 3;
-    const int r = quarter * 32 + lane;  // key row for S^T / dP^T, query row for dQ
+    // ---------------------------------------------------------------- threads
+    // Two warps per TMEM lane quarter, each taking half of the block's queries
+    // (of S^T and dP^T) and half of the head's columns (of dQ).
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int r = quarter * 32 + lane;  // key row of S^T / dP^T; query row of dQ
     const int key = k0 + r;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    const int tid = threadIdx.x - 64;  // 0..127
+    const int tid = threadIdx.x - 64;  // 0..255
     // the last query that sees this thread's key (before the key: no one does)
-    const int q_end = WIN ? (key < win.sinks || key > S - win.size ? S - 1 : key + win.size - 1) : 0;
-    const int64_t ldo = (int64_t)Hq * HD;
+    const int q_end = !WIN || key < win.sinks || key > S - win.size ? S - 1 : key + win.size - 1;
     bool ok = true;
-    // lse (log2 units) and D of the query block, one value per thread, loaded
-    // one block ahead so the global latency is off the critical path
+    // lse (log2 units) and D of the query block, one value per thread of the
+    // first 128, loaded one block ahead
     auto fetch = [&](int it_, float& lv, float& dv) {
       lv = 0.f;
       dv = 0.f;
-      if (it_ >= n_it) return;
+      if (it_ >= n_it || tid >= 128) return;
       const int h_ = g * grp + it_ / per_head;
       const int q_ = (j + it_ % per_head) * 128 + tid;
       if (q_ < S) {
@@ -880,154 +905,211 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         dv = delta[o];
       }
     };
+    // dQ of block it_ (this warp's 32 queries and 32 columns) into the warp's
+    // staging tile, in the tensor map's 128-byte swizzle, then one TMA
+    // reduce-add (or store).  The tile is rewritten only after the previous
+    // one has finished reading it.
+    const uint32_t stage = sDQS + (uint32_t)(warp - 2) * 4096u;
+    auto emit_dq = [&](int it_) -> bool {
+      const int bd = it_ & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(dq_full(bd), (it_ >> 1) & 1, abort_flag))) return false;
+      tc_fence_after();
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(lane_base + COL_DQ + 64 * bd + 32 * half, v);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(dq_free(bd));
+      if (lane == 0) bulk_wait_group_read0();
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         stage + (uint32_t)lane * 128u + (uint32_t)((k ^ (lane & 7)) * 16)),
+                     "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
+                     : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int h_ = g * grp + it_ / per_head;
+        const int qb_ = (j + it_ % per_head) * 128 + 32 * quarter;
+        if (qb_ < S) {  // rows past the sequence end are outside the map
+          if (DET)  // this key block's own slot of the dQ buffer
+            tma_store_3d(&tm_dq, stage, h_ * HD + 32 * half, qb_,
+                         (WIN ? dq_slot(win, j) : j) * (int)gridDim.z + b);
+          else
+            tma_reduce_add_3d(&tm_dq, stage, h_ * HD + 32 * half, qb_, b);
+        }
+        bulk_commit_group();
+      }
+      return true;
+    };
     float next_l, next_d;
     fetch(0, next_l, next_d);
+    const uint32_t rowoff = (uint32_t)r * 128u + (uint32_t)half * 16384u;
     for (int it = 0; it < n_it; ++it) {
-      const int h = g * grp + it / per_head;
-      const int q0 = (j + it % per_head) * 128;
-      const uint32_t ph = it & 1;
+      const int qc = (j + it % per_head) * 128 + 64 * half;  // first query of this thread's columns
       float* bL = sLD + (it & 1) * 256;
       float* bD = bL + 128;
-      // The buffer written here was last read for block it - 2, and every
-      // thread finished that before the MMA warp could issue block it - 1,
-      // whose S^T this thread has already waited for.
-      bL[tid] = next_l;
-      bD[tid] = next_d;
-      mbar_arrive(ld_full(it & 1));
+      // The buffer written here was last read for block it - 2; this thread
+      // has since waited for that block's P^T / dS^T to be consumed, which
+      // needed every thread to have finished computing it.
+      if (tid < 128) {
+        bL[tid] = next_l;
+        bD[tid] = next_d;
+        mbar_arrive(ld_full(it & 1));
+      }
       fetch(it + 1, next_l, next_d);
       ok = __all_sync(0xffffffffu, mbar_wait(ld_full(it & 1), (it >> 1) & 1, abort_flag));
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sp_full, ph, abort_flag));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sp_full, it & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t rowoff = (uint32_t)r * 128u;
+      uint32_t sr[2][32], dr[2][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t sr[32], dr[32];
-        tmem_ld_32x32b_x32(lane_base + 32 * c, sr);
-        tmem_ld_32x32b_x32(lane_base + COL_DP + 32 * c, dr);
-        tmem_ld_wait();
-        float p[32], ds[32];
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld_32x32b_x32(lane_base + 64 * half + 32 * c, sr[c]);
+        tmem_ld_32x32b_x32(lane_base + COL_DP + 64 * half + 32 * c, dr[c]);
+      }
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(s_free);  // S^T / dP^T are in registers: the next block may overwrite them
+      // P^T over S^T's registers, dS^T over dP^T's, packed
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int qq = 32 * c + e;
-          const int q = q0 + qq;
-          float pv = 0.f;
-          if (WIN ? key <= q && q <= q_end : q < S && key <= q)
-            pv = ex2_approx(fmaf(__uint_as_float(sr[e]), scale_log2, -bL[qq]));
-          p[e] = pv;
-          ds[e] = pv * (__uint_as_float(dr[e]) - bD[qq]);
-        }
-        const uint32_t box = (uint32_t)(c >> 1) * 16384u;
+      for (int c = 0; c < 2; ++c) {
+        const int q1 = qc + 32 * c;
+        const uint32_t seen = low_bits(q_end - q1 + 1) & ~low_bits(key - q1);
+        const float4* L4 = reinterpret_cast<const float4*>(bL + 64 * half + 32 * c);
+        const float4* D4 = reinterpret_cast<const float4*>(bD + 64 * half + 32 * c);
+        auto grad_tile = [&](auto mask_tag) {
+          constexpr bool kMask = decltype(mask_tag)::value;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 l4 = L4[k], d4 = D4[k];
+            const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+            const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
+            float pv[4], sv[4];
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const int e = 4 * k + i;
+              float x0 = __uint_as_float(sr[c][e]), x1 = __uint_as_float(sr[c][e + 1]);
+              fma2(x0, x1, scale_log2, -lv[i], -lv[i + 1]);
+              x0 = ex2_approx(x0);
+              x1 = ex2_approx(x1);
+              if (kMask && !(seen & (1u << e))) x0 = 0.f;
+              if (kMask && !(seen & (2u << e))) x1 = 0.f;
+              float d0 = __uint_as_float(dr[c][e]), d1 = __uint_as_float(dr[c][e + 1]);
+              add2(d0, d1, -dv[i], -dv[i + 1]);
+              mul2(d0, d1, x0, x1);
+              pv[i] = x0;
+              pv[i + 1] = x1;
+              sv[i] = d0;
+              sv[i + 1] = d1;
+            }
+            sr[c][2 * k] = pack2_bf16(pv[0], pv[1]);
+            sr[c][2 * k + 1] = pack2_bf16(pv[2], pv[3]);
+            dr[c][2 * k] = pack2_bf16(sv[0], sv[1]);
+            dr[c][2 * k + 1] = pack2_bf16(sv[2], sv[3]);
+          }
+        };
+        if (__all_sync(0xffffffffu, seen == 0xffffffffu))
+          grad_tile(std::false_type{});
+        else
+          grad_tile(std::true_type{});
+      }
+      if (it >= 1) {  // P^T, dS^T of the previous block consumed
+        ok = __all_sync(0xffffffffu, mbar_wait(pds_free, (it - 1) & 1, abort_flag));
+        if (!ok) break;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int jj = (c & 1) * 4 + k;
-          const uint32_t off = box + rowoff + (uint32_t)((jj ^ (r & 7)) * 16);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPt + off),
-                       "r"(pack2_bf16(p[8 * k], p[8 * k + 1])), "r"(pack2_bf16(p[8 * k + 2], p[8 * k + 3])),
-                       "r"(pack2_bf16(p[8 * k + 4], p[8 * k + 5])), "r"(pack2_bf16(p[8 * k + 6], p[8 * k + 7]))
+          const uint32_t off = rowoff + (uint32_t)(((4 * c + k) ^ (r & 7)) * 16);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPt + off), "r"(sr[c][4 * k]),
+                       "r"(sr[c][4 * k + 1]), "r"(sr[c][4 * k + 2]), "r"(sr[c][4 * k + 3])
                        : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sDSt + off),
-                       "r"(pack2_bf16(ds[8 * k], ds[8 * k + 1])), "r"(pack2_bf16(ds[8 * k + 2], ds[8 * k + 3])),
-                       "r"(pack2_bf16(ds[8 * k + 4], ds[8 * k + 5])), "r"(pack2_bf16(ds[8 * k + 6], ds[8 * k + 7]))
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sDSt + off), "r"(dr[c][4 * k]),
+                       "r"(dr[c][4 * k + 1]), "r"(dr[c][4 * k + 2]), "r"(dr[c][4 * k + 3])
                        : "memory");
         }
-      }
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(ps_full);
-      // dQ rows of this query block (thread = query row)
-      ok = __all_sync(0xffffffffu, mbar_wait(dq_full, ph, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      const int q = q0 + r;
-      // deterministic: this key block's own slot, plain stores
-      const int64_t slot = WIN ? dq_slot(win, j) : j;
-      const int64_t row = DET ? (slot * gridDim.z + b) * S + q : (int64_t)b * S + q;
-      float* dst = dq_acc + row * ldo + (int64_t)h * HD;
-#pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(lane_base + 32 * c, v);
-        tmem_ld_wait();
-        if (q < S) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 x = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
-                                         __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
-            if (DET)
-              *reinterpret_cast<float4*>(dst + 32 * c + 4 * k) = x;
-            else
-              atomicAdd(reinterpret_cast<float4*>(dst + 32 * c + 4 * k), x);
-          }
-        }
+      if (it >= 1) {  // dQ of the previous block, while the tensor core works on this one's
+        ok = emit_dq(it - 1);
+        if (!ok) break;
       }
-      tc_fence_before();
-      mbar_arrive(dq_free);
     }
+    if (ok) ok = emit_dq(n_it - 1);
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, abort_flag));
     if (ok) {
       tc_fence_after();
-      // dK: pairs (d, d + HD/2) get the inverse rotation of the key's position
-#pragma unroll
-      for (int c = 0; c < HD / 64; ++c) {
-        uint32_t x1[32], x2[32];
-        tmem_ld_32x32b_x32(lane_base + COL_DK + 32 * c, x1);
-        tmem_ld_32x32b_x32(lane_base + COL_DK + HD / 2 + 32 * c, x2);
+      // dK and dV rows go into the K and V tiles' shared memory (every MMA
+      // that read them has completed), in the tensor map's swizzled layout;
+      // one thread then stores both tiles with the TMA unit.
+      auto put = [&](uint32_t tile, int chunk, uint32_t a, uint32_t b_, uint32_t c_, uint32_t d_) {
+        const uint32_t addr = tile + (uint32_t)r * 128u + (uint32_t)((chunk ^ (r & 7)) * 16);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b_),
+                     "r"(c_), "r"(d_)
+                     : "memory");
+      };
+      // dK: pairs (d, d + HD/2) get the inverse rotation of the key's position;
+      // this warp takes d in [16 half, 16 half + 16) and their partners
+      {
+        uint32_t x1[16], x2[16];
+        tmem_ld_32x32b_x16(lane_base + COL_DK + 16 * half, x1);
+        tmem_ld_32x32b_x16(lane_base + COL_DK + HD / 2 + 16 * half, x2);
         tmem_ld_wait();
-        if (key < S) {
-          const int64_t ld = (int64_t)(Hq + 2 * Hkv) * HD;
-          __nv_bfloat16* krow = dqkv + ((int64_t)b * S + key) * ld + (int64_t)(Hq + g) * HD;
-          uint32_t o1[16], o2[16];
+        const int kp = key < S ? key : S - 1;  // rows past the end are computed, not stored
+        uint32_t o1[8], o2[8];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float a1 = __uint_as_float(x1[e]) * scale, b1 = __uint_as_float(x1[e + 1]) * scale;
-            float a2 = __uint_as_float(x2[e]) * scale, b2 = __uint_as_float(x2[e + 1]) * scale;
-            if (cs) {
-              const float2 ca = cs[(int64_t)key * (HD / 2) + 32 * c + e];
-              const float2 cb = cs[(int64_t)key * (HD / 2) + 32 * c + e + 1];
-              const float y1a = a1 * ca.x + a2 * ca.y, y2a = a2 * ca.x - a1 * ca.y;
-              const float y1b = b1 * cb.x + b2 * cb.y, y2b = b2 * cb.x - b1 * cb.y;
-              a1 = y1a; a2 = y2a; b1 = y1b; b2 = y2b;
-            }
-            o1[e / 2] = pack2_bf16(a1, b1);
-            o2[e / 2] = pack2_bf16(a2, b2);
+        for (int e = 0; e < 16; e += 2) {
+          float a1 = __uint_as_float(x1[e]) * scale, b1 = __uint_as_float(x1[e + 1]) * scale;
+          float a2 = __uint_as_float(x2[e]) * scale, b2 = __uint_as_float(x2[e + 1]) * scale;
+          if (cs) {
+            const float2 ca = cs[(int64_t)kp * (HD / 2) + 16 * half + e];
+            const float2 cb = cs[(int64_t)kp * (HD / 2) + 16 * half + e + 1];
+            const float y1a = a1 * ca.x + a2 * ca.y, y2a = a2 * ca.x - a1 * ca.y;
+            const float y1b = b1 * cb.x + b2 * cb.y, y2b = b2 * cb.x - b1 * cb.y;
+            a1 = y1a; a2 = y2a; b1 = y1b; b2 = y2b;
           }
+          o1[e / 2] = pack2_bf16(a1, b1);
+          o2[e / 2] = pack2_bf16(a2, b2);
+        }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            *reinterpret_cast<uint4*>(krow + 32 * c + 8 * k) = make_uint4(o1[4 * k], o1[4 * k + 1], o1[4 * k + 2], o1[4 * k + 3]);
-            *reinterpret_cast<uint4*>(krow + HD / 2 + 32 * c + 8 * k) = make_uint4(o2[4 * k], o2[4 * k + 1], o2[4 * k + 2], o2[4 * k + 3]);
-          }
+        for (int k = 0; k < 2; ++k) {
+          put(sK, 2 * half + k, o1[4 * k], o1[4 * k + 1], o1[4 * k + 2], o1[4 * k + 3]);
+          put(sK, 4 + 2 * half + k, o2[4 * k], o2[4 * k + 1], o2[4 * k + 2], o2[4 * k + 3]);
         }
       }
-#pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
+      {
         uint32_t v[32];
-        tmem_ld_32x32b_x32(lane_base + COL_DV + 32 * c, v);
+        tmem_ld_32x32b_x32(lane_base + COL_DV + 32 * half, v);
         tmem_ld_wait();
-        if (key < S) {
-          const int64_t ld = (int64_t)(Hq + 2 * Hkv) * HD;
-          __nv_bfloat16* vrow = dqkv + ((int64_t)b * S + key) * ld + (int64_t)(Hq + Hkv + g) * HD;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4 u;
-            u.x = pack2_bf16(__uint_as_float(v[8 * k + 0]), __uint_as_float(v[8 * k + 1]));
-            u.y = pack2_bf16(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3]));
-            u.z = pack2_bf16(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5]));
-            u.w = pack2_bf16(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7]));
-            *reinterpret_cast<uint4*>(vrow + 32 * c + 8 * k) = u;
-          }
-        }
+        for (int k = 0; k < 4; ++k)
+          put(sV, 4 * half + k, pack2_bf16(__uint_as_float(v[8 * k + 0]), __uint_as_float(v[8 * k + 1])),
+              pack2_bf16(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
+              pack2_bf16(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
+              pack2_bf16(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
       }
+      fence_proxy_async_smem();
     } else if (lane == 0) {
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
     }
+    if (lane == 0) bulk_wait_group0();  // this warp's dQ reduces are complete
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
+  } else if (threadIdx.x == 64 && !*abort_flag) {
+    // dK and dV tiles; key rows past the sequence end are outside the map
+    tma_store_3d(&tm_dkv, sK, (Hq + g) * HD, k0, b);
+    tma_store_3d(&tm_dkv, sV, (Hq + Hkv + g) * HD, k0, b);
+    bulk_commit_group();
+    bulk_wait_group0();
   }
 }
 
@@ -1553,37 +1635,47 @@ int fwd_pp(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int S,
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
-template <int HD, bool DET, bool WIN>
+template <bool DET, bool WIN>
 int bwd_tc(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
            const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq,
            int Hkv, const float2* cs, AttWindow win, int* err, cudaStream_t st) {
-  using C = AttBwdCfg<HD>;
+  using C = AttBwdCfg;
+  constexpr int HD = C::HD;
   auto fn = encode_fn_att();
   if (!fn) return -3;
   const int64_t W = (int64_t)(Hq + 2 * Hkv) * HD, WO = (int64_t)Hq * HD;
-  CUtensorMap tq, td;
-  cuuint32_t box[3] = {64, 128, 1};
+  CUtensorMap tq, td, tdq, tdkv;
+  cuuint32_t box[3] = {64, 128, 1}, box_dq[3] = {32, 32, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   cuuint64_t dq[3] = {(cuuint64_t)W, (cuuint64_t)S, (cuuint64_t)B};
   cuuint64_t sq[2] = {(cuuint64_t)(W * 2), (cuuint64_t)(S * W * 2)};
   cuuint64_t dd[3] = {(cuuint64_t)WO, (cuuint64_t)S, (cuuint64_t)B};
   cuuint64_t sd[2] = {(cuuint64_t)(WO * 2), (cuuint64_t)(S * WO * 2)};
-  if (fn(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(qkv), dq, sq, box,
-         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-      fn(&td, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(dout), dd, sd, box,
-         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  const int slots = WIN ? attn_window_dq_slots(S, win.size, win.sinks) : (S + 127) / 128;
+  cuuint64_t ddq[3] = {(cuuint64_t)WO, (cuuint64_t)S, (cuuint64_t)(DET ? (int64_t)B * slots : B)};
+  cuuint64_t sdq[2] = {(cuuint64_t)(WO * 4), (cuuint64_t)(S * WO * 4)};
+  auto enc = [&](CUtensorMap* m, CUtensorMapDataType type, const void* base, cuuint64_t* dims,
+                 cuuint64_t* strides, cuuint32_t* bx, CUtensorMapL2promotion l2) {
+    return fn(m, type, 3, const_cast<void*>(base), dims, strides, bx, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, l2,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  if (!enc(&tq, bf, qkv, dq, sq, box, l2) || !enc(&td, bf, dout, dd, sd, box, l2) ||
+      !enc(&tdkv, bf, dqkv, dq, sq, box, l2) ||
+      !enc(&tdq, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dq_acc, ddq, sdq, box_dq,
+           CU_TENSOR_MAP_L2_PROMOTION_NONE))
     return -3;
-  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc_kernel<HD, DET, WIN>), C::SMEM)) return -3;
+  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc_kernel<DET, WIN>), C::SMEM)) return -3;
   const int64_t T = (int64_t)B * S;
   if (!DET && cudaMemsetAsync(dq_acc, 0, (size_t)T * WO * sizeof(float), st) != cudaSuccess)
     return -3;
   attn_delta(o, dout, delta, B, S, Hq, HD, st);
   const float scale = 1.f / sqrtf((float)HD);
   dim3 grid((S + 127) / 128, Hkv, B);
-  attn_bwd_tc_kernel<HD, DET, WIN><<<grid, kAttThreads, C::SMEM, st>>>(
-      tq, td, lse, delta, dq_acc, dqkv, cs, S, Hq, Hkv, scale, scale * 1.4426950408889634f, win, err);
+  attn_bwd_tc_kernel<DET, WIN><<<grid, kAttBwdThreads, C::SMEM, st>>>(
+      tq, td, tdq, tdkv, lse, delta, cs, S, Hq, Hkv, scale, scale * 1.4426950408889634f, win, err);
   attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? (S + 127) / 128 : 0,
                    WIN ? win.size : 0, win.sinks, st);
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
@@ -1644,7 +1736,7 @@ int bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* d
         const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq,
         int Hkv, int hd, const float2* cs, AttWindow win, int* err, cudaStream_t st) {
   if (hd == 64)
-    return bwd_tc<64, DET, WIN>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, win, err, st);
+    return bwd_tc<DET, WIN>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, win, err, st);
   if (hd == 128)
     return bwd_tc2<DET, WIN>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, win, err, st);
   return -1;
