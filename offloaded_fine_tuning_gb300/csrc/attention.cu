@@ -15,6 +15,7 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
 #include "sf_internal.h"
 
 namespace sf {
@@ -30,10 +31,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // delta[b, h, s] = sum_j dO[t, h*hd + j] * O[t, h*hd + j]: TPR = hd / 8
 // threads per (token, head) row, each reading 16 bytes of O and of dO, summed
 // across the row's threads with shuffles.  Consecutive rows are consecutive
-// heads of a token, so a warp reads contiguous memory.
+// heads of a token, so a warp reads contiguous memory.  The thread also zeroes
+// the same eight columns of zero [T, Hq*hd] unless that is null (the buffer
+// that the backward adds dQ into).
 template <int TPR>
 __global__ void attn_delta_kernel(const bf16* __restrict__ o, const bf16* __restrict__ dout,
-                                  float* __restrict__ delta, int64_t rows, int S, int Hq) {
+                                  float* __restrict__ delta, float* __restrict__ zero, int64_t rows,
+                                  int S, int Hq) {
   constexpr int HD = TPR * 8;
   const int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t w = g / TPR;
@@ -43,6 +47,10 @@ __global__ void attn_delta_kernel(const bf16* __restrict__ o, const bf16* __rest
     const int64_t off = w * HD + sub * 8;  // row w = t * Hq + h starts at t*Hq*hd + h*hd
     const uint4 a = *reinterpret_cast<const uint4*>(o + off);
     const uint4 c = *reinterpret_cast<const uint4*>(dout + off);
+    if (zero) {
+      float4* z = reinterpret_cast<float4*>(zero + off);
+      z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
     const __nv_bfloat162* c2 = reinterpret_cast<const __nv_bfloat162*>(&c);
 #pragma unroll
@@ -71,6 +79,7 @@ __global__ void attn_delta_kernel(const bf16* __restrict__ o, const bf16* __rest
 __global__ void attn_dq_kernel(const float* __restrict__ dq_acc, bf16* __restrict__ dqkv,
                                int64_t tokens, int S, int Hq, int Hkv, int hd, float scale,
                                const float2* __restrict__ cs, int slots, int window, int sinks) {
+  wait_primary();
   const int half = hd / 2, groups = half / 8;
   const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= tokens * Hq * groups) return;
@@ -127,15 +136,15 @@ __global__ void attn_dq_kernel(const float* __restrict__ dq_acc, bf16* __restric
   *reinterpret_cast<uint4*>(dst + half) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
 }
 
-void attn_delta(const bf16* o, const bf16* dout, float* delta, int B, int S, int Hq, int hd,
-                cudaStream_t st) {
+void attn_delta(const bf16* o, const bf16* dout, float* delta, float* zero, int B, int S, int Hq,
+                int hd, cudaStream_t st) {
   const int64_t rows = (int64_t)B * S * Hq;
   const int64_t threads = rows * (hd / 8);
   const unsigned grid = (unsigned)((threads + 255) / 256);
   if (hd == 128)
-    attn_delta_kernel<16><<<grid, 256, 0, st>>>(o, dout, delta, rows, S, Hq);
+    attn_delta_kernel<16><<<grid, 256, 0, st>>>(o, dout, delta, zero, rows, S, Hq);
   else
-    attn_delta_kernel<8><<<grid, 256, 0, st>>>(o, dout, delta, rows, S, Hq);
+    attn_delta_kernel<8><<<grid, 256, 0, st>>>(o, dout, delta, zero, rows, S, Hq);
 }
 
 void attn_dq_finalize(const float* dq_acc, bf16* dqkv, int B, int S, int Hq, int Hkv, int hd,
@@ -143,8 +152,16 @@ void attn_dq_finalize(const float* dq_acc, bf16* dqkv, int B, int S, int Hq, int
                       cudaStream_t st) {
   const int64_t T = (int64_t)B * S;
   const int64_t n = T * Hq * (hd / 16);
-  attn_dq_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(dq_acc, dqkv, T, S, Hq, Hkv, hd, scale,
-                                                               cs, slots, window, sinks);
+  cudaLaunchAttribute after[1];
+  after[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  after[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((n + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = after;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, attn_dq_kernel, dq_acc, dqkv, T, S, Hq, Hkv, hd, scale, cs, slots, window, sinks);
 }
 
 }  // namespace sf

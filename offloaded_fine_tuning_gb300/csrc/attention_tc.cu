@@ -686,9 +686,11 @@ __device__ __forceinline__ int dq_slot(const AttWindow& win, int j) {
 }
 }  // namespace
 
-// Backward for head_dim 64.  One CTA per (128-key block j, kv head g, batch b)
-// walks every query head of the group and every 128-query block that sees its
-// keys.  Per (head, block):
+// Backward for head_dim 64.  An item is one (128-key block j, kv head g, batch
+// b): every query head of the group and every 128-query block that sees its
+// keys.  The CTAs are persistent, one per SM, and take the items longest first,
+// every other round in reverse order, so that long and short ones add up.  Per
+// (head, block):
 //   MMA:     S^T = K Q^T -> TMEM[0,128),  dP^T = V dO^T -> TMEM[128,256)
 //   threads: one per key row and half of the queries: P^T = exp2(S^T*scale*
 //            log2e - lse*log2e) (masked), dS^T = P^T * (dP^T - D), both to
@@ -706,7 +708,12 @@ __device__ __forceinline__ int dq_slot(const AttWindow& win, int j) {
 // blocks of 128 queries.  With 64-query blocks and two CTAs sharing an SM the
 // 24 MMAs per 64 queries ran 121 us against the unpipelined 128-query kernel's
 // 155 (8 x 1001 tokens, 16 heads, window 250) but 650 against 570 us where
-// walks are long (2 x 4096, 16 heads in groups of 4).
+// walks are long (2 x 4096, 16 heads in groups of 4).  With a CTA per item a
+// short window's items (four blocks) spent two thirds of their time on setting
+// up, the first loads and the last stores (125 us at the former shape): the
+// barriers' phases count on over all items, the next item's loads and S^T run
+// under the previous item's last dQ and its dK and dV, which leave through the
+// P^T and dS^T buffers, so K and V are free with the item's last MMA.
 namespace {
 constexpr int kAttBwdThreads = 320;  // TMA warp, MMA warp, 8 softmax-gradient warps
 struct AttBwdCfg {
@@ -722,7 +729,7 @@ struct AttBwdCfg {
   static constexpr int OFF_DQS = OFF_DST + 32768;    // dQ staging: 8 warps x [32 q][32 d] fp32
   static constexpr int OFF_LD = OFF_DQS + 8 * 4096;  // [2][lse 128 | D 128]
   static constexpr int OFF_BAR = OFF_LD + 2 * 256 * 4;
-  static constexpr int NBAR = 17;
+  static constexpr int NBAR = 21;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
 };
 static_assert(AttBwdCfg::SMEM <= 232448, "backward shared memory");
@@ -735,7 +742,7 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
                        const __grid_constant__ CUtensorMap tm_dq,
                        const __grid_constant__ CUtensorMap tm_dkv, const float* __restrict__ lse,
                        const float* __restrict__ delta, const float2* __restrict__ cs, int S,
-                       int Hq, int Hkv, float scale, float scale_log2, AttWindow win, int* err) {
+                       int Hq, int Hkv, int B, float scale, float scale_log2, AttWindow win, int* err) {
   using C = AttBwdCfg;
   constexpr int HD = C::HD;
   constexpr uint32_t ID_SP = umma_idesc_bf16(128, 128, false, false);  // S^T, dP^T
@@ -760,17 +767,29 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
   auto dq_full = [&](int i) { return b0 + 88u + 8u * i; };
   auto dq_free = [&](int i) { return b0 + 104u + 8u * i; };
   auto ld_full = [&](int i) { return b0 + 120u + 8u * i; };
+  const uint32_t kv_empty = b0 + 136, acc_free = b0 + 144, dkv_full = b0 + 152, dkv_free = b0 + 160;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int j, g, b;
-  grid_rank_first(j, g, b);  // key block 0 sees the most query blocks
-  const int grp = Hq / Hkv;
-  const int k0 = j * 128;
-  // query blocks j .. j + per_head - 1 can see these keys
-  const int per_head = (WIN ? last_query(win, k0, S) / 128 + 1 : (S + 127) / 128) - j;
-  const int n_it = grp * per_head;  // (head, query block) pairs
+  const int grp = Hq / Hkv, nkb = (S + 127) / 128;
+  const int num_items = nkb * Hkv * B;  // key block 0 sees the most query blocks
+  struct Item { int j, g, b, per_head, n_it; };
+  // this CTA's n-th item (n_it = 0: none left)
+  auto item_of = [&](int n) -> Item {
+    const int c = n & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+    const int t = n * (int)gridDim.x + c;
+    if (t >= num_items) return {0, 0, 0, 1, 0};
+    Item x;
+    x.j = t / (Hkv * B);
+    const int rem = t - x.j * (Hkv * B);
+    x.g = rem % Hkv;
+    x.b = rem / Hkv;
+    // query blocks j .. j + per_head - 1 can see these keys
+    x.per_head = (WIN ? last_query(win, x.j * 128, S) / 128 + 1 : nkb) - x.j;
+    x.n_it = grp * x.per_head;  // (head, query block) pairs
+    return x;
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -780,6 +799,10 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     mbar_init(pds_free, 1);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
+    mbar_init(kv_empty, 1);
+    mbar_init(acc_free, 256);
+    mbar_init(dkv_full, 256);
+    mbar_init(dkv_free, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(qdo_full(i), 1);
       mbar_init(qdo_empty(i), 1);
@@ -805,60 +828,81 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
 
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
-    mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
-    tma_load_3d(sK, &tm_qkv, kv_full, (Hq + g) * HD, k0, b);
-    tma_load_3d(sV, &tm_qkv, kv_full, (Hq + Hkv + g) * HD, k0, b);
     bool ok = true;
-    int issued = 0;
-    for (int it = 0; it < n_it; ++it) {
-      const int bq = it % C::NQ;
-      const int h = g * grp + it / per_head;
-      const int q0 = (j + it % per_head) * 128;
-      if (!mbar_wait(qdo_empty(bq), ((it / C::NQ) & 1) ^ 1, abort_flag)) { ok = false; break; }
-      mbar_arrive_expect_tx(qdo_full(bq), 2 * C::TILE);
-      tma_load_3d(sQ + bq * C::TILE, &tm_qkv, qdo_full(bq), h * HD, q0, b);
-      tma_load_3d(sDO + bq * C::TILE, &tm_do, qdo_full(bq), h * HD, q0, b);
-      issued = it + 1;
+    int issued = 0, kv_issued = 0;  // Q / dO stages and K / V tiles asked for
+    for (int n = 0; ok; ++n) {
+      const Item x = item_of(n);
+      if (x.n_it == 0) break;
+      if (n > 0 && !mbar_wait(kv_empty, (n - 1) & 1, abort_flag)) { ok = false; break; }
+      mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+      tma_load_3d(sK, &tm_qkv, kv_full, (Hq + x.g) * HD, x.j * 128, x.b);
+      tma_load_3d(sV, &tm_qkv, kv_full, (Hq + Hkv + x.g) * HD, x.j * 128, x.b);
+      kv_issued = n + 1;
+      for (int it = 0; it < x.n_it; ++it) {
+        const int bq = issued % C::NQ;
+        const int h = x.g * grp + it / x.per_head;
+        const int q0 = (x.j + it % x.per_head) * 128;
+        if (!mbar_wait(qdo_empty(bq), ((issued / C::NQ) & 1) ^ 1, abort_flag)) { ok = false; break; }
+        mbar_arrive_expect_tx(qdo_full(bq), 2 * C::TILE);
+        tma_load_3d(sQ + bq * C::TILE, &tm_qkv, qdo_full(bq), h * HD, q0, x.b);
+        tma_load_3d(sDO + bq * C::TILE, &tm_do, qdo_full(bq), h * HD, q0, x.b);
+        ++issued;
+      }
     }
     if (!ok) {
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
-      mbar_wait(kv_full, 0, nullptr);
+      if (kv_issued > 0) mbar_wait(kv_full, (kv_issued - 1) & 1, nullptr);
       for (int it = issued - 1; it >= 0 && it >= issued - C::NQ; --it)
         mbar_wait(qdo_full(it % C::NQ), (it / C::NQ) & 1, nullptr);
     }
   } else if (warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
-    bool ok = mbar_wait(kv_full, 0, abort_flag);
+    bool ok = true;
     // base descriptors; an operand at byte offset o is the base plus o / 16
     const uint64_t dK = smem_desc_sw128(sK, 16, 1024), dV = smem_desc_sw128(sV, 16, 1024);
     const uint64_t dQk = smem_desc_sw128(sQ, 16, 1024), dDOk = smem_desc_sw128(sDO, 16, 1024);
     const uint64_t dPt = smem_desc_sw128(sPt, 16, 1024), dDSt = smem_desc_sw128(sDSt, 16, 1024);
     const uint64_t dQm = smem_desc_sw128(sQ, 16384, 1024), dDOm = smem_desc_sw128(sDO, 16384, 1024);
     const uint64_t dKm = smem_desc_sw128(sK, 16384, 1024), dDStm = smem_desc_sw128(sDSt, 16384, 1024);
-    for (int it = 0; ok && it <= n_it; ++it) {
-      if (it < n_it) {  // S^T and dP^T of block it, once the threads hold block it - 1's
-        const int bq = it % C::NQ;
-        if (!mbar_wait(qdo_full(bq), (it / C::NQ) & 1, abort_flag)) { ok = false; break; }
-        if (it >= 1 && !mbar_wait(s_free, (it - 1) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t qo = (uint32_t)bq * (uint32_t)(C::TILE / 16);
+    // One step: S^T and dP^T of block G + 1, then dV, dK and dQ of block G,
+    // G counting the blocks of all items.
+    auto issue_sp = [&](int G) -> bool {  // once the threads hold block G - 1's
+      const int bq = G % C::NQ;
+      if (!mbar_wait(qdo_full(bq), (G / C::NQ) & 1, abort_flag)) return false;
+      if (G >= 1 && !mbar_wait(s_free, (G - 1) & 1, abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t qo = (uint32_t)bq * (uint32_t)(C::TILE / 16);
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          umma_bf16(tmem_base, dK + kk * 2, dQk + qo + kk * 2, ID_SP, kk > 0 ? 1u : 0u);
-          umma_bf16(tmem_base + COL_DP, dV + kk * 2, dDOk + qo + kk * 2, ID_SP, kk > 0 ? 1u : 0u);
-        }
-        umma_commit(sp_full);
+      for (int kk = 0; kk < HD / 16; ++kk) {
+        umma_bf16(tmem_base, dK + kk * 2, dQk + qo + kk * 2, ID_SP, kk > 0 ? 1u : 0u);
+        umma_bf16(tmem_base + COL_DP, dV + kk * 2, dDOk + qo + kk * 2, ID_SP, kk > 0 ? 1u : 0u);
       }
-      if (it >= 1) {  // dV, dK, dQ of block it - 1, once its P^T and dS^T are in shared memory
-        const int ip = it - 1, bq = ip % C::NQ, bd = ip & 1;
-        if (!mbar_wait(ps_full, ip & 1, abort_flag)) { ok = false; break; }
-        if (ip >= 2 && !mbar_wait(dq_free(bd), ((ip >> 1) - 1) & 1, abort_flag)) { ok = false; break; }
+      umma_commit(sp_full);
+      return true;
+    };
+    Item x = item_of(0);
+    int G = 0;
+    for (int n = 0; ok && x.n_it > 0; ++n) {
+      // the item's first S^T needs its K and V, which arrive once the previous
+      // item's last MMA has read the buffers
+      ok = mbar_wait(kv_full, n & 1, abort_flag) && issue_sp(G);
+      for (int it = 0; ok && it < x.n_it; ++it, ++G) {
+        if (it + 1 < x.n_it && !issue_sp(G + 1)) { ok = false; break; }
+        const int bq = G % C::NQ, bd = G & 1;
+        // P^T and dS^T of this block are in shared memory; its dQ buffer has
+        // been read; the accumulators of the previous item have been read
+        if (!mbar_wait(ps_full, G & 1, abort_flag) ||
+            (G >= 2 && !mbar_wait(dq_free(bd), ((G >> 1) - 1) & 1, abort_flag)) ||
+            (it == 0 && n > 0 && !mbar_wait(acc_free, (n - 1) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const uint32_t qo = (uint32_t)bq * (uint32_t)(C::TILE / 16);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {  // over the 128 queries
-          const uint32_t acc = (ip > 0 || kk > 0) ? 1u : 0u;
+          const uint32_t acc = (it > 0 || kk > 0) ? 1u : 0u;
           const uint32_t ao = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;
           umma_bf16(tmem_base + COL_DV, dPt + ao, dDOm + qo + kk * 128, ID_KV, acc);
           umma_bf16(tmem_base + COL_DK, dDSt + ao, dQm + qo + kk * 128, ID_KV, acc);
@@ -870,10 +914,13 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
         umma_commit(qdo_empty(bq));
         umma_commit(pds_free);
       }
+      if (ok) {
+        umma_commit(kv_empty);
+        umma_commit(acc_done);
+      }
+      x = item_of(n + 1);
     }
-    if (ok) {
-      umma_commit(acc_done);
-    } else {
+    if (!ok) {
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
       umma_commit(drain);
@@ -885,34 +932,31 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     // (of S^T and dP^T) and half of the head's columns (of dQ).
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const int r = quarter * 32 + lane;  // key row of S^T / dP^T; query row of dQ
-    const int key = k0 + r;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const int tid = threadIdx.x - 64;  // 0..255
-    // the last query that sees this thread's key (before the key: no one does)
-    const int q_end = !WIN || key < win.sinks || key > S - win.size ? S - 1 : key + win.size - 1;
     bool ok = true;
-    // lse (log2 units) and D of the query block, one value per thread of the
+    // lse (log2 units) and D of a query block, one value per thread of the
     // first 128, loaded one block ahead
-    auto fetch = [&](int it_, float& lv, float& dv) {
+    auto fetch = [&](const Item& x, int it_, float& lv, float& dv) {
       lv = 0.f;
       dv = 0.f;
-      if (it_ >= n_it || tid >= 128) return;
-      const int h_ = g * grp + it_ / per_head;
-      const int q_ = (j + it_ % per_head) * 128 + tid;
+      if (it_ >= x.n_it || tid >= 128) return;
+      const int h_ = x.g * grp + it_ / x.per_head;
+      const int q_ = (x.j + it_ % x.per_head) * 128 + tid;
       if (q_ < S) {
-        const int64_t o = ((int64_t)b * Hq + h_) * S + q_;
-        lv = lse[o] * 1.4426950408889634f;
+        const int64_t o = ((int64_t)x.b * Hq + h_) * S + q_;
+        lv = lse[o];
         dv = delta[o];
       }
     };
-    // dQ of block it_ (this warp's 32 queries and 32 columns) into the warp's
+    // dQ of an item's block it_, the G-th of all (this warp's 32 queries and 32 columns) into the warp's
     // staging tile, in the tensor map's 128-byte swizzle, then one TMA
     // reduce-add (or store).  The tile is rewritten only after the previous
     // one has finished reading it.
     const uint32_t stage = sDQS + (uint32_t)(warp - 2) * 4096u;
-    auto emit_dq = [&](int it_) -> bool {
-      const int bd = it_ & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(dq_full(bd), (it_ >> 1) & 1, abort_flag))) return false;
+    auto emit_dq = [&](const Item& x, int it_, int G) -> bool {
+      const int bd = G & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(dq_full(bd), (G >> 1) & 1, abort_flag))) return false;
       tc_fence_after();
       uint32_t v[32];
       tmem_ld_32x32b_x32(lane_base + COL_DQ + 64 * bd + 32 * half, v);
@@ -930,186 +974,209 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        const int h_ = g * grp + it_ / per_head;
-        const int qb_ = (j + it_ % per_head) * 128 + 32 * quarter;
+        const int h_ = x.g * grp + it_ / x.per_head;
+        const int qb_ = (x.j + it_ % x.per_head) * 128 + 32 * quarter;
         if (qb_ < S) {  // rows past the sequence end are outside the map
           if (DET)  // this key block's own slot of the dQ buffer
             tma_store_3d(&tm_dq, stage, h_ * HD + 32 * half, qb_,
-                         (WIN ? dq_slot(win, j) : j) * (int)gridDim.z + b);
+                         (WIN ? dq_slot(win, x.j) : x.j) * B + x.b);
           else
-            tma_reduce_add_3d(&tm_dq, stage, h_ * HD + 32 * half, qb_, b);
+            tma_reduce_add_3d(&tm_dq, stage, h_ * HD + 32 * half, qb_, x.b);
         }
         bulk_commit_group();
       }
       return true;
     };
+    wait_primary();  // D, and the zeros in dq_acc
     float next_l, next_d;
-    fetch(0, next_l, next_d);
     const uint32_t rowoff = (uint32_t)r * 128u + (uint32_t)half * 16384u;
-    for (int it = 0; it < n_it; ++it) {
-      const int qc = (j + it % per_head) * 128 + 64 * half;  // first query of this thread's columns
-      float* bL = sLD + (it & 1) * 256;
-      float* bD = bL + 128;
-      // The buffer written here was last read for block it - 2; this thread
-      // has since waited for that block's P^T / dS^T to be consumed, which
-      // needed every thread to have finished computing it.
-      if (tid < 128) {
-        bL[tid] = next_l;
-        bD[tid] = next_d;
-        mbar_arrive(ld_full(it & 1));
-      }
-      fetch(it + 1, next_l, next_d);
-      ok = __all_sync(0xffffffffu, mbar_wait(ld_full(it & 1), (it >> 1) & 1, abort_flag));
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sp_full, it & 1, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sr[2][32], dr[2][32];
+    Item x = item_of(0);
+    fetch(x, 0, next_l, next_d);
+    int G = 0;
+    for (int n = 0; ok && x.n_it > 0; ++n) {
+      const Item next = item_of(n + 1);
+      const int key = x.j * 128 + r;
+      // the last query that sees this thread's key (before the key: no one does)
+      const int q_end = !WIN || key < win.sinks || key > S - win.size ? S - 1 : key + win.size - 1;
+      for (int it = 0; it < x.n_it; ++it, ++G) {
+        const int qc = (x.j + it % x.per_head) * 128 + 64 * half;  // first query of this thread's columns
+        float* bL = sLD + (G & 1) * 256;
+        float* bD = bL + 128;
+        // The buffer written here was last read for block G - 2; this thread
+        // has since waited for that block's P^T / dS^T to be consumed, which
+        // needed every thread to have finished computing it.
+        if (tid < 128) {
+          bL[tid] = next_l * 1.4426950408889634f;
+          bD[tid] = next_d;
+          mbar_arrive(ld_full(G & 1));
+        }
+        if (it + 1 < x.n_it) fetch(x, it + 1, next_l, next_d);
+        else fetch(next, 0, next_l, next_d);
+        ok = __all_sync(0xffffffffu, mbar_wait(ld_full(G & 1), (G >> 1) & 1, abort_flag));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sp_full, G & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[2][32], dr[2][32];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        tmem_ld_32x32b_x32(lane_base + 64 * half + 32 * c, sr[c]);
-        tmem_ld_32x32b_x32(lane_base + COL_DP + 64 * half + 32 * c, dr[c]);
-      }
-      tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive(s_free);  // S^T / dP^T are in registers: the next block may overwrite them
-      // P^T over S^T's registers, dS^T over dP^T's, packed
+        for (int c = 0; c < 2; ++c) {
+          tmem_ld_32x32b_x32(lane_base + 64 * half + 32 * c, sr[c]);
+          tmem_ld_32x32b_x32(lane_base + COL_DP + 64 * half + 32 * c, dr[c]);
+        }
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(s_free);  // S^T / dP^T are in registers: the next block may overwrite them
+        // P^T over S^T's registers, dS^T over dP^T's, packed
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int q1 = qc + 32 * c;
-        const uint32_t seen = low_bits(q_end - q1 + 1) & ~low_bits(key - q1);
-        const float4* L4 = reinterpret_cast<const float4*>(bL + 64 * half + 32 * c);
-        const float4* D4 = reinterpret_cast<const float4*>(bD + 64 * half + 32 * c);
-        auto grad_tile = [&](auto mask_tag) {
-          constexpr bool kMask = decltype(mask_tag)::value;
+        for (int c = 0; c < 2; ++c) {
+          const int q1 = qc + 32 * c;
+          const uint32_t seen = low_bits(q_end - q1 + 1) & ~low_bits(key - q1);
+          const float4* L4 = reinterpret_cast<const float4*>(bL + 64 * half + 32 * c);
+          const float4* D4 = reinterpret_cast<const float4*>(bD + 64 * half + 32 * c);
+          auto grad_tile = [&](auto mask_tag) {
+            constexpr bool kMask = decltype(mask_tag)::value;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 l4 = L4[k], d4 = D4[k];
-            const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
-            const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
-            float pv[4], sv[4];
+            for (int k = 0; k < 8; ++k) {
+              const float4 l4 = L4[k], d4 = D4[k];
+              const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+              const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
+              float pv[4], sv[4];
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const int e = 4 * k + i;
-              float x0 = __uint_as_float(sr[c][e]), x1 = __uint_as_float(sr[c][e + 1]);
-              fma2(x0, x1, scale_log2, -lv[i], -lv[i + 1]);
-              x0 = ex2_approx(x0);
-              x1 = ex2_approx(x1);
-              if (kMask && !(seen & (1u << e))) x0 = 0.f;
-              if (kMask && !(seen & (2u << e))) x1 = 0.f;
-              float d0 = __uint_as_float(dr[c][e]), d1 = __uint_as_float(dr[c][e + 1]);
-              add2(d0, d1, -dv[i], -dv[i + 1]);
-              mul2(d0, d1, x0, x1);
-              pv[i] = x0;
-              pv[i + 1] = x1;
-              sv[i] = d0;
-              sv[i + 1] = d1;
+              for (int i = 0; i < 4; i += 2) {
+                const int e = 4 * k + i;
+                float x0 = __uint_as_float(sr[c][e]), x1 = __uint_as_float(sr[c][e + 1]);
+                fma2(x0, x1, scale_log2, -lv[i], -lv[i + 1]);
+                x0 = ex2_approx(x0);
+                x1 = ex2_approx(x1);
+                if (kMask && !(seen & (1u << e))) x0 = 0.f;
+                if (kMask && !(seen & (2u << e))) x1 = 0.f;
+                float d0 = __uint_as_float(dr[c][e]), d1 = __uint_as_float(dr[c][e + 1]);
+                add2(d0, d1, -dv[i], -dv[i + 1]);
+                mul2(d0, d1, x0, x1);
+                pv[i] = x0;
+                pv[i + 1] = x1;
+                sv[i] = d0;
+                sv[i + 1] = d1;
+              }
+              sr[c][2 * k] = pack2_bf16(pv[0], pv[1]);
+              sr[c][2 * k + 1] = pack2_bf16(pv[2], pv[3]);
+              dr[c][2 * k] = pack2_bf16(sv[0], sv[1]);
+              dr[c][2 * k + 1] = pack2_bf16(sv[2], sv[3]);
             }
-            sr[c][2 * k] = pack2_bf16(pv[0], pv[1]);
-            sr[c][2 * k + 1] = pack2_bf16(pv[2], pv[3]);
-            dr[c][2 * k] = pack2_bf16(sv[0], sv[1]);
-            dr[c][2 * k + 1] = pack2_bf16(sv[2], sv[3]);
+          };
+          if (__all_sync(0xffffffffu, seen == 0xffffffffu))
+            grad_tile(std::false_type{});
+          else
+            grad_tile(std::true_type{});
+        }
+        if (G >= 1) {  // P^T, dS^T of the previous block consumed
+          ok = __all_sync(0xffffffffu, mbar_wait(pds_free, (G - 1) & 1, abort_flag));
+          if (!ok) break;
+        }
+        // dK and dV of the previous item, staged in the same buffers, have been
+        // read by their TMA stores
+        if (it == 0 && n > 0) {
+          if (threadIdx.x == 64) {
+            bulk_wait_group_read0();
+            mbar_arrive(dkv_free);
           }
+          ok = __all_sync(0xffffffffu, mbar_wait(dkv_free, (n - 1) & 1, abort_flag));
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t off = rowoff + (uint32_t)(((4 * c + k) ^ (r & 7)) * 16);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPt + off), "r"(sr[c][4 * k]),
+                         "r"(sr[c][4 * k + 1]), "r"(sr[c][4 * k + 2]), "r"(sr[c][4 * k + 3])
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sDSt + off), "r"(dr[c][4 * k]),
+                         "r"(dr[c][4 * k + 1]), "r"(dr[c][4 * k + 2]), "r"(dr[c][4 * k + 3])
+                         : "memory");
+          }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(ps_full);
+        // dQ of the item's previous block, while the tensor core works on this one's
+        if (it >= 1 && !emit_dq(x, it - 1, G - 1)) { ok = false; break; }
+      }
+      if (ok) ok = emit_dq(x, x.n_it - 1, G - 1);
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, n & 1, abort_flag));
+      if (ok) {
+        tc_fence_after();
+        // dK and dV rows go into the P^T and dS^T buffers (every MMA that read
+        // them has completed), in the tensor map's swizzled layout; one thread
+        // then stores both tiles with the TMA unit.
+        auto put = [&](uint32_t tile, int chunk, uint32_t a, uint32_t b_, uint32_t c_, uint32_t d_) {
+          const uint32_t addr = tile + (uint32_t)r * 128u + (uint32_t)((chunk ^ (r & 7)) * 16);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b_),
+                       "r"(c_), "r"(d_)
+                       : "memory");
         };
-        if (__all_sync(0xffffffffu, seen == 0xffffffffu))
-          grad_tile(std::false_type{});
-        else
-          grad_tile(std::true_type{});
-      }
-      if (it >= 1) {  // P^T, dS^T of the previous block consumed
-        ok = __all_sync(0xffffffffu, mbar_wait(pds_free, (it - 1) & 1, abort_flag));
-        if (!ok) break;
-      }
+        // dK: pairs (d, d + HD/2) get the inverse rotation of the key's position;
+        // this warp takes d in [16 half, 16 half + 16) and their partners
+        {
+          uint32_t x1[16], x2[16];
+          tmem_ld_32x32b_x16(lane_base + COL_DK + 16 * half, x1);
+          tmem_ld_32x32b_x16(lane_base + COL_DK + HD / 2 + 16 * half, x2);
+          tmem_ld_wait();
+          const int kp = key < S ? key : S - 1;  // rows past the end are computed, not stored
+          uint32_t o1[8], o2[8];
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t off = rowoff + (uint32_t)(((4 * c + k) ^ (r & 7)) * 16);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPt + off), "r"(sr[c][4 * k]),
-                       "r"(sr[c][4 * k + 1]), "r"(sr[c][4 * k + 2]), "r"(sr[c][4 * k + 3])
-                       : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sDSt + off), "r"(dr[c][4 * k]),
-                       "r"(dr[c][4 * k + 1]), "r"(dr[c][4 * k + 2]), "r"(dr[c][4 * k + 3])
-                       : "memory");
-        }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(ps_full);
-      if (it >= 1) {  // dQ of the previous block, while the tensor core works on this one's
-        ok = emit_dq(it - 1);
-        if (!ok) break;
-      }
-    }
-    if (ok) ok = emit_dq(n_it - 1);
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, abort_flag));
-    if (ok) {
-      tc_fence_after();
-      // dK and dV rows go into the K and V tiles' shared memory (every MMA
-      // that read them has completed), in the tensor map's swizzled layout;
-      // one thread then stores both tiles with the TMA unit.
-      auto put = [&](uint32_t tile, int chunk, uint32_t a, uint32_t b_, uint32_t c_, uint32_t d_) {
-        const uint32_t addr = tile + (uint32_t)r * 128u + (uint32_t)((chunk ^ (r & 7)) * 16);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b_),
-                     "r"(c_), "r"(d_)
-                     : "memory");
-      };
-      // dK: pairs (d, d + HD/2) get the inverse rotation of the key's position;
-      // this warp takes d in [16 half, 16 half + 16) and their partners
-      {
-        uint32_t x1[16], x2[16];
-        tmem_ld_32x32b_x16(lane_base + COL_DK + 16 * half, x1);
-        tmem_ld_32x32b_x16(lane_base + COL_DK + HD / 2 + 16 * half, x2);
-        tmem_ld_wait();
-        const int kp = key < S ? key : S - 1;  // rows past the end are computed, not stored
-        uint32_t o1[8], o2[8];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          float a1 = __uint_as_float(x1[e]) * scale, b1 = __uint_as_float(x1[e + 1]) * scale;
-          float a2 = __uint_as_float(x2[e]) * scale, b2 = __uint_as_float(x2[e + 1]) * scale;
-          if (cs) {
-            const float2 ca = cs[(int64_t)kp * (HD / 2) + 16 * half + e];
-            const float2 cb = cs[(int64_t)kp * (HD / 2) + 16 * half + e + 1];
-            const float y1a = a1 * ca.x + a2 * ca.y, y2a = a2 * ca.x - a1 * ca.y;
-            const float y1b = b1 * cb.x + b2 * cb.y, y2b = b2 * cb.x - b1 * cb.y;
-            a1 = y1a; a2 = y2a; b1 = y1b; b2 = y2b;
+          for (int e = 0; e < 16; e += 2) {
+            float a1 = __uint_as_float(x1[e]) * scale, b1 = __uint_as_float(x1[e + 1]) * scale;
+            float a2 = __uint_as_float(x2[e]) * scale, b2 = __uint_as_float(x2[e + 1]) * scale;
+            if (cs) {
+              const float2 ca = cs[(int64_t)kp * (HD / 2) + 16 * half + e];
+              const float2 cb = cs[(int64_t)kp * (HD / 2) + 16 * half + e + 1];
+              const float y1a = a1 * ca.x + a2 * ca.y, y2a = a2 * ca.x - a1 * ca.y;
+              const float y1b = b1 * cb.x + b2 * cb.y, y2b = b2 * cb.x - b1 * cb.y;
+              a1 = y1a; a2 = y2a; b1 = y1b; b2 = y2b;
+            }
+            o1[e / 2] = pack2_bf16(a1, b1);
+            o2[e / 2] = pack2_bf16(a2, b2);
           }
-          o1[e / 2] = pack2_bf16(a1, b1);
-          o2[e / 2] = pack2_bf16(a2, b2);
-        }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          put(sK, 2 * half + k, o1[4 * k], o1[4 * k + 1], o1[4 * k + 2], o1[4 * k + 3]);
-          put(sK, 4 + 2 * half + k, o2[4 * k], o2[4 * k + 1], o2[4 * k + 2], o2[4 * k + 3]);
+          for (int k = 0; k < 2; ++k) {
+            put(sPt, 2 * half + k, o1[4 * k], o1[4 * k + 1], o1[4 * k + 2], o1[4 * k + 3]);
+            put(sPt, 4 + 2 * half + k, o2[4 * k], o2[4 * k + 1], o2[4 * k + 2], o2[4 * k + 3]);
+          }
+        }
+        {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(lane_base + COL_DV + 32 * half, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            put(sDSt, 4 * half + k, pack2_bf16(__uint_as_float(v[8 * k + 0]), __uint_as_float(v[8 * k + 1])),
+                pack2_bf16(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
+                pack2_bf16(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
+                pack2_bf16(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
+        }
+        tc_fence_before();
+        mbar_arrive(acc_free);  // the next item's dV and dK may be formed
+        fence_proxy_async_smem();
+        mbar_arrive(dkv_full);
+        if (warp == 2) ok = __all_sync(0xffffffffu, mbar_wait(dkv_full, n & 1, abort_flag));
+        if (ok && threadIdx.x == 64) {  // key rows past the sequence end are outside the map
+          tma_store_3d(&tm_dkv, sPt, (Hq + x.g) * HD, x.j * 128, x.b);
+          tma_store_3d(&tm_dkv, sDSt, (Hq + Hkv + x.g) * HD, x.j * 128, x.b);
+          bulk_commit_group();
         }
       }
-      {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(lane_base + COL_DV + 32 * half, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          put(sV, 4 * half + k, pack2_bf16(__uint_as_float(v[8 * k + 0]), __uint_as_float(v[8 * k + 1])),
-              pack2_bf16(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
-              pack2_bf16(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
-              pack2_bf16(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
-      }
-      fence_proxy_async_smem();
-    } else if (lane == 0) {
+      x = next;
+    }
+    if (!ok && lane == 0) {
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
     }
-    if (lane == 0) bulk_wait_group0();  // this warp's dQ reduces are complete
+    if (lane == 0) bulk_wait_group0();  // this warp's stores are complete
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
-  } else if (threadIdx.x == 64 && !*abort_flag) {
-    // dK and dV tiles; key rows past the sequence end are outside the map
-    tma_store_3d(&tm_dkv, sK, (Hq + g) * HD, k0, b);
-    tma_store_3d(&tm_dkv, sV, (Hq + Hkv + g) * HD, k0, b);
-    bulk_commit_group();
-    bulk_wait_group0();
   }
 }
 
@@ -1334,7 +1401,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       const int q_ = (first + it_ % per_head) * 64 + tid;
       if (q_ < S) {
         const int64_t o = ((int64_t)b * Hq + h_) * S + q_;
-        lv = lse[o] * 1.4426950408889634f;
+        lv = lse[o];
         dv = delta[o];
       }
     };
@@ -1373,6 +1440,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       stage_dq(it_, v);
       return true;
     };
+    wait_primary();  // D, and the zeros in dq_acc
     float next_l, next_d;
     fetch(0, next_l, next_d);
     const uint32_t rowoff = (uint32_t)r * 128u;
@@ -1385,7 +1453,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       // has since waited for that block's P^T / dS^T to be consumed, which
       // needed every thread to have finished computing it.
       if (tid < 64) {
-        bL[tid] = next_l;
+        bL[tid] = next_l * 1.4426950408889634f;
         bD[tid] = next_d;
         mbar_arrive(ld_full(it & 1));
       }
@@ -1588,6 +1656,23 @@ bool smem_attr_set(const void* kern, int bytes) {
   return true;
 }
 
+// Launch `kern` so that it may be set up while the stream's previous kernel
+// ends; it calls wait_primary() before it uses that kernel's results.
+template <class... P, class... A>
+bool launch_dependent(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute after[1];
+  after[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  after[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = after;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn_att() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -1668,14 +1753,13 @@ int bwd_tc(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16
            CU_TENSOR_MAP_L2_PROMOTION_NONE))
     return -3;
   if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc_kernel<DET, WIN>), C::SMEM)) return -3;
-  const int64_t T = (int64_t)B * S;
-  if (!DET && cudaMemsetAsync(dq_acc, 0, (size_t)T * WO * sizeof(float), st) != cudaSuccess)
-    return -3;
-  attn_delta(o, dout, delta, B, S, Hq, HD, st);
+  attn_delta(o, dout, delta, DET ? nullptr : dq_acc, B, S, Hq, HD, st);
   const float scale = 1.f / sqrtf((float)HD);
-  dim3 grid((S + 127) / 128, Hkv, B);
-  attn_bwd_tc_kernel<DET, WIN><<<grid, kAttBwdThreads, C::SMEM, st>>>(
-      tq, td, tdq, tdkv, lse, delta, cs, S, Hq, Hkv, scale, scale * 1.4426950408889634f, win, err);
+  const int items = (S + 127) / 128 * Hkv * B, sms = num_sms();
+  if (!launch_dependent(attn_bwd_tc_kernel<DET, WIN>, dim3(items < sms ? items : sms), kAttBwdThreads,
+                        C::SMEM, st, tq, td, tdq, tdkv, lse, (const float*)delta, cs, S, Hq, Hkv, B,
+                        scale, scale * 1.4426950408889634f, win, err))
+    return -3;
   attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? (S + 127) / 128 : 0,
                    WIN ? win.size : 0, win.sinks, st);
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
@@ -1714,15 +1798,13 @@ int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat1
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return -3;
   if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc2_kernel<DET, WIN>), C::SMEM)) return -3;
-  const int64_t T = (int64_t)B * S;
-  if (!DET && cudaMemsetAsync(dq_acc, 0, (size_t)T * WO * sizeof(float), st) != cudaSuccess)
-    return -3;
-  attn_delta(o, dout, delta, B, S, Hq, HD, st);
+  attn_delta(o, dout, delta, DET ? nullptr : dq_acc, B, S, Hq, HD, st);
   const float scale = 1.f / sqrtf((float)HD);
   dim3 grid((S + 127) / 128, Hkv, B);
-  attn_bwd_tc2_kernel<DET, WIN><<<grid, kAttBwd2Threads, C::SMEM, st>>>(
-      tkv, tq, td, tdq, tdkv, lse, delta, cs, S, Hq, Hkv, scale, scale * 1.4426950408889634f, win,
-      err);
+  if (!launch_dependent(attn_bwd_tc2_kernel<DET, WIN>, grid, kAttBwd2Threads, C::SMEM, st, tkv, tq, td,
+                        tdq, tdkv, lse, (const float*)delta, cs, S, Hq, Hkv, scale,
+                        scale * 1.4426950408889634f, win, err))
+    return -3;
   attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? nkb : 0, WIN ? win.size : 0,
                    win.sinks, st);
   return cudaGetLastError() == cudaSuccess ? 0 : -3;

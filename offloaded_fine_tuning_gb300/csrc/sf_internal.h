@@ -138,11 +138,13 @@ int attn_bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat
              const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B, int S,
              int Hq, int Hkv, int hd, const float2* cs, bool deterministic, int* err,
              cudaStream_t st);
-// delta[b, h, s] = sum_j dO * O over one head's row (attention.cu)
-void attn_delta(const __nv_bfloat16* o, const __nv_bfloat16* dout, float* delta, int B, int S,
-                int Hq, int hd, cudaStream_t st);
+// delta[b, h, s] = sum_j dO * O over one head's row (attention.cu); zeroes
+// zero [B*S, Hq*hd] unless it is null
+void attn_delta(const __nv_bfloat16* o, const __nv_bfloat16* dout, float* delta, float* zero, int B,
+                int S, int Hq, int hd, cudaStream_t st);
 // dQ = scale * (accumulated or slot-summed dq_acc), inverse RoPE, into the
 // query columns of dqkv (attention.cu); slots = 0 for one accumulated buffer.
+// Launched as the dependent of the backward kernel before it.
 void attn_dq_finalize(const float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq, int Hkv,
                       int hd, float scale, const float2* cs, int slots, int window, int sinks,
                       cudaStream_t st);
