@@ -709,28 +709,31 @@ __device__ __forceinline__ int dq_slot(const AttWindow& win, int j) {
 // 24 MMAs per 64 queries ran 121 us against the unpipelined 128-query kernel's
 // 155 (8 x 1001 tokens, 16 heads, window 250) but 650 against 570 us where
 // walks are long (2 x 4096, 16 heads in groups of 4).  With a CTA per item a
-// short window's items (four blocks) spent two thirds of their time on setting
-// up, the first loads and the last stores (125 us at the former shape): the
-// barriers' phases count on over all items, the next item's loads and S^T run
-// under the previous item's last dQ and its dK and dV, which leave through the
-// P^T and dS^T buffers, so K and V are free with the item's last MMA.
+// short window's items (four blocks) spent more time on setting up, the first
+// loads and the last stores than on their blocks.  So the barriers' phases
+// count on over all items, K and V have two stages, and the first block of the
+// next item is formed (S^T, P^T) before the previous item's dK and dV are
+// read; those leave through that item's own K and V buffers.
 namespace {
-constexpr int kAttBwdThreads = 320;  // TMA warp, MMA warp, 8 softmax-gradient warps
+// TMA warp, MMA warp, 8 softmax-gradient warps, dK / dV store warp
+constexpr int kAttBwdThreads = 352;
 struct AttBwdCfg {
   static constexpr int HD = 64;
   static constexpr int TILE = 16384;  // 128 rows x 64 hd
   static constexpr int NQ = 2;        // Q / dO stages
   static constexpr int OFF_K = 0;
-  static constexpr int OFF_V = TILE;
-  static constexpr int OFF_Q = 2 * TILE;
+  static constexpr int OFF_V = 2 * TILE;
+  static constexpr int OFF_Q = 4 * TILE;  // K and V: two stages each
   static constexpr int OFF_DO = OFF_Q + NQ * TILE;
   static constexpr int OFF_PT = OFF_DO + NQ * TILE;  // 128 keys x 128 queries, two boxes of 64
   static constexpr int OFF_DST = OFF_PT + 32768;
   static constexpr int OFF_DQS = OFF_DST + 32768;    // dQ staging: 8 warps x [32 q][32 d] fp32
   static constexpr int OFF_LD = OFF_DQS + 8 * 4096;  // [2][lse 128 | D 128]
   static constexpr int OFF_BAR = OFF_LD + 2 * 256 * 4;
-  static constexpr int NBAR = 21;
-  static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+  static constexpr int NBAR = 23;
+  // no room to align the base: it is 1024-byte aligned where a kernel has no
+  // static shared memory, which the kernel checks
+  static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
 };
 static_assert(AttBwdCfg::SMEM <= 232448, "backward shared memory");
 }  // namespace
@@ -752,22 +755,27 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
   constexpr uint32_t COL_DP = 128, COL_DQ = 256, COL_DV = 384, COL_DK = 448;
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  uint8_t* smem = smem_raw;
   const uint32_t s0 = smem_u32(smem);
+  if (s0 & 1023u) {
+    if (threadIdx.x == 0) record_error(err, kDevAttnTimeout);
+    return;
+  }
   const uint32_t sK = s0 + C::OFF_K, sV = s0 + C::OFF_V, sQ = s0 + C::OFF_Q, sDO = s0 + C::OFF_DO;
   const uint32_t sPt = s0 + C::OFF_PT, sDSt = s0 + C::OFF_DST, sDQS = s0 + C::OFF_DQS;
   float* sLD = reinterpret_cast<float*>(smem + C::OFF_LD);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   const uint32_t b0 = smem_u32(bars);
-  const uint32_t kv_full = b0, sp_full = b0 + 8, s_free = b0 + 16, ps_full = b0 + 24,
+  const uint32_t sp_full = b0 + 8, s_free = b0 + 16, ps_full = b0 + 24,
                  pds_free = b0 + 32, acc_done = b0 + 40, drain = b0 + 48;
   auto qdo_full = [&](int i) { return b0 + 56u + 8u * i; };
   auto qdo_empty = [&](int i) { return b0 + 72u + 8u * i; };
   auto dq_full = [&](int i) { return b0 + 88u + 8u * i; };
   auto dq_free = [&](int i) { return b0 + 104u + 8u * i; };
   auto ld_full = [&](int i) { return b0 + 120u + 8u * i; };
-  const uint32_t kv_empty = b0 + 136, acc_free = b0 + 144, dkv_full = b0 + 152, dkv_free = b0 + 160;
+  const uint32_t acc_free = b0 + 136, dkv_full = b0 + 144;
+  auto kv_full = [&](int i) { return b0 + 152u + 8u * i; };
+  auto kv_empty = [&](int i) { return b0 + 168u + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -792,20 +800,19 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
   };
 
   if (threadIdx.x == 0) {
-    mbar_init(kv_full, 1);
     mbar_init(sp_full, 1);
     mbar_init(s_free, 256);
     mbar_init(ps_full, 256);
     mbar_init(pds_free, 1);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
-    mbar_init(kv_empty, 1);
     mbar_init(acc_free, 256);
     mbar_init(dkv_full, 256);
-    mbar_init(dkv_free, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(qdo_full(i), 1);
       mbar_init(qdo_empty(i), 1);
+      mbar_init(kv_full(i), 1);
+      mbar_init(kv_empty(i), 1);
       mbar_init(dq_full(i), 1);
       mbar_init(dq_free(i), 256);
       mbar_init(ld_full(i), 128);
@@ -833,10 +840,11 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     for (int n = 0; ok; ++n) {
       const Item x = item_of(n);
       if (x.n_it == 0) break;
-      if (n > 0 && !mbar_wait(kv_empty, (n - 1) & 1, abort_flag)) { ok = false; break; }
-      mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
-      tma_load_3d(sK, &tm_qkv, kv_full, (Hq + x.g) * HD, x.j * 128, x.b);
-      tma_load_3d(sV, &tm_qkv, kv_full, (Hq + Hkv + x.g) * HD, x.j * 128, x.b);
+      const int ks = n & 1;
+      if (!mbar_wait(kv_empty(ks), ((n >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+      mbar_arrive_expect_tx(kv_full(ks), 2 * C::TILE);
+      tma_load_3d(sK + ks * C::TILE, &tm_qkv, kv_full(ks), (Hq + x.g) * HD, x.j * 128, x.b);
+      tma_load_3d(sV + ks * C::TILE, &tm_qkv, kv_full(ks), (Hq + Hkv + x.g) * HD, x.j * 128, x.b);
       kv_issued = n + 1;
       for (int it = 0; it < x.n_it; ++it) {
         const int bq = issued % C::NQ;
@@ -852,7 +860,8 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     if (!ok) {
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
-      if (kv_issued > 0) mbar_wait(kv_full, (kv_issued - 1) & 1, nullptr);
+      for (int n = kv_issued - 1; n >= 0 && n >= kv_issued - 2; --n)
+        mbar_wait(kv_full(n & 1), (n >> 1) & 1, nullptr);
       for (int it = issued - 1; it >= 0 && it >= issued - C::NQ; --it)
         mbar_wait(qdo_full(it % C::NQ), (it / C::NQ) & 1, nullptr);
     }
@@ -865,30 +874,37 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     const uint64_t dPt = smem_desc_sw128(sPt, 16, 1024), dDSt = smem_desc_sw128(sDSt, 16, 1024);
     const uint64_t dQm = smem_desc_sw128(sQ, 16384, 1024), dDOm = smem_desc_sw128(sDO, 16384, 1024);
     const uint64_t dKm = smem_desc_sw128(sK, 16384, 1024), dDStm = smem_desc_sw128(sDSt, 16384, 1024);
-    // One step: S^T and dP^T of block G + 1, then dV, dK and dQ of block G,
-    // G counting the blocks of all items.
-    auto issue_sp = [&](int G) -> bool {  // once the threads hold block G - 1's
-      const int bq = G % C::NQ;
+    // S^T and dP^T of block G, the first of item n or a later one, G counting
+    // the blocks of all items: once the threads hold block G - 1's
+    auto issue_sp = [&](int G, int n, bool first) -> bool {
+      const int bq = G % C::NQ, ks = n & 1;
+      if (first && !mbar_wait(kv_full(ks), (n >> 1) & 1, abort_flag)) return false;
       if (!mbar_wait(qdo_full(bq), (G / C::NQ) & 1, abort_flag)) return false;
       if (G >= 1 && !mbar_wait(s_free, (G - 1) & 1, abort_flag)) return false;
       tc_fence_after();
-      const uint32_t qo = (uint32_t)bq * (uint32_t)(C::TILE / 16);
+      const uint32_t qo = (uint32_t)bq * (uint32_t)(C::TILE / 16), ko = (uint32_t)ks * (uint32_t)(C::TILE / 16);
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk) {
-        umma_bf16(tmem_base, dK + kk * 2, dQk + qo + kk * 2, ID_SP, kk > 0 ? 1u : 0u);
-        umma_bf16(tmem_base + COL_DP, dV + kk * 2, dDOk + qo + kk * 2, ID_SP, kk > 0 ? 1u : 0u);
+        umma_bf16(tmem_base, dK + ko + kk * 2, dQk + qo + kk * 2, ID_SP, kk > 0 ? 1u : 0u);
+        umma_bf16(tmem_base + COL_DP, dV + ko + kk * 2, dDOk + qo + kk * 2, ID_SP, kk > 0 ? 1u : 0u);
       }
       umma_commit(sp_full);
       return true;
     };
     Item x = item_of(0);
     int G = 0;
+    if (x.n_it > 0) ok = issue_sp(0, 0, true);
     for (int n = 0; ok && x.n_it > 0; ++n) {
-      // the item's first S^T needs its K and V, which arrive once the previous
-      // item's last MMA has read the buffers
-      ok = mbar_wait(kv_full, n & 1, abort_flag) && issue_sp(G);
+      const Item next = item_of(n + 1);
+      const uint32_t ko = (uint32_t)(n & 1) * (uint32_t)(C::TILE / 16);
       for (int it = 0; ok && it < x.n_it; ++it, ++G) {
-        if (it + 1 < x.n_it && !issue_sp(G + 1)) { ok = false; break; }
+        // the next block first: the threads work on it while this one's other
+        // products run
+        const bool last = it + 1 == x.n_it;
+        if (!last ? !issue_sp(G + 1, n, false) : next.n_it > 0 && !issue_sp(G + 1, n + 1, true)) {
+          ok = false;
+          break;
+        }
         const int bq = G % C::NQ, bd = G & 1;
         // P^T and dS^T of this block are in shared memory; its dQ buffer has
         // been read; the accumulators of the previous item have been read
@@ -909,16 +925,13 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
         }
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)  // over the 128 keys
-          umma_bf16(tmem_base + COL_DQ + 64 * bd, dDStm + kk * 128, dKm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
+          umma_bf16(tmem_base + COL_DQ + 64 * bd, dDStm + kk * 128, dKm + ko + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
         umma_commit(dq_full(bd));
         umma_commit(qdo_empty(bq));
         umma_commit(pds_free);
       }
-      if (ok) {
-        umma_commit(kv_empty);
-        umma_commit(acc_done);
-      }
-      x = item_of(n + 1);
+      if (ok) umma_commit(acc_done);
+      x = next;
     }
     if (!ok) {
       record_error(err, kDevAttnTimeout);
@@ -926,7 +939,28 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       umma_commit(drain);
       mbar_wait(drain, 0, nullptr);
     }
-  } else if (warp >= 2) {
+  } else if (warp == 10 && lane == 0) {
+    // ---------------------------------------------------------------- dK and dV store
+    bool ok = true;
+    for (int n = 0;; ++n) {
+      const Item x = item_of(n);
+      if (x.n_it == 0) break;
+      ok = mbar_wait(dkv_full, n & 1, abort_flag);
+      if (!ok) break;
+      const uint32_t at = (uint32_t)(n & 1) * C::TILE;
+      // key rows past the sequence end are outside the map
+      tma_store_3d(&tm_dkv, sK + at, (Hq + x.g) * HD, x.j * 128, x.b);
+      tma_store_3d(&tm_dkv, sV + at, (Hq + Hkv + x.g) * HD, x.j * 128, x.b);
+      bulk_commit_group();
+      bulk_wait_group_read0();
+      mbar_arrive(kv_empty(n & 1));
+    }
+    if (!ok) {
+      record_error(err, kDevAttnTimeout);
+      *abort_flag = 1;
+    }
+    bulk_wait_group0();
+  } else if (warp >= 2 && warp < 10) {
     // ---------------------------------------------------------------- threads
     // Two warps per TMEM lane quarter, each taking half of the block's queries
     // (of S^T and dP^T) and half of the head's columns (of dQ).
@@ -987,13 +1021,77 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       }
       return true;
     };
+    // dK and dV of item n, once all its products are done: into its own K and V
+    // buffers (no MMA reads them any more), in the tensor map's swizzled
+    // layout, for the store warp.
+    auto finish = [&](const Item& x, int n) -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait(acc_done, n & 1, abort_flag))) return false;
+      tc_fence_after();
+      const int key = x.j * 128 + r;
+      auto put = [&](uint32_t tile, int chunk, uint32_t a, uint32_t b_, uint32_t c_, uint32_t d_) {
+        const uint32_t addr = tile + (uint32_t)(n & 1) * C::TILE + (uint32_t)r * 128u +
+                              (uint32_t)((chunk ^ (r & 7)) * 16);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b_),
+                     "r"(c_), "r"(d_)
+                     : "memory");
+      };
+      // dK: pairs (d, d + HD/2) get the inverse rotation of the key's position;
+      // this warp takes d in [16 half, 16 half + 16) and their partners
+      {
+        uint32_t x1[16], x2[16];
+        tmem_ld_32x32b_x16(lane_base + COL_DK + 16 * half, x1);
+        tmem_ld_32x32b_x16(lane_base + COL_DK + HD / 2 + 16 * half, x2);
+        tmem_ld_wait();
+        const int kp = key < S ? key : S - 1;  // rows past the end are computed, not stored
+        uint32_t o1[8], o2[8];
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          float a1 = __uint_as_float(x1[e]) * scale, b1 = __uint_as_float(x1[e + 1]) * scale;
+          float a2 = __uint_as_float(x2[e]) * scale, b2 = __uint_as_float(x2[e + 1]) * scale;
+          if (cs) {
+            const float2 ca = cs[(int64_t)kp * (HD / 2) + 16 * half + e];
+            const float2 cb = cs[(int64_t)kp * (HD / 2) + 16 * half + e + 1];
+            const float y1a = a1 * ca.x + a2 * ca.y, y2a = a2 * ca.x - a1 * ca.y;
+            const float y1b = b1 * cb.x + b2 * cb.y, y2b = b2 * cb.x - b1 * cb.y;
+            a1 = y1a; a2 = y2a; b1 = y1b; b2 = y2b;
+          }
+          o1[e / 2] = pack2_bf16(a1, b1);
+          o2[e / 2] = pack2_bf16(a2, b2);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          put(sK, 2 * half + k, o1[4 * k], o1[4 * k + 1], o1[4 * k + 2], o1[4 * k + 3]);
+          put(sK, 4 + 2 * half + k, o2[4 * k], o2[4 * k + 1], o2[4 * k + 2], o2[4 * k + 3]);
+        }
+      }
+      {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(lane_base + COL_DV + 32 * half, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          put(sV, 4 * half + k, pack2_bf16(__uint_as_float(v[8 * k + 0]), __uint_as_float(v[8 * k + 1])),
+              pack2_bf16(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
+              pack2_bf16(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
+              pack2_bf16(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
+      }
+      tc_fence_before();
+      mbar_arrive(acc_free);  // the next item's dV and dK may be formed
+      fence_proxy_async_smem();
+      // the store warp has taken the item before: its barrier cannot run ahead
+      if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(kv_empty((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag)))
+        return false;
+      mbar_arrive(dkv_full);
+      return true;
+    };
     wait_primary();  // D, and the zeros in dq_acc
     float next_l, next_d;
     const uint32_t rowoff = (uint32_t)r * 128u + (uint32_t)half * 16384u;
-    Item x = item_of(0);
+    Item x = item_of(0), prev = x;
     fetch(x, 0, next_l, next_d);
     int G = 0;
-    for (int n = 0; ok && x.n_it > 0; ++n) {
+    int n = 0;
+    for (; ok && x.n_it > 0; ++n) {
       const Item next = item_of(n + 1);
       const int key = x.j * 128 + r;
       // the last query that sees this thread's key (before the key: no one does)
@@ -1072,16 +1170,6 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(pds_free, (G - 1) & 1, abort_flag));
           if (!ok) break;
         }
-        // dK and dV of the previous item, staged in the same buffers, have been
-        // read by their TMA stores
-        if (it == 0 && n > 0) {
-          if (threadIdx.x == 64) {
-            bulk_wait_group_read0();
-            mbar_arrive(dkv_free);
-          }
-          ok = __all_sync(0xffffffffu, mbar_wait(dkv_free, (n - 1) & 1, abort_flag));
-          if (!ok) break;
-        }
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -1097,75 +1185,19 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(ps_full);
-        // dQ of the item's previous block, while the tensor core works on this one's
-        if (it >= 1 && !emit_dq(x, it - 1, G - 1)) { ok = false; break; }
+        // while the tensor core works on this block's products: dQ of the one
+        // before, and, at an item's first block, the previous item's dK and dV
+        if (it > 0) {
+          ok = emit_dq(x, it - 1, G - 1);
+        } else if (n > 0) {
+          ok = emit_dq(prev, prev.n_it - 1, G - 1) && finish(prev, n - 1);
+        }
+        if (!ok) break;
       }
-      if (ok) ok = emit_dq(x, x.n_it - 1, G - 1);
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, n & 1, abort_flag));
-      if (ok) {
-        tc_fence_after();
-        // dK and dV rows go into the P^T and dS^T buffers (every MMA that read
-        // them has completed), in the tensor map's swizzled layout; one thread
-        // then stores both tiles with the TMA unit.
-        auto put = [&](uint32_t tile, int chunk, uint32_t a, uint32_t b_, uint32_t c_, uint32_t d_) {
-          const uint32_t addr = tile + (uint32_t)r * 128u + (uint32_t)((chunk ^ (r & 7)) * 16);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b_),
-                       "r"(c_), "r"(d_)
-                       : "memory");
-        };
-        // dK: pairs (d, d + HD/2) get the inverse rotation of the key's position;
-        // this warp takes d in [16 half, 16 half + 16) and their partners
-        {
-          uint32_t x1[16], x2[16];
-          tmem_ld_32x32b_x16(lane_base + COL_DK + 16 * half, x1);
-          tmem_ld_32x32b_x16(lane_base + COL_DK + HD / 2 + 16 * half, x2);
-          tmem_ld_wait();
-          const int kp = key < S ? key : S - 1;  // rows past the end are computed, not stored
-          uint32_t o1[8], o2[8];
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float a1 = __uint_as_float(x1[e]) * scale, b1 = __uint_as_float(x1[e + 1]) * scale;
-            float a2 = __uint_as_float(x2[e]) * scale, b2 = __uint_as_float(x2[e + 1]) * scale;
-            if (cs) {
-              const float2 ca = cs[(int64_t)kp * (HD / 2) + 16 * half + e];
-              const float2 cb = cs[(int64_t)kp * (HD / 2) + 16 * half + e + 1];
-              const float y1a = a1 * ca.x + a2 * ca.y, y2a = a2 * ca.x - a1 * ca.y;
-              const float y1b = b1 * cb.x + b2 * cb.y, y2b = b2 * cb.x - b1 * cb.y;
-              a1 = y1a; a2 = y2a; b1 = y1b; b2 = y2b;
-            }
-            o1[e / 2] = pack2_bf16(a1, b1);
-            o2[e / 2] = pack2_bf16(a2, b2);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            put(sPt, 2 * half + k, o1[4 * k], o1[4 * k + 1], o1[4 * k + 2], o1[4 * k + 3]);
-            put(sPt, 4 + 2 * half + k, o2[4 * k], o2[4 * k + 1], o2[4 * k + 2], o2[4 * k + 3]);
-          }
-        }
-        {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(lane_base + COL_DV + 32 * half, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            put(sDSt, 4 * half + k, pack2_bf16(__uint_as_float(v[8 * k + 0]), __uint_as_float(v[8 * k + 1])),
-                pack2_bf16(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
-                pack2_bf16(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
-                pack2_bf16(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
-        }
-        tc_fence_before();
-        mbar_arrive(acc_free);  // the next item's dV and dK may be formed
-        fence_proxy_async_smem();
-        mbar_arrive(dkv_full);
-        if (warp == 2) ok = __all_sync(0xffffffffu, mbar_wait(dkv_full, n & 1, abort_flag));
-        if (ok && threadIdx.x == 64) {  // key rows past the sequence end are outside the map
-          tma_store_3d(&tm_dkv, sPt, (Hq + x.g) * HD, x.j * 128, x.b);
-          tma_store_3d(&tm_dkv, sDSt, (Hq + Hkv + x.g) * HD, x.j * 128, x.b);
-          bulk_commit_group();
-        }
-      }
+      prev = x;
       x = next;
     }
+    if (ok && n > 0) ok = emit_dq(prev, prev.n_it - 1, G - 1) && finish(prev, n - 1);
     if (!ok && lane == 0) {
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
