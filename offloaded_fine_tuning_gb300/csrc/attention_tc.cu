@@ -693,44 +693,47 @@ __device__ __forceinline__ int dq_slot(const AttWindow& win, int j) {
 // (head, block):
 //   MMA:     S^T = K Q^T -> TMEM[0,128),  dP^T = V dO^T -> TMEM[128,256)
 //   threads: one per key row and half of the queries: P^T = exp2(S^T*scale*
-//            log2e - lse*log2e) (masked), dS^T = P^T * (dP^T - D), both to
-//            shared memory (bf16, swizzled)
-//   MMA:     dV += P^T dO, dK += dS^T Q (TMEM[384,512), kept over the walk);
-//            dQ = dS K -> TMEM, two buffers [256,384)
+//            log2e - lse*log2e) (masked) -> TMEM[320,384) as bf16, dS^T = P^T *
+//            (dP^T - D) to shared memory (bf16, swizzled)
+//   MMA:     dV += P^T dO (P^T as the tensor-memory A), dK += dS^T Q
+//            (TMEM[384,512), kept over the walk); dQ = dS K -> TMEM[256,320)
 //   threads: one per query row and half of the columns: dQ through shared
 //            memory into the fp32 dq_acc by TMA reduce-add (or, deterministic,
 //            a TMA store into the key block's own slot)
 // dS^T is stored once and read both as the K-major A of dK and as the MN-major
 // A (dS) of dQ.  The threads release the S^T and dP^T columns once they hold
 // them in registers, so the next block's are formed while they work, and dV,
-// dK and dQ run behind.  One thread issues every MMA at 55 to 77 cycles each,
-// which bounds a block (32 MMAs, 24 of them 64 wide, 32 cycles of work): hence
-// blocks of 128 queries.  With 64-query blocks and two CTAs sharing an SM the
-// 24 MMAs per 64 queries ran 121 us against the unpipelined 128-query kernel's
-// 155 (8 x 1001 tokens, 16 heads, window 250) but 650 against 570 us where
-// walks are long (2 x 4096, 16 heads in groups of 4).  With a CTA per item a
-// short window's items (four blocks) spent more time on setting up, the first
-// loads and the last stores than on their blocks.  So the barriers' phases
-// count on over all items, K and V have two stages, and the first block of the
-// next item is formed (S^T, P^T) before the previous item's dK and dV are
-// read; those leave through that item's own K and V buffers.
+// dK and dQ run behind.
+//
+// What bounds it, from clock stamps of the roles: one thread issues every MMA
+// at 55 to 77 cycles each (32 a block, 24 of them 64 wide, 32 cycles of work:
+// 2,450 cycles a block), and the threads' 16,384 exponentials take at least
+// 1,024.  Hence blocks of 128 queries: 64-query blocks in two CTAs per SM (24
+// MMAs per 64 queries) lost where walks are long.  With two Q / dO stages the
+// loads of a block started only when the block two before it was done, 1,300
+// cycles of waiting a block; P^T in TMEM makes room for three.  lse and D come
+// from a warp of their own, two blocks ahead.  A CTA per item spent more time
+// on setting up, the first loads and the last stores than on a short window's
+// four blocks, so the barriers' phases count on over all items, K and V have
+// two stages, and the first block of the next item is formed (S^T, P^T) before
+// the previous item's dK and dV are read; those leave through that item's own
+// K and V buffers.
 namespace {
-// TMA warp, MMA warp, 8 softmax-gradient warps, dK / dV store warp
-constexpr int kAttBwdThreads = 352;
+// TMA warp, MMA warp, 8 softmax-gradient warps, dK / dV store warp, lse / D warp
+constexpr int kAttBwdThreads = 384;
 struct AttBwdCfg {
   static constexpr int HD = 64;
   static constexpr int TILE = 16384;  // 128 rows x 64 hd
-  static constexpr int NQ = 2;        // Q / dO stages
+  static constexpr int NQ = 3;        // Q / dO stages
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = 2 * TILE;
   static constexpr int OFF_Q = 4 * TILE;  // K and V: two stages each
   static constexpr int OFF_DO = OFF_Q + NQ * TILE;
-  static constexpr int OFF_PT = OFF_DO + NQ * TILE;  // 128 keys x 128 queries, two boxes of 64
-  static constexpr int OFF_DST = OFF_PT + 32768;
+  static constexpr int OFF_DST = OFF_DO + NQ * TILE;  // 128 keys x 128 queries, two boxes of 64
   static constexpr int OFF_DQS = OFF_DST + 32768;    // dQ staging: 8 warps x [32 q][32 d] fp32
   static constexpr int OFF_LD = OFF_DQS + 8 * 4096;  // [2][lse 128 | D 128]
   static constexpr int OFF_BAR = OFF_LD + 2 * 256 * 4;
-  static constexpr int NBAR = 23;
+  static constexpr int NBAR = 26;
   // no room to align the base: it is 1024-byte aligned where a kernel has no
   // static shared memory, which the kernel checks
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
@@ -752,7 +755,8 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
   constexpr uint32_t ID_KV = umma_idesc_bf16(128, HD, false, true);    // dV, dK
   constexpr uint32_t ID_Q = umma_idesc_bf16(128, HD, true, true);      // dQ
   constexpr uint32_t TMEM_COLS = 512;
-  constexpr uint32_t COL_DP = 128, COL_DQ = 256, COL_DV = 384, COL_DK = 448;
+  constexpr uint32_t COL_DP = 128, COL_DQ = 256, COL_P = 320, COL_DV = 384,
+                     COL_DK = 448;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
@@ -762,20 +766,19 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     return;
   }
   const uint32_t sK = s0 + C::OFF_K, sV = s0 + C::OFF_V, sQ = s0 + C::OFF_Q, sDO = s0 + C::OFF_DO;
-  const uint32_t sPt = s0 + C::OFF_PT, sDSt = s0 + C::OFF_DST, sDQS = s0 + C::OFF_DQS;
+  const uint32_t sDSt = s0 + C::OFF_DST, sDQS = s0 + C::OFF_DQS;
   float* sLD = reinterpret_cast<float*>(smem + C::OFF_LD);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   const uint32_t b0 = smem_u32(bars);
-  const uint32_t sp_full = b0 + 8, s_free = b0 + 16, ps_full = b0 + 24,
-                 pds_free = b0 + 32, acc_done = b0 + 40, drain = b0 + 48;
-  auto qdo_full = [&](int i) { return b0 + 56u + 8u * i; };
-  auto qdo_empty = [&](int i) { return b0 + 72u + 8u * i; };
-  auto dq_full = [&](int i) { return b0 + 88u + 8u * i; };
-  auto dq_free = [&](int i) { return b0 + 104u + 8u * i; };
-  auto ld_full = [&](int i) { return b0 + 120u + 8u * i; };
-  const uint32_t acc_free = b0 + 136, dkv_full = b0 + 144;
-  auto kv_full = [&](int i) { return b0 + 152u + 8u * i; };
-  auto kv_empty = [&](int i) { return b0 + 168u + 8u * i; };
+  const uint32_t sp_full = b0, s_free = b0 + 8, ps_full = b0 + 16, pds_free = b0 + 24,
+                 acc_done = b0 + 32, drain = b0 + 40, acc_free = b0 + 48, dkv_full = b0 + 56,
+                 dq_full = b0 + 64, dq_free = b0 + 72;
+  auto kv_full = [&](int i) { return b0 + 80u + 8u * i; };
+  auto kv_empty = [&](int i) { return b0 + 96u + 8u * i; };
+  auto ld_full = [&](int i) { return b0 + 112u + 8u * i; };
+  auto ld_empty = [&](int i) { return b0 + 128u + 8u * i; };
+  auto qdo_full = [&](int i) { return b0 + 144u + 8u * i; };
+  auto qdo_empty = [&](int i) { return b0 + 168u + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -799,6 +802,22 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     return x;
   };
 
+  // Blocks in the order of the walk: a head's query blocks, then the next
+  // head's, then the next item's (counted on, without a division per block).
+  struct Walk { Item x; int n, left, h, qb; };  // blocks left in the item, this one included
+  auto start = [&](int n) -> Walk {
+    const Item x = item_of(n);
+    return {x, n, x.n_it, x.g * grp, x.j};
+  };
+  auto advance = [&](Walk& w) {
+    if (--w.left == 0) {
+      w = start(w.n + 1);
+    } else if (++w.qb == w.x.j + w.x.per_head) {
+      w.qb = w.x.j;
+      ++w.h;
+    }
+  };
+
   if (threadIdx.x == 0) {
     mbar_init(sp_full, 1);
     mbar_init(s_free, 256);
@@ -808,14 +827,17 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     mbar_init(drain, 1);
     mbar_init(acc_free, 256);
     mbar_init(dkv_full, 256);
+    mbar_init(dq_full, 1);
+    mbar_init(dq_free, 256);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(qdo_full(i), 1);
-      mbar_init(qdo_empty(i), 1);
       mbar_init(kv_full(i), 1);
       mbar_init(kv_empty(i), 1);
-      mbar_init(dq_full(i), 1);
-      mbar_init(dq_free(i), 256);
-      mbar_init(ld_full(i), 128);
+      mbar_init(ld_full(i), 32);
+      mbar_init(ld_empty(i), 256);
+    }
+    for (int i = 0; i < C::NQ; ++i) {
+      mbar_init(qdo_full(i), 1);
+      mbar_init(qdo_empty(i), 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -871,7 +893,7 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     // base descriptors; an operand at byte offset o is the base plus o / 16
     const uint64_t dK = smem_desc_sw128(sK, 16, 1024), dV = smem_desc_sw128(sV, 16, 1024);
     const uint64_t dQk = smem_desc_sw128(sQ, 16, 1024), dDOk = smem_desc_sw128(sDO, 16, 1024);
-    const uint64_t dPt = smem_desc_sw128(sPt, 16, 1024), dDSt = smem_desc_sw128(sDSt, 16, 1024);
+    const uint64_t dDSt = smem_desc_sw128(sDSt, 16, 1024);
     const uint64_t dQm = smem_desc_sw128(sQ, 16384, 1024), dDOm = smem_desc_sw128(sDO, 16384, 1024);
     const uint64_t dKm = smem_desc_sw128(sK, 16384, 1024), dDStm = smem_desc_sw128(sDSt, 16384, 1024);
     // S^T and dP^T of block G, the first of item n or a later one, G counting
@@ -905,11 +927,10 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
           ok = false;
           break;
         }
-        const int bq = G % C::NQ, bd = G & 1;
-        // P^T and dS^T of this block are in shared memory; its dQ buffer has
-        // been read; the accumulators of the previous item have been read
+        const int bq = G % C::NQ;
+        // P^T and dS^T of this block are there, and the accumulators of the
+        // previous item have been read
         if (!mbar_wait(ps_full, G & 1, abort_flag) ||
-            (G >= 2 && !mbar_wait(dq_free(bd), ((G >> 1) - 1) & 1, abort_flag)) ||
             (it == 0 && n > 0 && !mbar_wait(acc_free, (n - 1) & 1, abort_flag))) {
           ok = false;
           break;
@@ -920,14 +941,20 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
         for (int kk = 0; kk < 8; ++kk) {  // over the 128 queries
           const uint32_t acc = (it > 0 || kk > 0) ? 1u : 0u;
           const uint32_t ao = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;
-          umma_bf16(tmem_base + COL_DV, dPt + ao, dDOm + qo + kk * 128, ID_KV, acc);
+          umma_bf16_ts(tmem_base + COL_DV, tmem_base + COL_P + kk * 8, dDOm + qo + kk * 128, ID_KV, acc);
           umma_bf16(tmem_base + COL_DK, dDSt + ao, dQm + qo + kk * 128, ID_KV, acc);
         }
+        umma_commit(qdo_empty(bq));
+        // dQ of the previous block has been read
+        if (G >= 1 && !mbar_wait(dq_free, (G - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)  // over the 128 keys
-          umma_bf16(tmem_base + COL_DQ + 64 * bd, dDStm + kk * 128, dKm + ko + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
-        umma_commit(dq_full(bd));
-        umma_commit(qdo_empty(bq));
+          umma_bf16(tmem_base + COL_DQ, dDStm + kk * 128, dKm + ko + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
+        umma_commit(dq_full);
         umma_commit(pds_free);
       }
       if (ok) umma_commit(acc_done);
@@ -960,6 +987,36 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       *abort_flag = 1;
     }
     bulk_wait_group0();
+  } else if (warp == 11) {
+    // ---------------------------------------------------------------- lse and D
+    // 128 of each (lse in log2 units; zeros behind the sequence's end) into one
+    // of two buffers, as soon as the block two before has been computed
+    wait_primary();  // D
+    bool ok = true;
+    Walk w = start(0);
+    for (int G = 0; w.left > 0; ++G, advance(w)) {
+      const int64_t row = ((int64_t)w.x.b * Hq + w.h) * S;
+      float lv[4], dv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int q = w.qb * 128 + 32 * i + lane;
+        lv[i] = q < S ? lse[row + q] * 1.4426950408889634f : 0.f;
+        dv[i] = q < S ? delta[row + q] : 0.f;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(ld_empty(G & 1), ((G >> 1) & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      float* bL = sLD + (G & 1) * 256 + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bL[32 * i] = lv[i];
+        bL[128 + 32 * i] = dv[i];
+      }
+      mbar_arrive(ld_full(G & 1));
+    }
+    if (!ok && lane == 0) {
+      record_error(err, kDevAttnTimeout);
+      *abort_flag = 1;
+    }
   } else if (warp >= 2 && warp < 10) {
     // ---------------------------------------------------------------- threads
     // Two warps per TMEM lane quarter, each taking half of the block's queries
@@ -967,36 +1024,20 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const int r = quarter * 32 + lane;  // key row of S^T / dP^T; query row of dQ
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    const int tid = threadIdx.x - 64;  // 0..255
     bool ok = true;
-    // lse (log2 units) and D of a query block, one value per thread of the
-    // first 128, loaded one block ahead
-    auto fetch = [&](const Item& x, int it_, float& lv, float& dv) {
-      lv = 0.f;
-      dv = 0.f;
-      if (it_ >= x.n_it || tid >= 128) return;
-      const int h_ = x.g * grp + it_ / x.per_head;
-      const int q_ = (x.j + it_ % x.per_head) * 128 + tid;
-      if (q_ < S) {
-        const int64_t o = ((int64_t)x.b * Hq + h_) * S + q_;
-        lv = lse[o];
-        dv = delta[o];
-      }
-    };
-    // dQ of an item's block it_, the G-th of all (this warp's 32 queries and 32 columns) into the warp's
+    // dQ of a block, the G-th of all (this warp's 32 queries and 32 columns) into the warp's
     // staging tile, in the tensor map's 128-byte swizzle, then one TMA
     // reduce-add (or store).  The tile is rewritten only after the previous
     // one has finished reading it.
     const uint32_t stage = sDQS + (uint32_t)(warp - 2) * 4096u;
-    auto emit_dq = [&](const Item& x, int it_, int G) -> bool {
-      const int bd = G & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(dq_full(bd), (G >> 1) & 1, abort_flag))) return false;
+    auto emit_dq = [&](const Walk& w, int G) -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait(dq_full, G & 1, abort_flag))) return false;
       tc_fence_after();
       uint32_t v[32];
-      tmem_ld_32x32b_x32(lane_base + COL_DQ + 64 * bd + 32 * half, v);
+      tmem_ld_32x32b_x32(lane_base + COL_DQ + 32 * half, v);
       tmem_ld_wait();
       tc_fence_before();
-      mbar_arrive(dq_free(bd));
+      mbar_arrive(dq_free);
       if (lane == 0) bulk_wait_group_read0();
       __syncwarp();
 #pragma unroll
@@ -1008,14 +1049,13 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        const int h_ = x.g * grp + it_ / x.per_head;
-        const int qb_ = (x.j + it_ % x.per_head) * 128 + 32 * quarter;
+        const int qb_ = w.qb * 128 + 32 * quarter;
         if (qb_ < S) {  // rows past the sequence end are outside the map
           if (DET)  // this key block's own slot of the dQ buffer
-            tma_store_3d(&tm_dq, stage, h_ * HD + 32 * half, qb_,
-                         (WIN ? dq_slot(win, x.j) : x.j) * B + x.b);
+            tma_store_3d(&tm_dq, stage, w.h * HD + 32 * half, qb_,
+                         (WIN ? dq_slot(win, w.x.j) : w.x.j) * B + w.x.b);
           else
-            tma_reduce_add_3d(&tm_dq, stage, h_ * HD + 32 * half, qb_, x.b);
+            tma_reduce_add_3d(&tm_dq, stage, w.h * HD + 32 * half, qb_, w.x.b);
         }
         bulk_commit_group();
       }
@@ -1084,120 +1124,109 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       mbar_arrive(dkv_full);
       return true;
     };
-    wait_primary();  // D, and the zeros in dq_acc
-    float next_l, next_d;
+    wait_primary();  // the zeros in dq_acc
     const uint32_t rowoff = (uint32_t)r * 128u + (uint32_t)half * 16384u;
-    Item x = item_of(0), prev = x;
-    fetch(x, 0, next_l, next_d);
+    Walk cur = start(0), prev = cur, next = cur;
+    advance(next);
     int G = 0;
-    int n = 0;
-    for (; ok && x.n_it > 0; ++n) {
-      const Item next = item_of(n + 1);
-      const int key = x.j * 128 + r;
+    for (; ok && cur.left > 0; ++G) {
+      const int key = cur.x.j * 128 + r;
       // the last query that sees this thread's key (before the key: no one does)
       const int q_end = !WIN || key < win.sinks || key > S - win.size ? S - 1 : key + win.size - 1;
-      for (int it = 0; it < x.n_it; ++it, ++G) {
-        const int qc = (x.j + it % x.per_head) * 128 + 64 * half;  // first query of this thread's columns
-        float* bL = sLD + (G & 1) * 256;
-        float* bD = bL + 128;
-        // The buffer written here was last read for block G - 2; this thread
-        // has since waited for that block's P^T / dS^T to be consumed, which
-        // needed every thread to have finished computing it.
-        if (tid < 128) {
-          bL[tid] = next_l * 1.4426950408889634f;
-          bD[tid] = next_d;
-          mbar_arrive(ld_full(G & 1));
-        }
-        if (it + 1 < x.n_it) fetch(x, it + 1, next_l, next_d);
-        else fetch(next, 0, next_l, next_d);
-        ok = __all_sync(0xffffffffu, mbar_wait(ld_full(G & 1), (G >> 1) & 1, abort_flag));
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sp_full, G & 1, abort_flag));
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t sr[2][32], dr[2][32];
+      const int qc = cur.qb * 128 + 64 * half;  // first query of this thread's columns
+      float* bL = sLD + (G & 1) * 256;
+      float* bD = bL + 128;
+      ok = __all_sync(0xffffffffu, mbar_wait(ld_full(G & 1), (G >> 1) & 1, abort_flag));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sp_full, G & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sr[2][32], dr[2][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          tmem_ld_32x32b_x32(lane_base + 64 * half + 32 * c, sr[c]);
-          tmem_ld_32x32b_x32(lane_base + COL_DP + 64 * half + 32 * c, dr[c]);
-        }
-        tmem_ld_wait();
-        tc_fence_before();
-        mbar_arrive(s_free);  // S^T / dP^T are in registers: the next block may overwrite them
-        // P^T over S^T's registers, dS^T over dP^T's, packed
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld_32x32b_x32(lane_base + 64 * half + 32 * c, sr[c]);
+        tmem_ld_32x32b_x32(lane_base + COL_DP + 64 * half + 32 * c, dr[c]);
+      }
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(s_free);  // S^T / dP^T are in registers: the next block may overwrite them
+      // P^T over S^T's registers, dS^T over dP^T's, packed
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int q1 = qc + 32 * c;
-          const uint32_t seen = low_bits(q_end - q1 + 1) & ~low_bits(key - q1);
-          const float4* L4 = reinterpret_cast<const float4*>(bL + 64 * half + 32 * c);
-          const float4* D4 = reinterpret_cast<const float4*>(bD + 64 * half + 32 * c);
-          auto grad_tile = [&](auto mask_tag) {
-            constexpr bool kMask = decltype(mask_tag)::value;
+      for (int c = 0; c < 2; ++c) {
+        const int q1 = qc + 32 * c;
+        const uint32_t seen = low_bits(q_end - q1 + 1) & ~low_bits(key - q1);
+        const float4* L4 = reinterpret_cast<const float4*>(bL + 64 * half + 32 * c);
+        const float4* D4 = reinterpret_cast<const float4*>(bD + 64 * half + 32 * c);
+        auto grad_tile = [&](auto mask_tag) {
+          constexpr bool kMask = decltype(mask_tag)::value;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 l4 = L4[k], d4 = D4[k];
-              const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
-              const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
-              float pv[4], sv[4];
+          for (int k = 0; k < 8; ++k) {
+            const float4 l4 = L4[k], d4 = D4[k];
+            const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+            const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
+            float pv[4], sv[4];
 #pragma unroll
-              for (int i = 0; i < 4; i += 2) {
-                const int e = 4 * k + i;
-                float x0 = __uint_as_float(sr[c][e]), x1 = __uint_as_float(sr[c][e + 1]);
-                fma2(x0, x1, scale_log2, -lv[i], -lv[i + 1]);
-                x0 = ex2_approx(x0);
-                x1 = ex2_approx(x1);
-                if (kMask && !(seen & (1u << e))) x0 = 0.f;
-                if (kMask && !(seen & (2u << e))) x1 = 0.f;
-                float d0 = __uint_as_float(dr[c][e]), d1 = __uint_as_float(dr[c][e + 1]);
-                add2(d0, d1, -dv[i], -dv[i + 1]);
-                mul2(d0, d1, x0, x1);
-                pv[i] = x0;
-                pv[i + 1] = x1;
-                sv[i] = d0;
-                sv[i + 1] = d1;
-              }
-              sr[c][2 * k] = pack2_bf16(pv[0], pv[1]);
-              sr[c][2 * k + 1] = pack2_bf16(pv[2], pv[3]);
-              dr[c][2 * k] = pack2_bf16(sv[0], sv[1]);
-              dr[c][2 * k + 1] = pack2_bf16(sv[2], sv[3]);
+            for (int i = 0; i < 4; i += 2) {
+              const int e = 4 * k + i;
+              float x0 = __uint_as_float(sr[c][e]), x1 = __uint_as_float(sr[c][e + 1]);
+              fma2(x0, x1, scale_log2, -lv[i], -lv[i + 1]);
+              x0 = ex2_approx(x0);
+              x1 = ex2_approx(x1);
+              if (kMask && !(seen & (1u << e))) x0 = 0.f;
+              if (kMask && !(seen & (2u << e))) x1 = 0.f;
+              float d0 = __uint_as_float(dr[c][e]), d1 = __uint_as_float(dr[c][e + 1]);
+              add2(d0, d1, -dv[i], -dv[i + 1]);
+              mul2(d0, d1, x0, x1);
+              pv[i] = x0;
+              pv[i + 1] = x1;
+              sv[i] = d0;
+              sv[i + 1] = d1;
             }
-          };
-          if (__all_sync(0xffffffffu, seen == 0xffffffffu))
-            grad_tile(std::false_type{});
-          else
-            grad_tile(std::true_type{});
-        }
-        if (G >= 1) {  // P^T, dS^T of the previous block consumed
-          ok = __all_sync(0xffffffffu, mbar_wait(pds_free, (G - 1) & 1, abort_flag));
-          if (!ok) break;
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t off = rowoff + (uint32_t)(((4 * c + k) ^ (r & 7)) * 16);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPt + off), "r"(sr[c][4 * k]),
-                         "r"(sr[c][4 * k + 1]), "r"(sr[c][4 * k + 2]), "r"(sr[c][4 * k + 3])
-                         : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sDSt + off), "r"(dr[c][4 * k]),
-                         "r"(dr[c][4 * k + 1]), "r"(dr[c][4 * k + 2]), "r"(dr[c][4 * k + 3])
-                         : "memory");
+            sr[c][2 * k] = pack2_bf16(pv[0], pv[1]);
+            sr[c][2 * k + 1] = pack2_bf16(pv[2], pv[3]);
+            dr[c][2 * k] = pack2_bf16(sv[0], sv[1]);
+            dr[c][2 * k + 1] = pack2_bf16(sv[2], sv[3]);
           }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        mbar_arrive(ps_full);
-        // while the tensor core works on this block's products: dQ of the one
-        // before, and, at an item's first block, the previous item's dK and dV
-        if (it > 0) {
-          ok = emit_dq(x, it - 1, G - 1);
-        } else if (n > 0) {
-          ok = emit_dq(prev, prev.n_it - 1, G - 1) && finish(prev, n - 1);
-        }
+        };
+        if (__all_sync(0xffffffffu, seen == 0xffffffffu))
+          grad_tile(std::false_type{});
+        else
+          grad_tile(std::true_type{});
+      }
+      mbar_arrive(ld_empty(G & 1));
+      if (G >= 1) {  // P^T, dS^T of the previous block consumed
+        ok = __all_sync(0xffffffffu, mbar_wait(pds_free, (G - 1) & 1, abort_flag));
         if (!ok) break;
       }
-      prev = x;
-      x = next;
+      {
+        uint32_t pk[32];  // P^T of the thread's 64 queries
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          pk[i] = sr[0][i];
+          pk[16 + i] = sr[1][i];
+        }
+        tmem_st_32x32b_x32(lane_base + COL_P + 32 * half, pk);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t off = rowoff + (uint32_t)(((4 * c + k) ^ (r & 7)) * 16);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sDSt + off), "r"(dr[c][4 * k]),
+                       "r"(dr[c][4 * k + 1]), "r"(dr[c][4 * k + 2]), "r"(dr[c][4 * k + 3])
+                       : "memory");
+        }
+      tmem_st_wait();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(ps_full);
+      // while the tensor core works on this block's products: dQ of the one
+      // before, and, at an item's first block, the previous item's dK and dV
+      if (G > 0) ok = emit_dq(prev, G - 1) && (prev.n == cur.n || finish(prev.x, prev.n));
+      prev = cur;
+      cur = next;
+      if (next.left > 0) advance(next);
     }
-    if (ok && n > 0) ok = emit_dq(prev, prev.n_it - 1, G - 1) && finish(prev, n - 1);
+    if (ok && G > 0) ok = emit_dq(prev, G - 1) && finish(prev.x, prev.n);
     if (!ok && lane == 0) {
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
