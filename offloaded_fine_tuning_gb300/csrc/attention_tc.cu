@@ -739,6 +739,23 @@ struct AttBwdCfg {
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
 };
 static_assert(AttBwdCfg::SMEM <= 232448, "backward shared memory");
+
+// Division of 0 <= t < 2^31 by a fixed d: one high product and a correction (m
+// = floor(2^32 / d), 2^32 - 1 for d = 1, so the estimate is the quotient or one
+// less).  The roles decode items with single threads on their critical path.
+struct FixedDiv {
+  uint32_t d, m;
+  FixedDiv(int d_) : d((uint32_t)d_), m(d_ == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / (uint32_t)d_)) {}
+  __device__ __forceinline__ int operator()(int t, int& rem) const {
+    uint32_t q = __umulhi((uint32_t)t, m), r = (uint32_t)t - q * d;
+    if (r >= d) {
+      ++q;
+      r -= d;
+    }
+    rem = (int)r;
+    return (int)q;
+  }
+};
 }  // namespace
 
 template <bool DET, bool WIN>
@@ -748,7 +765,8 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
                        const __grid_constant__ CUtensorMap tm_dq,
                        const __grid_constant__ CUtensorMap tm_dkv, const float* __restrict__ lse,
                        const float* __restrict__ delta, const float2* __restrict__ cs, int S,
-                       int Hq, int Hkv, int B, float scale, float scale_log2, AttWindow win, int* err) {
+                       int Hq, int Hkv, int B, FixedDiv per_block, FixedDiv per_batch, float scale,
+                       float scale_log2, AttWindow win, int* err) {
   using C = AttBwdCfg;
   constexpr int HD = C::HD;
   constexpr uint32_t ID_SP = umma_idesc_bf16(128, 128, false, false);  // S^T, dP^T
@@ -792,10 +810,9 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     const int t = n * (int)gridDim.x + c;
     if (t >= num_items) return {0, 0, 0, 1, 0};
     Item x;
-    x.j = t / (Hkv * B);
-    const int rem = t - x.j * (Hkv * B);
-    x.g = rem % Hkv;
-    x.b = rem / Hkv;
+    int rem;
+    x.j = per_block(t, rem);  // by Hkv * B
+    x.b = per_batch(rem, x.g);  // by Hkv
     // query blocks j .. j + per_head - 1 can see these keys
     x.per_head = (WIN ? last_query(win, x.j * 128, S) / 128 + 1 : nkb) - x.j;
     x.n_it = grp * x.per_head;  // (head, query block) pairs
@@ -913,11 +930,10 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       umma_commit(sp_full);
       return true;
     };
-    Item x = item_of(0);
+    Item x = item_of(0), next = item_of(1);
     int G = 0;
     if (x.n_it > 0) ok = issue_sp(0, 0, true);
     for (int n = 0; ok && x.n_it > 0; ++n) {
-      const Item next = item_of(n + 1);
       const uint32_t ko = (uint32_t)(n & 1) * (uint32_t)(C::TILE / 16);
       for (int it = 0; ok && it < x.n_it; ++it, ++G) {
         // the next block first: the threads work on it while this one's other
@@ -959,6 +975,7 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       }
       if (ok) umma_commit(acc_done);
       x = next;
+      next = item_of(n + 2);
     }
     if (!ok) {
       record_error(err, kDevAttnTimeout);
@@ -1030,7 +1047,8 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     // reduce-add (or store).  The tile is rewritten only after the previous
     // one has finished reading it.
     const uint32_t stage = sDQS + (uint32_t)(warp - 2) * 4096u;
-    auto emit_dq = [&](const Walk& w, int G) -> bool {
+    struct Done { int h, qb, b, j, n; };  // a block whose dQ is still to be stored
+    auto emit_dq = [&](const Done& w, int G) -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait(dq_full, G & 1, abort_flag))) return false;
       tc_fence_after();
       uint32_t v[32];
@@ -1053,9 +1071,9 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
         if (qb_ < S) {  // rows past the sequence end are outside the map
           if (DET)  // this key block's own slot of the dQ buffer
             tma_store_3d(&tm_dq, stage, w.h * HD + 32 * half, qb_,
-                         (WIN ? dq_slot(win, w.x.j) : w.x.j) * B + w.x.b);
+                         (WIN ? dq_slot(win, w.j) : w.j) * B + w.b);
           else
-            tma_reduce_add_3d(&tm_dq, stage, w.h * HD + 32 * half, qb_, w.x.b);
+            tma_reduce_add_3d(&tm_dq, stage, w.h * HD + 32 * half, qb_, w.b);
         }
         bulk_commit_group();
       }
@@ -1064,10 +1082,10 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     // dK and dV of item n, once all its products are done: into its own K and V
     // buffers (no MMA reads them any more), in the tensor map's swizzled
     // layout, for the store warp.
-    auto finish = [&](const Item& x, int n) -> bool {
+    auto finish = [&](int j, int n) -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait(acc_done, n & 1, abort_flag))) return false;
       tc_fence_after();
-      const int key = x.j * 128 + r;
+      const int key = j * 128 + r;
       auto put = [&](uint32_t tile, int chunk, uint32_t a, uint32_t b_, uint32_t c_, uint32_t d_) {
         const uint32_t addr = tile + (uint32_t)(n & 1) * C::TILE + (uint32_t)r * 128u +
                               (uint32_t)((chunk ^ (r & 7)) * 16);
@@ -1126,8 +1144,8 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     };
     wait_primary();  // the zeros in dq_acc
     const uint32_t rowoff = (uint32_t)r * 128u + (uint32_t)half * 16384u;
-    Walk cur = start(0), prev = cur, next = cur;
-    advance(next);
+    Walk cur = start(0);
+    Done prev{};
     int G = 0;
     for (; ok && cur.left > 0; ++G) {
       const int key = cur.x.j * 128 + r;
@@ -1221,12 +1239,11 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       mbar_arrive(ps_full);
       // while the tensor core works on this block's products: dQ of the one
       // before, and, at an item's first block, the previous item's dK and dV
-      if (G > 0) ok = emit_dq(prev, G - 1) && (prev.n == cur.n || finish(prev.x, prev.n));
-      prev = cur;
-      cur = next;
-      if (next.left > 0) advance(next);
+      if (G > 0) ok = emit_dq(prev, G - 1) && (prev.n == cur.n || finish(prev.j, prev.n));
+      prev = {cur.h, cur.qb, cur.x.b, cur.x.j, cur.n};
+      advance(cur);
     }
-    if (ok && G > 0) ok = emit_dq(prev, G - 1) && finish(prev.x, prev.n);
+    if (ok && G > 0) ok = emit_dq(prev, G - 1) && finish(prev.j, prev.n);
     if (!ok && lane == 0) {
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
@@ -1819,7 +1836,7 @@ int bwd_tc(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16
   const int items = (S + 127) / 128 * Hkv * B, sms = num_sms();
   if (!launch_dependent(attn_bwd_tc_kernel<DET, WIN>, dim3(items < sms ? items : sms), kAttBwdThreads,
                         C::SMEM, st, tq, td, tdq, tdkv, lse, (const float*)delta, cs, S, Hq, Hkv, B,
-                        scale, scale * 1.4426950408889634f, win, err))
+                        FixedDiv(Hkv * B), FixedDiv(Hkv), scale, scale * 1.4426950408889634f, win, err))
     return -3;
   attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? (S + 127) / 128 : 0,
                    WIN ? win.size : 0, win.sinks, st);
