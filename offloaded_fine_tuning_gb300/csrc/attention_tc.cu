@@ -1281,8 +1281,7 @@ struct AttBwd2Cfg {
   static constexpr int OFF_V = KV;
   static constexpr int OFF_Q = 2 * KV;
   static constexpr int OFF_DO = OFF_Q + NQ * QT;
-  static constexpr int OFF_PT = OFF_DO + NQ * QT;  // 128 keys x 64 queries
-  static constexpr int OFF_DST = OFF_PT + 16384;
+  static constexpr int OFF_DST = OFF_DO + NQ * QT;  // 128 keys x 64 queries
   static constexpr int OFF_DQS = OFF_DST + 16384;  // dQ staging: 8 warps x [32 q][32 d] fp32
   static constexpr int OFF_LD = OFF_DQS + 8 * 4096;  // [2][lse 64 | D 64]
   static constexpr int OFF_BAR = OFF_LD + 2 * 128 * 4;
@@ -1306,14 +1305,14 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
   constexpr uint32_t ID_KV = umma_idesc_bf16(128, HD, false, true);   // dV, dK
   constexpr uint32_t ID_Q = umma_idesc_bf16(128, 64, true, true);     // dQ^T
   constexpr uint32_t TMEM_COLS = 512;
-  constexpr uint32_t COL_DP = 64, COL_DQ = 128, COL_DV = 256, COL_DK = 384;
+  constexpr uint32_t COL_DP = 64, COL_DQ = 128, COL_P = 192, COL_DS = 224, COL_DV = 256, COL_DK = 384;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t s0 = smem_u32(smem);
   const uint32_t sK = s0 + C::OFF_K, sV = s0 + C::OFF_V, sQ = s0 + C::OFF_Q, sDO = s0 + C::OFF_DO;
-  const uint32_t sPt = s0 + C::OFF_PT, sDSt = s0 + C::OFF_DST, sDQS = s0 + C::OFF_DQS;
+  const uint32_t sDSt = s0 + C::OFF_DST, sDQS = s0 + C::OFF_DQS;
   float* sLD = reinterpret_cast<float*>(smem + C::OFF_LD);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   const uint32_t b0 = smem_u32(bars);
@@ -1321,8 +1320,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
   auto qdo_full = [&](int i) { return b0 + 8u * (1 + i); };
   auto qdo_empty = [&](int i) { return b0 + 8u * (4 + i); };
   const uint32_t sp_full = b0 + 56, s_free = b0 + 64, ps_full = b0 + 72, pds_free = b0 + 80;
-  auto dq_full = [&](int i) { return b0 + 88u + 8u * i; };
-  auto dq_free = [&](int i) { return b0 + 104u + 8u * i; };
+  const uint32_t dq_full = b0 + 88, dq_free = b0 + 104;
   const uint32_t acc_done = b0 + 120, drain = b0 + 128;
   auto ld_full = [&](int i) { return b0 + 136u + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
@@ -1349,10 +1347,10 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     mbar_init(ps_full, 256);
     mbar_init(pds_free, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(dq_full(i), 1);
-      mbar_init(dq_free(i), 256);
       mbar_init(ld_full(i), 64);
     }
+    mbar_init(dq_full, 1);
+    mbar_init(dq_free, 256);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -1410,7 +1408,6 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     // 14-bit address field cannot carry).
     const uint64_t dK = smem_desc_sw128(sK, 16, 1024), dV = smem_desc_sw128(sV, 16, 1024);
     const uint64_t dQk = smem_desc_sw128(sQ, 16, 1024), dDOk = smem_desc_sw128(sDO, 16, 1024);
-    const uint64_t dPt = smem_desc_sw128(sPt, 16, 1024), dDSt = smem_desc_sw128(sDSt, 16, 1024);
     const uint64_t dQm = smem_desc_sw128(sQ, 8192, 1024), dDOm = smem_desc_sw128(sDO, 8192, 1024);
     const uint64_t dKm = smem_desc_sw128(sK, 16384, 1024), dDStm = smem_desc_sw128(sDSt, 16384, 1024);
     for (int it = 0; ok && it <= n_it; ++it) {
@@ -1430,22 +1427,24 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
         umma_commit(sp_full);
       }
       if (it >= 1) {  // dV, dK, dQ^T of block it - 1, once its P^T and dS^T are in shared memory
-        const int ip = it - 1, bq = ip % C::NQ, bd = ip & 1;
+        const int ip = it - 1, bq = ip % C::NQ;
         if (!mbar_wait(ps_full, ip & 1, abort_flag)) { ok = false; break; }
-        if (ip >= 2 && !mbar_wait(dq_free(bd), ((ip >> 1) - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t qo = (uint32_t)bq * (uint32_t)(C::QT / 16);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {  // over the 64 queries
           const uint32_t acc = (ip > 0 || kk > 0) ? 1u : 0u;
-          umma_bf16(tmem_base + COL_DV, dPt + kk * 2, dDOm + qo + kk * 128, ID_KV, acc);
-          umma_bf16(tmem_base + COL_DK, dDSt + kk * 2, dQm + qo + kk * 128, ID_KV, acc);
+          umma_bf16_ts(tmem_base + COL_DV, tmem_base + COL_P + kk * 8, dDOm + qo + kk * 128, ID_KV, acc);
+          umma_bf16_ts(tmem_base + COL_DK, tmem_base + COL_DS + kk * 8, dQm + qo + kk * 128, ID_KV, acc);
         }
+        umma_commit(qdo_empty(bq));
+        // dQ^T of the previous block has been read
+        if (ip >= 1 && !mbar_wait(dq_free, (ip - 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)  // over the 128 keys
-          umma_bf16(tmem_base + COL_DQ + 64 * bd, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
-        umma_commit(dq_full(bd));
-        umma_commit(qdo_empty(bq));
+          umma_bf16(tmem_base + COL_DQ, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
+        umma_commit(dq_full);
         umma_commit(pds_free);
       }
     }
@@ -1510,11 +1509,13 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       }
     };
     auto emit_dq = [&](int it_) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(dq_full(it_ & 1), (it_ >> 1) & 1, abort_flag))) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait(dq_full, it_ & 1, abort_flag))) return false;
       tc_fence_after();
       uint32_t v[32];
-      tmem_ld_32x32b_x32(lane_base + COL_DQ + 64 * (it_ & 1) + 32 * half, v);
+      tmem_ld_32x32b_x32(lane_base + COL_DQ + 32 * half, v);
       tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(dq_free);
       stage_dq(it_, v);
       return true;
     };
@@ -1538,23 +1539,14 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       fetch(it + 1, next_l, next_d);
       ok = __all_sync(0xffffffffu, mbar_wait(ld_full(it & 1), (it >> 1) & 1, abort_flag));
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sp_full, it & 1, abort_flag));
-      // dQ^T of block it - 2 (its buffer is the one block it will use) is
-      // read together with this block's S^T and dP^T
-      if (ok && it >= 2)
-        ok = __all_sync(0xffffffffu, mbar_wait(dq_full(it & 1), ((it - 2) >> 1) & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      uint32_t sr[32], dr[32], qv[32];
+      uint32_t sr[32], dr[32];
       tmem_ld_32x32b_x32(lane_base + 32 * half, sr);
       tmem_ld_32x32b_x32(lane_base + COL_DP + 32 * half, dr);
-      if (it >= 2) tmem_ld_32x32b_x32(lane_base + COL_DQ + 64 * (it & 1) + 32 * half, qv);
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive(s_free);  // S^T / dP^T are in registers: the next block may overwrite them
-      if (it >= 2) {
-        mbar_arrive(dq_free(it & 1));
-        stage_dq(it - 2, qv);
-      }
       const float4* L4 = reinterpret_cast<const float4*>(bL + 32 * half);
       const float4* D4 = reinterpret_cast<const float4*>(bD + 32 * half);
       uint32_t pp[16], dd[16];
@@ -1608,23 +1600,24 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(pds_free, (it - 1) & 1, abort_flag));
         if (!ok) break;
       }
+      tmem_st_32x32b_x16(lane_base + COL_P + 16 * half, pp);
+      tmem_st_32x32b_x16(lane_base + COL_DS + 16 * half, dd);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int jj = half * 4 + k;  // 16-byte chunk of the 128-byte row
         const uint32_t off = rowoff + (uint32_t)((jj ^ (r & 7)) * 16);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPt + off), "r"(pp[4 * k]),
-                     "r"(pp[4 * k + 1]), "r"(pp[4 * k + 2]), "r"(pp[4 * k + 3])
-                     : "memory");
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sDSt + off), "r"(dd[4 * k]),
                      "r"(dd[4 * k + 1]), "r"(dd[4 * k + 2]), "r"(dd[4 * k + 3])
                      : "memory");
       }
+      tmem_st_wait();
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(ps_full);
+      // dQ^T of the previous block, while the tensor core works on this one's products
+      if (it >= 1 && !emit_dq(it - 1)) { ok = false; break; }
     }
-    // the last two blocks' dQ
-    for (int ip = n_it >= 2 ? n_it - 2 : 0; ok && ip < n_it; ++ip) ok = emit_dq(ip);
+    if (ok) ok = emit_dq(n_it - 1);
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, abort_flag));
     if (ok) {
       tc_fence_after();
