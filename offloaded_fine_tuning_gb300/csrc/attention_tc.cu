@@ -1378,12 +1378,10 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       tma_load_3d(sV + c * 16384, &tm_kv, kv_full, (Hq + Hkv + g) * HD + 64 * c, k0, b);
     }
     bool ok = true;
-    int issued = 0;
+    int issued = 0, bq = 0, bph = 0, wh = g * grp, wq = first;
     for (int it = 0; it < n_it; ++it) {
-      const int bq = it % C::NQ;
-      const int h = g * grp + it / per_head;
-      const int q0 = (first + it % per_head) * 64;
-      if (!mbar_wait(qdo_empty(bq), ((it / C::NQ) & 1) ^ 1, abort_flag)) { ok = false; break; }
+      const int q0 = wq * 64, h = wh;
+      if (!mbar_wait(qdo_empty(bq), bph ^ 1, abort_flag)) { ok = false; break; }
       mbar_arrive_expect_tx(qdo_full(bq), 2 * C::QT);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -1391,6 +1389,14 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
         tma_load_3d(sDO + bq * C::QT + c * 8192, &tm_do, qdo_full(bq), h * HD + 64 * c, q0, b);
       }
       issued = it + 1;
+      if (++bq == C::NQ) {
+        bq = 0;
+        bph ^= 1;
+      }
+      if (++wq == first + per_head) {
+        wq = first;
+        ++wh;
+      }
     }
     if (!ok) {
       record_error(err, kDevAttnTimeout);
@@ -1410,15 +1416,23 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     const uint64_t dQk = smem_desc_sw128(sQ, 16, 1024), dDOk = smem_desc_sw128(sDO, 16, 1024);
     const uint64_t dQm = smem_desc_sw128(sQ, 8192, 1024), dDOm = smem_desc_sw128(sDO, 8192, 1024);
     const uint64_t dKm = smem_desc_sw128(sK, 16384, 1024), dDStm = smem_desc_sw128(sDSt, 16384, 1024);
+    // A look at a barrier costs this thread about 100 cycles even when its phase
+    // is long over: the next step's are tested before the last MMAs of this one
+    // (the tensor core's queue holds two) and waited for where that was too
+    // early.  A test for a phase is only made once the phase before has been
+    // seen (its parity would be taken for a finished one's).
+    bool q_ready = false, s_ready = false, p_ready = false;
     for (int it = 0; ok && it <= n_it; ++it) {
+      p_ready = false;
       if (it < n_it) {  // S^T and dP^T of block it, once the threads hold block it - 1's
         const int bq = it % C::NQ;
-        if (!mbar_wait(qdo_full(bq), (it / C::NQ) & 1, abort_flag)) { ok = false; break; }
-        if (it >= 1 && !mbar_wait(s_free, (it - 1) & 1, abort_flag)) { ok = false; break; }
+        if (!q_ready && !mbar_wait(qdo_full(bq), (it / C::NQ) & 1, abort_flag)) { ok = false; break; }
+        if (it >= 1 && !s_ready && !mbar_wait(s_free, (it - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t qo = (uint32_t)bq * (uint32_t)(C::QT / 16);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
+          if (kk == 7 && it >= 1) p_ready = mbar_test(ps_full, (it - 1) & 1);
           const uint32_t ka = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;  // K / V: 128-row boxes
           const uint32_t qa = ((kk >> 2) * 8192 + (kk & 3) * 32) / 16;    // Q / dO: 64-row boxes
           umma_bf16(tmem_base, dK + ka, dQk + qo + qa, ID_SP, kk > 0 ? 1u : 0u);
@@ -1428,7 +1442,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       }
       if (it >= 1) {  // dV, dK, dQ^T of block it - 1, once its P^T and dS^T are in shared memory
         const int ip = it - 1, bq = ip % C::NQ;
-        if (!mbar_wait(ps_full, ip & 1, abort_flag)) { ok = false; break; }
+        if (!p_ready && !mbar_wait(ps_full, ip & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t qo = (uint32_t)bq * (uint32_t)(C::QT / 16);
 #pragma unroll
@@ -1442,8 +1456,13 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
         if (ip >= 1 && !mbar_wait(dq_free, (ip - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)  // over the 128 keys
+        for (int kk = 0; kk < 8; ++kk) {  // over the 128 keys
+          if (kk == 6) {
+            q_ready = it + 1 < n_it && mbar_test(qdo_full((it + 1) % C::NQ), ((it + 1) / C::NQ) & 1);
+            s_ready = it < n_it && mbar_test(s_free, it & 1);
+          }
           umma_bf16(tmem_base + COL_DQ, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
+        }
         umma_commit(dq_full);
         umma_commit(pds_free);
       }
@@ -1470,12 +1489,11 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     // the last query that sees this thread's key (before the key: no one does)
     const int q_end = WIN ? (key < win.sinks || key > S - win.size ? S - 1 : key + win.size - 1) : 0;
     bool ok = true;
-    auto fetch = [&](int it_, float& lv, float& dv) {
+    auto fetch = [&](int it_, int h_, int qq_, float& lv, float& dv) {
       lv = 0.f;
       dv = 0.f;
       if (it_ >= n_it || tid >= 64) return;
-      const int h_ = g * grp + it_ / per_head;
-      const int q_ = (first + it_ % per_head) * 64 + tid;
+      const int q_ = qq_ * 64 + tid;
       if (q_ < S) {
         const int64_t o = ((int64_t)b * Hq + h_) * S + q_;
         lv = lse[o];
@@ -1487,7 +1505,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     // reduce-add into the fp32 dQ buffer.  The tile is rewritten only after
     // the previous reduce has finished reading it.
     const uint32_t stage = sDQS + (uint32_t)(warp - 2) * 4096u;
-    auto stage_dq = [&](int it_, const uint32_t (&v)[32]) {
+    auto stage_dq = [&](int h_, int q_, const uint32_t (&v)[32]) {
       if (lane == 0) bulk_wait_group_read0();
       __syncwarp();
 #pragma unroll
@@ -1498,8 +1516,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        const int h_ = g * grp + it_ / per_head;
-        const int qb_ = (first + it_ % per_head) * 64 + 32 * half;
+        const int qb_ = q_ * 64 + 32 * half;
         if (DET)  // this key block's own slot of the dQ buffer
           tma_store_3d(&tm_dq, stage, h_ * HD + 32 * quarter, qb_,
                        (WIN ? dq_slot(win, j) : j) * (int)gridDim.z + b);
@@ -1508,7 +1525,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
         bulk_commit_group();
       }
     };
-    auto emit_dq = [&](int it_) -> bool {
+    auto emit_dq = [&](int it_, int h_, int q_) -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait(dq_full, it_ & 1, abort_flag))) return false;
       tc_fence_after();
       uint32_t v[32];
@@ -1516,15 +1533,16 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive(dq_free);
-      stage_dq(it_, v);
+      stage_dq(h_, q_, v);
       return true;
     };
     wait_primary();  // D, and the zeros in dq_acc
     float next_l, next_d;
-    fetch(0, next_l, next_d);
+    fetch(0, g * grp, first, next_l, next_d);
     const uint32_t rowoff = (uint32_t)r * 128u;
+    int wh = g * grp, wq = first, ph = 0, pq = 0;  // this block's head and query block; the previous one's
     for (int it = 0; it < n_it; ++it) {
-      const int q0 = (first + it % per_head) * 64;
+      const int q0 = wq * 64;
       const int qb = q0 + 32 * half;  // first query of this thread's columns
       float* bL = sLD + (it & 1) * 128;
       float* bD = bL + 64;
@@ -1536,7 +1554,8 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
         bD[tid] = next_d;
         mbar_arrive(ld_full(it & 1));
       }
-      fetch(it + 1, next_l, next_d);
+      const bool turn = wq + 1 == first + per_head;
+      fetch(it + 1, turn ? wh + 1 : wh, turn ? first : wq + 1, next_l, next_d);
       ok = __all_sync(0xffffffffu, mbar_wait(ld_full(it & 1), (it >> 1) & 1, abort_flag));
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sp_full, it & 1, abort_flag));
       if (!ok) break;
@@ -1615,9 +1634,15 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       tc_fence_before();
       mbar_arrive(ps_full);
       // dQ^T of the previous block, while the tensor core works on this one's products
-      if (it >= 1 && !emit_dq(it - 1)) { ok = false; break; }
+      if (it >= 1 && !emit_dq(it - 1, ph, pq)) { ok = false; break; }
+      ph = wh;
+      pq = wq;
+      if (++wq == first + per_head) {
+        wq = first;
+        ++wh;
+      }
     }
-    if (ok) ok = emit_dq(n_it - 1);
+    if (ok) ok = emit_dq(n_it - 1, ph, pq);
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, abort_flag));
     if (ok) {
       tc_fence_after();
