@@ -427,7 +427,10 @@ int sf_op_attn_window_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int32_t 
  * sf_op_attn_window_dq_scratch(...) elements (16-byte aligned).  With
  * deterministic != 0 the scratch has a slot for each key block that a query
  * block can see (about window / 128 + sinks / 128 + 2, not S / 128), summed in
- * key order.  The scratch size is -1 for bad sizes. */
+ * key order.  Partial sums of the sinks' dK and dV follow dQ in the scratch
+ * where the sequence is long (their keys are seen by every later query, so
+ * those queries are split into several items, joined in a fixed order).  The
+ * scratch size is -1 for bad sizes. */
 int sf_op_attn_window_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
                           const float* lse, float* delta, float* dq_acc, uint16_t* dqkv,
                           int32_t B, int32_t S, int32_t Hq, int32_t Hkv, int32_t hd,

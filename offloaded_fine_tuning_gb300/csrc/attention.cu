@@ -136,6 +136,56 @@ __global__ void attn_dq_kernel(const float* __restrict__ dq_acc, bf16* __restric
   *reinterpret_cast<uint4*>(dst + half) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
 }
 
+// dK and dV of the first blocks * 128 keys from the backward's partial sums
+// [B, Hkv, blocks, splits + 1, dK | dV, 128, hd]: part 0 has every key, the
+// others the sinks alone; they are added in their order.  dK is scaled and
+// rotated back as dQ is.  A thread takes 8 pairs of dK and the same of dV.
+__global__ void attn_sink_join_kernel(const float* __restrict__ part, bf16* __restrict__ dqkv,
+                                      int64_t rows, int S, int Hq, int Hkv, int hd, float scale,
+                                      const float2* __restrict__ cs, int blocks, int splits,
+                                      int sinks) {
+  wait_primary();
+  const int half = hd / 2, groups = half / 8;
+  const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t row = idx / groups;  // (b, g, key)
+  if (row >= rows) return;
+  const int gr = (int)(idx - row * groups);
+  const int64_t bg = row / (blocks * 128);
+  const int key = (int)(row - bg * (blocks * 128)), j = key / 128;
+  if (key >= S) return;
+  const int64_t step = (int64_t)256 * hd;  // floats of a part
+  const float* src = part + ((bg * blocks + j) * (splits + 1) * 256 + (key & 127)) * hd + gr * 8;
+  const int n = key < sinks ? splits + 1 : 1;
+  float x[4][8] = {};  // dK at gr * 8 and half + gr * 8, dV there
+  for (int c = 0; c < n; ++c, src += step)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float4* v = reinterpret_cast<const float4*>(src + (u >> 1) * 128 * hd + (u & 1) * half);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[u][4 * i] += v[i].x;
+        x[u][4 * i + 1] += v[i].y;
+        x[u][4 * i + 2] += v[i].z;
+        x[u][4 * i + 3] += v[i].w;
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = x[0][i] * scale, b = x[1][i] * scale;
+    const float2 c = cs ? cs[(int64_t)key * half + gr * 8 + i] : make_float2(1.f, 0.f);
+    x[0][i] = a * c.x + b * c.y;
+    x[1][i] = b * c.x - a * c.y;
+  }
+  const int64_t b = bg / Hkv;
+  const int g = (int)(bg - b * Hkv);
+  bf16* dst = dqkv + (b * S + key) * (int64_t)(Hq + 2 * Hkv) * hd + (int64_t)(Hq + g) * hd + gr * 8;
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    *reinterpret_cast<uint4*>(dst + (u >> 1) * (int64_t)Hkv * hd + (u & 1) * half) =
+        make_uint4(pack2(x[u][0], x[u][1]), pack2(x[u][2], x[u][3]), pack2(x[u][4], x[u][5]),
+                   pack2(x[u][6], x[u][7]));
+}
+
 void attn_delta(const bf16* o, const bf16* dout, float* delta, float* zero, int B, int S, int Hq,
                 int hd, cudaStream_t st) {
   const int64_t rows = (int64_t)B * S * Hq;
@@ -147,21 +197,34 @@ void attn_delta(const bf16* o, const bf16* dout, float* delta, float* zero, int 
     attn_delta_kernel<8><<<grid, 256, 0, st>>>(o, dout, delta, zero, rows, S, Hq);
 }
 
+template <class... P, class... A>
+static void launch_dependent(void (*kern)(P...), int64_t threads, cudaStream_t st, A... args) {
+  cudaLaunchAttribute after[1];
+  after[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  after[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((threads + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = after;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 void attn_dq_finalize(const float* dq_acc, bf16* dqkv, int B, int S, int Hq, int Hkv, int hd,
                       float scale, const float2* cs, int slots, int window, int sinks,
                       cudaStream_t st) {
   const int64_t T = (int64_t)B * S;
   const int64_t n = T * Hq * (hd / 16);
-  cudaLaunchAttribute after[1];
-  after[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  after[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((n + 255) / 256));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = after;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, attn_dq_kernel, dq_acc, dqkv, T, S, Hq, Hkv, hd, scale, cs, slots, window, sinks);
+  launch_dependent(attn_dq_kernel, n, st, dq_acc, dqkv, T, S, Hq, Hkv, hd, scale, cs, slots, window, sinks);
+}
+
+void attn_sink_join(const float* part, bf16* dqkv, int B, int S, int Hq, int Hkv, int hd,
+                    float scale, const float2* cs, int splits, int sinks, cudaStream_t st) {
+  const int blocks = (sinks + 127) / 128;
+  const int64_t rows = (int64_t)B * Hkv * blocks * 128;
+  launch_dependent(attn_sink_join_kernel, rows * (hd / 16), st, part, dqkv, rows, S, Hq, Hkv, hd, scale,
+                   cs, blocks, splits, sinks);
 }
 
 }  // namespace sf

@@ -126,8 +126,9 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
 
 // A sliding window with sinks (the kernels' WIN variants): query q sees key k
 // when k <= q and (q - k < size or k < sinks).  The host clips both to S.
+// splits: far parts of a sinks' key block in the backward (attn_window_splits).
 struct AttWindow {
-  int size, sinks;
+  int size, sinks, splits;
 };
 
 }  // namespace
@@ -408,10 +409,18 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
           }
           tc_fence_after();
           const uint64_t bv = dV + (uint32_t)vs * (uint32_t)(C::TILE / 16);
+          // O_t += P_t V: P as the tensor-memory A operand
+          if (WIN && keys < 128) {  // only the sinks
+#pragma unroll 1
+            for (int kk = 0; kk < keys / 16; ++kk)
+              umma_bf16_ts(tmem_base + O_COL + tt * HD, tmem_base + tt * 128 + kk * 8, bv + kk * (2048 / 16),
+                           ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+          } else {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // O_t += P_t V: P as the tensor-memory A operand
-            if (!WIN || kk * 16 < keys) umma_bf16_ts(tmem_base + O_COL + tt * HD, tmem_base + tt * 128 + kk * 8, bv + kk * (2048 / 16),
-                         ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 8; ++kk)
+              umma_bf16_ts(tmem_base + O_COL + tt * HD, tmem_base + tt * 128 + kk * 8, bv + kk * (2048 / 16),
+                           ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+          }
           if (last) umma_commit(o_done(tt));
           if (has_next) {
             if (last && !mbar_wait(q_full(tt), (uint32_t)((it + 1) & 1), abort_flag)) {
@@ -677,6 +686,68 @@ __device__ __forceinline__ int last_query(const AttWindow& win, int k0, int S) {
   const int q = k0 + 127 + win.size - 1;
   return k0 < win.sinks || q > S - 1 ? S - 1 : q;
 }
+// What one item of the backward works on: key block j against count query
+// blocks from the first on.  slot: where the item's dK and dV go, -1 for the
+// output itself, else fp32 partial sums that attn_sink_join adds.
+struct KeyWork {
+  int j, first, count, slot;
+};
+// The item of a rank, query blocks of QB.  A sinks' key block is seen by every
+// later query, which would make it an item many times the others' length (2 x
+// 8192 tokens, window 1024, 4 sinks: 512 steps against 72; longer than all the
+// rest of the work where the sequence is long and the window short).  So the
+// queries behind its window are split into win.splits items of their own, and
+// its other item (slot 0) is like every key block's (1 x 16384, 16 heads in
+// groups of 8, window 256, 4 sinks: 3328 us with one item, 355 us split).  The
+// parts come first, as they can be longer than the others (130 sinks there:
+// 343 us, 460 us with the parts spread between the key blocks).
+//
+// PART: the variants of the kernels for win.splits > 0; the decoding of items
+// and the parts' epilogue are on the critical path of short items (8 x 1001, 16
+// heads of 64, window 250: 93 us without, 100 us in one variant with them).
+template <int QB, bool WIN, bool PART>
+__device__ __forceinline__ KeyWork key_work(const AttWindow& win, int rank, int S) {
+  const int nq = (S + QB - 1) / QB;
+  if (!WIN) return {rank, rank * (128 / QB), nq - rank * (128 / QB), -1};
+  if (!PART) return {rank, rank * (128 / QB), last_query(win, rank * 128, S) / QB + 1 - rank * (128 / QB), -1};
+  const int ns = (win.sinks + 127) / 128, parts = ns * win.splits;
+  const bool part = rank < parts;
+  KeyWork w;
+  w.slot = -1;
+  w.j = rank - parts;
+  int c = 0;
+  if (part) {
+    w.j = rank / win.splits;
+    c = rank - w.j * win.splits;
+  }
+  const int seen = w.j * 128 + 127 + win.size - 1;  // the last query with a key in its window
+  const int end = seen > S - 1 ? nq : seen / QB + 1;
+  w.first = w.j * (128 / QB);
+  w.count = end - w.first;
+  if (part) {
+    const int n = nq - end, b0 = n * c / win.splits, b1 = n * (c + 1) / win.splits;
+    w.first = end + b0;
+    w.count = b1 - b0;
+    w.slot = c + 1;
+  } else if (w.j < ns) {
+    w.slot = 0;
+  }
+  return w;
+}
+// Keys of the item that have to be worked on: behind the window only the sinks
+// (rounded up to the MMAs' 16 keys).
+__device__ __forceinline__ int live_keys(const AttWindow& win, const KeyWork& w) {
+  const int n = (win.sinks - w.j * 128 + 15) & ~15;
+  return w.slot > 0 && n < 128 ? n : 128;
+}
+// Row r of the item's fp32 dK; its dV follows 128 rows later.
+template <int HD>
+__device__ __forceinline__ float* part_row(float* part, const AttWindow& win, const KeyWork& w, int g,
+                                           int Hkv, int b, int r) {
+  const int ns = (win.sinks + 127) / 128;
+  const int64_t at = (((int64_t)b * Hkv + g) * ns + w.j) * (win.splits + 1) + w.slot;
+  return part + (at * 256 + r) * HD;
+}
 // The deterministic variant's dQ slot of key block j: the sinks' blocks have
 // their own, the others take attn_window_slots of them in turn (attn_dq_kernel
 // sums the slots of a query's blocks in key order).
@@ -688,7 +759,7 @@ __device__ __forceinline__ int dq_slot(const AttWindow& win, int j) {
 
 // Backward for head_dim 64.  An item is one (128-key block j, kv head g, batch
 // b): every query head of the group and every 128-query block that sees its
-// keys.  The CTAs are persistent, one per SM, and take the items longest first,
+// keys (or a part of them, KeyWork).  The CTAs are persistent, one per SM, and take the items longest first,
 // every other round in reverse order, so that long and short ones add up.  Per
 // (head, block):
 //   MMA:     S^T = K Q^T -> TMEM[0,128),  dP^T = V dO^T -> TMEM[128,256)
@@ -758,7 +829,7 @@ struct FixedDiv {
 };
 }  // namespace
 
-template <bool DET, bool WIN>
+template <bool DET, bool WIN, bool PART>
 __global__ void __launch_bounds__(kAttBwdThreads, 1)
     attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv,
                        const __grid_constant__ CUtensorMap tm_do,
@@ -766,7 +837,7 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
                        const __grid_constant__ CUtensorMap tm_dkv, const float* __restrict__ lse,
                        const float* __restrict__ delta, const float2* __restrict__ cs, int S,
                        int Hq, int Hkv, int B, FixedDiv per_block, FixedDiv per_batch, float scale,
-                       float scale_log2, AttWindow win, int* err) {
+                       float scale_log2, AttWindow win, float* __restrict__ part, int* err) {
   using C = AttBwdCfg;
   constexpr int HD = C::HD;
   constexpr uint32_t ID_SP = umma_idesc_bf16(128, 128, false, false);  // S^T, dP^T
@@ -802,35 +873,34 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = Hq / Hkv, nkb = (S + 127) / 128;
-  const int num_items = nkb * Hkv * B;  // key block 0 sees the most query blocks
-  struct Item { int j, g, b, per_head, n_it; };
+  // without a window key block 0 sees the most query blocks
+  const int num_items = (nkb + (PART ? (win.sinks + 127) / 128 * win.splits : 0)) * Hkv * B;
+  struct Item { KeyWork w; int g, b, n_it; };
   // this CTA's n-th item (n_it = 0: none left)
   auto item_of = [&](int n) -> Item {
     const int c = n & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
     const int t = n * (int)gridDim.x + c;
-    if (t >= num_items) return {0, 0, 0, 1, 0};
+    if (t >= num_items) return {{0, 0, 1, -1}, 0, 0, 0};
     Item x;
     int rem;
-    x.j = per_block(t, rem);  // by Hkv * B
-    x.b = per_batch(rem, x.g);  // by Hkv
-    // query blocks j .. j + per_head - 1 can see these keys
-    x.per_head = (WIN ? last_query(win, x.j * 128, S) / 128 + 1 : nkb) - x.j;
-    x.n_it = grp * x.per_head;  // (head, query block) pairs
+    x.w = key_work<128, WIN, PART>(win, per_block(t, rem), S);  // t by Hkv * B
+    x.b = per_batch(rem, x.g);                             // by Hkv
+    x.n_it = grp * x.w.count;  // (head, query block) pairs
     return x;
   };
 
   // Blocks in the order of the walk: a head's query blocks, then the next
   // head's, then the next item's (counted on, without a division per block).
-  struct Walk { Item x; int n, left, h, qb; };  // blocks left in the item, this one included
+  struct Walk { int n, left, h, qb, j, b, first, end; };  // left: blocks of the item, this one included
   auto start = [&](int n) -> Walk {
     const Item x = item_of(n);
-    return {x, n, x.n_it, x.g * grp, x.j};
+    return {n, x.n_it, x.g * grp, x.w.first, x.w.j, x.b, x.w.first, x.w.first + x.w.count};
   };
   auto advance = [&](Walk& w) {
     if (--w.left == 0) {
       w = start(w.n + 1);
-    } else if (++w.qb == w.x.j + w.x.per_head) {
-      w.qb = w.x.j;
+    } else if (++w.qb == w.end) {
+      w.qb = w.first;
       ++w.h;
     }
   };
@@ -882,13 +952,13 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       const int ks = n & 1;
       if (!mbar_wait(kv_empty(ks), ((n >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
       mbar_arrive_expect_tx(kv_full(ks), 2 * C::TILE);
-      tma_load_3d(sK + ks * C::TILE, &tm_qkv, kv_full(ks), (Hq + x.g) * HD, x.j * 128, x.b);
-      tma_load_3d(sV + ks * C::TILE, &tm_qkv, kv_full(ks), (Hq + Hkv + x.g) * HD, x.j * 128, x.b);
+      tma_load_3d(sK + ks * C::TILE, &tm_qkv, kv_full(ks), (Hq + x.g) * HD, x.w.j * 128, x.b);
+      tma_load_3d(sV + ks * C::TILE, &tm_qkv, kv_full(ks), (Hq + Hkv + x.g) * HD, x.w.j * 128, x.b);
       kv_issued = n + 1;
       for (int it = 0; it < x.n_it; ++it) {
         const int bq = issued % C::NQ;
-        const int h = x.g * grp + it / x.per_head;
-        const int q0 = (x.j + it % x.per_head) * 128;
+        const int h = x.g * grp + it / x.w.count;
+        const int q0 = (x.w.first + it % x.w.count) * 128;
         if (!mbar_wait(qdo_empty(bq), ((issued / C::NQ) & 1) ^ 1, abort_flag)) { ok = false; break; }
         mbar_arrive_expect_tx(qdo_full(bq), 2 * C::TILE);
         tma_load_3d(sQ + bq * C::TILE, &tm_qkv, qdo_full(bq), h * HD, q0, x.b);
@@ -992,11 +1062,12 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       ok = mbar_wait(dkv_full, n & 1, abort_flag);
       if (!ok) break;
       const uint32_t at = (uint32_t)(n & 1) * C::TILE;
-      // key rows past the sequence end are outside the map
-      tma_store_3d(&tm_dkv, sK + at, (Hq + x.g) * HD, x.j * 128, x.b);
-      tma_store_3d(&tm_dkv, sV + at, (Hq + Hkv + x.g) * HD, x.j * 128, x.b);
-      bulk_commit_group();
-      bulk_wait_group_read0();
+      if (!PART || x.w.slot < 0) {  // key rows past the sequence end are outside the map
+        tma_store_3d(&tm_dkv, sK + at, (Hq + x.g) * HD, x.w.j * 128, x.b);
+        tma_store_3d(&tm_dkv, sV + at, (Hq + Hkv + x.g) * HD, x.w.j * 128, x.b);
+        bulk_commit_group();
+        bulk_wait_group_read0();
+      }
       mbar_arrive(kv_empty(n & 1));
     }
     if (!ok) {
@@ -1012,7 +1083,7 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     bool ok = true;
     Walk w = start(0);
     for (int G = 0; w.left > 0; ++G, advance(w)) {
-      const int64_t row = ((int64_t)w.x.b * Hq + w.h) * S;
+      const int64_t row = ((int64_t)w.b * Hq + w.h) * S;
       float lv[4], dv[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -1093,45 +1164,61 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
                      "r"(c_), "r"(d_)
                      : "memory");
       };
-      // dK: pairs (d, d + HD/2) get the inverse rotation of the key's position;
-      // this warp takes d in [16 half, 16 half + 16) and their partners
-      {
-        uint32_t x1[16], x2[16];
-        tmem_ld_32x32b_x16(lane_base + COL_DK + 16 * half, x1);
-        tmem_ld_32x32b_x16(lane_base + COL_DK + HD / 2 + 16 * half, x2);
-        tmem_ld_wait();
-        const int kp = key < S ? key : S - 1;  // rows past the end are computed, not stored
-        uint32_t o1[8], o2[8];
+      if (PART && j < (win.sinks + 127) / 128) {  // a part: fp32, neither scaled nor rotated
+        const Item x = item_of(n);
+        float* dst = part_row<HD>(part, win, x.w, x.g, Hkv, x.b, r) + 32 * half;
+        const bool live = r < live_keys(win, x.w);
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          float a1 = __uint_as_float(x1[e]) * scale, b1 = __uint_as_float(x1[e + 1]) * scale;
-          float a2 = __uint_as_float(x2[e]) * scale, b2 = __uint_as_float(x2[e + 1]) * scale;
-          if (cs) {
-            const float2 ca = cs[(int64_t)kp * (HD / 2) + 16 * half + e];
-            const float2 cb = cs[(int64_t)kp * (HD / 2) + 16 * half + e + 1];
-            const float y1a = a1 * ca.x + a2 * ca.y, y2a = a2 * ca.x - a1 * ca.y;
-            const float y1b = b1 * cb.x + b2 * cb.y, y2b = b2 * cb.x - b1 * cb.y;
-            a1 = y1a; a2 = y2a; b1 = y1b; b2 = y2b;
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(lane_base + (c ? COL_DV : COL_DK) + 32 * half, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 8 && live; ++k)
+            *reinterpret_cast<uint4*>(dst + c * 128 * HD + 4 * k) =
+                make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+      } else {
+        // dK: pairs (d, d + HD/2) get the inverse rotation of the key's position;
+        // this warp takes d in [16 half, 16 half + 16) and their partners
+        {
+          uint32_t x1[16], x2[16];
+          tmem_ld_32x32b_x16(lane_base + COL_DK + 16 * half, x1);
+          tmem_ld_32x32b_x16(lane_base + COL_DK + HD / 2 + 16 * half, x2);
+          tmem_ld_wait();
+          const int kp = key < S ? key : S - 1;  // rows past the end are computed, not stored
+          uint32_t o1[8], o2[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float a1 = __uint_as_float(x1[e]) * scale, b1 = __uint_as_float(x1[e + 1]) * scale;
+            float a2 = __uint_as_float(x2[e]) * scale, b2 = __uint_as_float(x2[e + 1]) * scale;
+            if (cs) {
+              const float2 ca = cs[(int64_t)kp * (HD / 2) + 16 * half + e];
+              const float2 cb = cs[(int64_t)kp * (HD / 2) + 16 * half + e + 1];
+              const float y1a = a1 * ca.x + a2 * ca.y, y2a = a2 * ca.x - a1 * ca.y;
+              const float y1b = b1 * cb.x + b2 * cb.y, y2b = b2 * cb.x - b1 * cb.y;
+              a1 = y1a; a2 = y2a; b1 = y1b; b2 = y2b;
+            }
+            o1[e / 2] = pack2_bf16(a1, b1);
+            o2[e / 2] = pack2_bf16(a2, b2);
           }
-          o1[e / 2] = pack2_bf16(a1, b1);
-          o2[e / 2] = pack2_bf16(a2, b2);
-        }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          put(sK, 2 * half + k, o1[4 * k], o1[4 * k + 1], o1[4 * k + 2], o1[4 * k + 3]);
-          put(sK, 4 + 2 * half + k, o2[4 * k], o2[4 * k + 1], o2[4 * k + 2], o2[4 * k + 3]);
+          for (int k = 0; k < 2; ++k) {
+            put(sK, 2 * half + k, o1[4 * k], o1[4 * k + 1], o1[4 * k + 2], o1[4 * k + 3]);
+            put(sK, 4 + 2 * half + k, o2[4 * k], o2[4 * k + 1], o2[4 * k + 2], o2[4 * k + 3]);
+          }
         }
-      }
-      {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(lane_base + COL_DV + 32 * half, v);
-        tmem_ld_wait();
+        {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(lane_base + COL_DV + 32 * half, v);
+          tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          put(sV, 4 * half + k, pack2_bf16(__uint_as_float(v[8 * k + 0]), __uint_as_float(v[8 * k + 1])),
-              pack2_bf16(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
-              pack2_bf16(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
-              pack2_bf16(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
+          for (int k = 0; k < 4; ++k)
+            put(sV, 4 * half + k, pack2_bf16(__uint_as_float(v[8 * k + 0]), __uint_as_float(v[8 * k + 1])),
+                pack2_bf16(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
+                pack2_bf16(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
+                pack2_bf16(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
+        }
       }
       tc_fence_before();
       mbar_arrive(acc_free);  // the next item's dV and dK may be formed
@@ -1148,7 +1235,7 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     Done prev{};
     int G = 0;
     for (; ok && cur.left > 0; ++G) {
-      const int key = cur.x.j * 128 + r;
+      const int key = cur.j * 128 + r;
       // the last query that sees this thread's key (before the key: no one does)
       const int q_end = !WIN || key < win.sinks || key > S - win.size ? S - 1 : key + win.size - 1;
       const int qc = cur.qb * 128 + 64 * half;  // first query of this thread's columns
@@ -1240,7 +1327,7 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
       // while the tensor core works on this block's products: dQ of the one
       // before, and, at an item's first block, the previous item's dK and dV
       if (G > 0) ok = emit_dq(prev, G - 1) && (prev.n == cur.n || finish(prev.j, prev.n));
-      prev = {cur.h, cur.qb, cur.x.b, cur.x.j, cur.n};
+      prev = {cur.h, cur.qb, cur.b, cur.j, cur.n};
       advance(cur);
     }
     if (ok && G > 0) ok = emit_dq(prev, G - 1) && finish(prev.j, prev.n);
@@ -1290,7 +1377,7 @@ struct AttBwd2Cfg {
 };
 }  // namespace
 
-template <bool DET, bool WIN>
+template <bool DET, bool WIN, bool PART>
 __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     attn_bwd_tc2_kernel(const __grid_constant__ CUtensorMap tm_kv,
                         const __grid_constant__ CUtensorMap tm_q,
@@ -1298,7 +1385,8 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
                         const __grid_constant__ CUtensorMap tm_dq,
                         const __grid_constant__ CUtensorMap tm_dkv, const float* __restrict__ lse,
                         const float* __restrict__ delta, const float2* __restrict__ cs, int S,
-                        int Hq, int Hkv, float scale, float scale_log2, AttWindow win, int* err) {
+                        int Hq, int Hkv, float scale, float scale_log2, AttWindow win,
+                        float* __restrict__ part, int* err) {
   using C = AttBwd2Cfg;
   constexpr int HD = 128;
   constexpr uint32_t ID_SP = umma_idesc_bf16(128, 64, false, false);  // S^T, dP^T
@@ -1327,13 +1415,13 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int j, g, b;
-  grid_rank_first(j, g, b);  // key block 0 sees the most query blocks
+  int rank, g, b;
+  grid_rank_first(rank, g, b);  // without a window key block 0 sees the most query blocks
+  const KeyWork work = key_work<64, WIN, PART>(win, rank, S);
   const int grp = Hq / Hkv;
-  const int k0 = j * 128;
-  const int nqb = (S + 63) / 64;
-  const int first = 2 * j;  // first 64-query block that can see these keys
-  const int per_head = (WIN ? last_query(win, k0, S) / 64 + 1 : nqb) - first;
+  const int j = work.j, k0 = j * 128;
+  const int first = work.first, per_head = work.count;  // 64-query blocks that see these keys
+  const int keys = PART ? live_keys(win, work) : 128;
   const int n_it = grp * per_head;
 
   if (threadIdx.x == 0) {
@@ -1455,13 +1543,20 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
         // dQ^T of the previous block has been read
         if (ip >= 1 && !mbar_wait(dq_free, (ip - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
+        if (PART && keys < 128) {  // only the sinks
+          q_ready = s_ready = false;
+#pragma unroll 1
+          for (int kk = 0; kk < keys / 16; ++kk)
+            umma_bf16(tmem_base + COL_DQ, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
+        } else {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {  // over the 128 keys
-          if (kk == 6) {
-            q_ready = it + 1 < n_it && mbar_test(qdo_full((it + 1) % C::NQ), ((it + 1) / C::NQ) & 1);
-            s_ready = it < n_it && mbar_test(s_free, it & 1);
+          for (int kk = 0; kk < 8; ++kk) {  // over the 128 keys
+            if (kk == 6) {
+              q_ready = it + 1 < n_it && mbar_test(qdo_full((it + 1) % C::NQ), ((it + 1) / C::NQ) & 1);
+              s_ready = it < n_it && mbar_test(s_free, it & 1);
+            }
+            umma_bf16(tmem_base + COL_DQ, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
           }
-          umma_bf16(tmem_base + COL_DQ, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
         }
         umma_commit(dq_full);
         umma_commit(pds_free);
@@ -1540,6 +1635,8 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     float next_l, next_d;
     fetch(0, g * grp, first, next_l, next_d);
     const uint32_t rowoff = (uint32_t)r * 128u;
+    // no key of this warp's lanes counts behind the window of a sinks' block
+    const bool idle = PART && quarter * 32 >= keys;
     int wh = g * grp, wq = first, ph = 0, pq = 0;  // this block's head and query block; the previous one's
     for (int it = 0; it < n_it; ++it) {
       const int q0 = wq * 64;
@@ -1561,9 +1658,11 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       if (!ok) break;
       tc_fence_after();
       uint32_t sr[32], dr[32];
-      tmem_ld_32x32b_x32(lane_base + 32 * half, sr);
-      tmem_ld_32x32b_x32(lane_base + COL_DP + 32 * half, dr);
-      tmem_ld_wait();
+      if (!idle) {
+        tmem_ld_32x32b_x32(lane_base + 32 * half, sr);
+        tmem_ld_32x32b_x32(lane_base + COL_DP + 32 * half, dr);
+        tmem_ld_wait();
+      }
       tc_fence_before();
       mbar_arrive(s_free);  // S^T / dP^T are in registers: the next block may overwrite them
       const float4* L4 = reinterpret_cast<const float4*>(bL + 32 * half);
@@ -1611,23 +1710,27 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       // Only blocks that touch the diagonal, the sequence end or the window's
       // start need the mask.
       const bool cut = WIN && qb + 31 - k0 >= win.size && k0 + 127 >= win.sinks;
-      if (qb < k0 + 128 || qb + 32 > S || cut)
+      if (idle) {
+      } else if (qb < k0 + 128 || qb + 32 > S || cut) {
         grad_tile(std::true_type{});
-      else
+      } else {
         grad_tile(std::false_type{});
+      }
       if (it >= 1) {  // P^T, dS^T of the previous block consumed
         ok = __all_sync(0xffffffffu, mbar_wait(pds_free, (it - 1) & 1, abort_flag));
         if (!ok) break;
       }
-      tmem_st_32x32b_x16(lane_base + COL_P + 16 * half, pp);
-      tmem_st_32x32b_x16(lane_base + COL_DS + 16 * half, dd);
+      if (!idle) {
+        tmem_st_32x32b_x16(lane_base + COL_P + 16 * half, pp);
+        tmem_st_32x32b_x16(lane_base + COL_DS + 16 * half, dd);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int jj = half * 4 + k;  // 16-byte chunk of the 128-byte row
-        const uint32_t off = rowoff + (uint32_t)((jj ^ (r & 7)) * 16);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sDSt + off), "r"(dd[4 * k]),
-                     "r"(dd[4 * k + 1]), "r"(dd[4 * k + 2]), "r"(dd[4 * k + 3])
-                     : "memory");
+        for (int k = 0; k < 4; ++k) {
+          const int jj = half * 4 + k;  // 16-byte chunk of the 128-byte row
+          const uint32_t off = rowoff + (uint32_t)((jj ^ (r & 7)) * 16);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sDSt + off), "r"(dd[4 * k]),
+                       "r"(dd[4 * k + 1]), "r"(dd[4 * k + 2]), "r"(dd[4 * k + 3])
+                       : "memory");
+        }
       }
       tmem_st_wait();
       fence_proxy_async_smem();
@@ -1646,62 +1749,76 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, abort_flag));
     if (ok) {
       tc_fence_after();
-      // dK and dV rows go into the K and V tiles' shared memory (every MMA
-      // that read them has completed), in the tensor map's swizzled layout;
-      // one thread then stores both tiles with the TMA unit.
-      auto put = [&](uint32_t tile, int col, uint32_t a, uint32_t b_, uint32_t c_, uint32_t d_) {
-        const int chunk = (col & 63) >> 3;  // 16-byte chunk of the 128-byte row
-        const uint32_t addr = tile + (uint32_t)(col >> 6) * 16384u + (uint32_t)r * 128u +
-                              (uint32_t)((chunk ^ (r & 7)) * 16);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b_),
-                     "r"(c_), "r"(d_)
-                     : "memory");
-      };
-      // dK: pairs (d, d + HD/2) get the inverse rotation of the key's position;
-      // this warp takes d in [32 half, 32 half + 32) and its partners
-      {
-        const int c = half;
-        uint32_t x1[32], x2[32];
-        tmem_ld_32x32b_x32(lane_base + COL_DK + 32 * c, x1);
-        tmem_ld_32x32b_x32(lane_base + COL_DK + HD / 2 + 32 * c, x2);
-        tmem_ld_wait();
+      if (PART && work.slot >= 0) {  // a part: fp32, neither scaled nor rotated
+        float* dst = part_row<HD>(part, win, work, g, Hkv, b, r) + 64 * half;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(lane_base + (c >> 1 ? COL_DV : COL_DK) + 64 * half + 32 * (c & 1), v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 8 && r < keys; ++k)
+            *reinterpret_cast<uint4*>(dst + (c >> 1) * 128 * HD + 32 * (c & 1) + 4 * k) =
+                make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+      } else {
+        // dK and dV rows go into the K and V tiles' shared memory (every MMA
+        // that read them has completed), in the tensor map's swizzled layout;
+        // one thread then stores both tiles with the TMA unit.
+        auto put = [&](uint32_t tile, int col, uint32_t a, uint32_t b_, uint32_t c_, uint32_t d_) {
+          const int chunk = (col & 63) >> 3;  // 16-byte chunk of the 128-byte row
+          const uint32_t addr = tile + (uint32_t)(col >> 6) * 16384u + (uint32_t)r * 128u +
+                                (uint32_t)((chunk ^ (r & 7)) * 16);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b_),
+                       "r"(c_), "r"(d_)
+                       : "memory");
+        };
+        // dK: pairs (d, d + HD/2) get the inverse rotation of the key's position;
+        // this warp takes d in [32 half, 32 half + 32) and its partners
         {
-          const int kp = key < S ? key : S - 1;  // rows past the end are computed, not stored
-          uint32_t o1[16], o2[16];
+          const int c = half;
+          uint32_t x1[32], x2[32];
+          tmem_ld_32x32b_x32(lane_base + COL_DK + 32 * c, x1);
+          tmem_ld_32x32b_x32(lane_base + COL_DK + HD / 2 + 32 * c, x2);
+          tmem_ld_wait();
+          {
+            const int kp = key < S ? key : S - 1;  // rows past the end are computed, not stored
+            uint32_t o1[16], o2[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float a1 = __uint_as_float(x1[e]) * scale, b1 = __uint_as_float(x1[e + 1]) * scale;
-            float a2 = __uint_as_float(x2[e]) * scale, b2 = __uint_as_float(x2[e + 1]) * scale;
-            if (cs) {
-              const float2 ca = cs[(int64_t)kp * (HD / 2) + 32 * c + e];
-              const float2 cb = cs[(int64_t)kp * (HD / 2) + 32 * c + e + 1];
-              const float y1a = a1 * ca.x + a2 * ca.y, y2a = a2 * ca.x - a1 * ca.y;
-              const float y1b = b1 * cb.x + b2 * cb.y, y2b = b2 * cb.x - b1 * cb.y;
-              a1 = y1a; a2 = y2a; b1 = y1b; b2 = y2b;
+            for (int e = 0; e < 32; e += 2) {
+              float a1 = __uint_as_float(x1[e]) * scale, b1 = __uint_as_float(x1[e + 1]) * scale;
+              float a2 = __uint_as_float(x2[e]) * scale, b2 = __uint_as_float(x2[e + 1]) * scale;
+              if (cs) {
+                const float2 ca = cs[(int64_t)kp * (HD / 2) + 32 * c + e];
+                const float2 cb = cs[(int64_t)kp * (HD / 2) + 32 * c + e + 1];
+                const float y1a = a1 * ca.x + a2 * ca.y, y2a = a2 * ca.x - a1 * ca.y;
+                const float y1b = b1 * cb.x + b2 * cb.y, y2b = b2 * cb.x - b1 * cb.y;
+                a1 = y1a; a2 = y2a; b1 = y1b; b2 = y2b;
+              }
+              o1[e / 2] = pack2_bf16(a1, b1);
+              o2[e / 2] = pack2_bf16(a2, b2);
             }
-            o1[e / 2] = pack2_bf16(a1, b1);
-            o2[e / 2] = pack2_bf16(a2, b2);
-          }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            put(sK, 32 * c + 8 * k, o1[4 * k], o1[4 * k + 1], o1[4 * k + 2], o1[4 * k + 3]);
-            put(sK, HD / 2 + 32 * c + 8 * k, o2[4 * k], o2[4 * k + 1], o2[4 * k + 2], o2[4 * k + 3]);
+            for (int k = 0; k < 4; ++k) {
+              put(sK, 32 * c + 8 * k, o1[4 * k], o1[4 * k + 1], o1[4 * k + 2], o1[4 * k + 3]);
+              put(sK, HD / 2 + 32 * c + 8 * k, o2[4 * k], o2[4 * k + 1], o2[4 * k + 2], o2[4 * k + 3]);
+            }
           }
         }
-      }
-      // dV: this warp takes columns [64 half, 64 half + 64)
+        // dV: this warp takes columns [64 half, 64 half + 64)
 #pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        const int c = 2 * half + cc;
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(lane_base + COL_DV + 32 * c, v);
-        tmem_ld_wait();
+        for (int cc = 0; cc < 2; ++cc) {
+          const int c = 2 * half + cc;
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(lane_base + COL_DV + 32 * c, v);
+          tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          put(sV, 32 * c + 8 * k, pack2_bf16(__uint_as_float(v[8 * k + 0]), __uint_as_float(v[8 * k + 1])),
-              pack2_bf16(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
-              pack2_bf16(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
-              pack2_bf16(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
+          for (int k = 0; k < 4; ++k)
+            put(sV, 32 * c + 8 * k, pack2_bf16(__uint_as_float(v[8 * k + 0]), __uint_as_float(v[8 * k + 1])),
+                pack2_bf16(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
+                pack2_bf16(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
+                pack2_bf16(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
+        }
       }
       fence_proxy_async_smem();
     } else if (lane == 0) {
@@ -1715,7 +1832,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
-  } else if (threadIdx.x == 64 && !*abort_flag) {
+  } else if (threadIdx.x == 64 && !*abort_flag && (!PART || work.slot < 0)) {
     // dK and dV tiles; key rows past the sequence end are outside the map
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -1816,7 +1933,7 @@ int fwd_pp(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int S,
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
-template <bool DET, bool WIN>
+template <bool DET, bool WIN, bool PART>
 int bwd_tc(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
            const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq,
            int Hkv, const float2* cs, AttWindow win, int* err, cudaStream_t st) {
@@ -1848,20 +1965,25 @@ int bwd_tc(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16
       !enc(&tdq, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dq_acc, ddq, sdq, box_dq,
            CU_TENSOR_MAP_L2_PROMOTION_NONE))
     return -3;
-  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc_kernel<DET, WIN>), C::SMEM)) return -3;
+  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc_kernel<DET, WIN, PART>), C::SMEM)) return -3;
   attn_delta(o, dout, delta, DET ? nullptr : dq_acc, B, S, Hq, HD, st);
   const float scale = 1.f / sqrtf((float)HD);
-  const int items = (S + 127) / 128 * Hkv * B, sms = num_sms();
-  if (!launch_dependent(attn_bwd_tc_kernel<DET, WIN>, dim3(items < sms ? items : sms), kAttBwdThreads,
+  const int ranks = (S + 127) / 128 + (PART ? (win.sinks + 127) / 128 * win.splits : 0);
+  const int items = ranks * Hkv * B, sms = num_sms();
+  // the sinks' partial dK and dV follow dQ in the scratch
+  float* part = dq_acc + (DET ? (int64_t)slots : 1) * B * S * WO;
+  if (!launch_dependent(attn_bwd_tc_kernel<DET, WIN, PART>, dim3(items < sms ? items : sms), kAttBwdThreads,
                         C::SMEM, st, tq, td, tdq, tdkv, lse, (const float*)delta, cs, S, Hq, Hkv, B,
-                        FixedDiv(Hkv * B), FixedDiv(Hkv), scale, scale * 1.4426950408889634f, win, err))
+                        FixedDiv(Hkv * B), FixedDiv(Hkv), scale, scale * 1.4426950408889634f, win, part, err))
     return -3;
+  if (PART)
+    attn_sink_join(part, dqkv, B, S, Hq, Hkv, HD, scale, cs, win.splits, win.sinks, st);
   attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? (S + 127) / 128 : 0,
                    WIN ? win.size : 0, win.sinks, st);
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
-template <bool DET, bool WIN>
+template <bool DET, bool WIN, bool PART>
 int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
             const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq,
             int Hkv, const float2* cs, AttWindow win, int* err, cudaStream_t st) {
@@ -1893,14 +2015,18 @@ int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat1
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return -3;
-  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc2_kernel<DET, WIN>), C::SMEM)) return -3;
+  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc2_kernel<DET, WIN, PART>), C::SMEM)) return -3;
   attn_delta(o, dout, delta, DET ? nullptr : dq_acc, B, S, Hq, HD, st);
   const float scale = 1.f / sqrtf((float)HD);
-  dim3 grid((S + 127) / 128, Hkv, B);
-  if (!launch_dependent(attn_bwd_tc2_kernel<DET, WIN>, grid, kAttBwd2Threads, C::SMEM, st, tkv, tq, td,
+  dim3 grid(nkb + (PART ? (win.sinks + 127) / 128 * win.splits : 0), Hkv, B);
+  // the sinks' partial dK and dV follow dQ in the scratch
+  float* part = dq_acc + (DET ? (int64_t)slots : 1) * B * S * WO;
+  if (!launch_dependent(attn_bwd_tc2_kernel<DET, WIN, PART>, grid, kAttBwd2Threads, C::SMEM, st, tkv, tq, td,
                         tdq, tdkv, lse, (const float*)delta, cs, S, Hq, Hkv, scale,
-                        scale * 1.4426950408889634f, win, err))
+                        scale * 1.4426950408889634f, win, part, err))
     return -3;
+  if (PART)
+    attn_sink_join(part, dqkv, B, S, Hq, Hkv, HD, scale, cs, win.splits, win.sinks, st);
   attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? nkb : 0, WIN ? win.size : 0,
                    win.sinks, st);
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
@@ -1909,18 +2035,31 @@ int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat1
 }  // namespace
 
 namespace {
-template <bool DET, bool WIN>
+template <bool DET, bool WIN, bool PART = false>
 int bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
         const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq,
         int Hkv, int hd, const float2* cs, AttWindow win, int* err, cudaStream_t st) {
   if (hd == 64)
-    return bwd_tc<DET, WIN>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, win, err, st);
+    return bwd_tc<DET, WIN, PART>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, win, err, st);
   if (hd == 128)
-    return bwd_tc2<DET, WIN>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, win, err, st);
+    return bwd_tc2<DET, WIN, PART>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, cs, win, err, st);
   return -1;
 }
-AttWindow clip(int window, int sinks, int S) {
-  return {window < S ? window : S, sinks < S ? sinks : S};
+// The window as the kernels take it.  At head dim 128, where the hardware deals
+// the items out, the sinks' queries are split only where one item with all of
+// them would take longer than an even share of the work: else it runs beside
+// the others from the start, its queries a little ahead of theirs (2 x 8192, 32
+// / 8 heads of 128, window 1024, 4 sinks: 964 us in one item, 1003 us split).
+// At 64 the items are dealt out in advance and a long one delays those behind
+// it (1 x 16384, 16 heads, window 1024, 64 sinks: 538 us and 384 us).
+AttWindow clip(int window, int sinks, int S, int B, int Hq, int Hkv, int hd) {
+  AttWindow win{window < S ? window : S, sinks < S ? sinks : S, attn_window_splits(S, window, sinks, hd)};
+  if (hd == 128 && win.splits > 0) {
+    const int64_t nq = (S + 63) / 64, near = (126 + win.size) / 64 + 1, ns = (win.sinks + 127) / 128;
+    const int64_t work = (int64_t)B * Hq * ((S + 127) / 128 * near + ns * (nq - near));
+    if ((int64_t)(Hq / Hkv) * nq * num_sms() <= work) win.splits = 0;
+  }
+  return win;
 }
 }  // namespace
 
@@ -1930,7 +2069,7 @@ int attn_bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat
              cudaStream_t st) {
   if (B <= 0 || S <= 0) return 0;
   if (Hkv <= 0 || Hq % Hkv) return -1;
-  const AttWindow all{S, 0};
+  const AttWindow all{S, 0, 0};
   return deterministic ? bwd<true, false>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv,
                                           hd, cs, all, err, st)
                        : bwd<false, false>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv,
@@ -1943,11 +2082,10 @@ int attn_window_bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv
                     bool deterministic, int* err, cudaStream_t st) {
   if (B <= 0 || S <= 0) return 0;
   if (Hkv <= 0 || Hq % Hkv || window < 1 || sinks < 0) return -1;
-  const AttWindow win = clip(window, sinks, S);
-  return deterministic ? bwd<true, true>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv,
-                                         hd, cs, win, err, st)
-                       : bwd<false, true>(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv,
-                                          hd, cs, win, err, st);
+  const AttWindow win = clip(window, sinks, S, B, Hq, Hkv, hd);
+  const auto fn = win.splits > 0 ? (deterministic ? bwd<true, true, true> : bwd<false, true, true>)
+                                 : (deterministic ? bwd<true, true> : bwd<false, true>);
+  return fn(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, hd, cs, win, err, st);
 }
 
 int attn_fwd(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int S, int Hq, int Hkv,
@@ -1955,7 +2093,7 @@ int attn_fwd(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int 
   if (B <= 0 || S <= 0) return 0;
   if (Hkv <= 0 || Hq % Hkv) return -1;
   if ((reinterpret_cast<uintptr_t>(qkv) & 15) != 0) return -1;
-  const AttWindow all{S, 0};
+  const AttWindow all{S, 0, 0};
   if (hd == 64) return fwd_pp<64, false>(qkv, o, lse, B, S, Hq, Hkv, all, err, st);
   if (hd == 128) return fwd_pp<128, false>(qkv, o, lse, B, S, Hq, Hkv, all, err, st);
   return -1;
@@ -1965,7 +2103,7 @@ int attn_window_fwd(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int 
                     int Hkv, int hd, int window, int sinks, int* err, cudaStream_t st) {
   if (B <= 0 || S <= 0) return 0;
   if (Hkv <= 0 || Hq % Hkv || window < 1 || sinks < 0) return -1;
-  const AttWindow win = clip(window, sinks, S);
+  const AttWindow win = clip(window, sinks, S, B, Hq, Hkv, hd);
   if (hd == 64) return fwd_pp<64, true>(qkv, o, lse, B, S, Hq, Hkv, win, err, st);
   if (hd == 128) return fwd_pp<128, true>(qkv, o, lse, B, S, Hq, Hkv, win, err, st);
   return -1;

@@ -204,7 +204,7 @@ int64_t sf_op_attn_window_dq_scratch(int32_t B, int32_t S_, int32_t Hq, int32_t 
                                      int32_t sinks, int32_t deterministic) {
   if (B < 0 || S_ < 0 || Hq < 1 || (hd != 64 && hd != 128) || window < 1 || sinks < 0) return -1;
   const int64_t slots = deterministic ? sf::attn_window_dq_slots(S_, window, sinks) : 1;
-  return slots * B * S_ * Hq * hd;
+  return slots * B * S_ * Hq * hd + sf::attn_window_part_floats(B, S_, Hq, hd, window, sinks);
 }
 
 int sf_op_attn_window_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,

@@ -167,6 +167,34 @@ __host__ __device__ constexpr int attn_window_dq_slots(int S, int window, int si
   const int ns = (k + 127) / 128, rest = (S + 127) / 128 - ns, turn = attn_window_slots(w);
   return ns + (rest < turn ? rest : turn);
 }
+// Items that the queries behind the window of a sinks' key block are split
+// into in the backward: each about as many query blocks as another key block
+// has, none empty, at most 32 in all; 0 (one item with the rest)
+// where there are fewer such queries than another block has, or more than 32
+// blocks of sinks, which make enough items anyway.
+constexpr int attn_window_splits(int S, int window, int sinks, int hd) {
+  const int w = window < S ? window : S, k = sinks < S ? sinks : S, qb = hd == 128 ? 64 : 128;
+  const int ns = (k + 127) / 128, nq = (S + qb - 1) / qb;
+  if (ns == 0 || ns > 32) return 0;
+  const int near = (126 + w) / qb + 1;                         // query blocks of key block 0's window
+  const int usual = near > 512 / qb ? near : 512 / qb;         // of an item
+  const int far = nq - near;                                   // behind it
+  const int least = nq - ((ns - 1) * 128 + 126 + w) / qb - 1;  // the last sinks' block's
+  if (far < usual || least < 1) return 0;
+  int f = (far + usual - 1) / usual;
+  f = f < 32 / ns ? f : 32 / ns;
+  return f < least ? f : least;
+}
+// Floats of the sinks' partial dK and dV (fp32 [B, Hkv, sinks' blocks, splits +
+// 1, dK and dV, 128, hd]).
+constexpr int64_t attn_window_part_floats(int B, int S, int Hkv, int hd, int window, int sinks) {
+  const int f = attn_window_splits(S, window, sinks, hd), k = sinks < S ? sinks : S;
+  return f ? (int64_t)B * Hkv * ((k + 127) / 128) * (f + 1) * 256 * hd : 0;
+}
+// dK and dV of the sinks' key blocks from those parts, in a fixed order
+// (attention.cu).  Launched as the dependent of the backward kernel.
+void attn_sink_join(const float* part, __nv_bfloat16* dqkv, int B, int S, int Hq, int Hkv, int hd,
+                    float scale, const float2* cs, int splits, int sinks, cudaStream_t st);
 
 // ---- norms of queries and keys with the rotation (qknorm.cu)
 // Rows of Hq query, Hkv key and Hkv value heads of hd columns (hd % 16 == 0,

@@ -301,6 +301,12 @@ WIN_CASES = [  # B, S, Hq, Hkv, hd, window, sinks
     (1, 900, 2, 2, 128, 320, 300),
     (1, 385, 2, 1, 128, 4000, 0),    # wider than the sequence: plain causal attention
     (1, 260, 2, 1, 64, 40, 900),     # every token is a sink
+    # long enough that the backward splits the queries behind the sinks' window
+    (1, 2100, 2, 1, 128, 100, 4),
+    (1, 2500, 4, 2, 64, 64, 130),
+    (2, 3000, 3, 1, 128, 64, 130),
+    (1, 4000, 2, 1, 64, 1, 1),
+    (2, 2600, 2, 2, 128, 300, 17),
 ]
 
 
