@@ -26,6 +26,7 @@ F32 = 2.0 ** -18
 SC = 2.0 ** -11
 EPS = 1e-5
 D64 = dict(dtype=torch.float64, device="cuda")
+F32T = dict(dtype=torch.float32, device="cuda")  # another test module changes the default type
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -39,7 +40,7 @@ def _lib():
 def gen(seed):
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
-    return lambda *s: torch.randn(*s, generator=g, device="cuda")
+    return lambda *s: torch.randn(*s, generator=g, **F32T)
 
 
 def within(got, ref, tol):
@@ -174,7 +175,7 @@ def test_qknorm_zero_rows_and_tiny_eps():
     for eps in (1e-5, 1e-30):
         y_ref, y_tol, dx_ref, dx_tol, _ = qk_ref(x, gq, gk, dy, Hq, Hkv, hd, pos, tab, eps)
         y, dx = torch.empty_like(x), torch.empty_like(x)
-        sc = torch.empty(sf.qknorm_rope_bwd_scratch(T, Hq, Hkv, hd), device="cuda")
+        sc = torch.empty(sf.qknorm_rope_bwd_scratch(T, Hq, Hkv, hd), **F32T)
         dg = torch.empty(2, hd, dtype=torch.bfloat16, device="cuda")
         a = (T, T, Hq, Hkv, hd, gq.data_ptr(), gk.data_ptr(), eps, tab.data_ptr(), 0)
         assert sf.op_qknorm_rope_fwd(x.data_ptr(), W, y.data_ptr(), W, *a, stream()) == 0
@@ -193,7 +194,7 @@ def test_qknorm_gradient_against_differences():
     tab, pos, n = table(T, hd), torch.arange(T, device="cuda"), (Hq + Hkv) * hd
     _, _, _, tol, (_, dqt, _, dkt) = qk_ref(x, gq, gk, dy, Hq, Hkv, hd, pos, tab)
     dx = torch.empty_like(x)
-    sc = torch.empty(sf.qknorm_rope_bwd_scratch(T, Hq, Hkv, hd), device="cuda")
+    sc = torch.empty(sf.qknorm_rope_bwd_scratch(T, Hq, Hkv, hd), **F32T)
     dg = torch.empty(2, hd, dtype=torch.bfloat16, device="cuda")
     assert sf.op_qknorm_rope_bwd(x.data_ptr(), W, dy.data_ptr(), W, dx.data_ptr(), W, T, T, Hq, Hkv, hd,
                                  gq.data_ptr(), gk.data_ptr(), EPS, tab.data_ptr(), 0, sc.data_ptr(),
@@ -374,7 +375,7 @@ def test_window_wider_than_the_sequence_is_causal_attention(hd, Hq):
     got = win_bwd(qkv, o, dout, lse, B, S, Hq, Hkv, hd, 2 ** 31 - 1, 2 ** 31 - 1, None, 1)
     dqkv = torch.empty_like(qkv)
     delta = torch.empty_like(lse)
-    acc = torch.empty(sf.attn_dq_scratch_floats(B, S, Hq, hd, 1), device="cuda")
+    acc = torch.empty(sf.attn_dq_scratch_floats(B, S, Hq, hd, 1), **F32T)
     assert sf.op_attn_bwd(qkv.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(), delta.data_ptr(),
                           acc.data_ptr(), dqkv.data_ptr(), B, S, Hq, Hkv, hd, 0, stream(), 1) == 0
     sync()
@@ -430,7 +431,7 @@ def ckpt_ref(x, top):
     """Codes (as their values), scales and loaded values by the stated fp32 rule."""
     rows, d = x.shape
     nb = (d + 127) // 128
-    xb = torch.zeros(rows, nb * 128, device="cuda")
+    xb = torch.zeros(rows, nb * 128, **F32T)
     xb[:, :d] = x
     xb = xb.reshape(rows, nb, 128).cpu().numpy()
     a = np.abs(xb).max(-1)
@@ -548,20 +549,20 @@ def test_ckpt8_norm_round_trip(rows, d, name, fmt, top):
 def test_ckpt8_special_blocks(name, fmt, top):
     """Zeros, tiny and huge magnitudes, infinities and NaN, each in its own block."""
     d = 128 * 7 + 8
-    x = torch.zeros(2, d, device="cuda")
+    x = torch.zeros(2, d, **F32T)
     x[0, 128:256] = 1e-38
-    x[0, 256:384] = torch.linspace(-3e38, 3e38, 128, device="cuda")
+    x[0, 256:384] = torch.linspace(-3e38, 3e38, 128, **F32T)
     x[0, 384:512] = 1.0
     x[0, 400] = float("inf")
     x[0, 512:640] = 2.0
     x[0, 600] = float("nan")
     x[0, 640:768] = 2.0 ** -100
     x[0, 768:896] = -2.0 ** -99
-    x[0, 896:] = torch.tensor([1.0, -1.0, 0.5, 1e-9, 0.0, -0.25, 0.9999, 2.0], device="cuda")
-    x[1] = torch.linspace(-1, 1, d, device="cuda")
+    x[0, 896:] = torch.tensor([1.0, -1.0, 0.5, 1e-9, 0.0, -0.25, 0.9999, 2.0], **F32T)
+    x[1] = torch.linspace(-1, 1, d, **F32T)
     c_ref, s_ref, v_ref = ckpt_ref(x, top)
     q = torch.empty(2, d, dtype=torch.uint8, device="cuda")
-    s, v = torch.empty(2, 8, device="cuda"), torch.empty(2, d, device="cuda")
+    s, v = torch.empty(2, 8, **F32T), torch.empty(2, d, **F32T)
     assert sf.op_ckpt8_save(x.data_ptr(), q.data_ptr(), s.data_ptr(), fmt, 2, d, stream()) == 0
     assert sf.op_ckpt8_load(q.data_ptr(), s.data_ptr(), v.data_ptr(), fmt, 2, d, stream()) == 0
     sync()
@@ -578,13 +579,13 @@ def test_ckpt8_special_blocks(name, fmt, top):
 
 @pytest.mark.parametrize("name,fmt,top", FMTS)
 def test_ckpt8_huge_magnitudes(name, fmt, top):
-    x = torch.empty(1, 256, device="cuda")
-    x[0, :128] = torch.linspace(-1.5e38, 1.5e38, 128, device="cuda") * 2
+    x = torch.empty(1, 256, **F32T)
+    x[0, :128] = torch.linspace(-1.5e38, 1.5e38, 128, **F32T) * 2
     x[0, 128:] = 3.4028234663852886e38
     x[0, 130] = -3.4028234663852886e38
     c_ref, s_ref, v_ref = ckpt_ref(x, top)
     q = torch.empty(1, 256, dtype=torch.uint8, device="cuda")
-    s, v = torch.empty(1, 2, device="cuda"), torch.empty(1, 256, device="cuda")
+    s, v = torch.empty(1, 2, **F32T), torch.empty(1, 256, **F32T)
     assert sf.op_ckpt8_save(x.data_ptr(), q.data_ptr(), s.data_ptr(), fmt, 1, 256, stream()) == 0
     assert sf.op_ckpt8_load(q.data_ptr(), s.data_ptr(), v.data_ptr(), fmt, 1, 256, stream()) == 0
     sync()
@@ -602,12 +603,12 @@ def test_ckpt8_backward_against_differences():
     q = torch.empty(rows, d, dtype=torch.uint8, device="cuda")
     sc = torch.empty_like(s)
     assert sf.op_ckpt8_save(x.data_ptr(), q.data_ptr(), sc.data_ptr(), 0, rows, d, stream()) == 0
-    y, r = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda"), torch.empty(rows, device="cuda")
+    y, r = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda"), torch.empty(rows, **F32T)
     assert sf.op_rmsnorm_fwd_load8(q.data_ptr(), sc.data_ptr(), g.data_ptr(), y.data_ptr(), r.data_ptr(), 0, 0,
                                    rows, d, EPS, stream()) == 0
-    dx, dxb = torch.empty(rows, d, device="cuda"), torch.empty(rows, d, dtype=torch.bfloat16, device="cuda")
+    dx, dxb = torch.empty(rows, d, **F32T), torch.empty(rows, d, dtype=torch.bfloat16, device="cuda")
     dg = torch.empty(d, dtype=torch.bfloat16, device="cuda")
-    part = torch.empty(sf.rmsnorm_bwd_scratch(rows, d), device="cuda")
+    part = torch.empty(sf.rmsnorm_bwd_scratch(rows, d), **F32T)
     assert sf.op_rmsnorm_bwd_load8(q.data_ptr(), sc.data_ptr(), g.data_ptr(), r.data_ptr(), dy.data_ptr(), 0,
                                    dx.data_ptr(), dxb.data_ptr(), dg.data_ptr(), part.data_ptr(), 0, rows, d,
                                    stream()) == 0
