@@ -89,7 +89,13 @@ typedef struct sf_ctx sf_ctx;
  *     stays in device memory; 1 = sliding activations: after a layer's
  *     forward its checkpoint is copied to pinned host memory and brought back
  *     just before that layer's backward, the device keeping a window of four
- *     (results are identical).
+ *     (results are identical); 2 = sliding activations in 8 bits: every layer
+ *     but the last three keeps its input as int8 codes with a scale for each
+ *     128 values (SF_CKPT_INT8 below; saved by the layer's first norm), and
+ *     those copies slide, a little over a quarter of the bytes, the device
+ *     keeping the last four.  The forward is exact; the recompute and the
+ *     backward of those layers run at the checkpoint's values (off by at most
+ *     1/254 of the largest of 128), so their gradients differ slightly.
  *   deterministic: 0 = the attention backward adds the dQ contributions of
  *     its key blocks into one fp32 buffer in whatever order they arrive, so
  *     the last bits of a gradient can differ between two identical steps;

@@ -202,6 +202,14 @@ struct sf_ctx {
   float* X = nullptr;       // checkpoints of the residual stream: L+1 slots, or 4 when they slide
   bool xoff = false;        // sliding activations: checkpoints live in pinned host memory
   float* x_pin = nullptr;   // [L][Tmax * d] host copies of the checkpoints
+  // 8-bit checkpoints (offload_activations 2): layers up to L - 4 keep their
+  // input as int8 codes and scales, in a window of four device buffers; those
+  // up to L - 8 slide to the host.  X is then the fp32 window of the forward,
+  // and holds a layer's loaded values during its backward.
+  bool x8 = false;
+  uint8_t* X8 = nullptr;      // [4][x8_cap]
+  uint8_t* x8_pin = nullptr;  // [L - 7][x8_cap]
+  int64_t x8_cap = 0;         // bytes of a checkpoint of Tmax tokens
   cudaEvent_t ev_xused[4] = {}, ev_xfree[4] = {}, ev_xready[4] = {};
   bf16 *u = nullptr, *qkv = nullptr, *o = nullptr, *w2 = nullptr, *mb = nullptr;
   float* ab32 = nullptr;  // gate and up outputs [T, 2F] fp32, kept for the SwiGLU backward
@@ -990,6 +998,18 @@ float* xck(sf_ctx* c, int l, int64_t T) {
   return c->X + (int64_t)l * T * c->d;
 }
 
+// The 8-bit checkpoint of T tokens at `base`: the codes, then the scales.
+struct Ck8 {
+  uint8_t* q = nullptr;
+  float* s = nullptr;
+};
+int64_t ck8_codes(int64_t T, int64_t d) { return round_up(T * d, 256); }
+int64_t ck8_bytes(int64_t T, int64_t d) { return ck8_codes(T, d) + T * ((d + 127) / 128) * 4; }
+Ck8 ck8(sf_ctx* c, int l, int64_t T) {
+  uint8_t* base = c->X8 + (int64_t)(l % 4) * c->x8_cap;
+  return {base, reinterpret_cast<float*>(base + ck8_codes(T, c->d))};
+}
+
 // ------------------------------------------------------------------ layer compute
 struct LayerW {
   const bf16 *g1, *wqkv, *bqkv, *wo, *g2, *wgu, *wd;  // bqkv null without projection biases
@@ -1009,24 +1029,33 @@ LayerG slot_g(sf_ctx* c, int s) {
 }
 
 // A gain gradient from the per-block partials: bf16, or fp16 times the loss scale.
-void grad_parts(sf_ctx* c, int d, bf16* out) {
+void grad_parts(sf_ctx* c, int d, bf16* out, int parts) {
   if (c->f16g)
-    sf::reduce_parts_f16(c->dg_part, c->dg_parts, d, reinterpret_cast<uint16_t*>(out), c->lscale, c->sC);
+    sf::reduce_parts_f16(c->dg_part, parts, d, reinterpret_cast<uint16_t*>(out), c->lscale, c->sC);
   else
-    sf::reduce_parts_bf16(c->dg_part, c->dg_parts, d, out, c->sC);
+    sf::reduce_parts_bf16(c->dg_part, parts, d, out, c->sC);
 }
+void grad_parts(sf_ctx* c, int d, bf16* out) { grad_parts(c, d, out, c->dg_parts); }
 
 // Forward of one layer from X_l (fp32) to X_{l+1}; with `full == false` the
 // final down projection is skipped (recompute for the backward needs only the
 // intermediates).  keep_ab stores the gate and up outputs in fp32 for the
 // SwiGLU backward (the recompute, and the last layer, whose backward follows
-// the head without a recompute).
-int layer_forward(sf_ctx* c, const LayerW& w, const float* Xin, float* Xout, int B, int S,
-                  bool full, bool keep_ab) {
+// the head without a recompute).  save8: the norm also saves X_l as an 8-bit
+// checkpoint; load8: X_l is loaded from one (and written to Xin).
+int layer_forward(sf_ctx* c, const LayerW& w, float* Xin, float* Xout, int B, int S,
+                  bool full, bool keep_ab, const Ck8* save8 = nullptr, const Ck8* load8 = nullptr) {
   sf_ctx* ctx = c;
   const int64_t T = (int64_t)B * S, d = c->d, F = c->F;
   const int Hq = c->cfg.n_heads, Hkv = c->cfg.n_kv_heads, hd = c->cfg.head_dim;
-  sf::rmsnorm_fwd(Xin, w.g1, c->u, c->rstd1, T, (int)d, c->cfg.rms_eps, c->sC);
+  if (load8)
+    sf::rmsnorm_fwd_load8(load8->q, load8->s, w.g1, c->u, c->rstd1, Xin, SF_CKPT_INT8, T, (int)d,
+                          c->cfg.rms_eps, c->sC);
+  else if (save8)
+    sf::rmsnorm_fwd_save8(Xin, w.g1, c->u, c->rstd1, save8->q, save8->s, SF_CKPT_INT8, T, (int)d,
+                          c->cfg.rms_eps, c->sC);
+  else
+    sf::rmsnorm_fwd(Xin, w.g1, c->u, c->rstd1, T, (int)d, c->cfg.rms_eps, c->sC);
   {
     // Q/K/V projection; its epilogue adds the biases (if any) to the fp32
     // accumulator, rotates the Q and K heads and rounds to bf16 once
@@ -1063,7 +1092,9 @@ int layer_forward(sf_ctx* c, const LayerW& w, const float* Xin, float* Xout, int
 
 // Backward of one layer.  On entry dX / dXb hold dLoss/dX_{l+1}; on exit they
 // hold dLoss/dX_l.  Weight gradients go into the slot's gradient area (bf16).
-int layer_backward(sf_ctx* c, const LayerW& w, const LayerG& g, const float* Xin, int B, int S) {
+// load8: X_l's 8-bit checkpoint, when the layer was recomputed from it.
+int layer_backward(sf_ctx* c, const LayerW& w, const LayerG& g, const float* Xin, int B, int S,
+                   const Ck8* load8) {
   sf_ctx* ctx = c;
   const int64_t T = (int64_t)B * S, d = c->d, F = c->F;
   const int Hq = c->cfg.n_heads, Hkv = c->cfg.n_kv_heads, hd = c->cfg.head_dim;
@@ -1103,9 +1134,19 @@ int layer_backward(sf_ctx* c, const LayerW& w, const LayerG& g, const float* Xin
   RET(gemm(c, sf::kNN, sf::kEpiF32, T, d, c->qkvdim, c->dqkv, c->qkvdim, w.wqkv, d, c->du, d));
   RET(gemm(c, sf::kTN, c->gepi(), c->qkvdim, d, T, c->dqkv, c->qkvdim, c->u, d, g.wqkv, d, nullptr,
            0, c->gscale()));
-  sf::rmsnorm_bwd(Xin, w.g1, c->rstd1, c->du, c->dh, c->dX, c->dXb, c->dg_part, c->dg_parts, T,
-                  (int)d, c->sC);
-  grad_parts(c, (int)d, g.g1);
+  if (load8) {
+    const int parts = sf::rmsnorm_bwd_load8_parts(T, (int)d);
+    if (!sf::rmsnorm_bwd_load8(load8->q, load8->s, w.g1, c->rstd1, c->du, c->dh, c->dX, c->dXb,
+                               c->dg_part, parts, SF_CKPT_INT8, T, (int)d, c->sC)) {
+      ctx->set_err("RMSNorm backward launch failed");
+      return SF_ECUDA;
+    }
+    grad_parts(c, (int)d, g.g1, parts);
+  } else {
+    sf::rmsnorm_bwd(Xin, w.g1, c->rstd1, c->du, c->dh, c->dX, c->dXb, c->dg_part, c->dg_parts, T,
+                    (int)d, c->sC);
+    grad_parts(c, (int)d, g.g1);
+  }
   c->launches += 7;  // 2 norm, 2 reduce, 3 attention (GEMMs are counted in gemm())
   return SF_OK;
 }
@@ -1265,7 +1306,10 @@ int init(sf_ctx* ctx) {
   ctx->ring.resize(ctx->R);
   for (int s = 0; s < ctx->R && ok; ++s) ok = dalloc(ctx, &ctx->ring[s], 2 * ctx->pack_elems);
   ctx->xoff = cf.offload_activations != 0;
+  ctx->x8 = cf.offload_activations == 2;
+  ctx->x8_cap = round_up(ck8_bytes(T, d), 256);
   ok = ok && dalloc(ctx, &ctx->X, (ctx->xoff ? 4 : L + 1) * T * d);
+  if (ctx->x8) ok = ok && dalloc(ctx, &ctx->X8, 4 * ctx->x8_cap);
   ok = ok && dalloc(ctx, &ctx->u, T * d) && dalloc(ctx, &ctx->qkv, T * ctx->qkvdim) &&
        dalloc(ctx, &ctx->o, T * ctx->qdim) && dalloc(ctx, &ctx->w2, T * d) &&
        dalloc(ctx, &ctx->ab32, T * 2 * F) && dalloc(ctx, &ctx->mb, T * F) &&
@@ -1329,7 +1373,8 @@ int init(sf_ctx* ctx) {
   ok = ok && new_floats(ctx, ctx->E, V * d) && new_floats(ctx, ctx->dE, V * d) &&
        (ctx->cstate ? new_halves(ctx, ctx->Em16, V * d) && new_halves(ctx, ctx->Ev16, V * d)
                     : new_floats(ctx, ctx->Em, V * d) && new_floats(ctx, ctx->Ev, V * d));
-  if (ok && ctx->xoff) ok = halloc(ctx, &ctx->x_pin, L * T * d);
+  if (ok && ctx->xoff && !ctx->x8) ok = halloc(ctx, &ctx->x_pin, L * T * d);
+  if (ok && ctx->x8 && L > 7) ok = halloc(ctx, &ctx->x8_pin, (L - 7) * ctx->x8_cap);
   ok = ok && halloc(ctx, &ctx->x0_pin, T * d) && halloc(ctx, &ctx->lab_pin, T) &&
        halloc(ctx, &ctx->loss_pin, 1) && halloc(ctx, &ctx->err_pin, 1);
   if (!ok) return SF_ENOMEM;
@@ -1525,16 +1570,30 @@ int step(sf_ctx* ctx, const int32_t* tokens, const int32_t* labels, int B, int S
       h2d += (double)V * d * 2 + (double)ctx->fn.elems * 2;
     }
     CK(cudaStreamWaitEvent(ctx->sC, ctx->ev_loaded[s], 0));
-    const float* Xin = xck(ctx, l, T);
+    float* Xin = xck(ctx, l, T);
     float* Xout = xck(ctx, l + 1, T);
     // sliding: X_{l+1}'s slot held X_{l-3}, whose copy to the host must be done
-    if (ctx->xoff && l + 1 >= 4) CK(cudaStreamWaitEvent(ctx->sC, ctx->ev_xfree[(l + 1) % 4], 0));
+    if (ctx->xoff && !ctx->x8 && l + 1 >= 4)
+      CK(cudaStreamWaitEvent(ctx->sC, ctx->ev_xfree[(l + 1) % 4], 0));
+    const bool save8 = ctx->x8 && l <= L - 4;
+    const Ck8 c8 = save8 ? ck8(ctx, l, T) : Ck8{};
+    // and the 8-bit buffer held X_{l-4}
+    if (save8 && l >= 4) CK(cudaStreamWaitEvent(ctx->sC, ctx->ev_xfree[l % 4], 0));
     {
       Timed tl(ctx, 2, 0.0);
-      RET(layer_forward(ctx, slot_w(ctx, s), Xin, Xout, B, S, true, l == L - 1));
+      RET(layer_forward(ctx, slot_w(ctx, s), Xin, Xout, B, S, true, l == L - 1, save8 ? &c8 : nullptr));
     }
     CK(cudaEventRecord(ctx->ev_free[s], ctx->sC));
-    if (ctx->xoff) {  // the checkpoint slides to the host while the next layers compute
+    if (ctx->x8) {
+      CK(cudaEventRecord(ctx->ev_xused[l % 4], ctx->sC));
+      if (l <= L - 8) {  // the last four saved ones stay
+        CK(cudaStreamWaitEvent(ctx->sD, ctx->ev_xused[l % 4], 0));
+        CK(cudaMemcpyAsync(ctx->x8_pin + (int64_t)l * ctx->x8_cap, c8.q, (size_t)ck8_bytes(T, d),
+                           cudaMemcpyDeviceToHost, ctx->sD));
+        CK(cudaEventRecord(ctx->ev_xfree[l % 4], ctx->sD));
+        d2h += (double)ck8_bytes(T, d);
+      }
+    } else if (ctx->xoff) {  // the checkpoint slides to the host while the next layers compute
       CK(cudaEventRecord(ctx->ev_xused[l % 4], ctx->sC));
       CK(cudaStreamWaitEvent(ctx->sD, ctx->ev_xused[l % 4], 0));
       CK(cudaMemcpyAsync(ctx->x_pin + (int64_t)l * T * d, Xin, (size_t)T * d * 4,
@@ -1556,13 +1615,20 @@ int step(sf_ctx* ctx, const int32_t* tokens, const int32_t* labels, int B, int S
   auto h2d_ck = [&](int l, cudaEvent_t after) -> int {
     CK(cudaStreamWaitEvent(ctx->sU, after, 0));
     CK(cudaStreamWaitEvent(ctx->sU, ctx->ev_xfree[l % 4], 0));
+    if (ctx->x8) {
+      CK(cudaMemcpyAsync(ck8(ctx, l, T).q, ctx->x8_pin + (int64_t)l * ctx->x8_cap,
+                         (size_t)ck8_bytes(T, d), cudaMemcpyHostToDevice, ctx->sU));
+      CK(cudaEventRecord(ctx->ev_xready[l % 4], ctx->sU));
+      h2d += (double)ck8_bytes(T, d);
+      return SF_OK;
+    }
     CK(cudaMemcpyAsync(xck(ctx, l, T), ctx->x_pin + (int64_t)l * T * d, (size_t)T * d * 4,
                        cudaMemcpyHostToDevice, ctx->sU));
     CK(cudaEventRecord(ctx->ev_xready[l % 4], ctx->sU));
     h2d += (double)T * d * 4;
     return SF_OK;
   };
-  if (ctx->xoff && L - 4 >= 0) RET(h2d_ck(L - 4, ctx->ev_head));
+  if (ctx->xoff && !ctx->x8 && L - 4 >= 0) RET(h2d_ck(L - 4, ctx->ev_head));
   CK(cudaStreamWaitEvent(ctx->sD, ctx->ev_head, 0));
   CK(cudaMemcpyAsync(ctx->lm.pack, ctx->dWlm16, (size_t)V * d * 2, cudaMemcpyDeviceToHost, ctx->sD));
   CK(cudaMemcpyAsync(ctx->fn.pack, ctx->dgf, (size_t)ctx->fn.elems * 2, cudaMemcpyDeviceToHost, ctx->sD));
@@ -1576,18 +1642,21 @@ int step(sf_ctx* ctx, const int32_t* tokens, const int32_t* labels, int B, int S
     const bool resident = l >= L - R;  // still in its slot from the forward
     if (!resident) CK(cudaStreamWaitEvent(ctx->sC, ctx->ev_loaded[s], 0));
     const LayerW w = slot_w(ctx, s);
-    const float* Xin = xck(ctx, l, T);
-    if (ctx->xoff && l <= L - 4) CK(cudaStreamWaitEvent(ctx->sC, ctx->ev_xready[l % 4], 0));
+    float* Xin = xck(ctx, l, T);
+    if (ctx->xoff && l <= L - (ctx->x8 ? 8 : 4)) CK(cudaStreamWaitEvent(ctx->sC, ctx->ev_xready[l % 4], 0));
+    const bool load8 = ctx->x8 && l <= L - 4;
+    const Ck8 c8 = load8 ? ck8(ctx, l, T) : Ck8{};
     // the last layer's intermediates are still in the workspace from the forward
     {
       Timed tl(ctx, 3, 0.0);
-      if (l != L - 1) RET(layer_forward(ctx, w, Xin, nullptr, B, S, false, true));
-      RET(layer_backward(ctx, w, slot_g(ctx, s), Xin, B, S));
+      if (l != L - 1)
+        RET(layer_forward(ctx, w, Xin, nullptr, B, S, false, true, nullptr, load8 ? &c8 : nullptr));
+      RET(layer_backward(ctx, w, slot_g(ctx, s), Xin, B, S, load8 ? &c8 : nullptr));
     }
     CK(cudaEventRecord(ctx->ev_grads[s], ctx->sC));
     if (ctx->xoff) {
       CK(cudaEventRecord(ctx->ev_xused[l % 4], ctx->sC));
-      if (l - 4 >= 0) RET(h2d_ck(l - 4, ctx->ev_xused[l % 4]));
+      if (l - 4 >= 0 && (!ctx->x8 || load8)) RET(h2d_ck(l - 4, ctx->ev_xused[l % 4]));
     }
     CK(cudaStreamWaitEvent(ctx->sD, ctx->ev_grads[s], 0));
     {

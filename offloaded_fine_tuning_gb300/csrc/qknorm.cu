@@ -29,8 +29,9 @@ typedef __nv_bfloat16 bf16;
 
 constexpr int kQkThreads = 128;
 constexpr int kQkWarps = kQkThreads / 32;
-constexpr int kQkCtas = 4;       // resident CTAs an SM is given
-constexpr int kQkFwdStages = 8;  // steps a lane has in flight, forward (x)
+constexpr int kQkFwdCtas = 5;    // resident CTAs an SM is given, forward
+constexpr int kQkBwdCtas = 4;    // and backward
+constexpr int kQkFwdStages = 5;  // steps a lane has in flight, forward (x)
 constexpr int kQkBwdStages = 5;  // and backward (x and dy)
 
 __device__ __forceinline__ void unpack(const uint4& u, float* f) {
@@ -194,7 +195,7 @@ __device__ __forceinline__ Steps steps_of(const QkNormArgs& a, bool q, bool k, b
 
 // Persistent CTAs; the value heads are copied unless the call is in place.
 template <int TPH>
-__global__ void __launch_bounds__(kQkThreads, kQkCtas)
+__global__ void __launch_bounds__(kQkThreads, kQkFwdCtas)
     qknorm_fwd_kernel(const QkNormArgs a, const bf16* x, int64_t ldx, bf16* y, int64_t ldy, int* err) {
   __shared__ __align__(16) uint8_t buf[2 * kQkFwdStages * kQkThreads * 16];
   const uint32_t ring = smem_u32(buf) + threadIdx.x * 16;
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas)
 // set of sums is in registers at a time), then the value heads are copied.
 // Every CTA writes the sums of its heads to its row of part [gridDim, 2 hd].
 template <int TPH>
-__global__ void __launch_bounds__(kQkThreads, kQkCtas)
+__global__ void __launch_bounds__(kQkThreads, kQkBwdCtas)
     qknorm_bwd_kernel(const QkNormArgs a, const bf16* __restrict__ x, int64_t ldx, const bf16* dy,
                       int64_t lddy, bf16* dx, int64_t lddx, float* __restrict__ part, int* err) {
   __shared__ __align__(16) uint8_t buf[4 * kQkBwdStages * kQkThreads * 16];
@@ -344,10 +345,10 @@ int lanes_per_head(int hd) {
 }
 
 // CTAs for n steps (each a group of 32 / TPH heads of a token): as many as the
-// steps fill, at most what the SMs hold at once.
-int qk_ctas(int64_t n) {
+// steps fill, at most per_sm for each SM.
+int qk_ctas(int64_t n, int per_sm) {
   const int64_t need = (n + kQkWarps - 1) / kQkWarps;
-  const int most = kQkCtas * num_sms();
+  const int most = per_sm * num_sms();
   return need < most ? (int)(need > 0 ? need : 1) : most;
 }
 
@@ -358,11 +359,12 @@ int64_t head_steps(int heads, int hd) {
 
 }  // namespace
 
-int qknorm_parts(int64_t tokens, int Hq, int hd) { return qk_ctas(tokens * head_steps(Hq, hd)); }
+int qknorm_parts(int64_t tokens, int Hq, int hd) { return qk_ctas(tokens * head_steps(Hq, hd), kQkBwdCtas); }
 
 void qknorm_rope_fwd(const QkNormArgs& a, const bf16* x, int64_t ldx, bf16* y, int64_t ldy,
                      int* err, cudaStream_t st) {
-  const int grid = qk_ctas(a.tokens * (head_steps(a.Hq, a.hd) + (x == y ? 1 : 2) * head_steps(a.Hkv, a.hd)));
+  const int grid = qk_ctas(a.tokens * (head_steps(a.Hq, a.hd) + (x == y ? 1 : 2) * head_steps(a.Hkv, a.hd)),
+                           kQkFwdCtas);
 #define SF_QK_FWD(T) qknorm_fwd_kernel<T><<<grid, kQkThreads, 0, st>>>(a, x, ldx, y, ldy, err)
   switch (lanes_per_head(a.hd)) {
     case 1: SF_QK_FWD(1); break;
