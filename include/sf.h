@@ -421,7 +421,7 @@ int sf_op_attn_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
  * query q sees key k when k <= q and (q - k < window or k < sinks): its own
  * and the window - 1 keys before it, and the first `sinks` tokens of its
  * sequence.  window >= 1 (window >= S: plain causal attention), sinks >= 0;
- * both may exceed S.  Key blocks that no query of a tile sees are not read; in
+ * both may exceed S.  B and Hkv at most 65535, S at most 2^30.  Key blocks that no query of a tile sees are not read; in
  * the blocks that are read, a value row has to be finite even where it is
  * masked (its weight is 0, and 0 * inf is NaN). */
 int sf_op_attn_window_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int32_t B, int32_t S,

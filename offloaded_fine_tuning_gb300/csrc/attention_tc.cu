@@ -1883,7 +1883,9 @@ bool launch_dependent(void (*kern)(P...), dim3 grid, int threads, int smem, cuda
   cfg.stream = st;
   cfg.attrs = after;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess;
+  if (cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn_att() {

@@ -185,11 +185,18 @@ int sf_op_attn_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
   return SF_OK;
 }
 
+// Sizes of the windowed attention; its backward's grid bounds B and Hkv.
+static bool window_sizes(int32_t B, int32_t S_, int32_t Hq, int32_t Hkv, int32_t hd, int32_t window,
+                         int32_t sinks) {
+  return B >= 0 && B <= 65535 && S_ >= 0 && S_ <= (1 << 30) && Hq >= 1 && Hkv >= 1 && Hkv <= 65535 &&
+         Hq % Hkv == 0 && (int64_t)Hq + 2 * (int64_t)Hkv <= (1 << 22) && (hd == 64 || hd == 128) &&
+         window >= 1 && sinks >= 0;
+}
+
 int sf_op_attn_window_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int32_t B, int32_t S_,
                           int32_t Hq, int32_t Hkv, int32_t hd, int32_t window, int32_t sinks,
                           void* stream) {
-  if (B < 0 || S_ < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (hd != 64 && hd != 128)) return SF_EINVAL;
-  if (window < 1 || sinks < 0) return SF_EINVAL;
+  if (!window_sizes(B, S_, Hq, Hkv, hd, window, sinks)) return SF_EINVAL;
   if (B == 0 || S_ == 0) return SF_OK;
   if (!qkv || !o || !lse || !al16(qkv) || !al16(o)) return SF_EINVAL;
   int* err = dev_err_word();
@@ -202,7 +209,7 @@ int sf_op_attn_window_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int32_t 
 
 int64_t sf_op_attn_window_dq_scratch(int32_t B, int32_t S_, int32_t Hq, int32_t hd, int32_t window,
                                      int32_t sinks, int32_t deterministic) {
-  if (B < 0 || S_ < 0 || Hq < 1 || (hd != 64 && hd != 128) || window < 1 || sinks < 0) return -1;
+  if (!window_sizes(B, S_, Hq, 1, hd, window, sinks)) return -1;
   const int64_t slots = deterministic ? sf::attn_window_dq_slots(S_, window, sinks) : 1;
   return slots * B * S_ * Hq * hd + sf::attn_window_part_floats(B, S_, Hq, hd, window, sinks);
 }
@@ -212,8 +219,7 @@ int sf_op_attn_window_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t
                           int32_t B, int32_t S_, int32_t Hq, int32_t Hkv, int32_t hd,
                           int32_t window, int32_t sinks, const float* table,
                           int32_t deterministic, void* stream) {
-  if (B < 0 || S_ < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (hd != 64 && hd != 128)) return SF_EINVAL;
-  if (window < 1 || sinks < 0) return SF_EINVAL;
+  if (!window_sizes(B, S_, Hq, Hkv, hd, window, sinks)) return SF_EINVAL;
   if (B == 0 || S_ == 0) return SF_OK;
   if (!qkv || !o || !dout || !lse || !delta || !dq_acc || !dqkv) return SF_EINVAL;
   if (!al16(qkv) || !al16(o) || !al16(dout) || !al16(dq_acc) || !al16(dqkv)) return SF_EINVAL;

@@ -52,7 +52,8 @@ def test_qknorm_scratch_sizes(sf):
 
 @pytest.mark.parametrize("bad", [
     dict(qkv=0), dict(o=0), dict(lse=0), dict(qkv=A + 8), dict(B=-1), dict(S=-1), dict(Hq=0), dict(Hkv=0),
-    dict(Hkv=3), dict(hd=96), dict(window=0), dict(window=-5), dict(sinks=-1)])
+    dict(Hkv=3), dict(hd=96), dict(window=0), dict(window=-5), dict(sinks=-1), dict(B=65536), dict(S=2 ** 30 + 1),
+    dict(Hq=65536, Hkv=65536), dict(Hq=2 ** 22, Hkv=1)])
 def test_window_forward_refuses(sf, bad):
     a = dict(qkv=A, o=A, lse=A, B=1, S=16, Hq=4, Hkv=2, hd=64, window=8, sinks=1)
     a.update(bad)
@@ -62,7 +63,7 @@ def test_window_forward_refuses(sf, bad):
 @pytest.mark.parametrize("bad", [
     dict(qkv=0), dict(o=0), dict(dout=0), dict(lse=0), dict(delta=0), dict(dq_acc=0), dict(dqkv=0),
     dict(dq_acc=A + 4), dict(dqkv=A + 8), dict(dout=A + 8), dict(table=A + 4), dict(Hkv=3), dict(hd=32),
-    dict(window=0), dict(sinks=-1)])
+    dict(window=0), dict(sinks=-1), dict(B=65536), dict(S=2 ** 31 - 1)])
 def test_window_backward_refuses(sf, bad):
     a = dict(qkv=A, o=A, dout=A, lse=A, delta=A, dq_acc=A, dqkv=A, B=1, S=16, Hq=4, Hkv=2, hd=64, window=8, sinks=1)
     a.update(bad)
@@ -100,7 +101,8 @@ def test_window_scratch_holds_every_visited_block(sf, S, window, sinks):
         ns, most = blocks_seen(S, window, sinks, qb)
         assert n % per == 0 and ns + max(0, most) <= n // per <= (S + 127) // 128
     for bad in ((-1, S, Hq, 64, 1, 0, 1), (B, -1, Hq, 64, 1, 0, 1), (B, S, 0, 64, 1, 0, 1), (B, S, Hq, 96, 1, 0, 1),
-                (B, S, Hq, 64, 0, 0, 1), (B, S, Hq, 64, 1, -1, 1)):
+                (B, S, Hq, 64, 0, 0, 1), (B, S, Hq, 64, 1, -1, 1), (65536, S, Hq, 64, 1, 0, 1),
+                (B, 2 ** 31 - 1, Hq, 64, 1, 0, 1)):
         assert sf.attn_window_dq_scratch_floats(*bad) == -1
 
 

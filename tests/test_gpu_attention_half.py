@@ -709,3 +709,129 @@ def test_attention_half_of_a_layer_with_a_checkpoint():
     assert rel(o, ref) <= 5 * BF
     for got, want in zip((dx, dgq, dgk, dg1), (grads[0], grads[2], grads[3], grads[1])):
         assert rel(got, want) <= 10 * BF
+
+
+def test_calls_on_two_streams_at_once():
+    """Two training-like chains with their own buffers on two streams, launched
+    without waiting: the same bits as one after the other."""
+    def chain(seed):
+        B, S, Hq, Hkv, hd, W, n, T, d = 1, 1100, 8, 2, 128, 200, 4, 1100, 1024
+        rnd = gen(seed)
+        qkv, dout = win_inputs(B, S, Hq, Hkv, hd, seed=seed)
+        x, gq, gk, dy, Wd = qk_inputs(T, Hq, Hkv, hd, seed=seed)
+        h, g, dyn = rnd(T, d), (1 + 0.1 * rnd(d)).bfloat16(), rnd(T, d)
+        tab = table(S, hd)
+        E = lambda dt, *s: torch.empty(*s, dtype=dt, device="cuda")
+        o, lse, dqkv = E(torch.bfloat16, T, Hq * hd), E(torch.float32, B, Hq, S), torch.empty_like(qkv)
+        delta = torch.empty_like(lse)
+        acc = E(torch.float32, sf.attn_window_dq_scratch_floats(B, S, Hq, hd, W, n, 1))
+        y, dx, sq = torch.empty_like(x), torch.empty_like(x), E(torch.float32, sf.qknorm_rope_bwd_scratch(T, Hq, Hkv, hd))
+        dgq, dgk = E(torch.bfloat16, hd), E(torch.bfloat16, hd)
+        q8, s8, yn, r = E(torch.uint8, T, d), E(torch.float32, T, d // 128), E(torch.bfloat16, T, d), E(torch.float32, T)
+        dh, dhb, dg, part = E(torch.float32, T, d), E(torch.bfloat16, T, d), E(torch.bfloat16, d), \
+            E(torch.float32, sf.rmsnorm_bwd_scratch(T, d))
+        p = lambda t: t.data_ptr()
+        keep = (qkv, dout, x, gq, gk, dy, h, g, dyn, tab, delta, acc, sq, part)
+
+        def run(st):
+            shape, qk = (B, S, Hq, Hkv, hd, W, n), (T, S, Hq, Hkv, hd, p(gq), p(gk), EPS, p(tab), 0)
+            for _ in range(3):
+                rc = [sf.op_attn_window_fwd(p(qkv), p(o), p(lse), *shape, st),
+                      sf.op_attn_window_bwd(p(qkv), p(o), p(dout), p(lse), p(delta), p(acc), p(dqkv), *shape, 0, st, 1),
+                      sf.op_qknorm_rope_fwd(p(x), Wd, p(y), Wd, *qk, st),
+                      sf.op_qknorm_rope_bwd(p(x), Wd, p(dy), Wd, p(dx), Wd, *qk, p(sq), p(dgq), p(dgk), st),
+                      sf.op_rmsnorm_fwd_save8(p(h), p(g), p(yn), p(r), p(q8), p(s8), 1, T, d, EPS, st),
+                      sf.op_rmsnorm_bwd_load8(p(q8), p(s8), p(g), p(r), p(dyn), 0, p(dh), p(dhb), p(dg), p(part), 1,
+                                              T, d, st)]
+                assert rc == [0] * 6, rc
+        return run, (o, lse, dqkv, y, dx, dgq, dgk, q8, s8, yn, dh, dg), keep
+
+    a, b = chain(31), chain(32)
+    for c in (a, b):
+        c[0](stream())
+        sync()
+    want = [[t.clone() for t in c[1]] for c in (a, b)]
+    for c in (a, b):
+        for t in c[1]:
+            t.zero_()
+    sync()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    a[0](s1.cuda_stream)
+    b[0](s2.cuda_stream)
+    sync()
+    for c, w in zip((a, b), want):
+        for got, ref in zip(c[1], w):
+            assert torch.equal(got, ref)
+
+
+# ------------------------------------------------------------------ offsets beyond 2^31 elements
+def test_qknorm_beyond_32_bit_offsets():
+    T, Hq, Hkv, hd = 360001, 32, 8, 128
+    W, tail = (Hq + 2 * Hkv) * hd, 5
+    assert T * W > 2 ** 31
+    small, gq, gk, dy_s, _ = qk_inputs(tail, Hq, Hkv, hd, seed=41)
+    tab = table(64, hd)
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    pos[-tail:] = torch.arange(7, 7 + tail, dtype=torch.int32, device="cuda")
+    x = torch.zeros(T, W, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros_like(x)
+    x[-tail:], dy[-tail:] = small, dy_s
+    p = lambda t: t.data_ptr()
+    outs = []
+    for xx, dd, pp, n in ((x, dy, pos, T), (small, dy_s, pos[-tail:].contiguous(), tail)):
+        sc = torch.empty(sf.qknorm_rope_bwd_scratch(n, Hq, Hkv, hd), **F32T)
+        dg = torch.empty(2, hd, dtype=torch.bfloat16, device="cuda")
+        y, dx = torch.empty_like(xx), torch.empty_like(xx)
+        qk = (n, 64, Hq, Hkv, hd, p(gq), p(gk), EPS, p(tab), p(pp))
+        assert sf.op_qknorm_rope_fwd(p(xx), W, p(y), W, *qk, stream()) == 0
+        assert sf.op_qknorm_rope_bwd(p(xx), W, p(dd), W, p(dx), W, *qk, p(sc), p(dg[0]), p(dg[1]), stream()) == 0
+        sync()
+        outs.append((y[-tail:].clone(), dx[-tail:].clone()))
+        assert n == tail or not (y[:-tail].any() or dx[:-tail].any())
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_window_beyond_32_bit_offsets():
+    B, S, Hq, Hkv, hd, W, n = 11, 2 ** 20 + 40, 1, 1, 64, 70, 2
+    assert B * S * 3 * hd > 2 ** 31
+    qkv, dout = win_inputs(B, S, Hq, Hkv, hd, seed=42)
+    o, lse = win_fwd(qkv, B, S, Hq, Hkv, hd, W, n)
+    got = win_bwd(qkv, o, dout, lse, B, S, Hq, Hkv, hd, W, n, None, 1)
+    last = slice((B - 1) * S, B * S)
+    o1, lse1 = win_fwd(qkv[last], 1, S, Hq, Hkv, hd, W, n)
+    assert torch.equal(o[last], o1) and torch.equal(lse[-1:], lse1)
+    one = win_bwd(qkv[last], o1, dout[last].contiguous(), lse1, 1, S, Hq, Hkv, hd, W, n, None, 1)
+    assert torch.equal(got[last], one)
+    # and its first 600 tokens against the definition
+    c = 600
+    ref, tol, _ = attn_ref(qkv[last][:c], 1, c, Hq, Hkv, hd, W, n)
+    within(o1[:c], ref, tol)
+
+
+def test_ckpt8_beyond_32_bit_offsets():
+    rows, d = 140000, 16384
+    assert rows * d > 2 ** 31
+    x = torch.zeros(rows, d, **F32T)
+    small, g, dy_s, _ = ckpt_inputs(3, d, seed=43)
+    x[-3:] = small
+    p = lambda t: t.data_ptr()
+    E = lambda dt, *s: torch.empty(*s, dtype=dt, device="cuda")
+    outs = []
+    for xx, n in ((x, rows), (small, 3)):
+        q, s, v, y, r = E(torch.uint8, n, d), E(torch.float32, n, d // 128), E(torch.float32, n, d), \
+            E(torch.bfloat16, n, d), E(torch.float32, n)
+        assert sf.op_ckpt8_save(p(xx), p(q), p(s), 0, n, d, stream()) == 0
+        assert sf.op_ckpt8_load(p(q), p(s), p(v), 0, n, d, stream()) == 0
+        assert sf.op_rmsnorm_fwd_load8(p(q), p(s), p(g), p(y), p(r), 0, 0, n, d, EPS, stream()) == 0
+        dy = torch.zeros(n, d, **F32T)
+        dy[-3:] = dy_s
+        part, dg, dxb = E(torch.float32, sf.rmsnorm_bwd_scratch(n, d)), E(torch.bfloat16, d), E(torch.bfloat16, n, d)
+        dx = E(torch.float32, n, d)
+        assert sf.op_rmsnorm_bwd_load8(p(q), p(s), p(g), p(r), p(dy), 0, p(dx), p(dxb), p(dg), p(part), 0, n, d,
+                                       stream()) == 0
+        sync()
+        outs.append([t[-3:].clone() for t in (q, s, v, y, r, dx, dxb)])
+        del q, s, v, y, dy, dx, dxb
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
