@@ -151,8 +151,10 @@ __device__ __forceinline__ void each_step(const QkNormArgs& a, const Steps& ss, 
       if (head(pf.i, kind, h)) {
         const int64_t c = (int64_t)h * hd + 8 * sub;
         const uint32_t at = ring + (uint32_t)(put * NS * kQkThreads) * 16u;
-        copy16(at, x + pf.t * ldx + c);
-        copy16(at + kQkThreads * 16, x + pf.t * ldx + c + half);
+        if (NS == 2 || kind < 2) {  // of the values only the gradient is needed
+          copy16(at, x + pf.t * ldx + c);
+          copy16(at + kQkThreads * 16, x + pf.t * ldx + c + half);
+        }
         if (NS == 4) {
           copy16(at + 2 * kQkThreads * 16, dy + pf.t * lddy + c);
           copy16(at + 3 * kQkThreads * 16, dy + pf.t * lddy + c + half);
@@ -244,7 +246,8 @@ __global__ void __launch_bounds__(kQkThreads, kQkFwdCtas)
 }
 
 // Persistent CTAs: all query heads, then all key heads (so one gain and one
-// set of sums is in registers at a time), then the value heads are copied.
+// set of sums is in registers at a time) with the value heads, which are copied
+// unless the call is in place.
 // Every CTA writes the sums of its heads to its row of part [gridDim, 2 hd].
 template <int TPH>
 __global__ void __launch_bounds__(kQkThreads, kQkBwdCtas)
@@ -266,8 +269,16 @@ __global__ void __launch_bounds__(kQkThreads, kQkBwdCtas)
     }
     int64_t at = -1;  // the token whose rotation is in co, si
     each_step<TPH, 4, kQkBwdStages>(
-        a, steps_of<TPH>(a, k == 0, k == 1, false), ring, x, ldx, dy, lddy,
-        [&](int64_t t, int, int h, bool live, const uint4 (&piece)[4]) {
+        a, steps_of<TPH>(a, k == 0, k == 1, k == 1 && dx != dy), ring, x, ldx, dy, lddy,
+        [&](int64_t t, int kind, int h, bool live, const uint4 (&piece)[4]) {
+          bf16* p = dx + t * lddx + (int64_t)h * a.hd + 8 * sub;
+          if (kind == 2) {
+            if (live) {
+              *reinterpret_cast<uint4*>(p) = piece[2];
+              *reinterpret_cast<uint4*>(p + half) = piece[3];
+            }
+            return;
+          }
           if (t != at) {
             if (in) rotation(a, t, sub, co, si, err);
             at = t;
@@ -297,7 +308,6 @@ __global__ void __launch_bounds__(kQkThreads, kQkBwdCtas)
             d2[i] = r * (g2[i] * d2[i] - m * x2[i]);
           }
           if (!live) return;
-          bf16* p = dx + t * lddx + (int64_t)h * a.hd + 8 * sub;
           *reinterpret_cast<uint4*>(p) = pack(d1);
           *reinterpret_cast<uint4*>(p + half) = pack(d2);
         });
@@ -327,15 +337,6 @@ __global__ void __launch_bounds__(kQkThreads, kQkBwdCtas)
     __syncthreads();
   }
   allow_dependents();
-  if (dx != dy)
-    each_step<TPH, 2, kQkFwdStages>(
-        a, steps_of<TPH>(a, false, false, true), ring, dy, lddy, nullptr, 0,
-        [&](int64_t t, int, int h, bool live, const uint4 (&piece)[2]) {
-          if (!live) return;
-          bf16* p = dx + t * lddx + (int64_t)h * a.hd + 8 * sub;
-          *reinterpret_cast<uint4*>(p) = piece[0];
-          *reinterpret_cast<uint4*>(p + half) = piece[1];
-        });
 }
 
 int lanes_per_head(int hd) {
