@@ -74,8 +74,7 @@ __global__ void attn_delta_kernel(const bf16* __restrict__ o, const bf16* __rest
 // [T, Hq*hd]; else slot j [T, Hq*hd] holds key block j's part, written for
 // positions s >= 128 j, and the parts are added in the order j = 0, 1, ...
 // With a window (> 0) only the sinks' key blocks and those from the start of
-// the window of s's query block (64 queries at head dim 128, else 128) have
-// parts, the latter in slots that blocks take in turn.
+// the window of s's query block (128 queries) have parts, the latter in slots that blocks take in turn.
 __global__ void attn_dq_kernel(const float* __restrict__ dq_acc, bf16* __restrict__ dqkv,
                                int64_t tokens, int S, int Hq, int Hkv, int hd, float scale,
                                const float2* __restrict__ cs, int slots, int window, int sinks) {
@@ -89,9 +88,8 @@ __global__ void attn_dq_kernel(const float* __restrict__ dq_acc, bf16* __restric
   const int64_t t = th / Hq;
   const int s = (int)(t % S);
   const int64_t ld = (int64_t)Hq * hd;
-  const int qb = hd == 128 ? 64 : 128;  // queries of a backward block
   const int ns = window > 0 ? (sinks + 127) / 128 : 0;
-  const int wb = window > 0 ? max(0, s / qb * qb - window + 1) / 128 : 0;
+  const int wb = window > 0 ? max(0, s / 128 * 128 - window + 1) / 128 : 0;
   auto slot_of = [&](int j) -> int64_t {
     return window > 0 && j >= ns ? ns + (j - ns) % attn_window_slots(window) : j;
   };

@@ -692,24 +692,24 @@ __device__ __forceinline__ int last_query(const AttWindow& win, int k0, int S) {
 struct KeyWork {
   int j, first, count, slot;
 };
-// The item of a rank, query blocks of QB.  A sinks' key block is seen by every
+// The item of a rank, query blocks of 128.  A sinks' key block is seen by every
 // later query, which would make it an item many times the others' length (2 x
-// 8192 tokens, window 1024, 4 sinks: 512 steps against 72; longer than all the
+// 8192 tokens, window 1024, 4 sinks: 256 steps against 36; longer than all the
 // rest of the work where the sequence is long and the window short).  So the
 // queries behind its window are split into win.splits items of their own, and
 // its other item (slot 0) is like every key block's (1 x 16384, 16 heads in
-// groups of 8, window 256, 4 sinks: 3328 us with one item, 355 us split).  The
+// groups of 8, window 256, 4 sinks: 3328 us with one item, 355 us split, both with an older kernel).  The
 // parts come first, as they can be longer than the others (130 sinks there:
-// 343 us, 460 us with the parts spread between the key blocks).
+// 343 us, 460 us with the parts spread between the key blocks, likewise).
 //
 // PART: the variants of the kernels for win.splits > 0; the decoding of items
 // and the parts' epilogue are on the critical path of short items (8 x 1001, 16
 // heads of 64, window 250: 93 us without, 100 us in one variant with them).
-template <int QB, bool WIN, bool PART>
+template <bool WIN, bool PART>
 __device__ __forceinline__ KeyWork key_work(const AttWindow& win, int rank, int S) {
-  const int nq = (S + QB - 1) / QB;
-  if (!WIN) return {rank, rank * (128 / QB), nq - rank * (128 / QB), -1};
-  if (!PART) return {rank, rank * (128 / QB), last_query(win, rank * 128, S) / QB + 1 - rank * (128 / QB), -1};
+  const int nq = (S + 127) / 128;
+  if (!WIN) return {rank, rank, nq - rank, -1};
+  if (!PART) return {rank, rank, last_query(win, rank * 128, S) / 128 + 1 - rank, -1};
   const int ns = (win.sinks + 127) / 128, parts = ns * win.splits;
   const bool part = rank < parts;
   KeyWork w;
@@ -721,8 +721,8 @@ __device__ __forceinline__ KeyWork key_work(const AttWindow& win, int rank, int 
     c = rank - w.j * win.splits;
   }
   const int seen = w.j * 128 + 127 + win.size - 1;  // the last query with a key in its window
-  const int end = seen > S - 1 ? nq : seen / QB + 1;
-  w.first = w.j * (128 / QB);
+  const int end = seen > S - 1 ? nq : seen / 128 + 1;
+  w.first = w.j;
   w.count = end - w.first;
   if (part) {
     const int n = nq - end, b0 = n * c / win.splits, b1 = n * (c + 1) / win.splits;
@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
     if (t >= num_items) return {{0, 0, 1, -1}, 0, 0, 0};
     Item x;
     int rem;
-    x.w = key_work<128, WIN, PART>(win, per_block(t, rem), S);  // t by Hkv * B
+    x.w = key_work<WIN, PART>(win, per_block(t, rem), S);  // t by Hkv * B
     x.b = per_batch(rem, x.g);                             // by Hkv
     x.n_it = grp * x.w.count;  // (head, query block) pairs
     return x;
@@ -1345,36 +1345,60 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
   }
 }
 
-// Backward for head_dim 128 with 64-query blocks.  The Q and dO tiles have
-// three stages, so loads run two blocks ahead.  dQ is formed transposed,
-// dQ^T = K^T dS^T (M = head_dim = 128), one thread per head-dim lane; each
-// warp stages its 32 x 32 piece in shared memory and the TMA unit adds it
-// into the fp32 dQ buffer (cp.reduce.async.bulk), so no thread issues atomics;
-// in the deterministic variant it stores the piece into this key block's own
-// slot instead, and the slots are summed in key order afterwards.  The threads copy S^T and dP^T into
-// registers and release those TMEM columns at once, so the MMA warp computes
-// the next block's S^T and dP^T, and this block's dV, dK and dQ^T, while
-// they work.  TMEM columns: S^T [0,64), dP^T [64,128), dQ^T two buffers
-// [128,256), dV [256,384), dK [384,512).  Every mbarrier below completes at
-// most once before its waiter has seen the previous completion (each has a
-// dependency chain through its waiter), so parity waits are unambiguous.
+// Backward for head_dim 128.  A CTA works on one item (as at head dim 64, in
+// longest-first order), block by block of 128 keys x 128 queries:
+//   MMA:     S^T = K Q^T -> TMEM[0,128)
+//   threads: P^T = exp2(S^T*scale*log2e - lse*log2e) (masked), kept in fp32
+//            registers, and as bf16 over the S^T columns that the warp has read
+//   MMA:     dP^T = V dO^T -> TMEM[128,256);  dV += P^T dO (P^T as the
+//            tensor-memory A; TMEM[256,384))
+//   threads: dS^T = P^T * (dP^T - D) to shared memory (bf16, swizzled)
+//   MMA:     dQ^T = K^T dS^T over the dP^T columns; dK += dS^T Q (TMEM[384,512))
+//   4 warps: dQ^T through shared memory into the fp32 dq_acc by TMA reduce-add
+//            (deterministic: by TMA store into the key block's own slot)
+// The accumulators take all of TMEM, hence the shared columns.  The MMAs of
+// block i are issued in the order dV(i), S^T(i+1), dQ^T(i), dK(i), dP^T(i+1):
+// the threads form dS^T(i) under the first two and P^T(i+1) under the next
+// two, and dQ^T is read under dK.  (P^T is overwritten by the next S^T, which
+// is issued after dV and so executes after it.)
+//
+// What bounds it: shared memory's 128 bytes a clock.  An MMA with both
+// operands in shared memory reads 4 + 4 KB in its 64 clocks, with P^T in TMEM
+// half of that: 2,304 clocks a block for operands, and 1,792 for Q and dO
+// coming in, dS^T, and dQ^T going through (its fp32 sums are 64 KB a block);
+// a block takes 4,450 clocks.  Blocks of 64 queries (MMAs 64 wide, which read
+// 6 KB in 32 clocks of work) took 2 x 2,450: 8 x 2048 tokens, 32 / 8 heads,
+// 897 us against 796 us for the whole backward (864 TFLOP/s); 2 x 8192, window
+// 1024, 4 sinks, 968 and 794 us.  Measured on the way: the threads storing dQ
+// themselves, as one reduction instruction per row, 862 us, and four warps of
+// their own doing so 918 us (such instructions leave an SM at 32 bytes a clock
+// and hold up the stores of dS^T behind them); dO's one buffer refilled after
+// the next but one Q, 1,020 us.
+// Testing the barriers a step ahead gained nothing here.
+//
+// Every mbarrier below completes at most once before its waiter has seen the
+// previous completion (each has a dependency chain through its waiter), so
+// parity waits are unambiguous.
 namespace {
-constexpr int kAttBwd2Threads = 320;  // TMA warp, MMA warp, 8 softmax-gradient warps
+constexpr int kAttBwd2Threads = 448;  // TMA warp, MMA warp, 8 softmax-gradient warps, 4 dQ warps
 struct AttBwd2Cfg {
   static constexpr int KV = 32768;  // 128 keys x 128 hd
-  static constexpr int QT = 16384;  // 64 queries x 128 hd
-  static constexpr int NQ = 3;      // Q / dO stages
+  static constexpr int QT = 32768;  // 128 queries x 128 hd
+  static constexpr int NQ = 2;      // Q stages (dO has one)
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = KV;
   static constexpr int OFF_Q = 2 * KV;
   static constexpr int OFF_DO = OFF_Q + NQ * QT;
-  static constexpr int OFF_DST = OFF_DO + NQ * QT;  // 128 keys x 64 queries
-  static constexpr int OFF_DQS = OFF_DST + 16384;  // dQ staging: 8 warps x [32 q][32 d] fp32
-  static constexpr int OFF_LD = OFF_DQS + 8 * 4096;  // [2][lse 64 | D 64]
-  static constexpr int OFF_BAR = OFF_LD + 2 * 128 * 4;
+  static constexpr int OFF_DST = OFF_DO + QT;      // 128 keys x 128 queries, two boxes of 64
+  static constexpr int OFF_DQS = OFF_DST + 32768;  // dQ staging: 4 warps x 2 x [32 q][32 d] fp32
+  static constexpr int OFF_LD = OFF_DQS + 32768;   // [2][lse 128 | D 128]
+  static constexpr int OFF_BAR = OFF_LD + 2 * 256 * 4;
   static constexpr int NBAR = 19;
-  static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+  // no room to align the base: it is 1024-byte aligned where a kernel has no
+  // static shared memory, which the kernel checks
+  static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
 };
+static_assert(AttBwd2Cfg::SMEM <= 232448, "backward shared memory");
 }  // namespace
 
 template <bool DET, bool WIN, bool PART>
@@ -1389,27 +1413,30 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
                         float* __restrict__ part, int* err) {
   using C = AttBwd2Cfg;
   constexpr int HD = 128;
-  constexpr uint32_t ID_SP = umma_idesc_bf16(128, 64, false, false);  // S^T, dP^T
-  constexpr uint32_t ID_KV = umma_idesc_bf16(128, HD, false, true);   // dV, dK
-  constexpr uint32_t ID_Q = umma_idesc_bf16(128, 64, true, true);     // dQ^T
+  constexpr uint32_t ID_SP = umma_idesc_bf16(128, 128, false, false);  // S^T, dP^T
+  constexpr uint32_t ID_KV = umma_idesc_bf16(128, HD, false, true);    // dV, dK
+  constexpr uint32_t ID_Q = umma_idesc_bf16(128, 128, true, true);     // dQ^T
   constexpr uint32_t TMEM_COLS = 512;
-  constexpr uint32_t COL_DP = 64, COL_DQ = 128, COL_P = 192, COL_DS = 224, COL_DV = 256, COL_DK = 384;
+  constexpr uint32_t COL_DP = 128, COL_DV = 256, COL_DK = 384;
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  uint8_t* smem = smem_raw;
   const uint32_t s0 = smem_u32(smem);
+  if (s0 & 1023u) {
+    if (threadIdx.x == 0) record_error(err, kDevAttnTimeout);
+    return;
+  }
   const uint32_t sK = s0 + C::OFF_K, sV = s0 + C::OFF_V, sQ = s0 + C::OFF_Q, sDO = s0 + C::OFF_DO;
   const uint32_t sDSt = s0 + C::OFF_DST, sDQS = s0 + C::OFF_DQS;
   float* sLD = reinterpret_cast<float*>(smem + C::OFF_LD);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   const uint32_t b0 = smem_u32(bars);
   const uint32_t kv_full = b0;
-  auto qdo_full = [&](int i) { return b0 + 8u * (1 + i); };
-  auto qdo_empty = [&](int i) { return b0 + 8u * (4 + i); };
-  const uint32_t sp_full = b0 + 56, s_free = b0 + 64, ps_full = b0 + 72, pds_free = b0 + 80;
-  const uint32_t dq_full = b0 + 88, dq_free = b0 + 104;
-  const uint32_t acc_done = b0 + 120, drain = b0 + 128;
+  auto q_full = [&](int i) { return b0 + 8u * (1 + i); };
+  auto q_empty = [&](int i) { return b0 + 8u * (4 + i); };
+  const uint32_t do_full = b0 + 56, do_empty = b0 + 64;
+  const uint32_t s_full = b0 + 72, p_full = b0 + 80, dp_full = b0 + 88, ds_full = b0 + 96;
+  const uint32_t dq_full = b0 + 104, dq_free = b0 + 112, acc_done = b0 + 120, drain = b0 + 128;
   auto ld_full = [&](int i) { return b0 + 136u + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -1417,28 +1444,28 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int rank, g, b;
   grid_rank_first(rank, g, b);  // without a window key block 0 sees the most query blocks
-  const KeyWork work = key_work<64, WIN, PART>(win, rank, S);
+  const KeyWork work = key_work<WIN, PART>(win, rank, S);
   const int grp = Hq / Hkv;
   const int j = work.j, k0 = j * 128;
-  const int first = work.first, per_head = work.count;  // 64-query blocks that see these keys
+  const int first = work.first, per_head = work.count;  // query blocks that see these keys
   const int keys = PART ? live_keys(win, work) : 128;
   const int n_it = grp * per_head;
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
     for (int i = 0; i < C::NQ; ++i) {
-      mbar_init(qdo_full(i), 1);
-      mbar_init(qdo_empty(i), 1);
+      mbar_init(q_full(i), 1);
+      mbar_init(q_empty(i), 1);
     }
-    mbar_init(sp_full, 1);
-    mbar_init(s_free, 256);
-    mbar_init(ps_full, 256);
-    mbar_init(pds_free, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(ld_full(i), 64);
-    }
+    mbar_init(do_full, 1);
+    mbar_init(do_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 256);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 256);
     mbar_init(dq_full, 1);
-    mbar_init(dq_free, 256);
+    mbar_init(dq_free, 128);
+    for (int i = 0; i < 2; ++i) mbar_init(ld_full(i), 128);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -1466,32 +1493,46 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       tma_load_3d(sV + c * 16384, &tm_kv, kv_full, (Hq + Hkv + g) * HD + 64 * c, k0, b);
     }
     bool ok = true;
-    int issued = 0, bq = 0, bph = 0, wh = g * grp, wq = first;
-    for (int it = 0; it < n_it; ++it) {
-      const int q0 = wq * 64, h = wh;
-      if (!mbar_wait(qdo_empty(bq), bph ^ 1, abort_flag)) { ok = false; break; }
-      mbar_arrive_expect_tx(qdo_full(bq), 2 * C::QT);
+    int q_issued = 0, do_issued = 0, bq = 0, bph = 0;
+    int qh = g * grp, qq = first, wh = qh, wq = first;  // head and query block of the next Q, dO
+    // in the order in which the buffers come free: dO of block it (after block
+    // it - 1's dV), then Q of block it + 1 (after block it - 1's dK)
+    for (int it = -1; it < n_it; ++it) {
+      if (it >= 0) {
+        if (!mbar_wait(do_empty, (it & 1) ^ 1, abort_flag)) { ok = false; break; }
+        mbar_arrive_expect_tx(do_full, C::QT);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        tma_load_3d(sQ + bq * C::QT + c * 8192, &tm_q, qdo_full(bq), h * HD + 64 * c, q0, b);
-        tma_load_3d(sDO + bq * C::QT + c * 8192, &tm_do, qdo_full(bq), h * HD + 64 * c, q0, b);
+        for (int c = 0; c < 2; ++c)
+          tma_load_3d(sDO + c * 16384, &tm_do, do_full, wh * HD + 64 * c, wq * 128, b);
+        ++do_issued;
+        if (++wq == first + per_head) {
+          wq = first;
+          ++wh;
+        }
       }
-      issued = it + 1;
+      if (it + 1 == n_it) break;
+      if (!mbar_wait(q_empty(bq), bph ^ 1, abort_flag)) { ok = false; break; }
+      mbar_arrive_expect_tx(q_full(bq), C::QT);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        tma_load_3d(sQ + bq * C::QT + c * 16384, &tm_q, q_full(bq), qh * HD + 64 * c, qq * 128, b);
+      ++q_issued;
       if (++bq == C::NQ) {
         bq = 0;
         bph ^= 1;
       }
-      if (++wq == first + per_head) {
-        wq = first;
-        ++wh;
+      if (++qq == first + per_head) {
+        qq = first;
+        ++qh;
       }
     }
     if (!ok) {
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
       mbar_wait(kv_full, 0, nullptr);
-      for (int it = issued - 1; it >= 0 && it >= issued - C::NQ; --it)
-        mbar_wait(qdo_full(it % C::NQ), (it / C::NQ) & 1, nullptr);
+      for (int it = q_issued - 1; it >= 0 && it >= q_issued - C::NQ; --it)
+        mbar_wait(q_full(it % C::NQ), (it / C::NQ) & 1, nullptr);
+      if (do_issued > 0) mbar_wait(do_full, (do_issued - 1) & 1, nullptr);
     }
   } else if (warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
@@ -1502,65 +1543,66 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     // 14-bit address field cannot carry).
     const uint64_t dK = smem_desc_sw128(sK, 16, 1024), dV = smem_desc_sw128(sV, 16, 1024);
     const uint64_t dQk = smem_desc_sw128(sQ, 16, 1024), dDOk = smem_desc_sw128(sDO, 16, 1024);
-    const uint64_t dQm = smem_desc_sw128(sQ, 8192, 1024), dDOm = smem_desc_sw128(sDO, 8192, 1024);
+    const uint64_t dQm = smem_desc_sw128(sQ, 16384, 1024), dDOm = smem_desc_sw128(sDO, 16384, 1024);
+    const uint64_t dDSt = smem_desc_sw128(sDSt, 16, 1024);
     const uint64_t dKm = smem_desc_sw128(sK, 16384, 1024), dDStm = smem_desc_sw128(sDSt, 16384, 1024);
-    // A look at a barrier costs this thread about 100 cycles even when its phase
-    // is long over: the next step's are tested before the last MMAs of this one
-    // (the tensor core's queue holds two) and waited for where that was too
-    // early.  A test for a phase is only made once the phase before has been
-    // seen (its parity would be taken for a finished one's).
-    bool q_ready = false, s_ready = false, p_ready = false;
-    for (int it = 0; ok && it <= n_it; ++it) {
-      p_ready = false;
-      if (it < n_it) {  // S^T and dP^T of block it, once the threads hold block it - 1's
-        const int bq = it % C::NQ;
-        if (!q_ready && !mbar_wait(qdo_full(bq), (it / C::NQ) & 1, abort_flag)) { ok = false; break; }
-        if (it >= 1 && !s_ready && !mbar_wait(s_free, (it - 1) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t qo = (uint32_t)bq * (uint32_t)(C::QT / 16);
+    auto issue_s = [&](int it) -> bool {
+      const int bq = it % C::NQ;
+      if (!mbar_wait(q_full(bq), (it / C::NQ) & 1, abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t qo = (uint32_t)bq * (uint32_t)(C::QT / 16);
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          if (kk == 7 && it >= 1) p_ready = mbar_test(ps_full, (it - 1) & 1);
-          const uint32_t ka = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;  // K / V: 128-row boxes
-          const uint32_t qa = ((kk >> 2) * 8192 + (kk & 3) * 32) / 16;    // Q / dO: 64-row boxes
-          umma_bf16(tmem_base, dK + ka, dQk + qo + qa, ID_SP, kk > 0 ? 1u : 0u);
-          umma_bf16(tmem_base + COL_DP, dV + ka, dDOk + qo + qa, ID_SP, kk > 0 ? 1u : 0u);
-        }
-        umma_commit(sp_full);
+      for (int kk = 0; kk < HD / 16; ++kk) {
+        const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;
+        umma_bf16(tmem_base, dK + o, dQk + qo + o, ID_SP, kk > 0 ? 1u : 0u);
       }
-      if (it >= 1) {  // dV, dK, dQ^T of block it - 1, once its P^T and dS^T are in shared memory
-        const int ip = it - 1, bq = ip % C::NQ;
-        if (!p_ready && !mbar_wait(ps_full, ip & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t qo = (uint32_t)bq * (uint32_t)(C::QT / 16);
+      umma_commit(s_full);
+      return true;
+    };
+    auto issue_dp = [&](int it) -> bool {
+      if (!mbar_wait(do_full, it & 1, abort_flag)) return false;
+      tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {  // over the 64 queries
-          const uint32_t acc = (ip > 0 || kk > 0) ? 1u : 0u;
-          umma_bf16_ts(tmem_base + COL_DV, tmem_base + COL_P + kk * 8, dDOm + qo + kk * 128, ID_KV, acc);
-          umma_bf16_ts(tmem_base + COL_DK, tmem_base + COL_DS + kk * 8, dQm + qo + kk * 128, ID_KV, acc);
-        }
-        umma_commit(qdo_empty(bq));
-        // dQ^T of the previous block has been read
-        if (ip >= 1 && !mbar_wait(dq_free, (ip - 1) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        if (PART && keys < 128) {  // only the sinks
-          q_ready = s_ready = false;
+      for (int kk = 0; kk < HD / 16; ++kk) {
+        const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;
+        umma_bf16(tmem_base + COL_DP, dV + o, dDOk + o, ID_SP, kk > 0 ? 1u : 0u);
+      }
+      umma_commit(dp_full);
+      return true;
+    };
+    if (ok) ok = issue_s(0) && issue_dp(0);
+    for (int it = 0; ok && it < n_it; ++it) {
+      // P^T of the block is there (and S^T has been read)
+      if (!mbar_wait(p_full, it & 1, abort_flag)) { ok = false; break; }
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)  // over the 128 queries
+        umma_bf16_ts(tmem_base + COL_DV, tmem_base + (kk >> 2) * 64 + (kk & 3) * 8, dDOm + kk * 128, ID_KV,
+                     (it > 0 || kk > 0) ? 1u : 0u);
+      umma_commit(do_empty);
+      // the next S^T, over P^T, which the tensor core has used by then
+      if (it + 1 < n_it && !issue_s(it + 1)) { ok = false; break; }
+      // dS^T is in shared memory, dP^T has been read: dQ^T takes its columns
+      if (!mbar_wait(ds_full, it & 1, abort_flag)) { ok = false; break; }
+      tc_fence_after();
+      if (PART && keys < 128) {  // only the sinks
 #pragma unroll 1
-          for (int kk = 0; kk < keys / 16; ++kk)
-            umma_bf16(tmem_base + COL_DQ, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
-        } else {
+        for (int kk = 0; kk < keys / 16; ++kk)
+          umma_bf16(tmem_base + COL_DP, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
+      } else {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {  // over the 128 keys
-            if (kk == 6) {
-              q_ready = it + 1 < n_it && mbar_test(qdo_full((it + 1) % C::NQ), ((it + 1) / C::NQ) & 1);
-              s_ready = it < n_it && mbar_test(s_free, it & 1);
-            }
-            umma_bf16(tmem_base + COL_DQ, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
-          }
-        }
-        umma_commit(dq_full);
-        umma_commit(pds_free);
+        for (int kk = 0; kk < 8; ++kk)  // over the 128 keys
+          umma_bf16(tmem_base + COL_DP, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
       }
+      umma_commit(dq_full);
+      const uint32_t qo = (uint32_t)(it % C::NQ) * (uint32_t)(C::QT / 16);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)  // over the 128 queries
+        umma_bf16(tmem_base + COL_DK, dDSt + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16, dQm + qo + kk * 128, ID_KV,
+                  (it > 0 || kk > 0) ? 1u : 0u);
+      umma_commit(q_empty(it % C::NQ));
+      // the next dP^T, once dQ^T has been read
+      if (it + 1 < n_it && (!mbar_wait(dq_free, it & 1, abort_flag) || !issue_dp(it + 1))) { ok = false; break; }
     }
     if (ok) {
       umma_commit(acc_done);
@@ -1570,11 +1612,68 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       umma_commit(drain);
       mbar_wait(drain, 0, nullptr);
     }
+  } else if (warp >= 10) {
+    // ---------------------------------------------------------------- dQ
+    // dQ^T of each block, a thread per head-dim lane, by 32 queries: out of TMEM,
+    // into one of the warp's two staging tiles, and from there the TMA unit
+    // adds it into the fp32 dQ buffer (deterministic: stores it into the key
+    // block's own slot).
+    const int quarter = warp & 3;
+    const uint32_t at = tmem_base + ((uint32_t)(quarter * 32) << 16) + COL_DP;
+    const uint32_t stage = sDQS + (uint32_t)quarter * 8192u;
+    wait_primary();  // the zeros in dq_acc
+    bool ok = true;
+    int h = g * grp, qb = first;
+    auto emit = [&](int c, const uint32_t (&v)[32]) {
+      const uint32_t tile = stage + (uint32_t)(c & 1) * 4096u;
+      if (lane == 0) bulk_wait_group_read1();
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + (uint32_t)e * 128u + (uint32_t)lane * 4u), "r"(v[e])
+                     : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int col = h * HD + 32 * quarter, q = qb * 128 + 32 * c;
+        if (DET)
+          tma_store_3d(&tm_dq, tile, col, q, (WIN ? dq_slot(win, j) : j) * (int)gridDim.z + b);
+        else
+          tma_reduce_add_3d(&tm_dq, tile, col, q, b);
+        bulk_commit_group();
+      }
+    };
+    for (int it = 0; it < n_it; ++it) {
+      ok = __all_sync(0xffffffffu, mbar_wait(dq_full, it & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t v0[32], v1[32], v2[32];
+      tmem_ld_32x32b_x32(at, v0);
+      tmem_ld_32x32b_x32(at + 32, v1);
+      tmem_ld_32x32b_x32(at + 64, v2);
+      tmem_ld_wait();
+      emit(0, v0);
+      tmem_ld_32x32b_x32(at + 96, v0);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(dq_free);
+      emit(1, v1);
+      emit(2, v2);
+      emit(3, v0);
+      if (++qb == first + per_head) {
+        qb = first;
+        ++h;
+      }
+    }
+    if (lane == 0) bulk_wait_group0();  // this warp's copies are complete
+    if (!ok && lane == 0) {
+      record_error(err, kDevAttnTimeout);
+      *abort_flag = 1;
+    }
   } else if (warp >= 2) {
     // ---------------------------------------------------------------- threads
-    // Eight warps: two per TMEM lane quarter, each taking one half (32) of the
-    // block's 64 query columns, so every scheduler has two warps to switch
-    // between and each thread handles 32 elements of a block.
+    // Eight warps: two per TMEM lane quarter, each taking one half (64) of the
+    // block's queries.
     const int quarter = warp & 3;
     const int half = (warp - 2) >> 2;
     const int r = quarter * 32 + lane;  // key row of S^T / dP^T; head-dim lane of dQ^T
@@ -1587,49 +1686,13 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     auto fetch = [&](int it_, int h_, int qq_, float& lv, float& dv) {
       lv = 0.f;
       dv = 0.f;
-      if (it_ >= n_it || tid >= 64) return;
-      const int q_ = qq_ * 64 + tid;
+      if (it_ >= n_it || tid >= 128) return;
+      const int q_ = qq_ * 128 + tid;
       if (q_ < S) {
         const int64_t o = ((int64_t)b * Hq + h_) * S + q_;
         lv = lse[o];
         dv = delta[o];
       }
-    };
-    // dQ^T of block it_ (this warp's 32 queries, head-dim lanes of its
-    // quarter) from registers into the warp's staging tile, then one TMA
-    // reduce-add into the fp32 dQ buffer.  The tile is rewritten only after
-    // the previous reduce has finished reading it.
-    const uint32_t stage = sDQS + (uint32_t)(warp - 2) * 4096u;
-    auto stage_dq = [&](int h_, int q_, const uint32_t (&v)[32]) {
-      if (lane == 0) bulk_wait_group_read0();
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + (uint32_t)e * 128u + (uint32_t)lane * 4u),
-                     "r"(v[e])
-                     : "memory");
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        const int qb_ = q_ * 64 + 32 * half;
-        if (DET)  // this key block's own slot of the dQ buffer
-          tma_store_3d(&tm_dq, stage, h_ * HD + 32 * quarter, qb_,
-                       (WIN ? dq_slot(win, j) : j) * (int)gridDim.z + b);
-        else
-          tma_reduce_add_3d(&tm_dq, stage, h_ * HD + 32 * quarter, qb_, b);
-        bulk_commit_group();
-      }
-    };
-    auto emit_dq = [&](int it_, int h_, int q_) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(dq_full, it_ & 1, abort_flag))) return false;
-      tc_fence_after();
-      uint32_t v[32];
-      tmem_ld_32x32b_x32(lane_base + COL_DQ + 32 * half, v);
-      tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive(dq_free);
-      stage_dq(h_, q_, v);
-      return true;
     };
     wait_primary();  // D, and the zeros in dq_acc
     float next_l, next_d;
@@ -1637,115 +1700,134 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
     const uint32_t rowoff = (uint32_t)r * 128u;
     // no key of this warp's lanes counts behind the window of a sinks' block
     const bool idle = PART && quarter * 32 >= keys;
-    int wh = g * grp, wq = first, ph = 0, pq = 0;  // this block's head and query block; the previous one's
-    for (int it = 0; it < n_it; ++it) {
-      const int q0 = wq * 64;
-      const int qb = q0 + 32 * half;  // first query of this thread's columns
-      float* bL = sLD + (it & 1) * 128;
-      float* bD = bL + 64;
-      // The buffer written here was last read for block it - 2; this thread
-      // has since waited for that block's P^T / dS^T to be consumed, which
-      // needed every thread to have finished computing it.
-      if (tid < 64) {
+    float p[64];  // P of the thread's key and 64 queries
+    // P^T of block it_ from S^T, in bf16 over its columns
+    auto form_p = [&](int it_, int h_, int q_, int nh, int nq) -> bool {
+      float* bL = sLD + (it_ & 1) * 256;
+      // The buffer written here was last read for dS^T of block it_ - 2; this
+      // thread has since seen block it_ - 1's dP^T, which was formed after
+      // every thread's dS^T of it_ - 2.
+      if (tid < 128) {
         bL[tid] = next_l * 1.4426950408889634f;
-        bD[tid] = next_d;
-        mbar_arrive(ld_full(it & 1));
+        bL[128 + tid] = next_d;
+        mbar_arrive(ld_full(it_ & 1));
       }
-      const bool turn = wq + 1 == first + per_head;
-      fetch(it + 1, turn ? wh + 1 : wh, turn ? first : wq + 1, next_l, next_d);
-      ok = __all_sync(0xffffffffu, mbar_wait(ld_full(it & 1), (it >> 1) & 1, abort_flag));
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sp_full, it & 1, abort_flag));
-      if (!ok) break;
+      fetch(it_ + 1, nh, nq, next_l, next_d);
+      bool good = __all_sync(0xffffffffu, mbar_wait(ld_full(it_ & 1), (it_ >> 1) & 1, abort_flag));
+      if (good) good = __all_sync(0xffffffffu, mbar_wait(s_full, it_ & 1, abort_flag));
+      if (!good) return false;
       tc_fence_after();
-      uint32_t sr[32], dr[32];
-      if (!idle) {
-        tmem_ld_32x32b_x32(lane_base + 32 * half, sr);
-        tmem_ld_32x32b_x32(lane_base + COL_DP + 32 * half, dr);
-        tmem_ld_wait();
-      }
-      tc_fence_before();
-      mbar_arrive(s_free);  // S^T / dP^T are in registers: the next block may overwrite them
-      const float4* L4 = reinterpret_cast<const float4*>(bL + 32 * half);
-      const float4* D4 = reinterpret_cast<const float4*>(bD + 32 * half);
-      uint32_t pp[16], dd[16];
-      const int e_lo = key - qb, e_hi = q_end - qb;  // this thread's visible columns (WIN)
-      auto grad_tile = [&](auto mask_tag) {
-        constexpr bool kMask = decltype(mask_tag)::value;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 l4 = L4[k], d4 = D4[k];
-          const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+      for (int c = 0; c < 4; ++c) {
+        if (idle) break;
+        uint32_t sr[16];
+        tmem_ld_32x32b_x16(lane_base + 64 * half + 16 * c, sr);
+        tmem_ld_wait();
+        const float4* L4 = reinterpret_cast<const float4*>(bL + 64 * half + 16 * c);
+        const int qb = q_ * 128 + 64 * half + 16 * c;     // first query of these columns
+        const int e_lo = key - qb, e_hi = q_end - qb;     // this thread's visible columns (WIN)
+        uint32_t pp[8];
+        auto tile = [&](auto mask_tag) {
+          constexpr bool kMask = decltype(mask_tag)::value;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 l4 = L4[k];
+            const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const int e = 4 * k + i;
+              // (x0, x1) = s * scale_log2 - lse * log2(e), one paired FMA
+              float x0 = __uint_as_float(sr[e]), x1 = __uint_as_float(sr[e + 1]);
+              fma2(x0, x1, scale_log2, -lv[i], -lv[i + 1]);
+              x0 = ex2_approx(x0);
+              x1 = ex2_approx(x1);
+              if (WIN) {
+                if (kMask && (e < e_lo || e > e_hi)) x0 = 0.f;
+                if (kMask && (e + 1 < e_lo || e + 1 > e_hi)) x1 = 0.f;
+              } else {
+                if (kMask && !(qb + e < S && key <= qb + e)) x0 = 0.f;
+                if (kMask && !(qb + e + 1 < S && key <= qb + e + 1)) x1 = 0.f;
+              }
+              p[16 * c + e] = x0;
+              p[16 * c + e + 1] = x1;
+              pp[2 * k + i / 2] = pack2_bf16(x0, x1);
+            }
+          }
+        };
+        // Only blocks that touch the diagonal, the sequence end or the window's
+        // start need the mask.
+        const bool cut = WIN && qb + 15 - k0 >= win.size && k0 + 127 >= win.sinks;
+        if (qb < k0 + 128 || qb + 16 > S || cut)
+          tile(std::true_type{});
+        else
+          tile(std::false_type{});
+        tmem_st_32x32b_x8(lane_base + 64 * half + 8 * c, pp);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(p_full);
+      return true;
+    };
+    // dS^T = P^T (dP^T - D) of block it_ into shared memory (the tile's readers
+    // of the block before were done before this dP^T)
+    auto form_ds = [&](int it_) -> bool {
+      const float* bD = sLD + (it_ & 1) * 256 + 128;
+      if (!__all_sync(0xffffffffu, mbar_wait(dp_full, it_ & 1, abort_flag))) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (idle) break;
+        uint32_t dr[16];
+        tmem_ld_32x32b_x16(lane_base + COL_DP + 64 * half + 16 * c, dr);
+        tmem_ld_wait();
+        const float4* D4 = reinterpret_cast<const float4*>(bD + 64 * half + 16 * c);
+        uint32_t dd[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 d4 = D4[k];
           const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
-          float pv[4], sv[4];
 #pragma unroll
           for (int i = 0; i < 4; i += 2) {
             const int e = 4 * k + i;
-            // (x0, x1) = s * scale_log2 - lse * log2(e), one paired FMA
-            float x0 = __uint_as_float(sr[e]), x1 = __uint_as_float(sr[e + 1]);
-            fma2(x0, x1, scale_log2, -lv[i], -lv[i + 1]);
-            x0 = ex2_approx(x0);
-            x1 = ex2_approx(x1);
-            if (WIN) {
-              if (kMask && (e < e_lo || e > e_hi)) x0 = 0.f;
-              if (kMask && (e + 1 < e_lo || e + 1 > e_hi)) x1 = 0.f;
-            } else {
-              if (kMask && !(qb + e < S && key <= qb + e)) x0 = 0.f;
-              if (kMask && !(qb + e + 1 < S && key <= qb + e + 1)) x1 = 0.f;
-            }
-            pv[i] = x0;
-            pv[i + 1] = x1;
-            // dS = P (dP - D): a paired subtract and a paired multiply
             float d0 = __uint_as_float(dr[e]), d1 = __uint_as_float(dr[e + 1]);
             add2(d0, d1, -dv[i], -dv[i + 1]);
-            mul2(d0, d1, x0, x1);
-            sv[i] = d0;
-            sv[i + 1] = d1;
+            mul2(d0, d1, p[16 * c + e], p[16 * c + e + 1]);
+            dd[2 * k + i / 2] = pack2_bf16(d0, d1);
           }
-          pp[2 * k] = pack2_bf16(pv[0], pv[1]);
-          pp[2 * k + 1] = pack2_bf16(pv[2], pv[3]);
-          dd[2 * k] = pack2_bf16(sv[0], sv[1]);
-          dd[2 * k + 1] = pack2_bf16(sv[2], sv[3]);
         }
-      };
-      // Only blocks that touch the diagonal, the sequence end or the window's
-      // start need the mask.
-      const bool cut = WIN && qb + 31 - k0 >= win.size && k0 + 127 >= win.sinks;
-      if (idle) {
-      } else if (qb < k0 + 128 || qb + 32 > S || cut) {
-        grad_tile(std::true_type{});
-      } else {
-        grad_tile(std::false_type{});
-      }
-      if (it >= 1) {  // P^T, dS^T of the previous block consumed
-        ok = __all_sync(0xffffffffu, mbar_wait(pds_free, (it - 1) & 1, abort_flag));
-        if (!ok) break;
-      }
-      if (!idle) {
-        tmem_st_32x32b_x16(lane_base + COL_P + 16 * half, pp);
-        tmem_st_32x32b_x16(lane_base + COL_DS + 16 * half, dd);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int jj = half * 4 + k;  // 16-byte chunk of the 128-byte row
-          const uint32_t off = rowoff + (uint32_t)((jj ^ (r & 7)) * 16);
+        for (int k = 0; k < 2; ++k) {
+          const int jj = c * 2 + k;  // 16-byte chunk of the 128-byte row
+          const uint32_t off = (uint32_t)half * 16384u + rowoff + (uint32_t)((jj ^ (r & 7)) * 16);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sDSt + off), "r"(dd[4 * k]),
                        "r"(dd[4 * k + 1]), "r"(dd[4 * k + 2]), "r"(dd[4 * k + 3])
                        : "memory");
         }
       }
-      tmem_st_wait();
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(ps_full);
-      // dQ^T of the previous block, while the tensor core works on this one's products
-      if (it >= 1 && !emit_dq(it - 1, ph, pq)) { ok = false; break; }
-      ph = wh;
-      pq = wq;
-      if (++wq == first + per_head) {
-        wq = first;
-        ++wh;
+      mbar_arrive(ds_full);
+      return true;
+    };
+    // head and query block of the block in hand, and of the next two
+    int wh = g * grp, wq = first;
+    auto step = [&](int& h_, int& q_) {
+      if (++q_ == first + per_head) {
+        q_ = first;
+        ++h_;
       }
+    };
+    int nh = wh, nq = wq;
+    step(nh, nq);
+    ok = form_p(0, wh, wq, nh, nq);
+    for (int it = 0; ok && it < n_it; ++it) {
+      ok = form_ds(it);
+      wh = nh;
+      wq = nq;
+      step(nh, nq);
+      // the next block's P^T while the tensor core forms dQ^T
+      if (ok && it + 1 < n_it) ok = form_p(it + 1, wh, wq, nh, nq);
     }
-    if (ok) ok = emit_dq(n_it - 1, ph, pq);
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, abort_flag));
     if (ok) {
       tc_fence_after();
@@ -1825,7 +1907,6 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       record_error(err, kDevAttnTimeout);
       *abort_flag = 1;
     }
-    if (lane == 0) bulk_wait_group0();  // this warp's dQ reduces are complete
   }
   tc_fence_before();
   __syncthreads();
@@ -1995,7 +2076,7 @@ int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat1
   if (!fn) return -3;
   const int64_t W = (int64_t)(Hq + 2 * Hkv) * HD, WO = (int64_t)Hq * HD;
   CUtensorMap tkv, tq, td, tdq, tdkv;
-  cuuint32_t box_kv[3] = {64, 128, 1}, box_q[3] = {64, 64, 1}, box_dq[3] = {32, 32, 1};
+  cuuint32_t box_kv[3] = {64, 128, 1}, box_q[3] = {64, 128, 1}, box_dq[3] = {32, 32, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   cuuint64_t dq[3] = {(cuuint64_t)W, (cuuint64_t)S, (cuuint64_t)B};
   cuuint64_t sq[2] = {(cuuint64_t)(W * 2), (cuuint64_t)(S * W * 2)};
@@ -2007,9 +2088,9 @@ int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat1
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  cuuint64_t sdq[2] = {(cuuint64_t)(WO * 4), (cuuint64_t)(S * WO * 4)};
   const int nkb = (S + 127) / 128;
   const int slots = WIN ? attn_window_dq_slots(S, win.size, win.sinks) : nkb;
+  cuuint64_t sdq[2] = {(cuuint64_t)(WO * 4), (cuuint64_t)(S * WO * 4)};
   cuuint64_t ddq[3] = {(cuuint64_t)WO, (cuuint64_t)S, (cuuint64_t)(DET ? (int64_t)B * slots : B)};
   if (!enc(&tkv, qkv, dq, sq, box_kv) || !enc(&tq, qkv, dq, sq, box_q) ||
       !enc(&td, dout, dd, sd, box_q) || !enc(&tdkv, dqkv, dq, sq, box_kv) ||
@@ -2051,13 +2132,13 @@ int bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* d
 // the items out, the sinks' queries are split only where one item with all of
 // them would take longer than an even share of the work: else it runs beside
 // the others from the start, its queries a little ahead of theirs (2 x 8192, 32
-// / 8 heads of 128, window 1024, 4 sinks: 964 us in one item, 1003 us split).
+// / 8 heads of 128, window 1024, 4 sinks: 794 us in one item, 846 us split).
 // At 64 the items are dealt out in advance and a long one delays those behind
 // it (1 x 16384, 16 heads, window 1024, 64 sinks: 538 us and 384 us).
 AttWindow clip(int window, int sinks, int S, int B, int Hq, int Hkv, int hd) {
-  AttWindow win{window < S ? window : S, sinks < S ? sinks : S, attn_window_splits(S, window, sinks, hd)};
+  AttWindow win{window < S ? window : S, sinks < S ? sinks : S, attn_window_splits(S, window, sinks)};
   if (hd == 128 && win.splits > 0) {
-    const int64_t nq = (S + 63) / 64, near = (126 + win.size) / 64 + 1, ns = (win.sinks + 127) / 128;
+    const int64_t nq = (S + 127) / 128, near = (126 + win.size) / 128 + 1, ns = (win.sinks + 127) / 128;
     const int64_t work = (int64_t)B * Hq * ((S + 127) / 128 * near + ns * (nq - near));
     if ((int64_t)(Hq / Hkv) * nq * num_sms() <= work) win.splits = 0;
   }

@@ -157,7 +157,7 @@ int attn_window_bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv
                     const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B,
                     int S, int Hq, int Hkv, int hd, int window, int sinks, const float2* cs,
                     bool deterministic, int* err, cudaStream_t st);
-// Key blocks of 128 that the windows of a query block (64 or 128 queries,
+// Key blocks of 128 that the windows of a query block (128 queries,
 // aligned) can reach: its own and those of the window - 1 keys before it.
 __host__ __device__ constexpr int attn_window_slots(int window) { return (window + 126) / 128 + 1; }
 // dQ slots of the deterministic backward: one for each of the sinks' key
@@ -172,14 +172,14 @@ __host__ __device__ constexpr int attn_window_dq_slots(int S, int window, int si
 // has, none empty, at most 32 in all; 0 (one item with the rest)
 // where there are fewer such queries than another block has, or more than 32
 // blocks of sinks, which make enough items anyway.
-constexpr int attn_window_splits(int S, int window, int sinks, int hd) {
-  const int w = window < S ? window : S, k = sinks < S ? sinks : S, qb = hd == 128 ? 64 : 128;
-  const int ns = (k + 127) / 128, nq = (S + qb - 1) / qb;
+constexpr int attn_window_splits(int S, int window, int sinks) {
+  const int w = window < S ? window : S, k = sinks < S ? sinks : S;
+  const int ns = (k + 127) / 128, nq = (S + 127) / 128;
   if (ns == 0 || ns > 32) return 0;
-  const int near = (126 + w) / qb + 1;                         // query blocks of key block 0's window
-  const int usual = near > 512 / qb ? near : 512 / qb;         // of an item
-  const int far = nq - near;                                   // behind it
-  const int least = nq - ((ns - 1) * 128 + 126 + w) / qb - 1;  // the last sinks' block's
+  const int near = (126 + w) / 128 + 1;                         // query blocks of key block 0's window
+  const int usual = near > 4 ? near : 4;                        // of an item
+  const int far = nq - near;                                    // behind it
+  const int least = nq - ((ns - 1) * 128 + 126 + w) / 128 - 1;  // the last sinks' block's
   if (far < usual || least < 1) return 0;
   int f = (far + usual - 1) / usual;
   f = f < 32 / ns ? f : 32 / ns;
@@ -188,7 +188,7 @@ constexpr int attn_window_splits(int S, int window, int sinks, int hd) {
 // Floats of the sinks' partial dK and dV (fp32 [B, Hkv, sinks' blocks, splits +
 // 1, dK and dV, 128, hd]).
 constexpr int64_t attn_window_part_floats(int B, int S, int Hkv, int hd, int window, int sinks) {
-  const int f = attn_window_splits(S, window, sinks, hd), k = sinks < S ? sinks : S;
+  const int f = attn_window_splits(S, window, sinks), k = sinks < S ? sinks : S;
   return f ? (int64_t)B * Hkv * ((k + 127) / 128) * (f + 1) * 256 * hd : 0;
 }
 // dK and dV of the sinks' key blocks from those parts, in a fixed order
