@@ -490,8 +490,10 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
       // by groups of 32 columns, read from TMEM once for the row max and once
       // for P: a group that none of the warp's rows sees is not read (its P is
       // 0), one that all see is not masked, and the others take one mask word
-      // per row (2 x 8192 tokens, window 1024: 390 us with the mask as
-      // comparisons on 128 columns).
+      // per row (2 x 8192 tokens, 32 / 8 heads of 128, window 1024, 4 sinks:
+      // 390 us with the mask as comparisons on 128 columns, 281 us so: 920
+      // TFLOP/s of visible pairs, 0.48 of the measured burst; with the cut
+      // blocks 1.14 times as many pairs are multiplied).
       auto block = [&](int j, int kb, long G, auto diag) -> bool {
         constexpr bool DIAG = decltype(diag)::value;
         if (!__all_sync(0xffffffffu, mbar_wait(s_full(tt), (uint32_t)(G & 1), abort_flag))) return false;
@@ -776,11 +778,14 @@ __device__ __forceinline__ int dq_slot(const AttWindow& win, int j) {
 // them in registers, so the next block's are formed while they work, and dV,
 // dK and dQ run behind.
 //
-// What bounds it, from clock stamps of the roles: one thread issues every MMA
-// at 55 to 77 cycles each (32 a block, 24 of them 64 wide, 32 cycles of work:
-// 2,450 cycles a block), and the threads' 16,384 exponentials take at least
-// 1,024.  Hence blocks of 128 queries: 64-query blocks in two CTAs per SM (24
-// MMAs per 64 queries) lost where walks are long.  With two Q / dO stages the
+// What bounds it: shared memory's 128 bytes a clock.  A block takes 2,450
+// clocks, and counted are 1,408 for the MMAs' operands (S^T, dP^T 512, dV 128,
+// dK 384, dQ 384), 256 for Q and dO coming in, 256 for dS^T and 512 for dQ
+// through its staging tiles; the threads' 16,384 exponentials take 1,024
+// beside them.  Hence blocks of 128 queries: 64-query blocks in two CTAs per SM
+// (MMAs 64 wide read 6 KB in 32 clocks of work) lost where walks are long.
+// Whole backward, 8 x 1024 tokens, 16 heads, causal: 193 us with 64-query
+// blocks, 97 us so (443 TFLOP/s).  With two Q / dO stages the
 // loads of a block started only when the block two before it was done, 1,300
 // cycles of waiting a block; P^T in TMEM makes room for three.  lse and D come
 // from a warp of their own, two blocks ahead.  A CTA per item spent more time
@@ -1368,8 +1373,8 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
 // coming in, dS^T, and dQ^T going through (its fp32 sums are 64 KB a block);
 // a block takes 4,450 clocks.  Blocks of 64 queries (MMAs 64 wide, which read
 // 6 KB in 32 clocks of work) took 2 x 2,450: 8 x 2048 tokens, 32 / 8 heads,
-// 897 us against 796 us for the whole backward (864 TFLOP/s); 2 x 8192, window
-// 1024, 4 sinks, 968 and 794 us.  Measured on the way: the threads storing dQ
+// 897 us against 790 us for the whole backward (870 TFLOP/s); 2 x 8192, window
+// 1024, 4 sinks, 968 and 787 us.  Measured on the way: the threads storing dQ
 // themselves, as one reduction instruction per row, 862 us, and four warps of
 // their own doing so 918 us (such instructions leave an SM at 32 bytes a clock
 // and hold up the stores of dS^T behind them); dO's one buffer refilled after

@@ -11,7 +11,10 @@
 // as zeros; a block that holds an infinity or a NaN has a NaN scale, so it
 // comes back as NaN and a step that diverged is not hidden.
 //
-// Every kernel here streams its rows once and is bound by memory traffic.  A
+// Every kernel here streams its rows once and is bound by memory traffic: 16384
+// x 4096, forward saving int8 70 us (6,740 GB/s), forward from the codes 70 us,
+// together 0.96 of a measured copy's rate; 4095 x 12288 e4m3, backward 133.7 us
+// with its gain sums (757 MB, 5,660 GB/s, 0.84; the sums' launch is 6 us).  A
 // lane holds four columns (a float4, or four codes), so a warp holds a block:
 // its largest magnitude is one integer warp reduction of |x|'s bits, which
 // order like the values, with infinities and NaNs on top.
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kThreads)
 // ------------------------------------------------------------------ RMSNorm forward
 // Groups of LANES threads (a power of two, 32 to 256) take a row each, so
 // that narrow rows fill a CTA too (65536 x 512: save 88.7 us with a CTA per
-// row); thread t of a group holds the quads t, t + LANES, ... (CH of them), so
+// row, 43.7 us so); thread t of a group holds the quads t, t + LANES, ... (CH of them), so
 // each warp holds whole blocks.  LOAD: the row comes from the codes (and is
 // written to xout unless that is null); else from x, and is saved.
 template <int LANES, int CH, int FMT, bool LOAD>
@@ -272,6 +275,9 @@ void norm_fwd8(const float* x, const bf16* g, bf16* y, float* rstd, uint8_t* q, 
 // rows, and d % 16 == 8 needs no special case, as a bulk copy would.  At CH 8
 // the ring holds dy and the codes, and dres is only brought into L2 ahead.
 // The gain gradient of a thread's columns stays in registers over all rows.
+// 4095 x 12288: 245 us with a row's loads held by registers, 133 us with the
+// ring; 16384 x 4096: 168 us, where the fp32 checkpoint's backward takes 190;
+// 4096 x 16384 (CH 8): 216 us, 4,680 GB/s, bound by dres's late loads.
 constexpr int kBwdThreads = 512;
 
 template <int CH>
