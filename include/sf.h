@@ -421,15 +421,17 @@ int sf_op_attn_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
  * query q sees key k when k <= q and (q - k < window or k < sinks): its own
  * and the window - 1 keys before it, and the first `sinks` tokens of its
  * sequence.  window >= 1 (window >= S: plain causal attention), sinks >= 0;
- * both may exceed S.  B and Hkv at most 65535, S at most 2^30.  Key blocks that no query of a tile sees are not read; in
- * the blocks that are read, a value row has to be finite even where it is
- * masked (its weight is 0, and 0 * inf is NaN). */
+ * both may exceed S.  B and Hkv at most 65535, S at most 2^30, qkv at most
+ * 2^38 elements.  Key blocks that no query of a tile sees are not read; in the
+ * blocks that are read, a value row has to be finite even where it is masked
+ * (its weight is 0, and 0 * inf is NaN). */
 int sf_op_attn_window_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int32_t B, int32_t S,
                           int32_t Hq, int32_t Hkv, int32_t hd, int32_t window, int32_t sinks,
                           void* stream);
 
 /* Backward of sf_op_attn_window_fwd: arguments as sf_op_attn_bwd with the
- * window and sinks of the forward.  dq_acc: fp32 of
+ * window and sinks of the forward; in the blocks that are read q, k, v and
+ * dout have to be finite, masked or not.  dq_acc: fp32 of
  * sf_op_attn_window_dq_scratch(...) elements (16-byte aligned).  With
  * deterministic != 0 the scratch has a slot for each key block that a query
  * block can see (about window / 128 + sinks / 128 + 2, not S / 128), summed in

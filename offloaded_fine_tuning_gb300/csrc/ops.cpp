@@ -188,9 +188,12 @@ int sf_op_attn_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
 // Sizes of the windowed attention; its backward's grid bounds B and Hkv.
 static bool window_sizes(int32_t B, int32_t S_, int32_t Hq, int32_t Hkv, int32_t hd, int32_t window,
                          int32_t sinks) {
-  return B >= 0 && B <= 65535 && S_ >= 0 && S_ <= (1 << 30) && Hq >= 1 && Hkv >= 1 && Hkv <= 65535 &&
-         Hq % Hkv == 0 && (int64_t)Hq + 2 * (int64_t)Hkv <= (1 << 22) && (hd == 64 || hd == 128) &&
-         window >= 1 && sinks >= 0;
+  if (!(B >= 0 && B <= 65535 && S_ >= 0 && S_ <= (1 << 30) && Hq >= 1 && Hkv >= 1 && Hkv <= 65535 &&
+        Hq % Hkv == 0 && (int64_t)Hq + 2 * (int64_t)Hkv <= (1 << 22) && (hd == 64 || hd == 128) &&
+        window >= 1 && sinks >= 0))
+    return false;
+  // no device holds more than 2^38 elements, and the scratch's size stays in 64 bits
+  return (int64_t)B * S_ <= ((int64_t)1 << 38) / (((int64_t)Hq + 2 * (int64_t)Hkv) * hd);
 }
 
 int sf_op_attn_window_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int32_t B, int32_t S_,

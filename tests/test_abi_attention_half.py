@@ -92,7 +92,7 @@ def blocks_seen(S, window, sinks, qb):
 @pytest.mark.parametrize("sinks", [0, 1, 128, 129, 4000])
 def test_window_scratch_holds_every_visited_block(sf, S, window, sinks):
     B, Hq = 2, 3
-    for hd, qb in ((64, 128), (128, 64)):
+    for hd, qb in ((64, 128), (128, 128)):
         per = B * S * Hq * hd
         # behind dQ: whole 128-key tiles of partial dK and dV, for sinks only
         extra = sf.attn_window_dq_scratch_floats(B, S, Hq, hd, window, sinks, 0) - per
@@ -104,6 +104,18 @@ def test_window_scratch_holds_every_visited_block(sf, S, window, sinks):
                 (B, S, Hq, 64, 0, 0, 1), (B, S, Hq, 64, 1, -1, 1), (65536, S, Hq, 64, 1, 0, 1),
                 (B, 2 ** 31 - 1, Hq, 64, 1, 0, 1)):
         assert sf.attn_window_dq_scratch_floats(*bad) == -1
+
+
+def test_window_of_more_elements_than_a_device_holds_is_refused(sf):
+    """Each size alone is allowed; their product would pass 64 bits in the scratch size."""
+    for B, S, Hq, Hkv, hd in ((65535, 1 << 30, 1 << 21, 1, 128), (1, 1 << 30, 1 << 20, 16, 64),
+                              (65535, 1 << 20, 512, 512, 128)):
+        assert sf.attn_window_dq_scratch_floats(B, S, Hq, hd, 64, 4, 1) == -1
+        assert sf.op_attn_window_fwd(A, A, A, B, S, Hq, Hkv, hd, 64, 4) == sf.SF_EINVAL
+        assert sf.op_attn_window_bwd(A, A, A, A, A, A, A, B, S, Hq, Hkv, hd, 64, 4) == sf.SF_EINVAL
+    # the largest one allowed: 2^38 elements of Q, K and V, a slot for each of its blocks
+    n = sf.attn_window_dq_scratch_floats(1, 1 << 30, 2, 64, 1 << 30, 0, 1)
+    assert n == (1 << 23) * (1 << 30) * 128
 
 
 def test_ckpt8_refuses(sf):
