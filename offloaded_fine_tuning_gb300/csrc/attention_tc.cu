@@ -42,18 +42,6 @@ namespace sf {
 
 namespace {
 
-// Grid position in longest-first order: the CTAs are dispatched roughly in
-// linear block order, so every CTA of rank 0 (the most work) is placed before
-// any CTA of rank 1, and so on, whatever the other two coordinates.
-__device__ __forceinline__ void grid_rank_first(int& rank, int& y, int& z) {
-  const int lin = (int)(blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z));
-  const int per = (int)(gridDim.y * gridDim.z);
-  rank = lin / per;
-  const int rem = lin - rank * per;
-  y = rem % (int)gridDim.y;
-  z = rem / (int)gridDim.y;
-}
-
 // 2^x on the special-function unit (relative error ~2^-22, flushes denormals).
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -1372,19 +1360,47 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
 // half of that: 2,304 clocks a block for operands, and 1,792 for Q and dO
 // coming in, dS^T, and dQ^T going through (its fp32 sums are 64 KB a block);
 // a block takes 4,450 clocks.  Blocks of 64 queries (MMAs 64 wide, which read
-// 6 KB in 32 clocks of work) took 2 x 2,450: 8 x 2048 tokens, 32 / 8 heads,
-// 897 us against 790 us for the whole backward (870 TFLOP/s); 2 x 8192, window
-// 1024, 4 sinks, 968 and 787 us.  Measured on the way: the threads storing dQ
-// themselves, as one reduction instruction per row, 862 us, and four warps of
-// their own doing so 918 us (such instructions leave an SM at 32 bytes a clock
-// and hold up the stores of dS^T behind them); dO's one buffer refilled after
-// the next but one Q, 1,020 us.
-// Testing the barriers a step ahead gained nothing here.
+// 6 KB in 32 clocks of work) took 2 x 2,450.  Whole backward, 8 x 2048 tokens,
+// 32 / 8 heads: 897 us then, 790 us with 128 queries, 711 us (967 TFLOP/s) with
+// the heads in chunks (head_chunks); 2 x 8192, window 1024, 4 sinks: 968 and
+// 787 us.  Measured on the way to 790: the threads storing dQ themselves, as one
+// reduction instruction per row, 862 us, and four warps of their own doing so
+// 918 us (such instructions leave an SM at 32 bytes a clock and hold up the
+// stores of dS^T behind them); dO's one buffer refilled after the next but one
+// Q, 1,020 us.  Testing the barriers a step ahead gained nothing here.
 //
 // Every mbarrier below completes at most once before its waiter has seen the
 // previous completion (each has a dependency chain through its waiter), so
 // parity waits are unambiguous.
 namespace {
+// The order of the items of a grid (ranks, kv heads, batch); CTAs are dispatched
+// roughly in linear block order.  Longest first over the whole grid (rank 0,
+// which without a window sees the most query blocks, for every head before rank
+// 1) balances the SMs, but each rank reads every head's Q and dO and adds to its
+// dQ anew, from DRAM where the heads do not fit into L2 together.  So without a
+// window the first `chunked` of the heads (of all batches) are taken `size` at a
+// time, longest first in each chunk (head_chunks).
+struct HeadChunks {
+  int size, chunked;
+  __device__ __forceinline__ void item(int& rank, int& g, int& b) const {
+    int lin = (int)(blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z));
+    const int ranks = (int)gridDim.x;
+    int head0 = 0, n = size;
+    if (lin < chunked * ranks) {
+      const int c = lin / (size * ranks);
+      head0 = c * size;
+      lin -= c * size * ranks;
+    } else {
+      head0 = chunked;
+      n = (int)(gridDim.y * gridDim.z) - chunked;
+      lin -= chunked * ranks;
+    }
+    rank = lin / n;
+    const int head = head0 + lin - rank * n;
+    b = head / (int)gridDim.y;
+    g = head - b * (int)gridDim.y;
+  }
+};
 constexpr int kAttBwd2Threads = 448;  // TMA warp, MMA warp, 8 softmax-gradient warps, 4 dQ warps
 struct AttBwd2Cfg {
   static constexpr int KV = 32768;  // 128 keys x 128 hd
@@ -1415,7 +1431,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
                         const __grid_constant__ CUtensorMap tm_dkv, const float* __restrict__ lse,
                         const float* __restrict__ delta, const float2* __restrict__ cs, int S,
                         int Hq, int Hkv, float scale, float scale_log2, AttWindow win,
-                        float* __restrict__ part, int* err) {
+                        HeadChunks chunks, float* __restrict__ part, int* err) {
   using C = AttBwd2Cfg;
   constexpr int HD = 128;
   constexpr uint32_t ID_SP = umma_idesc_bf16(128, 128, false, false);  // S^T, dP^T
@@ -1448,7 +1464,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int rank, g, b;
-  grid_rank_first(rank, g, b);  // without a window key block 0 sees the most query blocks
+  chunks.item(rank, g, b);
   const KeyWork work = key_work<WIN, PART>(win, rank, S);
   const int grp = Hq / Hkv;
   const int j = work.j, k0 = j * 128;
@@ -2071,6 +2087,26 @@ int bwd_tc(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
+// A chunk has an item for every SM.  The heads left for the end, longest first
+// together, are worth 1.2 times the longest item to each SM: with half of that
+// the ends of the SMs' work lie further apart (8 x 2048 tokens, 32 / 8 heads:
+// 790 us without chunks, 711 us so, 727 us with half; 8192 tokens, 8 heads: 296
+// us, and 313 us with half; 8 x 1024, 32 heads: 378 and 303 us; chunks of twice
+// the size 714 and 309 us).  With a window neighbouring ranks share most of what
+// they read, so nothing is gained (2 x 8192, window 1024: 736 us, 742 with
+// chunks).
+HeadChunks head_chunks(const dim3& grid, bool window) {
+  const int heads = (int)(grid.y * grid.z), sms = num_sms(), ranks = (int)grid.x;
+  HeadChunks c{heads, 0};
+  if (window) return c;
+  // an item of rank r has ranks - r blocks (times the group's heads)
+  const int tail = (12 * sms / 5 + ranks) / (ranks + 1), size = (sms + ranks - 1) / ranks;
+  if (heads < tail + size) return c;
+  c.size = size;
+  c.chunked = (heads - tail) / size * size;
+  return c;
+}
+
 template <bool DET, bool WIN, bool PART>
 int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* dout,
             const float* lse, float* delta, float* dq_acc, __nv_bfloat16* dqkv, int B, int S, int Hq,
@@ -2111,7 +2147,7 @@ int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat1
   float* part = dq_acc + (DET ? (int64_t)slots : 1) * B * S * WO;
   if (!launch_dependent(attn_bwd_tc2_kernel<DET, WIN, PART>, grid, kAttBwd2Threads, C::SMEM, st, tkv, tq, td,
                         tdq, tdkv, lse, (const float*)delta, cs, S, Hq, Hkv, scale,
-                        scale * 1.4426950408889634f, win, part, err))
+                        scale * 1.4426950408889634f, win, head_chunks(grid, WIN), part, err))
     return -3;
   if (PART)
     attn_sink_join(part, dqkv, B, S, Hq, Hkv, HD, scale, cs, win.splits, win.sinks, st);
@@ -2170,6 +2206,8 @@ int attn_window_bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv
                     bool deterministic, int* err, cudaStream_t st) {
   if (B <= 0 || S <= 0) return 0;
   if (Hkv <= 0 || Hq % Hkv || window < 1 || sinks < 0) return -1;
+  if (window >= S || sinks >= S)  // nothing but the causal mask (which has a slot per key block too)
+    return attn_bwd(qkv, o, dout, lse, delta, dq_acc, dqkv, B, S, Hq, Hkv, hd, cs, deterministic, err, st);
   const AttWindow win = clip(window, sinks, S, B, Hq, Hkv, hd);
   const auto fn = win.splits > 0 ? (deterministic ? bwd<true, true, true> : bwd<false, true, true>)
                                  : (deterministic ? bwd<true, true> : bwd<false, true>);
@@ -2191,6 +2229,7 @@ int attn_window_fwd(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int 
                     int Hkv, int hd, int window, int sinks, int* err, cudaStream_t st) {
   if (B <= 0 || S <= 0) return 0;
   if (Hkv <= 0 || Hq % Hkv || window < 1 || sinks < 0) return -1;
+  if (window >= S || sinks >= S) return attn_fwd(qkv, o, lse, B, S, Hq, Hkv, hd, err, st);
   const AttWindow win = clip(window, sinks, S, B, Hq, Hkv, hd);
   if (hd == 64) return fwd_pp<64, true>(qkv, o, lse, B, S, Hq, Hkv, win, err, st);
   if (hd == 128) return fwd_pp<128, true>(qkv, o, lse, B, S, Hq, Hkv, win, err, st);
