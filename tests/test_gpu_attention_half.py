@@ -363,6 +363,23 @@ def test_window_backward(B, S, Hq, Hkv, hd, window, sinks, det):
         assert torch.equal(again, got)
 
 
+@pytest.mark.parametrize("det", [0, 1])
+@pytest.mark.parametrize("B,S,Hq,Hkv,hd", [
+    (8, 390, 16, 16, 128),   # 128 heads and batches of four key blocks: one chunk and the rest
+    (3, 1000, 80, 40, 128),  # 120 of eight: several chunks
+    (3, 1000, 80, 40, 64),
+])
+def test_backward_of_many_heads(B, S, Hq, Hkv, hd, det):
+    """Without a window the backward takes heads in chunks where there are many."""
+    qkv, dout = win_inputs(B, S, Hq, Hkv, hd, seed=4)
+    o, lse = win_fwd(qkv, B, S, Hq, Hkv, hd, S, 0)
+    got = win_bwd(qkv, o, dout, lse, B, S, Hq, Hkv, hd, S, 0, None, det)
+    for b in range(B):  # one sequence at a time: the float64 scores of all are too large
+        rows = slice(b * S, (b + 1) * S)
+        ref, tol = attn_bwd_ref(qkv[rows], o[rows], dout[rows], lse[b:b + 1], 1, S, Hq, Hkv, hd, S, 0)
+        within(got[rows], ref, tol)
+
+
 @pytest.mark.parametrize("hd,Hq", [(64, 4), (128, 4), (128, 3)])
 def test_window_wider_than_the_sequence_is_causal_attention(hd, Hq):
     B, S, Hkv = 2, 390, 1
