@@ -766,13 +766,17 @@ __device__ __forceinline__ int dq_slot(const AttWindow& win, int j) {
 // them in registers, so the next block's are formed while they work, and dV,
 // dK and dQ run behind.
 //
-// What bounds it: shared memory's 128 bytes a clock.  A block takes 2,450
-// clocks, and counted are 1,408 for the MMAs' operands (S^T, dP^T 512, dV 128,
-// dK 384, dQ 384), 256 for Q and dO coming in, 256 for dS^T and 512 for dQ
-// through its staging tiles; the threads' 16,384 exponentials take 1,024
-// beside them.  Hence blocks of 128 queries: 64-query blocks in two CTAs per SM
-// (MMAs 64 wide read 6 KB in 32 clocks of work) lost where walks are long.
-// Whole backward, 8 x 1024 tokens, 16 heads, causal: 193 us with 64-query
+// What bounds it: a block takes 3,900 clocks in a long walk (clock stamps).  One
+// thread needs 2,550 to issue the 32 MMAs, which is shared memory's 128 bytes a
+// clock: counted are 1,408 for their operands (S^T, dP^T 512, dV 128, dK 384, dQ
+// 384), 256 for Q and dO coming in, 256 for dS^T and 512 for dQ through its
+// staging tiles.  Another 630 it waits for P^T and dS^T, since the threads'
+// chain is as long (1,450 for the exponentials and dS^T, 400 to store, 830 for
+// dQ).  Four warps of their own for dQ, dK and dV leave the threads fewer
+// registers, so that S^T and dP^T are released later: 268 us against 256 us (2 x
+// 4096 tokens, 16 / 4 heads).  Blocks have 128 queries: 64-query blocks in two
+// CTAs per SM (MMAs 64 wide read 6 KB in 32 clocks of work) lost where walks are
+// long.  Whole backward, 8 x 1024 tokens, 16 heads, causal: 193 us with 64-query
 // blocks, 97 us so (443 TFLOP/s).  With two Q / dO stages the
 // loads of a block started only when the block two before it was done, 1,300
 // cycles of waiting a block; P^T in TMEM makes room for three.  lse and D come
