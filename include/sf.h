@@ -95,7 +95,8 @@ typedef struct sf_ctx sf_ctx;
  *     those copies slide, a little over a quarter of the bytes, the device
  *     keeping the last four.  The forward is exact; the recompute and the
  *     backward of those layers run at the checkpoint's values (off by at most
- *     1/254 of the largest of 128), so their gradients differ slightly.
+ *     1/254 of the largest of 128), so their gradients differ slightly.  Any
+ *     other value is refused (SF_EINVAL).
  *   deterministic: 0 = the attention backward adds the dQ contributions of
  *     its key blocks into one fp32 buffer in whatever order they arrive, so
  *     the last bits of a gradient can differ between two identical steps;

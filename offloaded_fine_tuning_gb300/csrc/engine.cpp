@@ -1241,6 +1241,7 @@ const char* validate(const sf_config* c) {
       c->deterministic < 0 || c->deterministic > 1 || c->bf16_adam_state < 0 ||
       c->bf16_adam_state > 1 || c->fp16_grads < 0 || c->fp16_grads > 1)
     return "qkv_bias, tie_embeddings, deterministic, bf16_adam_state and fp16_grads must be 0 or 1";
+  if (c->offload_activations < 0 || c->offload_activations > 2) return "offload_activations must be 0, 1 or 2";
   if (!(c->loss_scale >= 0.f) || c->loss_scale > 16777216.f) return "loss_scale must be in [0, 2^24]";
   return nullptr;
 }
