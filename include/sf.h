@@ -93,9 +93,11 @@ typedef struct sf_ctx sf_ctx;
  *     but the last three keeps its input as int8 codes with a scale for each
  *     128 values (SF_CKPT_INT8 below; saved by the layer's first norm), and
  *     those copies slide, a little over a quarter of the bytes, the device
- *     keeping the last four.  The forward is exact; the recompute and the
- *     backward of those layers run at the checkpoint's values (off by at most
- *     1/254 of the largest of 128), so their gradients differ slightly.  Any
+ *     keeping the last four.  The forward, and with
+ *     `deterministic` the last three layers' gradients, are bit for bit those
+ *     of 0; the recompute and the backward of the layers before run at the
+ *     checkpoint's values (off by at most 1/254 of the largest of 128), so
+ *     their gradients differ slightly.  Any
  *     other value is refused (SF_EINVAL).
  *   deterministic: 0 = the attention backward adds the dQ contributions of
  *     its key blocks into one fp32 buffer in whatever order they arrive, so
@@ -498,8 +500,9 @@ int sf_op_ckpt8_save(const float* x, uint8_t* q, float* scale, int32_t fmt, int6
                      int32_t d, void* stream);
 int sf_op_ckpt8_load(const uint8_t* q, const float* scale, float* x, int32_t fmt, int64_t rows,
                      int32_t d, void* stream);
-/* sf_op_rmsnorm_fwd of x (y and rstd from x itself, not from its codes) that
- * also saves x, reading x once: the forward of a checkpointed layer. */
+/* sf_op_rmsnorm_fwd of x (y and rstd from x itself, not from its codes, and bit
+ * for bit that call's) that also saves x, reading x once: the forward of a
+ * checkpointed layer. */
 int sf_op_rmsnorm_fwd_save8(const float* x, const uint16_t* g, uint16_t* y, float* rstd,
                             uint8_t* q, float* scale, int32_t fmt, int64_t rows, int32_t d,
                             float eps, void* stream);

@@ -167,11 +167,19 @@ __global__ void __launch_bounds__(kThreads)
 // row, 43.7 us so); thread t of a group holds the quads t, t + LANES, ... (CH of them), so
 // each warp holds whole blocks.  LOAD: the row comes from the codes (and is
 // written to xout unless that is null); else from x, and is saved.
+// When saving, the squares are added in rmsnorm_fwd's order, so that saving
+// changes no bit of y and rstd: there thread t of 256 has the quads t, t + 256,
+// ..., and its eight warps' sums meet in a tree (w with w ^ 4, w ^ 2, w ^ 1).  A
+// thread of a narrower group stands for SUMS threads of those, whose sums it
+// keeps apart until their warps' sums are joined in that tree (65536 x 1024:
+// 82.6 us, 80.5 us with one sum; no difference at 512 and 2048).
 template <int LANES, int CH, int FMT, bool LOAD>
 __global__ void __launch_bounds__(kThreads)
     norm_fwd8_kernel(const float* __restrict__ x, const bf16* __restrict__ g,
                      bf16* __restrict__ y, float* __restrict__ rstd_out, uint8_t* q, float* scale,
                      float* __restrict__ xout, int64_t rows, int nb, int d, float eps) {
+  constexpr int SUMS = LOAD ? 1 : kThreads / LANES < CH ? kThreads / LANES : CH;
+  static_assert(SUMS == 1 || CH == 4, "the joins below");
   __shared__ float sh[kThreads / 32];
   const int group = threadIdx.x / LANES, t = threadIdx.x % LANES;
   const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + group;
@@ -179,7 +187,7 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t* qr = reinterpret_cast<uint32_t*>(q + row * d);
   float* sr = scale + row * nb;
   float4 v[CH];
-  float ss = 0.f;
+  float part[SUMS] = {};
   if (LOAD) {
     uint32_t c[CH];
     float s[CH];
@@ -201,7 +209,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 #pragma unroll
   for (int k = 0; k < CH; ++k)
-    ss += v[k].x * v[k].x + v[k].y * v[k].y + v[k].z * v[k].z + v[k].w * v[k].w;
+    part[k % SUMS] += v[k].x * v[k].x + v[k].y * v[k].y + v[k].z * v[k].z + v[k].w * v[k].w;
   if (!LOAD) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -221,7 +229,10 @@ __global__ void __launch_bounds__(kThreads)
       if (i < n4) xo[i] = v[k];
     }
   }
-  ss = warp_sum(ss);
+#pragma unroll
+  for (int k = 0; k < SUMS; ++k) part[k] = warp_sum(part[k]);
+  float ss = SUMS == 4 ? (part[0] + part[2 % SUMS]) + (part[1 % SUMS] + part[3 % SUMS])
+             : SUMS == 2 ? part[0] + part[1 % SUMS] : part[0];
   if (LANES > 32) {
     if (lane == 0) sh[threadIdx.x >> 5] = ss;
     __syncthreads();
