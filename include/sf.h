@@ -513,7 +513,8 @@ int sf_op_rmsnorm_fwd_load8(const uint8_t* q, const float* scale, const uint16_t
                             float* rstd, float* x, int32_t fmt, int64_t rows, int32_t d, float eps,
                             void* stream);
 /* sf_op_rmsnorm_bwd at the values of codes and scales (rstd: theirs, from
- * sf_op_rmsnorm_fwd_load8).  scratch as sf_op_rmsnorm_bwd. */
+ * sf_op_rmsnorm_fwd_load8).  scratch as sf_op_rmsnorm_bwd.  dx may be dres or
+ * dy. */
 int sf_op_rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const uint16_t* g,
                             const float* rstd, const float* dy, const float* dres, float* dx,
                             uint16_t* dxb, uint16_t* dg, float* scratch, int32_t fmt, int64_t rows,

@@ -286,6 +286,8 @@ void norm_fwd8(const float* x, const bf16* g, bf16* y, float* rstd, uint8_t* q, 
 // rows, and d % 16 == 8 needs no special case, as a bulk copy would.  At CH 8
 // the ring holds dy and the codes, and dres is only brought into L2 ahead.
 // The gain gradient of a thread's columns stays in registers over all rows.
+// dx may be dres or dy: a thread reads its quads of a row before it writes them,
+// and no other thread touches them.
 // 4095 x 12288: 245 us with a row's loads held by registers, 133 us with the
 // ring; 16384 x 4096: 168 us, where the fp32 checkpoint's backward takes 190;
 // 4096 x 16384 (CH 8): 216 us, 4,680 GB/s, bound by dres's late loads.
@@ -307,6 +309,13 @@ static_assert(BwdRing<8>::STAGES * BwdRing<8>::STAGE <= 230000, "ring of 8 quads
 __device__ __forceinline__ void async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// A load that may be moved ahead of the kernel's stores to dx: with dx over the
+// array that it reads, only the same thread writes the place, after this load.
+__device__ __forceinline__ float4 load_early(const float* p) {
+  float4 v;
+  asm("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -315,9 +324,8 @@ template <int CH, int FMT>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     norm_bwd8_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scale,
                      const bf16* __restrict__ g, const float* __restrict__ rstd,
-                     const float* __restrict__ dy, const float* __restrict__ dres,
-                     float* __restrict__ dx, bf16* __restrict__ dxb, float* __restrict__ dg_part,
-                     int64_t rows, int nb, int d, int lanes) {
+                     const float* dy, const float* dres, float* dx, bf16* __restrict__ dxb,
+                     float* __restrict__ dg_part, int64_t rows, int nb, int d, int lanes) {
   using R = BwdRing<CH>;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sums[2][kBwdThreads / 32];  // the warps' sums of a row, of two rows in turn
@@ -405,7 +413,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         float4 xh = decode<FMT>(sq[at], ss[k]);
         xh = make_float4(xh.x * r, xh.y * r, xh.z * r, xh.w * r);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (dres) o = R::RES ? sdr[at] : reinterpret_cast<const float4*>(dres + row * d)[i];
+        if (dres) o = R::RES ? sdr[at] : load_early(dres + row * d + 4 * i);
         o.x += r * (w.x * dv.x - xh.x * dot);
         o.y += r * (w.y * dv.y - xh.y * dot);
         o.z += r * (w.z * dv.z - xh.z * dot);
