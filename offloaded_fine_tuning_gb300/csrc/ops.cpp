@@ -17,6 +17,9 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// an array that kernels read or write element by element
+template <class T>
+bool al1(const T* p) { return (reinterpret_cast<uintptr_t>(p) & (sizeof(T) - 1)) == 0; }
 
 // One device error word per device, created on first use.
 constexpr int kMaxDev = 64;
@@ -201,7 +204,7 @@ int sf_op_attn_window_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int32_t 
                           void* stream) {
   if (!window_sizes(B, S_, Hq, Hkv, hd, window, sinks)) return SF_EINVAL;
   if (B == 0 || S_ == 0) return SF_OK;
-  if (!qkv || !o || !lse || !al16(qkv) || !al16(o)) return SF_EINVAL;
+  if (!qkv || !o || !lse || !al16(qkv) || !al16(o) || !al1(lse)) return SF_EINVAL;
   int* err = dev_err_word();
   if (!err) return SF_ECUDA;
   if (sf::attn_window_fwd(reinterpret_cast<const bf16*>(qkv), reinterpret_cast<bf16*>(o), lse, B,
@@ -226,7 +229,7 @@ int sf_op_attn_window_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t
   if (B == 0 || S_ == 0) return SF_OK;
   if (!qkv || !o || !dout || !lse || !delta || !dq_acc || !dqkv) return SF_EINVAL;
   if (!al16(qkv) || !al16(o) || !al16(dout) || !al16(dq_acc) || !al16(dqkv)) return SF_EINVAL;
-  if (reinterpret_cast<uintptr_t>(table) & 7) return SF_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(table) & 7) || !al1(lse) || !al1(delta)) return SF_EINVAL;
   int* err = dev_err_word();
   if (!err) return SF_ECUDA;
   if (sf::attn_window_bwd(reinterpret_cast<const bf16*>(qkv), reinterpret_cast<const bf16*>(o),
@@ -250,7 +253,7 @@ static bool qknorm_check(int64_t tokens, int32_t seq, int32_t Hq, int32_t Hkv, i
                          const uint16_t* gq, const uint16_t* gk, float eps, const float* table,
                          const int32_t* pos, sf::QkNormArgs* a) {
   if (seq < 1 || !(eps > 0.f) || !gq || !gk || !table || !al16(gq) || !al16(gk) || !al16(table) ||
-      (reinterpret_cast<uintptr_t>(pos) & 3))
+      !al1(pos))
     return false;
   a->tokens = tokens; a->seq = seq; a->Hq = Hq; a->Hkv = Hkv; a->hd = hd;
   a->gq = reinterpret_cast<const bf16*>(gq);
@@ -296,9 +299,7 @@ int sf_op_qknorm_rope_bwd(const uint16_t* x, int64_t ldx, const uint16_t* dy, in
   sf::QkNormArgs a;
   if (!qknorm_check(tokens, seq, Hq, Hkv, head_dim, gq, gk, eps, table, pos, &a)) return SF_EINVAL;
   if (!x || !dy || !dx || !scratch || !dgq || !dgk) return SF_EINVAL;
-  if (!al16(x) || !al16(dy) || !al16(dx) || !al16(scratch) ||
-      ((reinterpret_cast<uintptr_t>(dgq) | reinterpret_cast<uintptr_t>(dgk)) & 1))
-    return SF_EINVAL;
+  if (!al16(x) || !al16(dy) || !al16(dx) || !al16(scratch) || !al1(dgq) || !al1(dgk)) return SF_EINVAL;
   int* err = dev_err_word();
   if (!err) return SF_ECUDA;
   sf::qknorm_rope_bwd(a, reinterpret_cast<const bf16*>(x), ldx, reinterpret_cast<const bf16*>(dy),
@@ -342,7 +343,7 @@ int sf_op_rmsnorm_fwd_save8(const float* x, const uint16_t* g, uint16_t* y, floa
   if (!ckpt8_sizes(fmt, rows, d) || !(eps > 0.f)) return SF_EINVAL;
   if (rows == 0) return SF_OK;
   if (!x || !g || !y || !rstd || !q || !scale) return SF_EINVAL;
-  if (!al16(x) || !al16(y) || !al16(q) || !al16(scale) || !al16(g)) return SF_EINVAL;
+  if (!al16(x) || !al16(y) || !al16(q) || !al16(scale) || !al16(g) || !al1(rstd)) return SF_EINVAL;
   sf::rmsnorm_fwd_save8(x, reinterpret_cast<const bf16*>(g), reinterpret_cast<bf16*>(y), rstd, q,
                         scale, fmt, rows, d, eps, S(stream));
   return launched();
@@ -354,7 +355,7 @@ int sf_op_rmsnorm_fwd_load8(const uint8_t* q, const float* scale, const uint16_t
   if (!ckpt8_sizes(fmt, rows, d) || !(eps > 0.f)) return SF_EINVAL;
   if (rows == 0) return SF_OK;
   if (!q || !scale || !g || !y || !rstd) return SF_EINVAL;
-  if (!al16(q) || !al16(scale) || !al16(g) || !al16(y) || !al16(x)) return SF_EINVAL;
+  if (!al16(q) || !al16(scale) || !al16(g) || !al16(y) || !al16(x) || !al1(rstd)) return SF_EINVAL;
   sf::rmsnorm_fwd_load8(q, scale, reinterpret_cast<const bf16*>(g), reinterpret_cast<bf16*>(y),
                         rstd, x, fmt, rows, d, eps, S(stream));
   return launched();
@@ -367,7 +368,7 @@ int sf_op_rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const uint16_t
   if (!ckpt8_sizes(fmt, rows, d) || rows < 1) return SF_EINVAL;
   if (!q || !scale || !g || !rstd || !dy || !dx || !dxb || !dg || !scratch) return SF_EINVAL;
   if (!al16(q) || !al16(scale) || !al16(g) || !al16(dy) || !al16(dres) || !al16(dx) ||
-      !al16(dxb) || !al16(scratch))
+      !al16(dxb) || !al16(scratch) || !al1(rstd) || !al1(dg))
     return SF_EINVAL;
   const int parts = sf::rmsnorm_bwd_load8_parts(rows, d);
   if (!sf::rmsnorm_bwd_load8(q, scale, reinterpret_cast<const bf16*>(g), rstd, dy, dres, dx,

@@ -21,3 +21,21 @@ def test_unknown_activation_mode_is_refused(sf, value):
     assert sf.lib().sf_init_model(ctypes.byref(cfg), ctypes.byref(h)) == sf.SF_EINVAL
     assert not h.value
     assert b"offload_activations" in sf.lib().sf_last_error(None)
+
+
+A = 4096  # an aligned address that is never read: every call below is refused
+
+
+@pytest.mark.parametrize("call,at,step", [
+    ("op_attn_window_fwd", 2, 2), ("op_attn_window_bwd", 3, 2), ("op_attn_window_bwd", 4, 1),
+    ("op_rmsnorm_fwd_save8", 3, 2), ("op_rmsnorm_fwd_load8", 4, 2), ("op_rmsnorm_bwd_load8", 3, 2),
+    ("op_rmsnorm_bwd_load8", 8, 1)])
+def test_arrays_between_their_elements_are_refused(sf, call, at, step):
+    """lse, delta, rstd and dg start at a whole element of their type: between two
+    of them the kernels' accesses would fault."""
+    pointers, rest = {"op_attn_window_fwd": (3, (1, 16, 4, 2, 64, 8, 1)), "op_attn_window_bwd": (7, (1, 16, 4, 2, 64, 8, 1)),
+                      "op_rmsnorm_fwd_save8": (6, (0, 4, 128, 1e-5)), "op_rmsnorm_fwd_load8": (6, (0, 4, 128, 1e-5)),
+                      "op_rmsnorm_bwd_load8": (10, (0, 4, 128))}[call]
+    p = [A] * pointers
+    p[at] = A + step
+    assert getattr(sf, call)(*p, *rest) == sf.SF_EINVAL
