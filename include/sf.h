@@ -610,7 +610,8 @@ int sf_op_rmsnorm_bwd_noalloc(const float* x, const uint16_t* g, const float* rs
  * device.  0: no error; 1, 2, 3: a bounded wait ran out in a GEMM, an
  * attention or a cross-entropy kernel; 4: sf_op_lce met a label at or beyond
  * the vocabulary; 5: sf_op_qknorm_rope_fwd or _bwd met a position outside the
- * rotation table.  The first code a launch writes stays.  Synchronises the
+ * rotation table; 6: an attention backward found its shared memory misaligned
+ * and wrote nothing.  The first code a launch writes stays.  Synchronises the
  * device. */
 int sf_op_device_error(int32_t* out);
 

@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
   uint8_t* smem = smem_raw;
   const uint32_t s0 = smem_u32(smem);
   if (s0 & 1023u) {
-    if (threadIdx.x == 0) record_error(err, kDevAttnTimeout);
+    if (threadIdx.x == 0) record_error(err, kDevSharedBase);
     return;
   }
   const uint32_t sK = s0 + C::OFF_K, sV = s0 + C::OFF_V, sQ = s0 + C::OFF_Q, sDO = s0 + C::OFF_DO;
@@ -1448,7 +1448,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
   uint8_t* smem = smem_raw;
   const uint32_t s0 = smem_u32(smem);
   if (s0 & 1023u) {
-    if (threadIdx.x == 0) record_error(err, kDevAttnTimeout);
+    if (threadIdx.x == 0) record_error(err, kDevSharedBase);
     return;
   }
   const uint32_t sK = s0 + C::OFF_K, sV = s0 + C::OFF_V, sQ = s0 + C::OFF_Q, sDO = s0 + C::OFF_DO;

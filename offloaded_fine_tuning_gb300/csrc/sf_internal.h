@@ -15,6 +15,7 @@ enum DevErr : int {
   kDevCeTimeout = 3,
   kDevCeBadLabel = 4,  // a label at or beyond the vocabulary (the row is ignored)
   kDevBadPosition = 5,  // a position outside the rotation table (the token is not rotated)
+  kDevSharedBase = 6,   // an attention backward's shared memory does not start on 1024 bytes (nothing is written)
 };
 
 // Operand layouts of C[M,N] = A * B (all matrices row-major in memory):

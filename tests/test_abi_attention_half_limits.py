@@ -1,10 +1,14 @@
 """Refusals of the attention half's operators and of the engine's mode for
 8-bit activations that are answered on the host, before any CUDA call."""
 import ctypes
+import os
+import re
 
 import pytest
 
 from inputs import CONFIGS
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -39,3 +43,18 @@ def test_arrays_between_their_elements_are_refused(sf, call, at, step):
     p = [A] * pointers
     p[at] = A + step
     assert getattr(sf, call)(*p, *rest) == sf.SF_EINVAL
+
+
+def test_header_lists_every_device_error():
+    """Each code that a kernel can write is explained at sf_op_device_error, and a
+    kernel that waited for nothing does not report a timeout."""
+    src = lambda *p: open(os.path.join(ROOT, *p)).read()
+    csrc = ("offloaded_fine_tuning_gb300", "csrc")
+    codes = dict(re.findall(r"(kDev\w+) = (\d+)", src(*csrc, "sf_internal.h")))
+    head = src("include", "sf.h")
+    text = head[:head.index("int sf_op_device_error")].rsplit("/*", 1)[1]
+    for value in codes.values():
+        assert re.search(rf"\b{value}[,:]", text), value
+    aligned = re.findall(r"if \(s0 & 1023u\) \{\s*if \(threadIdx.x == 0\) record_error\(err, (\w+)\)",
+                         src(*csrc, "attention_tc.cu"))
+    assert aligned == ["kDevSharedBase"] * 2
