@@ -15,6 +15,7 @@
 
 #include <cstdint>
 
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "sf_internal.h"
 
@@ -184,29 +185,17 @@ __global__ void attn_sink_join_kernel(const float* __restrict__ part, bf16* __re
                    pack2(x[u][6], x[u][7]));
 }
 
+// CTAs of 256 threads for that many threads
+static dim3 grid256(int64_t threads) { return dim3((unsigned)((threads + 255) / 256)); }
+
 void attn_delta(const bf16* o, const bf16* dout, float* delta, float* zero, int B, int S, int Hq,
                 int hd, cudaStream_t st) {
   const int64_t rows = (int64_t)B * S * Hq;
-  const int64_t threads = rows * (hd / 8);
-  const unsigned grid = (unsigned)((threads + 255) / 256);
+  const dim3 grid = grid256(rows * (hd / 8));
   if (hd == 128)
     attn_delta_kernel<16><<<grid, 256, 0, st>>>(o, dout, delta, zero, rows, S, Hq);
   else
     attn_delta_kernel<8><<<grid, 256, 0, st>>>(o, dout, delta, zero, rows, S, Hq);
-}
-
-template <class... P, class... A>
-static void launch_dependent(void (*kern)(P...), int64_t threads, cudaStream_t st, A... args) {
-  cudaLaunchAttribute after[1];
-  after[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  after[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((threads + 255) / 256));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = after;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
 void attn_dq_finalize(const float* dq_acc, bf16* dqkv, int B, int S, int Hq, int Hkv, int hd,
@@ -214,15 +203,15 @@ void attn_dq_finalize(const float* dq_acc, bf16* dqkv, int B, int S, int Hq, int
                       cudaStream_t st) {
   const int64_t T = (int64_t)B * S;
   const int64_t n = T * Hq * (hd / 16);
-  launch_dependent(attn_dq_kernel, n, st, dq_acc, dqkv, T, S, Hq, Hkv, hd, scale, cs, slots, window, sinks);
+  launch_dependent(attn_dq_kernel, grid256(n), 256, 0, st, dq_acc, dqkv, T, S, Hq, Hkv, hd, scale, cs, slots, window, sinks);
 }
 
 void attn_sink_join(const float* part, bf16* dqkv, int B, int S, int Hq, int Hkv, int hd,
                     float scale, const float2* cs, int splits, int sinks, cudaStream_t st) {
   const int blocks = (sinks + 127) / 128;
   const int64_t rows = (int64_t)B * Hkv * blocks * 128;
-  launch_dependent(attn_sink_join_kernel, rows * (hd / 16), st, part, dqkv, rows, S, Hq, Hkv, hd, scale,
-                   cs, blocks, splits, sinks);
+  launch_dependent(attn_sink_join_kernel, grid256(rows * (hd / 16)), 256, 0, st, part, dqkv, rows, S, Hq, Hkv,
+                   hd, scale, cs, blocks, splits, sinks);
 }
 
 }  // namespace sf

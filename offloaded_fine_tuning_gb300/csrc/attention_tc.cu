@@ -32,9 +32,8 @@
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
-#include <utility>
-#include <vector>
 
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "sf_internal.h"
 
@@ -1953,47 +1952,6 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
 // ------------------------------------------------------------------ host side
 namespace {
 
-// Reserve `bytes` of dynamic shared memory for `kern` on the current device,
-// once per kernel and device (the attribute is per device).
-bool smem_attr_set(const void* kern, int bytes) {
-  constexpr int kMaxDev = 64;
-  static std::mutex mu;
-  static std::vector<std::pair<const void*, int>> done;  // (kernel, device)
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) {
-    cudaGetLastError();
-    return false;
-  }
-  std::lock_guard<std::mutex> l(mu);
-  for (const auto& e : done)
-    if (e.first == kern && e.second == dev) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  done.emplace_back(kern, dev);
-  return true;
-}
-
-// Launch `kern` so that it may be set up while the stream's previous kernel
-// ends; it calls wait_primary() before it uses that kernel's results.
-template <class... P, class... A>
-bool launch_dependent(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
-  cudaLaunchAttribute after[1];
-  after[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  after[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cfg.attrs = after;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess) return true;
-  cudaGetLastError();
-  return false;
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn_att() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -2029,7 +1987,7 @@ int fwd_pp(const __nv_bfloat16* qkv, __nv_bfloat16* o, float* lse, int B, int S,
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return -3;
-  if (!smem_attr_set(reinterpret_cast<const void*>(attn_fwd_pp_kernel<HD, WIN>), C::SMEM)) return -3;
+  if (!reserve_smem<attn_fwd_pp_kernel<HD, WIN>>(C::SMEM)) return -3;
   // two query heads of a group per item when the group size is even, else
   // two consecutive query blocks of one head
   const int pair_heads = (Hq / Hkv) % 2 == 0 ? 1 : 0;
@@ -2073,7 +2031,7 @@ int bwd_tc(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16
       !enc(&tdq, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dq_acc, ddq, sdq, box_dq,
            CU_TENSOR_MAP_L2_PROMOTION_NONE))
     return -3;
-  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc_kernel<DET, WIN, PART>), C::SMEM)) return -3;
+  if (!reserve_smem<attn_bwd_tc_kernel<DET, WIN, PART>>(C::SMEM)) return -3;
   attn_delta(o, dout, delta, DET ? nullptr : dq_acc, B, S, Hq, HD, st);
   const float scale = 1.f / sqrtf((float)HD);
   const int ranks = (S + 127) / 128 + (PART ? (win.sinks + 127) / 128 * win.splits : 0);
@@ -2082,8 +2040,10 @@ int bwd_tc(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16
   float* part = dq_acc + (DET ? (int64_t)slots : 1) * B * S * WO;
   if (!launch_dependent(attn_bwd_tc_kernel<DET, WIN, PART>, dim3(items < sms ? items : sms), kAttBwdThreads,
                         C::SMEM, st, tq, td, tdq, tdkv, lse, (const float*)delta, cs, S, Hq, Hkv, B,
-                        FixedDiv(Hkv * B), FixedDiv(Hkv), scale, scale * 1.4426950408889634f, win, part, err))
+                        FixedDiv(Hkv * B), FixedDiv(Hkv), scale, scale * 1.4426950408889634f, win, part, err)) {
+    cudaGetLastError();
     return -3;
+  }
   if (PART)
     attn_sink_join(part, dqkv, B, S, Hq, Hkv, HD, scale, cs, win.splits, win.sinks, st);
   attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? (S + 127) / 128 : 0,
@@ -2143,7 +2103,7 @@ int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat1
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return -3;
-  if (!smem_attr_set(reinterpret_cast<const void*>(attn_bwd_tc2_kernel<DET, WIN, PART>), C::SMEM)) return -3;
+  if (!reserve_smem<attn_bwd_tc2_kernel<DET, WIN, PART>>(C::SMEM)) return -3;
   attn_delta(o, dout, delta, DET ? nullptr : dq_acc, B, S, Hq, HD, st);
   const float scale = 1.f / sqrtf((float)HD);
   dim3 grid(nkb + (PART ? (win.sinks + 127) / 128 * win.splits : 0), Hkv, B);
@@ -2151,8 +2111,10 @@ int bwd_tc2(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat1
   float* part = dq_acc + (DET ? (int64_t)slots : 1) * B * S * WO;
   if (!launch_dependent(attn_bwd_tc2_kernel<DET, WIN, PART>, grid, kAttBwd2Threads, C::SMEM, st, tkv, tq, td,
                         tdq, tdkv, lse, (const float*)delta, cs, S, Hq, Hkv, scale,
-                        scale * 1.4426950408889634f, win, head_chunks(grid, WIN), part, err))
+                        scale * 1.4426950408889634f, win, head_chunks(grid, WIN), part, err)) {
+    cudaGetLastError();
     return -3;
+  }
   if (PART)
     attn_sink_join(part, dqkv, B, S, Hq, Hkv, HD, scale, cs, win.splits, win.sinks, st);
   attn_dq_finalize(dq_acc, dqkv, B, S, Hq, Hkv, HD, scale, cs, DET ? nkb : 0, WIN ? win.size : 0,

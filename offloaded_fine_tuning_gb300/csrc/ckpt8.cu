@@ -24,10 +24,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <mutex>
-#include <utility>
-#include <vector>
 
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "sf.h"
 #include "sf_internal.h"
@@ -457,34 +455,18 @@ int bwd_lanes(int d) {
   return n;
 }
 
-// Reserve a kernel's dynamic shared memory on the current device, once.
-bool reserve_smem(const void* kern, int bytes) {
-  static std::mutex mu;
-  static std::vector<std::pair<const void*, int>> done;  // (kernel, device)
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  std::lock_guard<std::mutex> l(mu);
-  for (const auto& e : done)
-    if (e.first == kern && e.second == dev) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return false;
-  done.emplace_back(kern, dev);
-  return true;
-}
-
 template <int CH, int FMT>
 bool norm_bwd8(const uint8_t* q, const float* scale, const bf16* g, const float* rstd,
                const float* dy, const float* dres, float* dx, bf16* dxb, float* dg_part, int parts,
                int64_t rows, int d, cudaStream_t st) {
   using R = BwdRing<CH>;
-  const auto kern = norm_bwd8_kernel<CH, FMT>;
-  if (!reserve_smem(reinterpret_cast<const void*>(kern), R::STAGES * R::STAGE)) return false;
+  if (!reserve_smem<norm_bwd8_kernel<CH, FMT>>(R::STAGES * R::STAGE)) return false;
   const int lanes = bwd_lanes(d);
   const int64_t per = (rows + (int64_t)parts * (kBwdThreads / lanes) - 1) / ((int64_t)parts * (kBwdThreads / lanes));
   // few rows a group: no more of the ring than they use
   const int smem = (int)(per < R::STAGES ? per : R::STAGES) * R::STAGE;
-  kern<<<parts, kBwdThreads, smem, st>>>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, rows,
-                                         (d + kBlock - 1) / kBlock, d, lanes);
+  norm_bwd8_kernel<CH, FMT><<<parts, kBwdThreads, smem, st>>>(q, scale, g, rstd, dy, dres, dx, dxb, dg_part, rows,
+                                                              (d + kBlock - 1) / kBlock, d, lanes);
   return true;
 }
 

@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "sf.h"
 #include "sf_internal.h"
@@ -381,16 +382,8 @@ __global__ void __launch_bounds__(1024)
 
 void gain_sums(const float* part, int parts, int n1, __nv_bfloat16* out1, int n2,
                __nv_bfloat16* out2, cudaStream_t st) {
-  cudaLaunchAttribute after[1];
-  after[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  after[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((n1 + n2 + 31) / 32));
-  cfg.blockDim = dim3(1024);
-  cfg.stream = st;
-  cfg.attrs = after;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, gain_sums_kernel, part, parts, n1, out1, n2, out2);
+  launch_dependent(gain_sums_kernel, dim3((unsigned)((n1 + n2 + 31) / 32)), 1024, 0, st, part, parts, n1, out1, n2,
+                   out2);
 }
 
 // Column sums of x [rows, cols] bf16 (row stride ld) as fp32 partials:
