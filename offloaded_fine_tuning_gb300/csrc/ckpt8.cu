@@ -95,11 +95,6 @@ __device__ __forceinline__ float4 decode(uint32_t q, float scale) {
   return make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
   const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
@@ -304,18 +299,12 @@ static_assert(BwdRing<4>::STAGES * BwdRing<4>::STAGE <= 230000, "ring of 4 quads
 static_assert(BwdRing<6>::STAGES * BwdRing<6>::STAGE <= 230000, "ring of 6 quads");
 static_assert(BwdRing<8>::STAGES * BwdRing<8>::STAGE <= 230000, "ring of 8 quads");
 
-__device__ __forceinline__ void async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // A load that may be moved ahead of the kernel's stores to dx: with dx over the
 // array that it reads, only the same thread writes the place, after this load.
 __device__ __forceinline__ float4 load_early(const float* p) {
   float4 v;
   asm("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
   return v;
-}
-__device__ __forceinline__ void async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 template <int CH, int FMT>
@@ -350,21 +339,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int i = t + k * lanes;
         if (i < n4) {
           const uint32_t at = (uint32_t)(k * kBwdThreads + threadIdx.x);
-          async16(st + R::DY + at * 16, dy + row * d + 4 * i);
+          cp_async16(st + R::DY + at * 16, dy + row * d + 4 * i);
           if (dres) {
-            if (R::RES) async16(st + R::DRES + at * 16, dres + row * d + 4 * i);
+            if (R::RES) cp_async16(st + R::DRES + at * 16, dres + row * d + 4 * i);
             else asm volatile("prefetch.global.L2 [%0];" ::"l"(dres + row * d + 4 * i));
           }
-          async4(st + R::CODES + at * 4, q + row * d + 4 * i);
+          cp_async4(st + R::CODES + at * 4, q + row * d + 4 * i);
         }
       }
       // lane k < CH copies the scale of the warp's k-th block
       const int i0 = (t & ~31) + lane * lanes;
       if (lane < CH && i0 < n4)
-        async4(st + R::SCALES + (uint32_t)(warp * 12 + lane) * 4, scale + row * nb + (i0 >> 5));
-      if (lane == 8) async4(st + R::SCALES + (uint32_t)(warp * 12 + 8) * 4, rstd + row);
+        cp_async4(st + R::SCALES + (uint32_t)(warp * 12 + lane) * 4, scale + row * nb + (i0 >> 5));
+      if (lane == 8) cp_async4(st + R::SCALES + (uint32_t)(warp * 12 + 8) * 4, rstd + row);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    cp_async_commit();
     put = put + 1 == R::STAGES ? 0 : put + 1;
   };
   const int64_t row0 = (int64_t)blockIdx.x * groups + group;
@@ -373,7 +362,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll 1
   for (int64_t row = row0; row < rows; row += stride) {
     issue(row + (R::STAGES - 1) * stride);
-    asm volatile("cp.async.wait_group %0;" ::"n"(R::STAGES - 1) : "memory");
+    cp_async_wait<R::STAGES - 1>();
     __syncwarp();
     const uint8_t* st = ring + get * R::STAGE;
     const float4* sdy = reinterpret_cast<const float4*>(st + R::DY);
@@ -423,7 +412,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();  // the warp's scales have been read: the next copies may replace them
     get = get + 1 == R::STAGES ? 0 : get + 1;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  cp_async_wait<0>();
   allow_dependents();
   float4* part = reinterpret_cast<float4*>(dg_part + (int64_t)blockIdx.x * d);
   if (groups == 1) {

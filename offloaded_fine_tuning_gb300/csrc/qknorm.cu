@@ -91,9 +91,6 @@ __device__ __forceinline__ void rotation(const QkNormArgs& a, int64_t t, int sub
   }
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t src) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -160,17 +157,17 @@ __device__ __forceinline__ void each_step(const QkNormArgs& a, const Steps& ss, 
         const int64_t c = (int64_t)h * hd + 8 * sub;
         const uint32_t at = ring + (uint32_t)(put * NS * kQkThreads) * 16u;
         if (NS == 2 || kind < 2) {  // of the values only the gradient is needed
-          copy16(at, x + pf.t * ldx + c);
-          copy16(at + kQkThreads * 16, x + pf.t * ldx + c + half);
+          cp_async16(at, x + pf.t * ldx + c);
+          cp_async16(at + kQkThreads * 16, x + pf.t * ldx + c + half);
         }
         if (NS == 4) {
-          copy16(at + 2 * kQkThreads * 16, dy + pf.t * lddy + c);
-          copy16(at + 3 * kQkThreads * 16, dy + pf.t * lddy + c + half);
+          cp_async16(at + 2 * kQkThreads * 16, dy + pf.t * lddy + c);
+          cp_async16(at + 3 * kQkThreads * 16, dy + pf.t * lddy + c + half);
         }
       }
       advance(pf);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    cp_async_commit();
     put = put + 1 == STAGES ? 0 : put + 1;
   };
 #pragma unroll 1
@@ -178,7 +175,7 @@ __device__ __forceinline__ void each_step(const QkNormArgs& a, const Steps& ss, 
   int get = 0;
 #pragma unroll 1
   while (cur.left > 0) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    cp_async_wait<STAGES - 2>();
     int kind, h;
     const bool live = head(cur.i, kind, h);
     uint4 piece[NS];
@@ -193,7 +190,7 @@ __device__ __forceinline__ void each_step(const QkNormArgs& a, const Steps& ss, 
     advance(cur);
     get = get + 1 == STAGES ? 0 : get + 1;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  cp_async_wait<0>();
 }
 
 template <int TPH>
