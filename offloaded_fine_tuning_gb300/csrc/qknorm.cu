@@ -100,18 +100,23 @@ __device__ __forceinline__ uint4 lds16(uint32_t src) {
   return v;
 }
 
-// Head ranges that a token's steps go through: steps of 32 / TPH heads, first
-// the query heads, then the key heads, then (vals) the value heads.
+// Head ranges that a token's steps go through: steps of 32 / TPH heads, of the
+// query heads, the key heads and the value heads.
 struct Steps {
   int q, k, v;
   __device__ __forceinline__ int all() const { return q + k + v; }
 };
 
-// All steps of all tokens in token order, of which each warp takes an equal
-// contiguous range.  A lane copies its 16-byte pieces of the steps ahead (NS
-// of them a step: both halves of x, and of dy) into its own places of a ring
-// in shared memory, STAGES - 1 steps before it reads them back, so no barrier
-// is needed and the bytes in flight do not depend on registers.
+// The steps of all tokens in token order, of which each warp takes an equal
+// contiguous range.  The forward (NS == 2) goes through a token's query, key and
+// value steps in turn.  The backward (NS == 4) takes one kind of normed heads at a
+// time; the value steps, as many as the key steps, follow these one by one, so
+// that the heads that a warp sums a gain's gradient over are the same whether or
+// not the value heads are copied.
+// A lane copies its 16-byte pieces of the steps ahead (NS of them a step: both
+// halves of x, and of dy) into its own places of a ring in shared memory, STAGES
+// - 1 steps before it reads them back, so no barrier is needed and the bytes in
+// flight do not depend on registers.
 // body(t, kind, h, live, piece[NS]) gets the token, the kind of head (0 query,
 // 1 key, 2 value), the lane's head and whether the lane holds a piece of it.
 template <int TPH, int NS, int STAGES, class Body>
@@ -119,32 +124,41 @@ __device__ __forceinline__ void each_step(const QkNormArgs& a, const Steps& ss, 
                                           const bf16* x, int64_t ldx, const bf16* dy, int64_t lddy,
                                           Body&& body) {
   constexpr int G = 32 / TPH;
+  constexpr bool BWD = NS == 4;
   const int lane = threadIdx.x & 31, sub = lane % TPH, slot = lane / TPH;
-  const int steps = ss.all(), hd = a.hd, half = hd / 2;
+  const int hd = a.hd, half = hd / 2;
   const bool in = 8 * sub < half;
-  const int64_t n = a.tokens * steps;
+  const int val = BWD && ss.v > 0 ? 1 : 0;  // every other step is of value heads
+  const int all = ss.all(), per = all >> val;  // steps of a token, and what ranges count
   // kind and head of the lane at step i; false where it has none
   auto head = [&](int i, int& kind, int& h) -> bool {
-    kind = i < ss.q ? 0 : i < ss.q + ss.k ? 1 : 2;
-    h = (i - (kind == 0 ? 0 : kind == 1 ? ss.q : ss.q + ss.k)) * G + slot;
-    const bool live = in && h < (kind == 0 ? a.Hq : a.Hkv);
+    bool live;
+    if (BWD) {
+      h = (i >> val) * G + slot;
+      live = in && h < (ss.q ? a.Hq : a.Hkv);
+      kind = i & val ? 2 : ss.q ? 0 : 1;
+    } else {
+      kind = i < ss.q ? 0 : i < ss.q + ss.k ? 1 : 2;
+      h = (i - (kind == 0 ? 0 : kind == 1 ? ss.q : ss.q + ss.k)) * G + slot;
+      live = in && h < (kind == 0 ? a.Hq : a.Hkv);
+    }
     h += kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + a.Hkv;
     return live;
   };
-  const int64_t warps = (int64_t)gridDim.x * kQkWarps;
+  const int64_t warps = (int64_t)gridDim.x * kQkWarps, n = a.tokens * per;
   const int64_t w = (int64_t)blockIdx.x * kQkWarps + (threadIdx.x >> 5);
   // warp w's range: n / warps steps, the first n % warps warps one more
   const int64_t each = n / warps, more = n - each * warps;
   const int64_t begin = w * each + (w < more ? w : more);
-  const int left0 = (int)(each + (w < more ? 1 : 0));
+  const int left0 = (int)(each + (w < more ? 1 : 0)) << val;
   struct Cursor {
     int64_t t;
     int i, left;
   };
-  Cursor pf{begin / steps, (int)(begin % steps), left0}, cur = pf;
+  Cursor pf{begin / per, (int)(begin % per) << val, left0}, cur = pf;
   auto advance = [&](Cursor& c) {
     --c.left;
-    if (++c.i == steps) {
+    if (++c.i == all) {
       c.i = 0;
       ++c.t;
     }

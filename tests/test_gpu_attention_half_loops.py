@@ -105,6 +105,27 @@ def test_qknorm_of_many_steps_and_four_strides(Hq, Hkv, hd, pads):
     within(dgk, sums[2], BF * sums[2].abs() + sums[3])
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,hd", [(5948, 3, 1, 64), (3, 8, 8, 144), (5, 9, 3, 176), (55, 8, 8, 256),
+                                         (47, 16, 8, 80), (2748, 35, 5, 256), (5003, 16, 2, 128), (1, 1, 1, 16)])
+def test_qknorm_gain_sums_in_place_and_beside(T, Hq, Hkv, hd):
+    """The same order of the gains' sums whether the value heads are copied or stay."""
+    x, gq, gk, dy, W = qk_inputs(T, Hq, Hkv, hd)
+    tab, p = table(T, hd), lambda t: t.data_ptr()
+    out = []
+    for place in (False, True, False):
+        d = dy.clone()
+        dx = d if place else torch.empty_like(d)
+        sc = torch.empty(sf.qknorm_rope_bwd_scratch(T, Hq, Hkv, hd), **F32T)
+        dg = torch.empty(2, hd, dtype=torch.bfloat16, device="cuda")
+        assert sf.op_qknorm_rope_bwd(p(x), W, p(d), W, p(dx), W, T, T, Hq, Hkv, hd, p(gq), p(gk), EPS, p(tab), 0,
+                                     p(sc), p(dg[0]), p(dg[1]), stream()) == 0
+        sync()
+        out.append((dx, dg, sc))
+    for other in out[1:]:
+        for a, b in zip(out[0], other):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ windowed attention
 MANY_ITEMS = [  # B, S, Hq, Hkv, hd, window, sinks: several items for each SM, forward and (head dim 64) backward
     (8, 1001, 16, 16, 64, 250, 0),
