@@ -400,7 +400,7 @@ def run_ours(args, c):
     host_gbs = sf.probe_host_bandwidth(0, 8 << 30)
 
     m = load_model(sf, c, args.ring or c.ring_slots, 0 if args.sync_updates else 1,
-                   1 if args.offload_activations else 0, 1 if args.bf16_adam_state else 0)
+                   args.offload_activations, 1 if args.bf16_adam_state else 0)
     adam = sf.Adam(lr=1e-5, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0)
     # a fresh batch each step; with --micro N
     # a step is N micro-batches of the workload's batch, summed before the update
@@ -529,7 +529,8 @@ def run_ours(args, c):
                    "layers": c.n_layers, "ring_slots": args.ring or c.ring_slots,
                    "parallelism": "single-gpu layer sliding",
                    "host_updates": "synchronous" if args.sync_updates else "overlap next step",
-                   "activations": "sliding (host)" if args.offload_activations else "resident",
+                   "activations": ("resident", "sliding (host)",
+                                   "sliding (host), int8 checkpoints")[args.offload_activations],
                    "adam_state": "bf16, stochastic rounding" if args.bf16_adam_state else "fp32",
                    "l2": "inputs larger than L2 (each step streams every layer's weights and gradients)"},
         "e2e": {"value": e2e, "unit": UNIT, "h2d_bytes_per_step": int(h2d),
@@ -879,8 +880,9 @@ def main():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-gpu-path", action="store_true",
                     help="skip the two extra steps timed without the optimizer")
-    ap.add_argument("--offload-activations", action="store_true",
-                    help="sliding activations: layer checkpoints go to pinned host memory")
+    ap.add_argument("--offload-activations", type=int, nargs="?", const=1, default=0, choices=(0, 1, 2),
+                    help="sliding activations: layer checkpoints go to pinned host memory, in fp32 (1, "
+                         "the default of the bare option) or as int8 codes (2)")
     ap.add_argument("--bf16-adam-state", action="store_true",
                     help="host Adam moments stored as bf16 with stochastic rounding")
     ap.add_argument("--sync-updates", action="store_true",
