@@ -92,8 +92,9 @@ typedef struct sf_ctx sf_ctx;
  *     (results are identical); 2 = sliding activations in 8 bits: every layer
  *     but the last three keeps its input as int8 codes with a scale for each
  *     128 values (SF_CKPT_INT8 below; saved by the layer's first norm), and
- *     those copies slide, a little over a quarter of the bytes, the device
- *     keeping the last four.  The forward, and with
+ *     those copies slide, a little over a quarter of the bytes.  The device
+ *     keeps the last four of them beside the fp32 window of four, so it holds
+ *     more than with 1; the host and the link hold and carry less.  The forward, and with
  *     `deterministic` the last three layers' gradients, are bit for bit those
  *     of 0; the recompute and the backward of the layers before run at the
  *     checkpoint's values (off by at most 1/254 of the largest of 128), so
@@ -441,7 +442,8 @@ int sf_op_attn_window_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int32_t 
  * key order.  Partial sums of the sinks' dK and dV follow dQ in the scratch
  * where the sequence is long (their keys are seen by every later query, so
  * those queries are split into several items, joined in a fixed order).  The
- * scratch size is -1 for bad sizes. */
+ * scratch size holds for every Hkv, with room for Hkv = Hq; it is -1 for bad
+ * sizes. */
 int sf_op_attn_window_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
                           const float* lse, float* delta, float* dq_acc, uint16_t* dqkv,
                           int32_t B, int32_t S, int32_t Hq, int32_t Hkv, int32_t hd,
@@ -491,6 +493,8 @@ int64_t sf_op_qknorm_rope_bwd_scratch(int64_t tokens, int32_t Hq, int32_t Hkv, i
  * (T / a)), value = code * scale, each operation in fp32 rounded to nearest
  * even.  A block with a < 2^-100 is stored as zeros (scale 0); a block that
  * holds an infinity or a NaN gets a NaN scale, so its values load as NaN.
+ * Because scale is rounded, a code of T can load as up to 2^-23 more than a, and
+ * so as infinity where a is within 2^-23 of itself of the largest fp32 value.
  * d a multiple of 8 in [8, 16384], buffers 16-byte aligned, rows < 2^31. */
 #define SF_CKPT_INT8 0
 #define SF_CKPT_E4M3 1

@@ -396,7 +396,10 @@ __global__ void __launch_bounds__(kAttFwd2Threads, 1)
           }
           tc_fence_after();
           const uint64_t bv = dV + (uint32_t)vs * (uint32_t)(C::TILE / 16);
-          // O_t += P_t V: P as the tensor-memory A operand
+          // O_t += P_t V: P as the tensor-memory A operand.  Two loops, as the
+          // full one is on this thread's critical path: one loop that tests keys
+          // before each MMA gives the same results and costs 2% (window 1024
+          // at head dim 128: 283 and 289 us).
           if (WIN && keys < 128) {  // only the sinks
 #pragma unroll 1
             for (int kk = 0; kk < keys / 16; ++kk)
@@ -687,13 +690,13 @@ struct KeyWork {
 // rest of the work where the sequence is long and the window short).  So the
 // queries behind its window are split into win.splits items of their own, and
 // its other item (slot 0) is like every key block's (1 x 16384, 16 heads in
-// groups of 8, window 256, 4 sinks: 3328 us with one item, 355 us split, both with an older kernel).  The
-// parts come first, as they can be longer than the others (130 sinks there:
-// 343 us, 460 us with the parts spread between the key blocks, likewise).
+// groups of 8, window 256, 4 sinks: head dim 128 2,479 us with one item, 303 us
+// split; 64 1,987 and 223 us).  The parts come first, as they can be longer than
+// the others (130 sinks there: 286 and 271 us; 364 and 356 us with them last).
 //
 // PART: the variants of the kernels for win.splits > 0; the decoding of items
 // and the parts' epilogue are on the critical path of short items (8 x 1001, 16
-// heads of 64, window 250: 93 us without, 100 us in one variant with them).
+// heads of 64, window 250: 85 us without, 93 us in one variant with them).
 template <bool WIN, bool PART>
 __device__ __forceinline__ KeyWork key_work(const AttWindow& win, int rank, int S) {
   const int nq = (S + 127) / 128;
@@ -1365,8 +1368,9 @@ __global__ void __launch_bounds__(kAttBwdThreads, 1)
 // a block takes 4,450 clocks.  Blocks of 64 queries (MMAs 64 wide, which read
 // 6 KB in 32 clocks of work) took 2 x 2,450.  Whole backward, 8 x 2048 tokens,
 // 32 / 8 heads: 897 us then, 790 us with 128 queries, 711 us (967 TFLOP/s) with
-// the heads in chunks (head_chunks); 2 x 8192, window 1024, 4 sinks: 968 and
-// 787 us.  Measured on the way to 790: the threads storing dQ themselves, as one
+// the heads in chunks (head_chunks); 2 x 8192, window 1024, 4 sinks: 968 us
+// then, now 793 us in repeated calls and up to 822 us on a box that does other
+// work in between (deterministic 1,200 us).  Measured on the way to 790: the threads storing dQ themselves, as one
 // reduction instruction per row, 862 us, and four warps of their own doing so
 // 918 us (such instructions leave an SM at 32 bytes a clock and hold up the
 // stores of dS^T behind them); dO's one buffer refilled after the next but one
@@ -1609,7 +1613,7 @@ __global__ void __launch_bounds__(kAttBwd2Threads, 1)
       // dS^T is in shared memory, dP^T has been read: dQ^T takes its columns
       if (!mbar_wait(ds_full, it & 1, abort_flag)) { ok = false; break; }
       tc_fence_after();
-      if (PART && keys < 128) {  // only the sinks
+      if (PART && keys < 128) {  // only the sinks (apart from the full loop: 1 to 2%, as in the forward)
 #pragma unroll 1
         for (int kk = 0; kk < keys / 16; ++kk)
           umma_bf16(tmem_base + COL_DP, dKm + kk * 128, dDStm + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
@@ -2139,9 +2143,9 @@ int bwd(const __nv_bfloat16* qkv, const __nv_bfloat16* o, const __nv_bfloat16* d
 // the items out, the sinks' queries are split only where one item with all of
 // them would take longer than an even share of the work: else it runs beside
 // the others from the start, its queries a little ahead of theirs (2 x 8192, 32
-// / 8 heads of 128, window 1024, 4 sinks: 794 us in one item, 846 us split).
+// / 8 heads of 128, window 1024, 4 sinks: 792 us in one item, 841 us split).
 // At 64 the items are dealt out in advance and a long one delays those behind
-// it (1 x 16384, 16 heads, window 1024, 64 sinks: 538 us and 384 us).
+// it (1 x 16384, 16 heads, window 1024, 64 sinks: 505 us and 372 us).
 AttWindow clip(int window, int sinks, int S, int B, int Hq, int Hkv, int hd) {
   AttWindow win{window < S ? window : S, sinks < S ? sinks : S, attn_window_splits(S, window, sinks)};
   if (hd == 128 && win.splits > 0) {

@@ -14,7 +14,8 @@
 // Every kernel here streams its rows once and is bound by memory traffic: 16384
 // x 4096, forward saving int8 70 us (6,740 GB/s), forward from the codes 70 us,
 // together 0.96 of a measured copy's rate; 4095 x 12288 e4m3, backward 133.7 us
-// with its gain sums (757 MB, 5,660 GB/s, 0.84; the sums' launch is 6 us).  A
+// with its gain sums (757 MB, 5,660 GB/s, 0.84; the sums' launch is 6 us).  Alone,
+// at 16384 x 4096 (337 MB): save 72 us (int8; e4m3 70), load 76 us (e4m3 56).  A
 // lane holds four columns (a float4, or four codes), so a warp holds a block:
 // its largest magnitude is one integer warp reduction of |x|'s bits, which
 // order like the values, with infinities and NaNs on top.
@@ -273,11 +274,12 @@ void norm_fwd8(const float* x, const bf16* g, bf16* y, float* rstd, uint8_t* q, 
 // columns: 4 up to d = 8192 (narrower rows run several at a time), then 6 and
 // 8.  A thread copies its quads of the rows ahead (dy, dres and the codes, 36
 // bytes a quad; a warp's scales and the row's rstd with them) into its own
-// places of a ring in shared memory with cp.async and reads them back itself:
-// 74 KB (CH 4, three rows deep) to 110 KB (CH 6, two) are in flight per SM
-// whatever the registers hold, no barrier but the row's sum stands between
-// rows, and d % 16 == 8 needs no special case, as a bulk copy would.  At CH 8
-// the ring holds dy and the codes, and dres is only brought into L2 ahead.
+// places of a ring in shared memory with cp.async and reads them back itself.
+// While a row is computed the others of the ring are in flight, whatever the
+// registers hold: 147 KB per SM at CH 4 (three rows of 74 KB), 110 KB at CH 6
+// (two rows), and at CH 8 82 KB (two rows, where the ring holds dy and the codes,
+// and dres is only brought into L2 ahead).  No barrier but the row's sum stands
+// between rows, and d % 16 == 8 needs no special case, as a bulk copy would.
 // The gain gradient of a thread's columns stays in registers over all rows.
 // dx may be dres or dy: a thread reads its quads of a row before it writes them,
 // and no other thread touches them.

@@ -14,13 +14,15 @@
 // needs no exchange and the sums take log2(TPH) shuffles.  Every load and
 // store is 16 bytes.
 //
-// 16384 tokens, 32 + 8 + 8 heads of 128: forward 68.4 us (403 MB, 5,890 GB/s,
-// 0.87 of a measured copy's rate), backward with its gain sums 100.3 us (571
-// MB, 5,690 GB/s, 0.84; the sums' launch is 6 us of it).  With the rows in
-// flight held by registers (256 threads a CTA) these took 79.8 and 140 us.
-// 5003 packed tokens of 16 + 2 + 2 heads with positions, in place, backward:
-// 26 us where the bytes take 11: the second phase has few steps to a warp, and
-// its first rows, the rotations and the gain sums' launch are not hidden.
+// 16384 tokens, 32 + 8 + 8 heads of 128: forward 68.1 us (403 MB, 5,920 GB/s,
+// 0.87 of a measured copy's rate), backward with its gain sums 97.9 us (571
+// MB, 5,830 GB/s, 0.86; the sums' launch is 6 us of it); in place, where the
+// value heads stay, 62 and 93 us.  With the rows in flight held by registers
+// (256 threads a CTA) the first two took 79.8 and 140 us.
+// 5003 packed tokens of 16 + 2 + 2 heads with positions, backward, the value
+// heads copied: 25.7 us where the bytes take 11: the second phase has few steps
+// to a warp, and its first rows, the rotations and the gain sums' launch are not
+// hidden.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -37,8 +39,11 @@ typedef __nv_bfloat16 bf16;
 
 constexpr int kQkThreads = 128;
 constexpr int kQkWarps = kQkThreads / 32;
-constexpr int kQkFwdCtas = 5;    // resident CTAs an SM is given, forward (4: 71.7 us, 6: 80 us above)
-constexpr int kQkBwdCtas = 4;    // and backward (3: 104.6 us; 5 leaves too few registers, 166 us)
+// Resident CTAs an SM is given, as measured when they were chosen (the first size
+// above): forward 4, 5, 6: 71.7, 68.6, 80 us; backward 3, 4, 5: 104.6, 100.3 and
+// (too few registers) 166 us.
+constexpr int kQkFwdCtas = 5;
+constexpr int kQkBwdCtas = 4;
 constexpr int kQkFwdStages = 5;  // steps a lane has in flight, forward (x)
 constexpr int kQkBwdStages = 5;  // and backward (x and dy)
 
