@@ -1694,6 +1694,8 @@ int step(sf_ctx* ctx, const int32_t* tokens, const int32_t* labels, int B, int S
   if (*ctx->err_pin != 0) {
     ctx->set_err(*ctx->err_pin == sf::kDevCeBadLabel
                      ? "a label outside the vocabulary reached the cross-entropy kernel (code %d)"
+                 : *ctx->err_pin == sf::kDevSharedBase
+                     ? "an attention kernel's shared memory is misaligned (code %d)"
                      : "device wait limit reached in a kernel (code %d)",
                  *ctx->err_pin);
     ctx->poisoned = true;
