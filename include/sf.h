@@ -524,6 +524,66 @@ int sf_op_rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const uint16_t
                             uint16_t* dxb, uint16_t* dg, float* scratch, int32_t fmt, int64_t rows,
                             int32_t d, void* stream);
 
+/* Types of the elements of a void* argument. */
+#define SF_BF16 0
+#define SF_F32 1
+
+/* Dropout without a stored mask: y[i] = x[i] / (1 - q) where element i is kept,
+ * else 0 (whatever x[i] is).  Whether it is kept follows from seed, offset and
+ * i: Philox4x32-10 (Salmon et al. 2011) with key seed and the 128-bit counter
+ * (i / 8, offset), the octet in the low half, gives four words for eight
+ * elements, 16 bits each, word (i % 8) / 2, the even element in its low half.
+ * An element is kept when its bits are at least T = p * 65536 rounded to
+ * nearest (ties to even), and q = T / 65536 is the probability that takes effect.  The
+ * gradient is the same call on the gradient of y, with the same seed and offset.
+ * Calls whose masks have to differ need another offset (or seed) each.  When
+ * step != NULL, *step (a uint64 on the device, 8-byte aligned) is added to
+ * offset, modulo 2^64, when the kernel runs: a captured graph draws a new mask
+ * at each replay when *step changes in between.
+ * x and y of type SF_BF16 or SF_F32, n elements, 16-byte aligned; y may be x.
+ * p >= 0 and T < 65536; n at most 2^40, and may be 0. */
+int sf_op_dropout(const void* x, void* y, int32_t type, int64_t n, float p, uint64_t seed,
+                  uint64_t offset, const uint64_t* step, void* stream);
+
+/* The join of a block's output h with the residual stream x, with the norms
+ * after the block and before the next one:
+ *   u = h                                    (g_post == NULL)
+ *   u = g_post * h / sqrt(mean(h^2) + eps)   (a norm after the block)
+ *   u = gate * u                             (gate != NULL)
+ *   v = dropout(u) with p, seed, offset, step as sf_op_dropout on [rows, d]
+ *   xout = alpha * x + beta * v
+ *   y = g_next * xout / sqrt(mean(xout^2) + eps)   (g_next != NULL)
+ * x, xout fp32 [rows, d] (xout may be x); h [rows, d] of type h_type (SF_BF16 or
+ * SF_F32); g_post, gate, g_next bf16 [d], each may be NULL; y bf16 [rows, d];
+ * rstd_post, rstd_next fp32 [rows] get 1/sqrt(...) of the two norms, for the
+ * backward.  y and rstd_next are not used without g_next, rstd_post without
+ * g_post.  All in fp32, y rounded once.  d a multiple of 8 in [8, 16384], rows
+ * < 2^31 (may be 0), matrices and gains 16-byte aligned, alpha and beta finite. */
+int sf_op_join_fwd(const float* x, const void* h, int32_t h_type, const uint16_t* g_post,
+                   const uint16_t* gate, const uint16_t* g_next, float alpha, float beta, float p,
+                   uint64_t seed, uint64_t offset, const uint64_t* step, float* xout, uint16_t* y,
+                   float* rstd_post, float* rstd_next, int64_t rows, int32_t d, float eps,
+                   void* stream);
+
+/* Backward of sf_op_join_fwd from its xout, h, rstd_post and rstd_next, with the
+ * same gains, scales, p, seed, offset and *step.  dy fp32 [rows, d] is the
+ * gradient of y (needed with g_next, not used without), dres fp32 [rows, d] the
+ * gradient of xout from elsewhere (NULL: none; needed without g_next):
+ *   D = dres + rstd_next*(g_next*dy - xhat*mean(g_next*dy*xhat)),
+ *   dx = alpha * D, and dh the gradient through beta, dropout, gate and norm.
+ * dx fp32 [rows, d] (may be dy or dres); dh of h's type.  dg_post, dgate,
+ * dg_next bf16 [d]: the gradients of the gains that are given (not used for
+ * the others), summed over the rows in a fixed order (bit-reproducible).
+ * scratch: fp32 of sf_op_join_bwd_scratch(rows, d) elements (-1 for bad sizes),
+ * 16-byte aligned, needed with any gain.  rows >= 1. */
+int sf_op_join_bwd(const float* xout, const void* h, int32_t h_type, const uint16_t* g_post,
+                   const uint16_t* gate, const uint16_t* g_next, float alpha, float beta, float p,
+                   uint64_t seed, uint64_t offset, const uint64_t* step, const float* rstd_post,
+                   const float* rstd_next, const float* dy, const float* dres, float* dx, void* dh,
+                   uint16_t* dg_post, uint16_t* dgate, uint16_t* dg_next, float* scratch,
+                   int64_t rows, int32_t d, void* stream);
+int64_t sf_op_join_bwd_scratch(int64_t rows, int32_t d);
+
 /* m = silu(a) * b with ab = [a | b] bf16 [rows, 2*ffn]; m bf16 [rows, ffn]. */
 int sf_op_swiglu_fwd(const uint16_t* ab, uint16_t* m, int64_t rows, int32_t ffn, void* stream);
 /* dab = [dm * b * s(1 + a(1-s)) | dm * silu(a)], s = sigmoid(a). */
@@ -586,6 +646,63 @@ int64_t sf_op_lce_workspace_bytes(int64_t n, int32_t v, int64_t chunk_rows);
  * sum); 0 before any call.  No device work. */
 int64_t sf_op_lce_launches(void);
 
+/* Log probabilities of given tokens from rows of logits.  z [rows, ldz] of type
+ * z_type (SF_BF16 or SF_F32), its first vocab columns; with t = scale * z
+ * (scale: one over the temperature, in [2^-20, 2^20]):
+ *   lse[r] = log sum_v exp(t[r, v]),
+ *   logp[r] = t[r, token] - lse[r], or 0 where the token is negative,
+ *   entropy[r] = -sum_v p log p, p = softmax(t[r])  (NULL: not computed),
+ *   ids[r, 0 .. top), top_logp[r, 0 .. top): the ids and log probabilities of
+ *   the top largest logits, in falling order, equal logits by the lower id.
+ * tokens int32 [rows] on the device, so this call cannot check them: a token >=
+ * vocab sets the device error word to 4 and its row is treated as one without
+ * a token (SF_IGNORE_INDEX).  A logit of -inf has probability 0; a row of
+ * nothing else has lse, top_logp and its token's logp -inf and entropy 0.  A
+ * row with a NaN or +inf has NaN for each of them (but 0 for no token) and ids
+ * -1.  Sums in fp32.  top in [0, 32], at most vocab; ids and top_logp are not
+ * used with top 0.  ldz a multiple of 8, z 16-byte aligned; vocab in [1, 2^24],
+ * rows < 2^31 (may be 0). */
+#define SF_LOGPROB_TOP_MAX 32
+int sf_op_logprob_rows(const void* z, int32_t z_type, int64_t ldz, const int32_t* tokens,
+                       int64_t rows, int32_t vocab, float scale, float* logp, float* lse,
+                       float* entropy, int32_t top, int32_t* ids, float* top_logp, void* stream);
+
+/* Backward of sf_op_logprob_rows: dlogp and dentropy fp32 [rows] are the
+ * gradients of logp and entropy (dentropy NULL: none, and entropy is not used),
+ * lse and entropy the forward's;
+ *   dz = scale * (dlogp * (onehot(token) - p) - dentropy * p * (log p + entropy))
+ * as bf16 [rows, lddz], the first vocab columns (the operand of the head's dH
+ * and dW products).  dlogp of a row without a token is not used; a row whose
+ * two gradients are then 0 gets zeros whatever its logits are, and so does a
+ * row of -inf.  dz may be z where z_type is SF_BF16 and lddz == ldz. */
+int sf_op_logprob_rows_bwd(const void* z, int32_t z_type, int64_t ldz, const int32_t* tokens,
+                           int64_t rows, int32_t vocab, float scale, const float* lse,
+                           const float* entropy, const float* dlogp, const float* dentropy,
+                           uint16_t* dz, int64_t lddz, void* stream);
+
+/* sf_op_logprob_rows of the logits h W^T (fp32, never stored beyond one chunk of
+ * chunk_rows rows): h bf16 [n, d], w bf16 [v, d], tokens int32 [n] (device);
+ * d and v multiples of 8, v at most 2^24, n >= 1.  workspace:
+ * sf_op_lm_logprob_workspace_bytes(n, v, chunk_rows) bytes (4 for each logit of a
+ * chunk; -1 for bad sizes), 256-byte aligned.  Errors and the device error word
+ * as sf_op_gemm and sf_op_logprob_rows. */
+int sf_op_lm_logprob(const uint16_t* h, const uint16_t* w, const int32_t* tokens, int64_t n,
+                     int32_t d, int32_t v, float scale, int64_t chunk_rows, void* workspace,
+                     float* logp, float* lse, float* entropy, int32_t top, int32_t* ids,
+                     float* top_logp, void* stream);
+int64_t sf_op_lm_logprob_workspace_bytes(int64_t n, int32_t v, int64_t chunk_rows);
+
+/* Backward of sf_op_lm_logprob (logits recomputed chunk by chunk): with dz of
+ * sf_op_logprob_rows_bwd, dh bf16 [n, d] = dz W and dw bf16 [v, d] = dz^T h, fp32
+ * sums rounded once.  workspace: sf_op_lm_logprob_bwd_workspace_bytes(n, d, v,
+ * chunk_rows) bytes (-1 for bad sizes), 256-byte aligned: a chunk's fp32 logits
+ * and bf16 dz and, where n > chunk_rows, the fp32 sum of dw over the chunks. */
+int sf_op_lm_logprob_bwd(const uint16_t* h, const uint16_t* w, const int32_t* tokens, int64_t n,
+                         int32_t d, int32_t v, float scale, int64_t chunk_rows, const float* lse,
+                         const float* entropy, const float* dlogp, const float* dentropy,
+                         void* workspace, uint16_t* dh, uint16_t* dw, void* stream);
+int64_t sf_op_lm_logprob_bwd_workspace_bytes(int64_t n, int32_t d, int32_t v, int64_t chunk_rows);
+
 /* sf_op_rmsnorm_bwd_noalloc: the same operation and results as
  * sf_op_rmsnorm_bwd, for callers that cannot allocate device memory (for
  * instance code inside a host application whose memory manager owns the
@@ -612,7 +729,8 @@ int sf_op_rmsnorm_bwd_noalloc(const float* x, const uint16_t* g, const float* rs
 
 /* Read and clear the device error word of the kernel API on the current
  * device.  0: no error; 1, 2, 3: a bounded wait ran out in a GEMM, an
- * attention or a cross-entropy kernel; 4: sf_op_lce met a label at or beyond
+ * attention or a cross-entropy kernel; 4: sf_op_lce met a label, or
+ * sf_op_logprob_rows, sf_op_lm_logprob or their backwards a token, at or beyond
  * the vocabulary; 5: sf_op_qknorm_rope_fwd or _bwd met a position outside the
  * rotation table; 6: an attention backward found its shared memory misaligned
  * and wrote nothing.  The first code a launch writes stays.  Synchronises the

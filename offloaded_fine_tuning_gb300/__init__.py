@@ -29,6 +29,10 @@ NT, NN, TN = 0, 1, 2
 EPI_BF16, EPI_F32, EPI_F32_ADD, EPI_F32_ACC = 0, 1, 2, 3
 # formats of an 8-bit checkpoint
 CKPT_INT8, CKPT_E4M3 = 0, 1
+# element types of arguments that take either
+BF16, F32 = 0, 1
+# the most alternatives that op_logprob_rows gives
+LOGPROB_TOP_MAX = 32
 
 
 class SfError(RuntimeError):
@@ -79,6 +83,8 @@ TRACE_KINDS = {1: "step_begin", 2: "gathered", 3: "wait_unit_begin", 4: "wait_un
 _lib = None
 
 _VP, _I32, _I64, _F32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_U64 = ctypes.c_uint64
+_DROP = [_F32, _U64, _U64, _VP]  # p, seed, offset, step
 _SIGS = {
     "sf_unit_numel": (_SZ, [ctypes.POINTER(Config), _I32]),
     "sf_init_model": (ctypes.c_int, [ctypes.POINTER(Config), ctypes.POINTER(_VP)]),
@@ -136,6 +142,21 @@ _SIGS = {
     "sf_op_rmsnorm_fwd_save8": (ctypes.c_int, [_VP] * 6 + [_I32, _I64, _I32, _F32, _VP]),
     "sf_op_rmsnorm_fwd_load8": (ctypes.c_int, [_VP] * 6 + [_I32, _I64, _I32, _F32, _VP]),
     "sf_op_rmsnorm_bwd_load8": (ctypes.c_int, [_VP] * 10 + [_I32, _I64, _I32, _VP]),
+    "sf_op_dropout": (ctypes.c_int, [_VP, _VP, _I32, _I64] + _DROP + [_VP]),
+    "sf_op_join_fwd": (ctypes.c_int, [_VP, _VP, _I32, _VP, _VP, _VP, _F32, _F32] + _DROP + [_VP] * 4 +
+                       [_I64, _I32, _F32, _VP]),
+    "sf_op_join_bwd": (ctypes.c_int, [_VP, _VP, _I32, _VP, _VP, _VP, _F32, _F32] + _DROP + [_VP] * 10 +
+                       [_I64, _I32, _VP]),
+    "sf_op_join_bwd_scratch": (_I64, [_I64, _I32]),
+    "sf_op_logprob_rows": (ctypes.c_int, [_VP, _I32, _I64, _VP, _I64, _I32, _F32, _VP, _VP, _VP, _I32, _VP,
+                                          _VP, _VP]),
+    "sf_op_logprob_rows_bwd": (ctypes.c_int, [_VP, _I32, _I64, _VP, _I64, _I32, _F32] + [_VP] * 5 +
+                               [_I64, _VP]),
+    "sf_op_lm_logprob": (ctypes.c_int, [_VP, _VP, _VP, _I64, _I32, _I32, _F32, _I64] + [_VP] * 4 +
+                         [_I32, _VP, _VP, _VP]),
+    "sf_op_lm_logprob_workspace_bytes": (_I64, [_I64, _I32, _I64]),
+    "sf_op_lm_logprob_bwd": (ctypes.c_int, [_VP, _VP, _VP, _I64, _I32, _I32, _F32, _I64] + [_VP] * 8),
+    "sf_op_lm_logprob_bwd_workspace_bytes": (_I64, [_I64, _I32, _I32, _I64]),
     "sf_op_swiglu_fwd": (ctypes.c_int, [_VP, _VP, _I64, _I32, _VP]),
     "sf_op_swiglu_bwd": (ctypes.c_int, [_VP, _VP, _VP, _I64, _I32, _VP]),
     "sf_op_lce": (ctypes.c_int, [_VP, _VP, _VP, _I64, _I32, _I32, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
@@ -495,6 +516,65 @@ def op_rmsnorm_fwd_load8(q, scale, g, y, rstd, x, fmt, rows, d, eps, stream=0) -
 def op_rmsnorm_bwd_load8(q, scale, g, rstd, dy, dres, dx, dxb, dg, scratch, fmt, rows, d, stream=0) -> int:
     return lib().sf_op_rmsnorm_bwd_load8(q, scale, g, rstd, dy, dres or None, dx, dxb, dg, scratch, fmt,
                                          rows, d, _s(stream))
+
+
+def op_dropout(x, y, type, n, p, seed, offset, step=0, stream=0) -> int:
+    """Dropout without a stored mask; the gradient is the same call on dy.  y may be x."""
+    return lib().sf_op_dropout(x, y, type, n, p, seed, offset, step or None, _s(stream))
+
+
+def op_join_fwd(x, h, h_type, g_post, gate, g_next, alpha, beta, p, seed, offset, xout, y, rstd_post,
+                rstd_next, rows, d, eps, step=0, stream=0) -> int:
+    """xout = alpha x + beta dropout(gate * norm(h)) and its norm y; 0 for a gain: without it."""
+    return lib().sf_op_join_fwd(x, h, h_type, g_post or None, gate or None, g_next or None, alpha, beta, p, seed,
+                                offset, step or None, xout, y or None, rstd_post or None, rstd_next or None, rows,
+                                d, eps, _s(stream))
+
+
+def op_join_bwd(xout, h, h_type, g_post, gate, g_next, alpha, beta, p, seed, offset, rstd_post, rstd_next, dy,
+                dres, dx, dh, dg_post, dgate, dg_next, scratch, rows, d, step=0, stream=0) -> int:
+    return lib().sf_op_join_bwd(xout, h, h_type, g_post or None, gate or None, g_next or None, alpha, beta, p, seed,
+                                offset, step or None, rstd_post or None, rstd_next or None, dy or None,
+                                dres or None, dx, dh, dg_post or None, dgate or None, dg_next or None,
+                                scratch or None, rows, d, _s(stream))
+
+
+def join_bwd_scratch(rows, d) -> int:
+    return int(lib().sf_op_join_bwd_scratch(rows, d))
+
+
+def op_logprob_rows(z, z_type, ldz, tokens, rows, vocab, scale, logp, lse, entropy=0, top=0, ids=0, top_logp=0,
+                    stream=0) -> int:
+    """Log probabilities of tokens from logits, with entropy (0: none) and the `top` most likely ids."""
+    return lib().sf_op_logprob_rows(z, z_type, ldz, tokens, rows, vocab, scale, logp, lse, entropy or None, top,
+                                    ids or None, top_logp or None, _s(stream))
+
+
+def op_logprob_rows_bwd(z, z_type, ldz, tokens, rows, vocab, scale, lse, entropy, dlogp, dentropy, dz, lddz,
+                        stream=0) -> int:
+    return lib().sf_op_logprob_rows_bwd(z, z_type, ldz, tokens, rows, vocab, scale, lse, entropy or None, dlogp,
+                                        dentropy or None, dz, lddz, _s(stream))
+
+
+def op_lm_logprob(h, w, tokens, n, d, v, scale, chunk_rows, workspace, logp, lse, entropy=0, top=0, ids=0,
+                  top_logp=0, stream=0) -> int:
+    """op_logprob_rows of the logits h w^T, which exist one chunk of rows at a time."""
+    return lib().sf_op_lm_logprob(h, w, tokens, n, d, v, scale, chunk_rows, workspace, logp, lse, entropy or None,
+                                  top, ids or None, top_logp or None, _s(stream))
+
+
+def lm_logprob_workspace_bytes(n, v, chunk_rows) -> int:
+    return int(lib().sf_op_lm_logprob_workspace_bytes(n, v, chunk_rows))
+
+
+def op_lm_logprob_bwd(h, w, tokens, n, d, v, scale, chunk_rows, lse, entropy, dlogp, dentropy, workspace, dh, dw,
+                      stream=0) -> int:
+    return lib().sf_op_lm_logprob_bwd(h, w, tokens, n, d, v, scale, chunk_rows, lse, entropy or None, dlogp,
+                                      dentropy or None, workspace, dh, dw, _s(stream))
+
+
+def lm_logprob_bwd_workspace_bytes(n, d, v, chunk_rows) -> int:
+    return int(lib().sf_op_lm_logprob_bwd_workspace_bytes(n, d, v, chunk_rows))
 
 
 def op_swiglu_fwd(ab, m, rows, ffn, stream=0) -> int:

@@ -380,6 +380,101 @@ int sf_op_rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const uint16_t
   return launched();
 }
 
+// The mask of sf_op_dropout; false for a p or step that is refused.
+static bool drop_args(float p, uint64_t seed, uint64_t offset, const uint64_t* step, sf::DropArgs* a) {
+  if (!(p >= 0.f && p <= 1.f) || !al1(step)) return false;
+  const long t = std::lrint((double)p * 65536.0);
+  if (t > 65535) return false;
+  a->top = (uint32_t)t << 16;
+  a->scale = (float)(65536.0 / (65536.0 - (double)t));
+  a->seed = seed;
+  a->offset = offset;
+  a->step = step;
+  return true;
+}
+static bool a_type(int32_t t) { return t == SF_BF16 || t == SF_F32; }
+
+int sf_op_dropout(const void* x, void* y, int32_t type, int64_t n, float p, uint64_t seed,
+                  uint64_t offset, const uint64_t* step, void* stream) {
+  sf::DropArgs a;
+  if (!a_type(type) || n < 0 || n > ((int64_t)1 << 40) || !drop_args(p, seed, offset, step, &a))
+    return SF_EINVAL;
+  if (n == 0) return SF_OK;
+  if (!x || !y || !al16(x) || !al16(y)) return SF_EINVAL;
+  sf::dropout(x, y, type == SF_F32, n, a, S(stream));
+  return launched();
+}
+
+// What both directions of the join take.
+static bool join_sizes(int64_t rows, int32_t d) {
+  return rows >= 0 && rows <= INT32_MAX && d >= 8 && d % 8 == 0 && d <= 16384;
+}
+static bool join_args(int32_t h_type, const uint16_t* g_post, const uint16_t* gate,
+                      const uint16_t* g_next, float alpha, float beta, float p, uint64_t seed,
+                      uint64_t offset, const uint64_t* step, int64_t rows, int32_t d, sf::JoinArgs* a) {
+  if (!a_type(h_type) || !std::isfinite(alpha) || !std::isfinite(beta) || !join_sizes(rows, d) ||
+      !al16(g_post) || !al16(gate) || !al16(g_next) || !drop_args(p, seed, offset, step, &a->drop))
+    return false;
+  a->rows = rows;
+  a->d = d;
+  a->g_post = reinterpret_cast<const bf16*>(g_post);
+  a->gate = reinterpret_cast<const bf16*>(gate);
+  a->g_next = reinterpret_cast<const bf16*>(g_next);
+  a->alpha = alpha;
+  a->beta = beta;
+  return true;
+}
+
+int sf_op_join_fwd(const float* x, const void* h, int32_t h_type, const uint16_t* g_post,
+                   const uint16_t* gate, const uint16_t* g_next, float alpha, float beta, float p,
+                   uint64_t seed, uint64_t offset, const uint64_t* step, float* xout, uint16_t* y,
+                   float* rstd_post, float* rstd_next, int64_t rows, int32_t d, float eps,
+                   void* stream) {
+  sf::JoinArgs a;
+  if (!join_args(h_type, g_post, gate, g_next, alpha, beta, p, seed, offset, step, rows, d, &a))
+    return SF_EINVAL;
+  if ((g_post || g_next) && !(eps > 0.f)) return SF_EINVAL;
+  if (rows == 0) return SF_OK;
+  if (!x || !h || !xout || !al16(x) || !al16(h) || !al16(xout)) return SF_EINVAL;
+  if (g_post && (!rstd_post || !al1(rstd_post))) return SF_EINVAL;
+  if (g_next && (!y || !rstd_next || !al16(y) || !al1(rstd_next))) return SF_EINVAL;
+  sf::join_fwd(a, x, h, h_type == SF_F32, xout, reinterpret_cast<bf16*>(y), rstd_post, rstd_next,
+               eps, S(stream));
+  return launched();
+}
+
+int64_t sf_op_join_bwd_scratch(int64_t rows, int32_t d) {
+  if (!join_sizes(rows, d)) return -1;
+  return (int64_t)sf::join_bwd_parts(rows, d) * 2 * d;
+}
+
+int sf_op_join_bwd(const float* xout, const void* h, int32_t h_type, const uint16_t* g_post,
+                   const uint16_t* gate, const uint16_t* g_next, float alpha, float beta, float p,
+                   uint64_t seed, uint64_t offset, const uint64_t* step, const float* rstd_post,
+                   const float* rstd_next, const float* dy, const float* dres, float* dx, void* dh,
+                   uint16_t* dg_post, uint16_t* dgate, uint16_t* dg_next, float* scratch,
+                   int64_t rows, int32_t d, void* stream) {
+  sf::JoinArgs a;
+  if (!join_args(h_type, g_post, gate, g_next, alpha, beta, p, seed, offset, step, rows, d, &a) || rows < 1)
+    return SF_EINVAL;
+  if (!xout || !h || !dx || !dh || !al16(xout) || !al16(h) || !al16(dx) || !al16(dh) || !al16(dres))
+    return SF_EINVAL;
+  if (dx == xout || dh == h) return SF_EINVAL;
+  if (g_next ? (!dy || !rstd_next || !dg_next || !al16(dy) || !al1(rstd_next) || !al1(dg_next)) : !dres)
+    return SF_EINVAL;
+  if (g_post && (!rstd_post || !dg_post || !al1(rstd_post) || !al1(dg_post))) return SF_EINVAL;
+  if (gate && (!dgate || !al1(dgate))) return SF_EINVAL;
+  if ((g_post || gate || g_next) && (!scratch || !al16(scratch))) return SF_EINVAL;
+  if (!sf::join_bwd(a, xout, h, h_type == SF_F32, rstd_post, rstd_next, dy, dres, dx, dh,
+                    reinterpret_cast<bf16*>(g_post ? dg_post : nullptr),
+                    reinterpret_cast<bf16*>(gate ? dgate : nullptr),
+                    reinterpret_cast<bf16*>(g_next ? dg_next : nullptr), scratch, S(stream))) {
+    cudaGetLastError();
+    return SF_ECUDA;
+  }
+  return launched();
+}
+
 int sf_op_swiglu_fwd(const uint16_t* ab, uint16_t* m, int64_t rows, int32_t ffn, void* stream) {
   if (rows < 0 || ffn < 8 || ffn % 8) return SF_EINVAL;
   if (rows == 0) return SF_OK;
@@ -460,6 +555,139 @@ int sf_op_lce(const uint16_t* h, const uint16_t* w, const int32_t* labels, int64
 }
 
 int64_t sf_op_lce_launches(void) { return lce_launches; }
+
+// What both directions of the log probabilities take.
+static bool logprob_sizes(int32_t z_type, int64_t ldz, int64_t rows, int32_t vocab, float scale) {
+  return a_type(z_type) && rows >= 0 && rows <= INT32_MAX && vocab >= 1 && vocab <= (1 << 24) &&
+         ldz >= vocab && ldz % 8 == 0 && scale >= 9.5367431640625e-07f && scale <= 1048576.f;
+}
+static bool logprob_outputs(float* logp, float* lse, float* entropy, int32_t vocab, int32_t top, int32_t* ids,
+                            float* top_logp) {
+  if (!logp || !lse || !al1(logp) || !al1(lse) || !al1(entropy)) return false;
+  if (top < 0 || top > SF_LOGPROB_TOP_MAX || top > vocab) return false;
+  return top == 0 || (ids && top_logp && al1(ids) && al1(top_logp));
+}
+static bool logprob_gradients(const float* lse, const float* entropy, const float* dlogp, const float* dentropy) {
+  return lse && dlogp && al1(lse) && al1(dlogp) && (!dentropy || (entropy && al1(entropy) && al1(dentropy)));
+}
+
+int sf_op_logprob_rows(const void* z, int32_t z_type, int64_t ldz, const int32_t* tokens,
+                       int64_t rows, int32_t vocab, float scale, float* logp, float* lse,
+                       float* entropy, int32_t top, int32_t* ids, float* top_logp, void* stream) {
+  if (!logprob_sizes(z_type, ldz, rows, vocab, scale)) return SF_EINVAL;
+  if (top < 0 || top > SF_LOGPROB_TOP_MAX || top > vocab) return SF_EINVAL;
+  if (rows == 0) return SF_OK;
+  if (!z || !tokens || !al16(z) || !al1(tokens)) return SF_EINVAL;
+  if (!logprob_outputs(logp, lse, entropy, vocab, top, ids, top_logp)) return SF_EINVAL;
+  int* err = dev_err_word();
+  if (!err) return SF_ECUDA;
+  sf::logprob_rows(z, z_type == SF_F32, ldz, tokens, rows, vocab, scale, logp, lse, entropy, top, ids,
+                   top_logp, err, S(stream));
+  return launched();
+}
+
+int sf_op_logprob_rows_bwd(const void* z, int32_t z_type, int64_t ldz, const int32_t* tokens,
+                           int64_t rows, int32_t vocab, float scale, const float* lse,
+                           const float* entropy, const float* dlogp, const float* dentropy,
+                           uint16_t* dz, int64_t lddz, void* stream) {
+  if (!logprob_sizes(z_type, ldz, rows, vocab, scale) || lddz < vocab || lddz % 8) return SF_EINVAL;
+  if (rows == 0) return SF_OK;
+  if (!z || !tokens || !dz || !al16(z) || !al1(tokens) || !al16(dz)) return SF_EINVAL;
+  if (!logprob_gradients(lse, entropy, dlogp, dentropy)) return SF_EINVAL;
+  if (dz == z && (z_type != SF_BF16 || lddz != ldz)) return SF_EINVAL;
+  int* err = dev_err_word();
+  if (!err) return SF_ECUDA;
+  sf::logprob_rows_bwd(z, z_type == SF_F32, ldz, tokens, rows, vocab, scale, lse, entropy, dlogp, dentropy,
+                       reinterpret_cast<bf16*>(dz), lddz, err, S(stream));
+  return launched();
+}
+
+// The head of the log probabilities: sizes, and a chunk's place in the workspace.
+static bool lm_logprob_sizes(int64_t n, int32_t d, int32_t v, int64_t chunk_rows) {
+  return n >= 1 && n <= INT32_MAX && d >= 8 && d % 8 == 0 && v >= 8 && v % 8 == 0 && v <= (1 << 24) &&
+         chunk_rows >= 1;
+}
+static int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+
+int64_t sf_op_lm_logprob_workspace_bytes(int64_t n, int32_t v, int64_t chunk_rows) {
+  if (!lm_logprob_sizes(n, 8, v, chunk_rows)) return -1;
+  return up256(std::min(n, chunk_rows) * v * 4);
+}
+
+int64_t sf_op_lm_logprob_bwd_workspace_bytes(int64_t n, int32_t d, int32_t v, int64_t chunk_rows) {
+  if (!lm_logprob_sizes(n, d, v, chunk_rows)) return -1;
+  const int64_t c = std::min(n, chunk_rows);
+  return up256(c * v * 4) + up256(c * v * 2) + (n > c ? up256((int64_t)v * d * 4) : 0);
+}
+
+int sf_op_lm_logprob(const uint16_t* h, const uint16_t* w, const int32_t* tokens, int64_t n,
+                     int32_t d, int32_t v, float scale, int64_t chunk_rows, void* workspace,
+                     float* logp, float* lse, float* entropy, int32_t top, int32_t* ids,
+                     float* top_logp, void* stream) {
+  if (!lm_logprob_sizes(n, d, v, chunk_rows) || !logprob_sizes(SF_F32, v, n, v, scale)) return SF_EINVAL;
+  if (!h || !w || !tokens || !workspace || !al16(h) || !al16(w) || !al1(tokens) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return SF_EINVAL;
+  if (!logprob_outputs(logp, lse, entropy, v, top, ids, top_logp)) return SF_EINVAL;
+  int* err = dev_err_word();
+  if (!err) return SF_ECUDA;
+  const int64_t c = std::min(n, chunk_rows);
+  float* zf = static_cast<float*>(workspace);
+  char why[128];
+  for (int64_t r0 = 0; r0 < n; r0 += c) {
+    const int64_t rows = std::min(c, n - r0);
+    sf::GemmArgs z;
+    z.layout = sf::kNT; z.epi = sf::kEpiF32; z.M = rows; z.N = v; z.K = d;
+    z.A = h + r0 * d; z.lda = d; z.B = w; z.ldb = d; z.C = zf; z.ldc = v;
+    if (sf::gemm(z, err, S(stream), why) != 0) return SF_ECUDA;
+    sf::logprob_rows(zf, true, v, tokens + r0, rows, v, scale, logp + r0, lse + r0, entropy ? entropy + r0 : nullptr,
+                     top, top ? ids + r0 * top : nullptr, top ? top_logp + r0 * top : nullptr, err, S(stream));
+  }
+  return launched();
+}
+
+int sf_op_lm_logprob_bwd(const uint16_t* h, const uint16_t* w, const int32_t* tokens, int64_t n,
+                         int32_t d, int32_t v, float scale, int64_t chunk_rows, const float* lse,
+                         const float* entropy, const float* dlogp, const float* dentropy,
+                         void* workspace, uint16_t* dh, uint16_t* dw, void* stream) {
+  if (!lm_logprob_sizes(n, d, v, chunk_rows) || !logprob_sizes(SF_F32, v, n, v, scale)) return SF_EINVAL;
+  if (!h || !w || !tokens || !workspace || !dh || !dw || !al16(h) || !al16(w) || !al1(tokens) || !al16(dh) ||
+      !al16(dw) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return SF_EINVAL;
+  if (!logprob_gradients(lse, entropy, dlogp, dentropy)) return SF_EINVAL;
+  int* err = dev_err_word();
+  if (!err) return SF_ECUDA;
+  const int64_t c = std::min(n, chunk_rows);
+  char* ws = static_cast<char*>(workspace);
+  float* zf = reinterpret_cast<float*>(ws);
+  bf16* dz = reinterpret_cast<bf16*>(ws + up256(c * v * 4));
+  float* sum = reinterpret_cast<float*>(ws + up256(c * v * 4) + up256(c * v * 2));
+  char why[128];
+  cudaStream_t st = S(stream);
+  for (int64_t r0 = 0; r0 < n; r0 += c) {
+    const int64_t rows = std::min(c, n - r0);
+    const bool first = r0 == 0, last = r0 + rows == n;
+    sf::GemmArgs z;
+    z.layout = sf::kNT; z.epi = sf::kEpiF32; z.M = rows; z.N = v; z.K = d;
+    z.A = h + r0 * d; z.lda = d; z.B = w; z.ldb = d; z.C = zf; z.ldc = v;
+    if (sf::gemm(z, err, st, why) != 0) return SF_ECUDA;
+    sf::logprob_rows_bwd(zf, true, v, tokens + r0, rows, v, scale, lse + r0, entropy ? entropy + r0 : nullptr,
+                         dlogp + r0, dentropy ? dentropy + r0 : nullptr, dz, v, err, st);
+    sf::GemmArgs gx;
+    gx.layout = sf::kNN; gx.epi = sf::kEpiBF16; gx.M = rows; gx.N = d; gx.K = v;
+    gx.A = dz; gx.lda = v; gx.B = w; gx.ldb = d; gx.C = dh + r0 * d; gx.ldc = d;
+    if (sf::gemm(gx, err, st, why) != 0) return SF_ECUDA;
+    // dW: fp32 sums over the chunks; the last chunk's product adds the sum and rounds it once
+    sf::GemmArgs gw;
+    gw.layout = sf::kTN; gw.epi = last ? sf::kEpiBF16Acc : first ? sf::kEpiF32 : sf::kEpiF32Acc;
+    gw.M = v; gw.N = d; gw.K = rows; gw.A = dz; gw.lda = v; gw.B = h + r0 * d; gw.ldb = d; gw.ldc = d;
+    gw.C = last ? static_cast<void*>(dw) : sum;
+    gw.R = last && !first ? sum : nullptr;
+    gw.ldr = d;
+    if (sf::gemm(gw, err, st, why) != 0) return SF_ECUDA;
+  }
+  return launched();
+}
 
 // The fused-epilogue projections: argument checks in sf::gemm_check.
 static int run_gemm(const sf::GemmArgs& g, cudaStream_t st) {

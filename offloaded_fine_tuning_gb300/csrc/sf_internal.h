@@ -13,7 +13,7 @@ enum DevErr : int {
   kDevGemmTimeout = 1,
   kDevAttnTimeout = 2,
   kDevCeTimeout = 3,
-  kDevCeBadLabel = 4,  // a label at or beyond the vocabulary (the row is ignored)
+  kDevCeBadLabel = 4,  // a label or token at or beyond the vocabulary (the row is ignored)
   kDevBadPosition = 5,  // a position outside the rotation table (the token is not rotated)
   kDevSharedBase = 6,   // an attention backward's shared memory does not start on 1024 bytes (nothing is written)
 };
@@ -241,6 +241,47 @@ bool rmsnorm_bwd_load8(const uint8_t* q, const float* scale, const __nv_bfloat16
                        const float* rstd, const float* dy, const float* dres, float* dx,
                        __nv_bfloat16* dxb, float* dg_part, int parts, int fmt, int64_t rows, int d,
                        cudaStream_t st);
+
+// ---- dropout and the join with the residual stream (join.cu)
+// Which elements dropout keeps (sf.h has the rule): top = 2^16 T (0: all of
+// them), scale = 2^16 / (2^16 - T), and the generator's key and counter.
+struct DropArgs {
+  uint32_t top = 0;
+  float scale = 1.f;
+  uint64_t seed = 0, offset = 0;
+  const uint64_t* step = nullptr;
+};
+void dropout(const void* x, void* y, bool f32, int64_t n, const DropArgs& a, cudaStream_t st);
+
+// Rows of d columns (d % 8 == 0, 8 to 16384); g_post, gate and g_next may be null.
+struct JoinArgs {
+  int64_t rows = 0;
+  int d = 0;
+  const __nv_bfloat16 *g_post = nullptr, *gate = nullptr, *g_next = nullptr;
+  float alpha = 1.f, beta = 1.f;
+  DropArgs drop;
+};
+void join_fwd(const JoinArgs& a, const float* x, const void* h, bool h32, float* xout,
+              __nv_bfloat16* y, float* rstd_post, float* rstd_next, float eps, cudaStream_t st);
+// part: fp32 [join_bwd_parts, 2, d].  False: no launch.
+int join_bwd_parts(int64_t rows, int d);
+bool join_bwd(const JoinArgs& a, const float* xout, const void* h, bool h32,
+              const float* rstd_post, const float* rstd_next, const float* dy, const float* dres,
+              float* dx, void* dh, __nv_bfloat16* dg_post, __nv_bfloat16* dgate,
+              __nv_bfloat16* dg_next, float* part, cudaStream_t st);
+
+// ---- log probabilities of given tokens (logprob.cu); z fp32 or bf16, row
+// stride ld (a multiple of 8), 16-byte aligned.  entropy may be null; top <= 32
+// alternatives; a token at or beyond the vocabulary writes kDevCeBadLabel to
+// *err.
+void logprob_rows(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows,
+                  int vocab, float scale, float* logp, float* lse, float* entropy, int top,
+                  int32_t* ids, float* top_logp, int* err, cudaStream_t st);
+// dz may be z where z is bf16; dentropy (with entropy) may be null.
+void logprob_rows_bwd(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows,
+                      int vocab, float scale, const float* lse, const float* entropy,
+                      const float* dlogp, const float* dentropy, __nv_bfloat16* dz, int64_t lddz,
+                      int* err, cudaStream_t st);
 
 int num_sms();
 
