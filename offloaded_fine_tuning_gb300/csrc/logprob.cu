@@ -63,133 +63,229 @@ __device__ __forceinline__ void load8(const bf16* p, float (&f)[8]) {
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); }
 
-// The maximum, the sum and the weighted sum of a set of logits.
+// The maximum, the sum and the weighted sum of a set of logits; the sum's
+// rounding errors are kept beside it, because log S of a peaked row (S near 1)
+// shows them.
 struct Sums {
-  float m, s, t;
+  float m, s, low, t;
 };
 __device__ __forceinline__ void raise(Sums& a, float m, float c) {
   const float dm = fmaxf(a.m - m, kFar), f = exp2_fast(dm * c);
   a.t = f * fmaf(a.s, dm, a.t);
   a.s *= f;
+  a.low *= f;
   a.m = m;
 }
-__device__ __forceinline__ void add(Sums& a, float z, float c) {
-  const float x = z - a.m, e = exp2_fast(x * c);
-  a.s += e;
-  a.t = fmaf(e, fmaxf(x, kFar), a.t);
+__device__ __forceinline__ void add_sum(Sums& a, float s) {
+  const float sum = a.s + s, b = sum - a.s;
+  a.low += (a.s - (sum - b)) + (s - b);
+  a.s = sum;
 }
 __device__ __forceinline__ Sums merge(Sums a, Sums b, float c) {
   const float m = fmaxf(a.m, b.m);
   raise(a, m, c);
   raise(b, m, c);
-  return {m, a.s + b.s, a.t + b.t};
+  add_sum(a, b.s);
+  a.low += b.low;
+  a.t += b.t;
+  return a;
+}
+// N logits at once: one look at the maximum, and a tree of their exponentials.
+template <bool ENT, int N>
+__device__ __forceinline__ void add(Sums& a, const float (&z)[N], float c) {
+  float m = z[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) m = fmaxf(m, z[j]);
+  if (m > a.m) raise(a, m, c);
+  float e[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float x = z[j] - a.m;
+    e[j] = exp2_fast(x * c);
+    if (ENT) a.t = fmaf(e[j], fmaxf(x, kFar), a.t);
+  }
+#pragma unroll
+  for (int w = N / 2; w > 0; w /= 2)
+#pragma unroll
+    for (int j = 0; j < w; ++j) e[j] += e[j + w];
+  add_sum(a, e[0]);
 }
 
 // The order of the alternatives: larger values first, then lower ids.
-__device__ __forceinline__ bool before(float v, int i, float w, int j) { return v > w || (v == w && i < j); }
+struct Logit {
+  float v;
+  int i;
+};
+__device__ __forceinline__ bool before(Logit a, Logit b) { return a.v > b.v || (a.v == b.v && a.i < b.i); }
 
 constexpr int kThreads = 256;
+constexpr int kList = 512;    // candidates that a CTA holds
+constexpr int kMaxCluster = 8;
 
-// Forward: a CTA takes a row.
-template <typename T>
+// The place of a in a list, were the list in order.
+__device__ __forceinline__ int place(const Logit* list, int n, Logit a) {
+  int r = 0;
+  for (int j = 0; j < n; ++j) r += before(list[j], a);
+  return r;
+}
+
+// Forward: a cluster of CTAs (one, or several where there are few rows) takes a
+// row, each CTA a range of it, and reads it once.
+//
+// The alternatives come from the threads' own maxima, which the sums need
+// anyway: the top-th largest of them, v, is a bound that at least `top` logits
+// reach, and only threads whose maximum reaches it can hold such a logit.
+// Those threads' logits (about top / kThreads of the row) are read again, and
+// what reaches the bound is put in order by counting.  Where more reach it than
+// the list holds (equal logits, masked rows), the top-th of those that it does
+// hold is the next bound.  Each such round leaves out at least kList - top of
+// them, and the low ids come first, so that rows of one value end in two.
+template <typename T, bool ENT>
 __global__ void __launch_bounds__(kThreads)
     logprob_rows_kernel(const T* __restrict__ z, int64_t ld, const int32_t* __restrict__ tokens, int vocab,
                         float scale, float* __restrict__ logp, float* __restrict__ lse_out,
                         float* __restrict__ entropy, int top, int32_t* __restrict__ ids,
                         float* __restrict__ top_logp, int* err) {
+  constexpr int U = sizeof(T) == 4 ? 2 : 4;  // octets in flight: 64 bytes
   __shared__ Sums part[kThreads / 32];
-  __shared__ float best_v[kThreads / 32];
-  __shared__ int best_i[kThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x;
+  __shared__ __align__(16) Sums total;         // read by the cluster
+  __shared__ Logit best[SF_LOGPROB_TOP_MAX];   // read by the cluster
+  __shared__ __align__(16) float maxima[kThreads];
+  __shared__ int hot[kThreads];
+  __shared__ Logit list[kList];
+  __shared__ Logit bound;
+  __shared__ int hot_n, list_n;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t ncl;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncl));
+  const uint32_t rank = cluster_ctarank();
+  const int64_t row = blockIdx.x / ncl;
   const T* zr = z + row * ld;
   const float c = scale * kLog2e;
-  const int n8 = vocab >> 3;
-  Sums a = {-FLT_MAX, 0.f, 0.f};
-  for (int i = threadIdx.x; i < n8; i += kThreads) {
+  const float minus_inf = -__uint_as_float(0x7f800000u);
+  const int n8 = vocab >> 3, each = (n8 + (int)ncl - 1) / (int)ncl;
+  const int lo = min((int)rank * each, n8), hi = min(lo + each, n8);
+  const int tail = rank == ncl - 1 && tid < (vocab & 7) ? 8 * n8 + tid : -1;  // the last logits, one a thread
+  if (tid == 0) hot_n = list_n = 0;
+  Sums a = {-FLT_MAX, 0.f, 0.f, 0.f};
+  int i = lo + tid;
+  for (; i + (U - 1) * kThreads < hi; i += U * kThreads) {
+    float f[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load8(zr + 8 * (i + u * kThreads), f[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) add<ENT>(a, f[u], c);
+  }
+  for (; i < hi; i += kThreads) {
     float f[8];
     load8(zr + 8 * i, f);
-    float m = f[0];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) m = fmaxf(m, f[j]);
-    if (m > a.m) raise(a, m, c);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) add(a, f[j], c);
+    add<ENT>(a, f, c);
   }
-  if (8 * n8 + threadIdx.x < vocab) {
-    const float f = to_float(zr[8 * n8 + threadIdx.x]);
-    if (f > a.m) raise(a, f, c);
-    add(a, f, c);
+  if (tail >= 0) {
+    const float f[1] = {to_float(zr[tail])};
+    add<ENT>(a, f, c);
   }
+  maxima[tid] = a.s == 0.f ? minus_inf : a.m;  // s is at least 1 with any logit above -inf
+  const float mine = maxima[tid];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     a = merge(a, {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                  __shfl_xor_sync(0xffffffffu, a.t, o)}, c);
+                  __shfl_xor_sync(0xffffffffu, a.low, o), __shfl_xor_sync(0xffffffffu, a.t, o)}, c);
   if (lane == 0) part[warp] = a;
   __syncthreads();
-  a = part[0];
-  for (int w = 1; w < kThreads / 32; ++w) a = merge(a, part[w], c);
-  // s is at least 1 where any logit is above -inf
-  const bool none = a.s == 0.f;
-  const float log_s = logf(a.s);
-  const float minus_inf = -__uint_as_float(0x7f800000u);
-  auto value = [&](float v) { return none ? minus_inf : fmaf(v - a.m, scale, -log_s); };
-  if (threadIdx.x == 0) {
-    int token = tokens[row];
-    if (token >= vocab) {  // outside the vocabulary: reported, and the row ignored
-      record_error(err, kDevCeBadLabel);
-      token = -1;
-    }
-    logp[row] = token < 0 ? 0.f : value(to_float(zr[token]));
-    lse_out[row] = none ? minus_inf : fmaf(a.m, scale, log_s);
-    if (entropy) entropy[row] = none ? 0.f : log_s - scale * (a.t / a.s);
+  if (warp == 0) {
+    a = part[0];
+    for (int w = 1; w < kThreads / 32; ++w) a = merge(a, part[w], c);
+    if (lane == 0) total = a;
   }
-  // the alternatives, one after another: the first in order behind the last one
-  float last_v = __uint_as_float(0x7f800000u);
-  int last_i = -1;
-  for (int r = 0; r < top; ++r) {
-    float v = minus_inf;
-    int at = INT_MAX;
-    auto look = [&](float w, int j) {
-      if (before(last_v, last_i, w, j) && before(w, j, v, at)) {
-        v = w;
-        at = j;
+  if (top > 0) {
+    int r = 0;
+    for (int j = 0; j < kThreads / 4; ++j) {
+      const float4 q = reinterpret_cast<const float4*>(maxima)[j];
+      r += (q.x > mine || (q.x == mine && 4 * j < tid)) + (q.y > mine || (q.y == mine && 4 * j + 1 < tid)) +
+           (q.z > mine || (q.z == mine && 4 * j + 2 < tid)) + (q.w > mine || (q.w == mine && 4 * j + 3 < tid));
+    }
+    if (r == top - 1) bound = {mine, INT_MAX};
+    __syncthreads();
+    Logit least = bound;
+    if (mine >= least.v) hot[atomicAdd(&hot_n, 1)] = tid;
+    __syncthreads();
+    const int nh = hot_n, items = nh * ((hi - lo + kThreads - 1) / kThreads);
+    auto look = [&](float v, int at) {
+      if (v > least.v || (v == least.v && at <= least.i)) {  // never a NaN: the list has one order
+        const int k = atomicAdd(&list_n, 1);
+        if (k < kList) list[k] = {v, at};
       }
     };
-    if (a.s == a.s) {
-      for (int i = threadIdx.x; i < n8; i += kThreads) {
-        float f[8];
-        load8(zr + 8 * i, f);
+    int n;
+    while (true) {
+      for (int k = tid; k < items; k += kThreads) {
+        const int at = lo + k / nh * kThreads + hot[k % nh];
+        if (at < hi) {
+          float f[8];
+          load8(zr + 8 * at, f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) look(f[j], 8 * i + j);
+          for (int j = 0; j < 8; ++j) look(f[j], 8 * at + j);
+        }
       }
-      if (8 * n8 + threadIdx.x < vocab) look(to_float(zr[8 * n8 + threadIdx.x]), 8 * n8 + threadIdx.x);
+      if (tail >= 0) look(to_float(zr[tail]), tail);
+      __syncthreads();
+      n = list_n;
+      if (n <= kList) break;
+      for (int k = tid; k < kList; k += kThreads)
+        if (place(list, kList, list[k]) == top - 1) bound = list[k];
+      __syncthreads();
+      least = bound;
+      if (tid == 0) list_n = 0;
+      __syncthreads();
     }
-    auto join = [&](float w, int j) {
-      if (before(w, j, v, at)) {
-        v = w;
-        at = j;
-      }
-    };
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) join(__shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, at, o));
-    if (lane == 0) {
-      best_v[warp] = v;
-      best_i[warp] = at;
-    }
-    __syncthreads();
-    v = best_v[0];
-    at = best_i[0];
-    for (int w = 1; w < kThreads / 32; ++w) join(best_v[w], best_i[w]);
-    __syncthreads();
-    last_v = v;
-    last_i = at;
-    if (threadIdx.x == 0) {
-      const bool bad = !(a.s == a.s);
-      ids[row * top + r] = bad ? -1 : at;
-      top_logp[row * top + r] = bad ? a.s : value(v);
+    if (tid >= n && tid < top) best[tid] = {minus_inf, INT_MAX};  // a range shorter than top
+    for (int k = tid; k < n; k += kThreads) {
+      const int r2 = place(list, n, list[k]);
+      if (r2 < top) best[r2] = list[k];
     }
   }
+  if (ncl > 1) cluster_sync_all();
+  else __syncthreads();
+  if (rank == 0) {
+    Sums all = total;
+    for (uint32_t q = 1; q < ncl; ++q) {
+      const uint32_t at = mapa_shared(smem_u32(&total), q);
+      const float2 x = ld_shared_cluster_f32x2(at), y = ld_shared_cluster_f32x2(at + 8);
+      all = merge(all, {x.x, x.y, y.x, y.y}, c);
+    }
+    const bool none = all.s == 0.f, bad = !(all.s == all.s);
+    const float log_s = logf(all.s) + all.low / all.s;
+    auto value = [&](float v) { return none ? minus_inf : fmaf(v - all.m, scale, -log_s); };
+    if (tid == 0) {
+      int token = tokens[row];
+      if (token >= vocab) {  // outside the vocabulary: reported, and the row ignored
+        record_error(err, kDevCeBadLabel);
+        token = -1;
+      }
+      logp[row] = token < 0 ? 0.f : value(to_float(zr[token]));
+      lse_out[row] = none ? minus_inf : fmaf(all.m, scale, log_s);
+      if (ENT) entropy[row] = none ? 0.f : log_s - scale * (all.t / all.s);
+    }
+    if (ncl > 1) {  // the ranges' alternatives in one order
+      const int n = (int)ncl * top;
+      for (int k = tid; k < n; k += kThreads) {
+        const float2 x = ld_shared_cluster_f32x2(mapa_shared(smem_u32(&best[k % top]), k / top));
+        list[k] = {x.x, __float_as_int(x.y)};
+      }
+      __syncthreads();
+      for (int k = tid; k < n; k += kThreads) {
+        const int r = place(list, n, list[k]);
+        if (r < top) best[r] = list[k];  // the others have been read
+      }
+      __syncthreads();
+    }
+    if (tid < top) {
+      ids[row * top + tid] = bad ? -1 : best[tid].i;
+      top_logp[row * top + tid] = bad ? all.s : value(best[tid].v);
+    }
+  }
+  if (ncl > 1) cluster_sync_all();  // the first CTA has read its peers' results
 }
 
 // Backward, element by element from the row's lse and entropy:
@@ -248,15 +344,42 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-void logprob_rows(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows, int vocab, float scale,
+// CTAs of a row: enough for four on each SM, each with two octets a thread or
+// more.
+static int row_ctas(int64_t rows, int vocab) {
+  int n = 1;
+  while (n < kMaxCluster && rows * n * 2 <= 4 * num_sms() && vocab >= 2 * n * kThreads * 16) n *= 2;
+  return n;
+}
+
+template <typename T, bool ENT>
+static bool logprob_rows_as(const T* z, int64_t ld, const int32_t* tokens, int64_t rows, int vocab, float scale,
+                            float* logp, float* lse, float* entropy, int top, int32_t* ids, float* top_logp, int* err,
+                            cudaStream_t st) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)row_ctas(rows, vocab);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rows * attr[0].val.clusterDim.x);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, logprob_rows_kernel<T, ENT>, z, ld, tokens, vocab, scale, logp, lse, entropy, top,
+                            ids, top_logp, err) == cudaSuccess;
+}
+
+bool logprob_rows(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows, int vocab, float scale,
                   float* logp, float* lse, float* entropy, int top, int32_t* ids, float* top_logp, int* err,
                   cudaStream_t st) {
-  if (f32)
-    logprob_rows_kernel<<<(unsigned)rows, kThreads, 0, st>>>(static_cast<const float*>(z), ld, tokens, vocab, scale,
-                                                             logp, lse, entropy, top, ids, top_logp, err);
-  else
-    logprob_rows_kernel<<<(unsigned)rows, kThreads, 0, st>>>(static_cast<const bf16*>(z), ld, tokens, vocab, scale,
-                                                             logp, lse, entropy, top, ids, top_logp, err);
+#define SF_LOGPROB(T, ENT)                                                                                        \
+  logprob_rows_as<T, ENT>(static_cast<const T*>(z), ld, tokens, rows, vocab, scale, logp, lse, entropy, top, ids, \
+                          top_logp, err, st)
+  if (f32) return entropy ? SF_LOGPROB(float, true) : SF_LOGPROB(float, false);
+  return entropy ? SF_LOGPROB(bf16, true) : SF_LOGPROB(bf16, false);
+#undef SF_LOGPROB
 }
 
 void logprob_rows_bwd(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows, int vocab,

@@ -581,8 +581,11 @@ int sf_op_logprob_rows(const void* z, int32_t z_type, int64_t ldz, const int32_t
   if (!logprob_outputs(logp, lse, entropy, vocab, top, ids, top_logp)) return SF_EINVAL;
   int* err = dev_err_word();
   if (!err) return SF_ECUDA;
-  sf::logprob_rows(z, z_type == SF_F32, ldz, tokens, rows, vocab, scale, logp, lse, entropy, top, ids,
-                   top_logp, err, S(stream));
+  if (!sf::logprob_rows(z, z_type == SF_F32, ldz, tokens, rows, vocab, scale, logp, lse, entropy, top,
+                        ids, top_logp, err, S(stream))) {
+    cudaGetLastError();
+    return SF_ECUDA;
+  }
   return launched();
 }
 
@@ -640,8 +643,12 @@ int sf_op_lm_logprob(const uint16_t* h, const uint16_t* w, const int32_t* tokens
     z.layout = sf::kNT; z.epi = sf::kEpiF32; z.M = rows; z.N = v; z.K = d;
     z.A = h + r0 * d; z.lda = d; z.B = w; z.ldb = d; z.C = zf; z.ldc = v;
     if (sf::gemm(z, err, S(stream), why) != 0) return SF_ECUDA;
-    sf::logprob_rows(zf, true, v, tokens + r0, rows, v, scale, logp + r0, lse + r0, entropy ? entropy + r0 : nullptr,
-                     top, top ? ids + r0 * top : nullptr, top ? top_logp + r0 * top : nullptr, err, S(stream));
+    if (!sf::logprob_rows(zf, true, v, tokens + r0, rows, v, scale, logp + r0, lse + r0,
+                          entropy ? entropy + r0 : nullptr, top, top ? ids + r0 * top : nullptr,
+                          top ? top_logp + r0 * top : nullptr, err, S(stream))) {
+      cudaGetLastError();
+      return SF_ECUDA;
+    }
   }
   return launched();
 }

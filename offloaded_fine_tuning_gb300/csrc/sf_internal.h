@@ -273,8 +273,8 @@ bool join_bwd(const JoinArgs& a, const float* xout, const void* h, bool h32,
 // ---- log probabilities of given tokens (logprob.cu); z fp32 or bf16, row
 // stride ld (a multiple of 8), 16-byte aligned.  entropy may be null; top <= 32
 // alternatives; a token at or beyond the vocabulary writes kDevCeBadLabel to
-// *err.
-void logprob_rows(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows,
+// *err.  False: no launch.
+bool logprob_rows(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows,
                   int vocab, float scale, float* logp, float* lse, float* entropy, int top,
                   int32_t* ids, float* top_logp, int* err, cudaStream_t st);
 // dz may be z where z is bf16; dentropy (with entropy) may be null.
