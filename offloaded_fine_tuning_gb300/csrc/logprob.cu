@@ -120,38 +120,49 @@ __device__ __forceinline__ bool before(Logit a, Logit b) { return a.v > b.v || (
 
 constexpr int kThreads = 256;
 constexpr int kList = 512;    // candidates that a CTA holds
+constexpr int kGroups = 64;   // sets of threads whose maxima bound the alternatives
 constexpr int kMaxCluster = 8;
 
-// The place of a in a list, were the list in order.
-__device__ __forceinline__ int place(const Logit* list, int n, Logit a) {
-  int r = 0;
-  for (int j = 0; j < n; ++j) r += before(list[j], a);
-  return r;
+// The places that the entries of a list would have were it in order: four
+// neighbouring threads count for an entry, and what() gets it with its place.
+template <int NT, class F>
+__device__ __forceinline__ void places(const Logit* list, int n, F what) {
+  const int part = threadIdx.x & 3;
+  for (int k = threadIdx.x >> 2; (k & ~7) < n; k += NT / 4) {  // a warp's eight entries together
+    const Logit a = k < n ? list[k] : Logit{0.f, 0};
+    int r = 0;
+    for (int j = part; j < n; j += 4) r += before(list[j], a);
+    r += __shfl_xor_sync(0xffffffffu, r, 1);
+    r += __shfl_xor_sync(0xffffffffu, r, 2);
+    if (part == 0 && k < n) what(a, r);
+  }
 }
 
-// Forward: a cluster of CTAs (one, or several where there are few rows) takes a
-// row, each CTA a range of it, and reads it once.
+// Forward: a cluster of CTAs (one, or several where there are few rows) of NT
+// threads takes a row, each CTA a range of it, and reads it once.
 //
 // The alternatives come from the threads' own maxima, which the sums need
-// anyway: the top-th largest of them, v, is a bound that at least `top` logits
-// reach, and only threads whose maximum reaches it can hold such a logit.
-// Those threads' logits (about top / kThreads of the row) are read again, and
-// what reaches the bound is put in order by counting.  Where more reach it than
-// the list holds (equal logits, masked rows), the top-th of those that it does
-// hold is the next bound.  Each such round leaves out at least kList - top of
-// them, and the low ids come first, so that rows of one value end in two.
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(kThreads)
+// anyway: of the maxima of 64 sets of threads the top-th largest, v, is a bound
+// that at least `top` logits reach (about 64 log(64 / (64 - top)) of them, 24
+// for 20), and only threads whose maximum reaches it can hold such a logit.
+// Those threads' logits are read again, and what reaches the bound is put in
+// order by counting.  Where more reach it than the list holds (equal logits,
+// masked rows), the top-th of those that it does hold is the next bound.  Each
+// such round leaves out at least kList - top of them, and the low ids come
+// first, so that rows of one value end in two.
+template <typename T, bool ENT, int NT>
+__global__ void __launch_bounds__(NT)
     logprob_rows_kernel(const T* __restrict__ z, int64_t ld, const int32_t* __restrict__ tokens, int vocab,
                         float scale, float* __restrict__ logp, float* __restrict__ lse_out,
                         float* __restrict__ entropy, int top, int32_t* __restrict__ ids,
                         float* __restrict__ top_logp, int* err) {
   constexpr int U = sizeof(T) == 4 ? 2 : 4;  // octets in flight: 64 bytes
-  __shared__ Sums part[kThreads / 32];
+  constexpr int SHARE = NT / kGroups;        // threads of a set
+  __shared__ Sums part[NT / 32];
   __shared__ __align__(16) Sums total;         // read by the cluster
   __shared__ Logit best[SF_LOGPROB_TOP_MAX];   // read by the cluster
-  __shared__ __align__(16) float maxima[kThreads];
-  __shared__ int hot[kThreads];
+  __shared__ __align__(16) float maxima[kGroups];
+  __shared__ int hot[NT];
   __shared__ Logit list[kList];
   __shared__ Logit bound;
   __shared__ int hot_n, list_n;
@@ -169,14 +180,14 @@ __global__ void __launch_bounds__(kThreads)
   if (tid == 0) hot_n = list_n = 0;
   Sums a = {-FLT_MAX, 0.f, 0.f, 0.f};
   int i = lo + tid;
-  for (; i + (U - 1) * kThreads < hi; i += U * kThreads) {
+  for (; i + (U - 1) * NT < hi; i += U * NT) {
     float f[U][8];
 #pragma unroll
-    for (int u = 0; u < U; ++u) load8(zr + 8 * (i + u * kThreads), f[u]);
+    for (int u = 0; u < U; ++u) load8(zr + 8 * (i + u * NT), f[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) add<ENT>(a, f[u], c);
   }
-  for (; i < hi; i += kThreads) {
+  for (; i < hi; i += NT) {
     float f[8];
     load8(zr + 8 * i, f);
     add<ENT>(a, f, c);
@@ -185,32 +196,43 @@ __global__ void __launch_bounds__(kThreads)
     const float f[1] = {to_float(zr[tail])};
     add<ENT>(a, f, c);
   }
-  maxima[tid] = a.s == 0.f ? minus_inf : a.m;  // s is at least 1 with any logit above -inf
-  const float mine = maxima[tid];
+  const float mine = a.s == 0.f ? minus_inf : a.m;  // s is at least 1 with any logit above -inf
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     a = merge(a, {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
                   __shfl_xor_sync(0xffffffffu, a.low, o), __shfl_xor_sync(0xffffffffu, a.t, o)}, c);
   if (lane == 0) part[warp] = a;
+  if (top > 0) {
+    float group = mine;
+#pragma unroll
+    for (int o = 1; o < SHARE; o *= 2) group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, o));
+    if (tid % SHARE == 0) maxima[tid / SHARE] = group;
+    __syncthreads();
+    // the SHARE threads of a set count the larger ones of the others, a part each
+    int r = 0;
+#pragma unroll
+    for (int j = 0; j < kGroups / SHARE / 4; ++j) {
+      const int at = tid % SHARE * (kGroups / SHARE) + 4 * j;
+      const float4 q = *reinterpret_cast<const float4*>(maxima + at);
+      const int me = tid / SHARE;
+      r += (q.x > group || (q.x == group && at < me)) + (q.y > group || (q.y == group && at + 1 < me)) +
+           (q.z > group || (q.z == group && at + 2 < me)) + (q.w > group || (q.w == group && at + 3 < me));
+    }
+#pragma unroll
+    for (int o = 1; o < SHARE; o *= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
+    if (r == top - 1) bound = {group, INT_MAX};  // each thread of one set
+  }
   __syncthreads();
   if (warp == 0) {
     a = part[0];
-    for (int w = 1; w < kThreads / 32; ++w) a = merge(a, part[w], c);
+    for (int w = 1; w < NT / 32; ++w) a = merge(a, part[w], c);
     if (lane == 0) total = a;
   }
   if (top > 0) {
-    int r = 0;
-    for (int j = 0; j < kThreads / 4; ++j) {
-      const float4 q = reinterpret_cast<const float4*>(maxima)[j];
-      r += (q.x > mine || (q.x == mine && 4 * j < tid)) + (q.y > mine || (q.y == mine && 4 * j + 1 < tid)) +
-           (q.z > mine || (q.z == mine && 4 * j + 2 < tid)) + (q.w > mine || (q.w == mine && 4 * j + 3 < tid));
-    }
-    if (r == top - 1) bound = {mine, INT_MAX};
-    __syncthreads();
     Logit least = bound;
     if (mine >= least.v) hot[atomicAdd(&hot_n, 1)] = tid;
     __syncthreads();
-    const int nh = hot_n, items = nh * ((hi - lo + kThreads - 1) / kThreads);
+    const int nh = hot_n, items = nh * ((hi - lo + NT - 1) / NT);
     auto look = [&](float v, int at) {
       if (v > least.v || (v == least.v && at <= least.i)) {  // never a NaN: the list has one order
         const int k = atomicAdd(&list_n, 1);
@@ -219,8 +241,8 @@ __global__ void __launch_bounds__(kThreads)
     };
     int n;
     while (true) {
-      for (int k = tid; k < items; k += kThreads) {
-        const int at = lo + k / nh * kThreads + hot[k % nh];
+      for (int k = tid; k < items; k += NT) {
+        const int at = lo + k / nh * NT + hot[k % nh];
         if (at < hi) {
           float f[8];
           load8(zr + 8 * at, f);
@@ -232,18 +254,18 @@ __global__ void __launch_bounds__(kThreads)
       __syncthreads();
       n = list_n;
       if (n <= kList) break;
-      for (int k = tid; k < kList; k += kThreads)
-        if (place(list, kList, list[k]) == top - 1) bound = list[k];
+      places<NT>(list, kList, [&](Logit b, int r) {
+        if (r == top - 1) bound = b;
+      });
       __syncthreads();
       least = bound;
       if (tid == 0) list_n = 0;
       __syncthreads();
     }
     if (tid >= n && tid < top) best[tid] = {minus_inf, INT_MAX};  // a range shorter than top
-    for (int k = tid; k < n; k += kThreads) {
-      const int r2 = place(list, n, list[k]);
-      if (r2 < top) best[r2] = list[k];
-    }
+    places<NT>(list, n, [&](Logit b, int r) {
+      if (r < top) best[r] = b;
+    });
   }
   if (ncl > 1) cluster_sync_all();
   else __syncthreads();
@@ -269,15 +291,14 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (ncl > 1) {  // the ranges' alternatives in one order
       const int n = (int)ncl * top;
-      for (int k = tid; k < n; k += kThreads) {
+      for (int k = tid; k < n; k += NT) {
         const float2 x = ld_shared_cluster_f32x2(mapa_shared(smem_u32(&best[k % top]), k / top));
         list[k] = {x.x, __float_as_int(x.y)};
       }
       __syncthreads();
-      for (int k = tid; k < n; k += kThreads) {
-        const int r = place(list, n, list[k]);
-        if (r < top) best[r] = list[k];  // the others have been read
-      }
+      places<NT>(list, n, [&](Logit b, int r) {
+        if (r < top) best[r] = b;
+      });
       __syncthreads();
     }
     if (tid < top) {
@@ -344,38 +365,56 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-// CTAs of a row: enough for four on each SM, each with two octets a thread or
-// more.
-static int row_ctas(int64_t rows, int vocab) {
+// Short rows: 64 threads a row, many rows at a time.  Few rows: 1024 threads, up
+// to eight CTAs each, as long as all of a row's threads have two octets or more.
+// Else 256 threads a row.
+struct RowShape {
+  int threads, ctas;
+};
+static RowShape row_shape(int64_t rows, int vocab) {
+  if (vocab <= 4096) return {64, 1};
+  if (rows > num_sms()) return {256, 1};
   int n = 1;
-  while (n < kMaxCluster && rows * n * 2 <= 4 * num_sms() && vocab >= 2 * n * kThreads * 16) n *= 2;
-  return n;
+  while (n < kMaxCluster && rows * n * 2 <= num_sms() && vocab >= 2 * n * 1024 * 8) n *= 2;
+  return {1024, n};
 }
 
-template <typename T, bool ENT>
+template <typename T, bool ENT, int NT>
 static bool logprob_rows_as(const T* z, int64_t ld, const int32_t* tokens, int64_t rows, int vocab, float scale,
                             float* logp, float* lse, float* entropy, int top, int32_t* ids, float* top_logp, int* err,
-                            cudaStream_t st) {
+                            int ctas, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)row_ctas(rows, vocab);
+  attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rows * attr[0].val.clusterDim.x);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)rows * (unsigned)ctas);
+  cfg.blockDim = dim3(NT);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprob_rows_kernel<T, ENT>, z, ld, tokens, vocab, scale, logp, lse, entropy, top,
-                            ids, top_logp, err) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, logprob_rows_kernel<T, ENT, NT>, z, ld, tokens, vocab, scale, logp, lse, entropy,
+                            top, ids, top_logp, err) == cudaSuccess;
+}
+
+template <typename T, bool ENT>
+static bool logprob_rows_of(const T* z, int64_t ld, const int32_t* tokens, int64_t rows, int vocab, float scale,
+                            float* logp, float* lse, float* entropy, int top, int32_t* ids, float* top_logp, int* err,
+                            cudaStream_t st) {
+  const RowShape s = row_shape(rows, vocab);
+#define SF_LOGPROB(NT)                                                                                              \
+  logprob_rows_as<T, ENT, NT>(z, ld, tokens, rows, vocab, scale, logp, lse, entropy, top, ids, top_logp, err, s.ctas, \
+                              st)
+  return s.threads == 64 ? SF_LOGPROB(64) : s.threads == 256 ? SF_LOGPROB(256) : SF_LOGPROB(1024);
+#undef SF_LOGPROB
 }
 
 bool logprob_rows(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows, int vocab, float scale,
                   float* logp, float* lse, float* entropy, int top, int32_t* ids, float* top_logp, int* err,
                   cudaStream_t st) {
 #define SF_LOGPROB(T, ENT)                                                                                        \
-  logprob_rows_as<T, ENT>(static_cast<const T*>(z), ld, tokens, rows, vocab, scale, logp, lse, entropy, top, ids, \
+  logprob_rows_of<T, ENT>(static_cast<const T*>(z), ld, tokens, rows, vocab, scale, logp, lse, entropy, top, ids, \
                           top_logp, err, st)
   if (f32) return entropy ? SF_LOGPROB(float, true) : SF_LOGPROB(float, false);
   return entropy ? SF_LOGPROB(bf16, true) : SF_LOGPROB(bf16, false);
