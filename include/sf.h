@@ -733,7 +733,7 @@ int sf_op_rmsnorm_bwd_noalloc(const float* x, const uint16_t* g, const float* rs
  * sf_op_logprob_rows, sf_op_lm_logprob or their backwards a token, at or beyond
  * the vocabulary; 5: sf_op_qknorm_rope_fwd or _bwd met a position outside the
  * rotation table; 6: an attention backward found its shared memory misaligned
- * and wrote nothing.  The first code a launch writes stays.  Synchronises the
+ * and wrote nothing; 7: a bounded wait ran out in sf_op_join_bwd.  The first code a launch writes stays.  Synchronises the
  * device. */
 int sf_op_device_error(int32_t* out);
 

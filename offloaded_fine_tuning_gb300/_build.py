@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsfslide.so")
 SOURCES = ["gemm.cu", "attention.cu", "elementwise.cu", "engine.cpp", "ops.cpp", "noalloc.cu", "attention_tc.cu", "qknorm.cu",
-           "ckpt8.cu", "join.cu", "logprob.cu"]
+           "ckpt8.cu", "join.cu", "join_bwd.cu", "logprob.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

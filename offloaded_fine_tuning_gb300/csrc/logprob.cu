@@ -91,8 +91,9 @@ __device__ __forceinline__ Sums merge(Sums a, Sums b, float c) {
   return a;
 }
 // N logits at once: one look at the maximum, and a tree of their exponentials.
+// Returns their maximum.
 template <bool ENT, int N>
-__device__ __forceinline__ void add(Sums& a, const float (&z)[N], float c) {
+__device__ __forceinline__ float add(Sums& a, const float (&z)[N], float c) {
   float m = z[0];
 #pragma unroll
   for (int j = 1; j < N; ++j) m = fmaxf(m, z[j]);
@@ -109,6 +110,7 @@ __device__ __forceinline__ void add(Sums& a, const float (&z)[N], float c) {
 #pragma unroll
     for (int j = 0; j < w; ++j) e[j] += e[j + w];
   add_sum(a, e[0]);
+  return m;
 }
 
 // The order of the alternatives: larger values first, then lower ids.
@@ -144,12 +146,15 @@ __device__ __forceinline__ void places(const Logit* list, int n, F what) {
 // The alternatives come from the threads' own maxima, which the sums need
 // anyway: of the maxima of 64 sets of threads the top-th largest, v, is a bound
 // that at least `top` logits reach (about 64 log(64 / (64 - top)) of them, 24
-// for 20), and only threads whose maximum reaches it can hold such a logit.
-// Those threads' logits are read again, and what reaches the bound is put in
-// order by counting.  Where more reach it than the list holds (equal logits,
-// masked rows), the top-th of those that it does hold is the next bound.  Each
-// such round leaves out at least kList - top of them, and the low ids come
-// first, so that rows of one value end in two.
+// for 20), and only threads whose maximum reaches it can hold such a logit.  A
+// thread keeps the maxima of up to SPANS spans of its logits, so that only the
+// spans that reach the bound are read again, and what reaches it is put in
+// order by counting (4096 x 128256 fp32, 20 alternatives: 383 us with the
+// threads' whole ranges read again, which L2 no longer holds, 314 us so).  Where
+// more reach it than the list holds (equal logits, masked rows), the top-th of
+// those that it does hold is the next bound.  Each such round leaves out at
+// least kList - top of them, and the low ids come first, so that rows of one
+// value end in two.
 template <typename T, bool ENT, int NT>
 __global__ void __launch_bounds__(NT)
     logprob_rows_kernel(const T* __restrict__ z, int64_t ld, const int32_t* __restrict__ tokens, int vocab,
@@ -158,11 +163,13 @@ __global__ void __launch_bounds__(NT)
                         float* __restrict__ top_logp, int* err) {
   constexpr int U = sizeof(T) == 4 ? 2 : 4;  // octets in flight: 64 bytes
   constexpr int SHARE = NT / kGroups;        // threads of a set
+  constexpr int SPANS = NT == 256 || NT == 512 ? 8 : 1;
   __shared__ Sums part[NT / 32];
   __shared__ __align__(16) Sums total;         // read by the cluster
   __shared__ Logit best[SF_LOGPROB_TOP_MAX];   // read by the cluster
   __shared__ __align__(16) float maxima[kGroups];
-  __shared__ int hot[NT];
+  __shared__ float span_max[SPANS > 1 ? SPANS * NT : 1];
+  __shared__ uint16_t hot[SPANS * NT];  // span * NT + thread
   __shared__ Logit list[kList];
   __shared__ Logit bound;
   __shared__ int hot_n, list_n;
@@ -178,19 +185,27 @@ __global__ void __launch_bounds__(NT)
   const int lo = min((int)rank * each, n8), hi = min(lo + each, n8);
   const int tail = rank == ncl - 1 && tid < (vocab & 7) ? 8 * n8 + tid : -1;  // the last logits, one a thread
   if (tid == 0) hot_n = list_n = 0;
+  const int octets = (hi - lo + NT - 1) / NT;                        // of a thread
+  const int length = ((octets + SPANS - 1) / SPANS + U - 1) / U * U;  // of a span
   Sums a = {-FLT_MAX, 0.f, 0.f, 0.f};
-  int i = lo + tid;
-  for (; i + (U - 1) * NT < hi; i += U * NT) {
-    float f[U][8];
+#pragma unroll 1
+  for (int s = 0; s < SPANS; ++s) {
+    float m = minus_inf;
+    int i = lo + tid + s * length * NT;
+    const int end = SPANS == 1 ? hi : min(i + length * NT, hi);
+    for (; i + (U - 1) * NT < end; i += U * NT) {
+      float f[U][8];
 #pragma unroll
-    for (int u = 0; u < U; ++u) load8(zr + 8 * (i + u * NT), f[u]);
+      for (int u = 0; u < U; ++u) load8(zr + 8 * (i + u * NT), f[u]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) add<ENT>(a, f[u], c);
-  }
-  for (; i < hi; i += NT) {
-    float f[8];
-    load8(zr + 8 * i, f);
-    add<ENT>(a, f, c);
+      for (int u = 0; u < U; ++u) m = fmaxf(m, add<ENT>(a, f[u], c));
+    }
+    for (; i < end; i += NT) {
+      float f[8];
+      load8(zr + 8 * i, f);
+      m = fmaxf(m, add<ENT>(a, f, c));
+    }
+    if (SPANS > 1 && top > 0) span_max[s * NT + tid] = m;
   }
   if (tail >= 0) {
     const float f[1] = {to_float(zr[tail])};
@@ -230,9 +245,12 @@ __global__ void __launch_bounds__(NT)
   }
   if (top > 0) {
     Logit least = bound;
-    if (mine >= least.v) hot[atomicAdd(&hot_n, 1)] = tid;
+    if (mine >= least.v) {
+      for (int s = 0; s < SPANS; ++s)
+        if (SPANS == 1 || span_max[s * NT + tid] >= least.v) hot[atomicAdd(&hot_n, 1)] = (uint16_t)(s * NT + tid);
+    }
     __syncthreads();
-    const int nh = hot_n, items = nh * ((hi - lo + NT - 1) / NT);
+    const int nh = hot_n, items = nh * min(length, octets);
     auto look = [&](float v, int at) {
       if (v > least.v || (v == least.v && at <= least.i)) {  // never a NaN: the list has one order
         const int k = atomicAdd(&list_n, 1);
@@ -242,7 +260,7 @@ __global__ void __launch_bounds__(NT)
     int n;
     while (true) {
       for (int k = tid; k < items; k += NT) {
-        const int at = lo + k / nh * NT + hot[k % nh];
+        const int unit = hot[k % nh], at = lo + (unit / NT * length + k / nh) * NT + unit % NT;
         if (at < hi) {
           float f[8];
           load8(zr + 8 * at, f);
@@ -365,17 +383,22 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-// Short rows: 64 threads a row, many rows at a time.  Few rows: 1024 threads, up
-// to eight CTAs each, as long as all of a row's threads have two octets or more.
-// Else 256 threads a row.
+// Threads of a row.  Many rows: as few as still give each a dozen octets, so
+// that one row's reductions hide behind the loads of others.  Few rows: more of
+// them, up to eight CTAs of 1024.
 struct RowShape {
   int threads, ctas;
 };
 static RowShape row_shape(int64_t rows, int vocab) {
-  if (vocab <= 4096) return {64, 1};
-  if (rows > num_sms()) return {256, 1};
+  if (vocab <= 1536) return {64, 1};
+  if (vocab <= 16384) return {128, 1};
+  if (rows > 2 * num_sms()) return {256, 1};
+  if (rows > num_sms()) return {512, 1};
   int n = 1;
-  while (n < kMaxCluster && rows * n * 2 <= num_sms() && vocab >= 2 * n * 1024 * 8) n *= 2;
+  // clusters of eight leave SMs without one: 16 of them take two turns
+  while (n < kMaxCluster && rows * n * 2 <= num_sms() && vocab >= 2 * n * 1024 * 8 &&
+         (n < 4 || rows * 12 <= num_sms()))
+    n *= 2;
   return {1024, n};
 }
 
@@ -406,7 +429,13 @@ static bool logprob_rows_of(const T* z, int64_t ld, const int32_t* tokens, int64
 #define SF_LOGPROB(NT)                                                                                              \
   logprob_rows_as<T, ENT, NT>(z, ld, tokens, rows, vocab, scale, logp, lse, entropy, top, ids, top_logp, err, s.ctas, \
                               st)
-  return s.threads == 64 ? SF_LOGPROB(64) : s.threads == 256 ? SF_LOGPROB(256) : SF_LOGPROB(1024);
+  switch (s.threads) {
+    case 64: return SF_LOGPROB(64);
+    case 128: return SF_LOGPROB(128);
+    case 256: return SF_LOGPROB(256);
+    case 512: return SF_LOGPROB(512);
+    default: return SF_LOGPROB(1024);
+  }
 #undef SF_LOGPROB
 }
 

@@ -465,10 +465,12 @@ int sf_op_join_bwd(const float* xout, const void* h, int32_t h_type, const uint1
   if (g_post && (!rstd_post || !dg_post || !al1(rstd_post) || !al1(dg_post))) return SF_EINVAL;
   if (gate && (!dgate || !al1(dgate))) return SF_EINVAL;
   if ((g_post || gate || g_next) && (!scratch || !al16(scratch))) return SF_EINVAL;
+  int* err = dev_err_word();
+  if (!err) return SF_ECUDA;
   if (!sf::join_bwd(a, xout, h, h_type == SF_F32, rstd_post, rstd_next, dy, dres, dx, dh,
                     reinterpret_cast<bf16*>(g_post ? dg_post : nullptr),
                     reinterpret_cast<bf16*>(gate ? dgate : nullptr),
-                    reinterpret_cast<bf16*>(g_next ? dg_next : nullptr), scratch, S(stream))) {
+                    reinterpret_cast<bf16*>(g_next ? dg_next : nullptr), scratch, err, S(stream))) {
     cudaGetLastError();
     return SF_ECUDA;
   }

@@ -16,6 +16,7 @@ enum DevErr : int {
   kDevCeBadLabel = 4,  // a label or token at or beyond the vocabulary (the row is ignored)
   kDevBadPosition = 5,  // a position outside the rotation table (the token is not rotated)
   kDevSharedBase = 6,   // an attention backward's shared memory does not start on 1024 bytes (nothing is written)
+  kDevJoinTimeout = 7,
 };
 
 // Operand layouts of C[M,N] = A * B (all matrices row-major in memory):
@@ -263,12 +264,13 @@ struct JoinArgs {
 };
 void join_fwd(const JoinArgs& a, const float* x, const void* h, bool h32, float* xout,
               __nv_bfloat16* y, float* rstd_post, float* rstd_next, float eps, cudaStream_t st);
-// part: fp32 [join_bwd_parts, 2, d].  False: no launch.
+// part: fp32 [join_bwd_parts, 2, d].  A wait that runs out writes kDevJoinTimeout to
+// *err.  False: no launch.
 int join_bwd_parts(int64_t rows, int d);
 bool join_bwd(const JoinArgs& a, const float* xout, const void* h, bool h32,
               const float* rstd_post, const float* rstd_next, const float* dy, const float* dres,
               float* dx, void* dh, __nv_bfloat16* dg_post, __nv_bfloat16* dgate,
-              __nv_bfloat16* dg_next, float* part, cudaStream_t st);
+              __nv_bfloat16* dg_next, float* part, int* err, cudaStream_t st);
 
 // ---- log probabilities of given tokens (logprob.cu); z fp32 or bf16, row
 // stride ld (a multiple of 8), 16-byte aligned.  entropy may be null; top <= 32
