@@ -49,11 +49,6 @@ __device__ __forceinline__ float4 unpack4(uint2 u) {
 // ------------------------------------------------------------------ the join
 // A thread's quads of four columns; h is bf16 or fp32.
 template <bool H32>
-__device__ __forceinline__ float4 load_h(const void* h, int64_t at) {
-  if (H32) return *reinterpret_cast<const float4*>(static_cast<const float*>(h) + at);
-  return unpack4(*reinterpret_cast<const uint2*>(static_cast<const bf16*>(h) + at));
-}
-template <bool H32>
 __device__ __forceinline__ void store_h(void* h, int64_t at, const float4& v) {
   if (H32) *reinterpret_cast<float4*>(static_cast<float*>(h) + at) = v;
   else *reinterpret_cast<uint2*>(static_cast<bf16*>(h) + at) = pack4(v.x, v.y, v.z, v.w);
@@ -68,7 +63,7 @@ __device__ __forceinline__ float4 mul(const float4& a, float b) {
   return make_float4(a.x * b, a.y * b, a.z * b, a.w * b);
 }
 __device__ __forceinline__ float dot(const float4& a, const float4& b) {
-  return (a.x * b.x + a.y * b.y) + (a.z * b.z + a.w * b.w);
+  return fmaf(a.x, b.x, a.y * b.y) + fmaf(a.z, b.z, a.w * b.w);
 }
 // The elements of a quad that its two words keep, and 0 for the others.
 __device__ __forceinline__ float4 pick(const float4& a, uint2 w, uint32_t top) {
@@ -76,23 +71,18 @@ __device__ __forceinline__ float4 pick(const float4& a, uint2 w, uint32_t top) {
                      keep_hi(w.y, top) ? a.w : 0.f);
 }
 
-// The words of a thread's quads i = t + k * lanes (k < Q) of a row that starts
-// at quad `at` of the tensor (both even).  Two neighbouring lanes hold the two
-// halves of each octet: the even one asks the generator for the octets of even
-// k, the odd one for those of odd k.
-template <int Q>
-__device__ __forceinline__ void row_words(int64_t at, int t, int lanes, uint64_t offset, uint64_t seed,
-                                          uint2 (&words)[Q]) {
-  const bool odd = t & 1;
-#pragma unroll
-  for (int k = 0; k < Q; k += 2) {
-    const Words w = philox((uint64_t)((at + t + (k + odd) * lanes) >> 1), offset, seed);
-    const uint2 mine = odd ? make_uint2(w.c, w.d) : make_uint2(w.a, w.b);
-    const uint2 theirs = odd ? make_uint2(w.a, w.b) : make_uint2(w.c, w.d);
-    const uint2 got = make_uint2(__shfl_xor_sync(0xffffffffu, theirs.x, 1), __shfl_xor_sync(0xffffffffu, theirs.y, 1));
-    words[k] = odd ? got : mine;
-    words[k + 1] = odd ? mine : got;
-  }
+// The words of two of a thread's quads, `quad` and, `lanes` further, another, both
+// counted from the start of the tensor.  Two neighbouring lanes hold the two
+// halves of each octet: the even one asks the generator for the octet of both
+// first quads, the odd one for that of the second.
+__device__ __forceinline__ void pair_words(int64_t quad, int lanes, bool odd, uint64_t offset, uint64_t seed,
+                                           uint2& first, uint2& second) {
+  const Words w = philox((uint64_t)((quad + (odd ? lanes : 0)) >> 1), offset, seed);
+  const uint2 mine = odd ? make_uint2(w.c, w.d) : make_uint2(w.a, w.b);
+  const uint2 theirs = odd ? make_uint2(w.a, w.b) : make_uint2(w.c, w.d);
+  const uint2 got = make_uint2(__shfl_xor_sync(0xffffffffu, theirs.x, 1), __shfl_xor_sync(0xffffffffu, theirs.y, 1));
+  first = odd ? got : mine;
+  second = odd ? mine : got;
 }
 
 }  // namespace sf

@@ -8,6 +8,11 @@
 //   dg_next = sum over rows of dy x' r2,  A = sum over rows of v h r1,
 //   dg_post = gate A,  dgate = g_post A.
 //
+// Both means come from one pass over a row, because v is linear in D:
+//   sum(w v h) = beta (sum(m w h (dres + r2 g_next dy)) - k sum(m w h x')),
+// with m the kept elements' factor and k = r2^3 mean(g_next dy x').  So a row's
+// threads meet once, for three sums, and everything else is a second pass.
+//
 // It streams its arrays once and is bound by memory traffic: 20 bytes an element
 // with h in bf16.
 #include <cuda_bf16.h>
@@ -25,24 +30,27 @@ namespace sf {
 
 namespace {
 
-// CTAs of NT threads, as many as fit on the SMs, in groups of LANES threads that
-// take a row each, so that a thread holds at most Q quads of four columns: four,
-// or two with h in fp32.  Rows wider than 512 threads hold are shared by a
-// cluster of CL CTAs of 256, two CTAs an SM.  A thread copies its quads of the
-// rows ahead (xout, dy, dres and h, 56 or 64 bytes a quad) into its own places of
-// a ring in shared memory with cp.async and reads them back itself, each array
-// as soon as the row before has been read from there.  The ring has as many
-// stages as fit: two of 115 KB for 512 threads, more where rows are narrow or
+// One CTA of 512 threads per SM, in groups of LANES threads that take a row each,
+// so that a thread holds Q quads of four columns: up to four, or three with h in
+// fp32.  Wider rows are shared by a cluster of CL CTAs.  A thread copies its
+// quads of the rows ahead (xout, dy, dres and h, 56 or 64 bytes a quad) into its own places of
+// a ring in shared memory with cp.async and reads them back itself.  The ring has
+// as many stages as fit: two of 115 KB for 512 threads, more where rows are narrow or
 // arrays are not there.  dx may be dres or dy: a thread has read its quads of a row
-// before it writes them, and no other touches them.  No barrier but the two
-// sums of a row stands between rows, and the gains' sums of a thread's columns
-// stay in its registers over all of them.
-template <int NT>
-constexpr int kRingBytes = NT == 512 ? 230000 : 114000;
+// before it writes them, and no other touches them.  No barrier but the one for a
+// row's sums stands between rows, and the gains' sums of a thread's columns stay
+// in its registers over all of them.
+// The loops over a thread's quads have no branches, so that the quads' chains
+// run beside one another: quads beyond the row are copied as zeros and not
+// stored, and what an absent array would hold is read from another one and
+// not used.  (With a branch for each quad and array 84 instructions an element
+// were issued, and 16384 x 4096 without a second norm took 171 us.)
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kRingBytes = 230000;
 
-// Places of a stage's arrays, in bytes, for the quads that a thread uses.
+// Places of a stage's arrays, in bytes (0 for an absent one).
 struct BwdRing {
-  int quads = 0, stages = 0, stage = 0;
+  int stages = 0, stage = 0, last = 0;     // last: the place of the last stage
   int dy = 0, dres = 0, h = 0, stats = 0;  // xout at 0; stats: a row's two rstd for each warp
 };
 
@@ -55,8 +63,12 @@ __device__ __forceinline__ void wait_stage(int stages) {
   else cp_async_wait<7>();
 }
 
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+// 16 or 8 bytes, or as many zeros where `there` is false (nothing is read then).
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async8_if(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
 }
 // A float into another CTA's shared memory, counted on that CTA's mbarrier
 // (shared::cluster addresses).  It orders nothing else, so it does not wait for
@@ -74,17 +86,17 @@ __device__ __forceinline__ void add_mul(float4& s, const float4& a, float b) {
   s.w = fmaf(a.w, b, s.w);
 }
 
-template <bool H32, int NT, int LANES, int CL>
-__global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2)
+template <bool H32, int LANES, int Q, int CL>
+__global__ void __launch_bounds__(kThreads, 1)
     join_bwd_kernel(JoinArgs a, const float* __restrict__ xout, const void* __restrict__ h,
                     const float* __restrict__ rstd_post, const float* __restrict__ rstd_next,
                     const float* dy, const float* dres, float* dx, void* __restrict__ dh,
                     float* __restrict__ part, BwdRing r, int* err) {
-  static_assert(CL == 1 || LANES == NT, "a cluster's CTAs hold one row");
-  constexpr int Q = H32 ? 2 : 4, WARPS = NT / 32, GROUPS = NT / LANES, HB = H32 ? 16 : 8;
+  static_assert(CL == 1 || LANES == kThreads, "a cluster's CTAs hold one row");
+  constexpr int NT = kThreads, WARPS = kWarps, GROUPS = NT / LANES, HB = H32 ? 16 : 8;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float sums[4][CL * WARPS];  // the warps' sums, of four sums in turn; the cluster's
-  __shared__ __align__(8) uint64_t bars[4];
+  __shared__ float sums[2][3][CL * WARPS];  // the warps' sums, of two rows in turn; the cluster's
+  __shared__ __align__(8) uint64_t bars[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = tid / LANES, t = tid % LANES;
   const int rank = CL > 1 ? (int)cluster_ctarank() : 0;
@@ -108,90 +120,107 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2)
   const uint64_t offset = a.drop.top ? launch_offset(a.drop) : 0;
   const float factor = a.beta * a.drop.scale;
   const uint32_t base = smem_u32(ring) + tid * 16;
-  int uses = 0;
+  int uses = 0;       // a warp comes to the next row but one only after all have read this row's sums
   bool dead = false;  // a wait ran out: no more waits
-  auto sum = [&](float v) {
-    v = warp_sum(v);
-    const int par = uses & 3;
+  auto row_sums = [&](float (&v)[3]) {
+    const int par = uses & 1;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) v[j] = warp_sum(v[j]);
     if (CL > 1) {
       const uint32_t bar = smem_u32(&bars[par]);
-      if (tid == 0) mbar_arrive_expect_tx(bar, CL * WARPS * 4);
-      if (lane < CL)
-        st_async(mapa_shared(smem_u32(&sums[par][rank * WARPS + warp]), lane), v, mapa_shared(bar, lane));
-      if (!dead && !mbar_wait(bar, (uses >> 2) & 1, nullptr)) {
+      if (tid == 0) mbar_arrive_expect_tx(bar, CL * WARPS * 12);
+      if (lane < CL) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          st_async(mapa_shared(smem_u32(&sums[par][j][rank * WARPS + warp]), lane), v[j], mapa_shared(bar, lane));
+      }
+      if (!dead && !mbar_wait(bar, (uses >> 1) & 1, nullptr)) {
         record_error(err, kDevJoinTimeout);
         dead = true;
       }
-      v = lane < CL * WARPS ? sums[par][lane] : 0.f;
-      if (CL * WARPS > 32) v += sums[par][32 + lane];
-      v = warp_sum(v);
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        v[j] = lane < CL * WARPS ? sums[par][j][lane] : 0.f;
+        if (CL * WARPS > 32) v[j] += sums[par][j][32 + lane];
+        v[j] = warp_sum(v[j]);
+      }
     } else if (LANES > 32) {
-      if (lane == 0) sums[par][warp] = v;
+      if (lane < 3) sums[par][lane][warp] = lane == 0 ? v[0] : lane == 1 ? v[1] : v[2];
       asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(LANES) : "memory");
       constexpr int n = LANES / 32;
-      v = warp_sum(lane < n ? sums[par][group * n + lane] : 0.f);
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        v[j] = lane < n ? sums[par][j][group * n + lane] : 0.f;
+#pragma unroll
+        for (int o = n / 2; o > 0; o /= 2) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+        v[j] = __shfl_sync(0xffffffffu, v[j], 0);
+      }
     }
     ++uses;
-    return v;
   };
-  // the copies of a row into a stage, in two parts: what the second sum needs
-  // no more, and the rest
-  auto issue_x = [&](int64_t row, int stage) {
-    if (row >= a.rows) return;
-    const uint32_t st = base + (uint32_t)(stage * r.stage);
-    const int64_t from = row * a.d + 4 * first;
-#pragma unroll
-    for (int k = 0; k < Q; ++k) {
-      if (first + k * LANES < q1) {
-        if (next) {
-          cp_async16(st + k * NT * 16, xout + from + k * LANES * 4);
-          cp_async16(st + r.dy + k * NT * 16, dy + from + k * LANES * 4);
-        }
-        if (dres) cp_async16(st + r.dres + k * NT * 16, dres + from + k * LANES * 4);
-      }
-    }
-  };
-  auto issue_h = [&](int64_t row, int stage) {
-    if (row < a.rows) {
-      const uint32_t st = base - tid * 16 + (uint32_t)(stage * r.stage);
-      const int64_t from = row * a.d + 4 * first;
-      if (gains) {
+  const uint32_t rows = (uint32_t)a.rows;
+  auto issue = [&](uint32_t row, uint32_t stage) {
+    if (row < rows) {
+      const uint32_t st = base + stage;
+      const int64_t from = (int64_t)row * a.d + 4 * first;
+      auto copy = [&](uint32_t to, const float* p) {
 #pragma unroll
         for (int k = 0; k < Q; ++k) {
-          if (first + k * LANES < q1) {
-            const uint32_t to = st + r.h + (uint32_t)(tid * HB + k * NT * HB);
-            if (H32) cp_async16(to, static_cast<const float*>(h) + from + k * LANES * 4);
-            else cp_async8(to, static_cast<const bf16*>(h) + from + k * LANES * 4);
-          }
+          const bool there = first + k * LANES < q1;
+          cp_async16_if(to + k * NT * 16, there ? p + from + k * LANES * 4 : p, there);
+        }
+      };
+      if (next) {
+        copy(st, xout);
+        copy(st + r.dy, dy);
+      }
+      if (dres) copy(st + r.dres, dres);
+      if (gains && H32) copy(st + r.h, static_cast<const float*>(h));
+      if (gains && !H32) {
+#pragma unroll
+        for (int k = 0; k < Q; ++k) {
+          const bool there = first + k * LANES < q1;
+          cp_async8_if(st + r.h - tid * 8 + k * NT * 8,
+                       static_cast<const bf16*>(h) + (there ? from + k * LANES * 4 : 0), there);
         }
       }
-      if (lane == 0 && next) cp_async4(st + r.stats + warp * 8, rstd_next + row);
-      if (lane == 1 && post) cp_async4(st + r.stats + warp * 8 + 4, rstd_post + row);
+      if (lane == 0 && next) cp_async4(st - tid * 16 + r.stats + warp * 8, rstd_next + row);
+      if (lane == 1 && post) cp_async4(st - tid * 16 + r.stats + warp * 8 + 4, rstd_post + row);
     }
     cp_async_commit();
   };
-  const int64_t stride = (int64_t)(gridDim.x / CL) * GROUPS;
-  const int64_t row0 = (int64_t)(blockIdx.x / CL) * GROUPS + group;
+  // rows below 2^31, and a few strides beyond: 32 bits without a sign
+  const uint32_t stride = gridDim.x / CL * GROUPS;
+  uint32_t row = blockIdx.x / CL * GROUPS + group;
   for (int k = 0; k < r.stages; ++k) {
-    issue_x(row0 + k * stride, k);
-    issue_h(row0 + k * stride, k);
+    issue(row + k * stride, k * r.stage);
   }
   if (CL > 1) {
     if (tid == 0) {
-      for (int k = 0; k < 4; ++k) mbar_init(smem_u32(&bars[k]), 1);
+      for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&bars[k]), 1);
       fence_mbar_init();
     }
     cluster_sync_all();  // the peers' shared memory may be written
   }
-  int stage = 0;
+  const uint32_t ahead = r.stages * stride;
+  uint32_t stage = 0;  // its place in the ring
 #pragma unroll 1
-  for (int64_t row = row0; row < a.rows; row += stride) {
-    const int64_t at = row * a.d + 4 * first;
-    uint2 words[Q];
-    if (a.drop.top) row_words<Q>(row * n4 + q0, t, LANES, offset, a.drop.seed, words);
+  for (; row < rows; row += stride) {
+    const int64_t at = (int64_t)row * a.d + 4 * first;
+    uint2 words[Q] = {};
+    if (a.drop.top) {
+      const int64_t quad = (int64_t)row * n4 + first;
+#pragma unroll
+      for (int k = 0; k + 1 < Q; k += 2)
+        pair_words(quad + k * LANES, LANES, t & 1, offset, a.drop.seed, words[k], words[k + 1]);
+      if constexpr (Q & 1) {
+        const Words x = philox((uint64_t)((quad + (Q - 1) * LANES) >> 1), offset, a.drop.seed);
+        words[Q - 1] = t & 1 ? make_uint2(x.c, x.d) : make_uint2(x.a, x.b);
+      }
+    }
     wait_stage(r.stages);
     __syncwarp();
-    const uint8_t* st = ring + stage * r.stage;
+    const uint8_t* st = ring + stage;
     const float4* sx = reinterpret_cast<const float4*>(st) + tid;
     const float4* sdy = reinterpret_cast<const float4*>(st + r.dy) + tid;
     const float4* sdr = reinterpret_cast<const float4*>(st + r.dres) + tid;
@@ -200,76 +229,79 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2)
       if (H32) return reinterpret_cast<const float4*>(st + r.h)[k * NT + tid];
       return unpack4(reinterpret_cast<const uint2*>(st + r.h)[k * NT + tid]);
     };
-    const float r2 = next ? stats[0] : 0.f, r1 = post ? stats[1] : 1.f;
-    float c1 = 0.f;
+    const float r2 = stats[0], r1 = post ? stats[1] : 1.f;
+    // dres + r2 g_next dy of quad k; its kept elements of h w (top 0 keeps all)
+    auto known = [&](int k) {
+      float4 o = sdr[k * NT];
+      if (!dres) o = zero;
+      add_mul(o, mul(unpack4(gn[k]), sdy[k * NT]), r2);
+      return o;
+    };
+    auto keep = [&](int k, const float4& v) { return pick(v, words[k], a.drop.top); };
+    float v[3] = {0.f, 0.f, 0.f};
     if (next) {
 #pragma unroll
       for (int k = 0; k < Q; ++k) {
-        if (first + k * LANES < q1) {
-          const float4 p = mul(sx[k * NT], sdy[k * NT]);
-          add_mul(next_sum[k], p, r2);
-          c1 += dot(p, unpack4(gn[k]));
-        }
-      }
-      c1 = sum(c1) / a.d * r2 * r2 * r2;  // in this order: r2^3 alone may overflow
-    }
-    float4 dv[Q];
-    float c2 = 0.f;
-#pragma unroll
-    for (int k = 0; k < Q; ++k) {
-      if (first + k * LANES < q1) {
-        float4 o = zero;
-        if (dres) o = sdr[k * NT];
-        if (next) {
-          add_mul(o, mul(unpack4(gn[k]), sdy[k * NT]), r2);
-          add_mul(o, sx[k * NT], -c1);
-        }
-        *reinterpret_cast<float4*>(dx + at + k * LANES * 4) = mul(o, a.alpha);
-        o = mul(o, factor);
-        if (a.drop.top) o = pick(o, words[k], a.drop.top);
-        dv[k] = mul(o, w[k]);
-        if (gains) {
-          const float4 hv = load_hh(k);
-          add_mul(branch_sum[k], mul(hv, o), r1);
-          c2 += dot(hv, dv[k]);
-        }
-      }
-    }
-    issue_x(row + r.stages * stride, stage);
-    if (post) c2 = sum(c2) / a.d * r1 * r1 * r1;
-#pragma unroll
-    for (int k = 0; k < Q; ++k) {
-      if (first + k * LANES < q1) {
-        float4 o = dv[k];
+        const float4 x = sx[k * NT], p = mul(x, sdy[k * NT]);
+        add_mul(next_sum[k], p, r2);
+        v[0] += dot(p, unpack4(gn[k]));
         if (post) {
-          o = mul(o, r1);
-          add_mul(o, load_hh(k), -c2);
+          const float4 hw = keep(k, mul(load_hh(k), w[k]));
+          v[1] += dot(hw, known(k));
+          v[2] += dot(hw, x);
         }
-        store_h<H32>(dh, at + k * LANES * 4, o);
       }
+    } else if (post) {
+#pragma unroll
+      for (int k = 0; k < Q; ++k) v[1] += dot(keep(k, mul(load_hh(k), w[k])), sdr[k * NT]);
+    }
+    if (next || post) row_sums(v);
+    const float c1 = next ? v[0] / a.d * r2 * r2 * r2 : 0.f;  // in this order: r2^3 alone may overflow
+    const float c2 = post ? factor * (v[1] - c1 * v[2]) / a.d * r1 * r1 * r1 : 0.f;
+    // the rest of a quad from D
+    auto finish = [&](int k, float4 o) {
+      const bool there = first + k * LANES < q1;
+      if (there) *reinterpret_cast<float4*>(dx + at + k * LANES * 4) = mul(o, a.alpha);
+      o = keep(k, mul(o, factor));
+      const float4 hv = load_hh(k);
+      add_mul(branch_sum[k], mul(hv, o), r1);
+      o = mul(mul(o, w[k]), r1);
+      if (post) add_mul(o, hv, -c2);
+      if (there) store_h<H32>(dh, at + k * LANES * 4, o);
+    };
+    if (next) {
+#pragma unroll
+      for (int k = 0; k < Q; ++k) {
+        float4 o = known(k);
+        add_mul(o, sx[k * NT], -c1);
+        finish(k, o);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < Q; ++k) finish(k, sdr[k * NT]);
     }
     __syncwarp();  // the warp's statistics have been read: the next copies may replace them
-    issue_h(row + r.stages * stride, stage);
-    stage = stage + 1 == r.stages ? 0 : stage + 1;
+    issue(row + ahead, stage);
+    stage = stage == (uint32_t)r.last ? 0 : stage + r.stage;
   }
   cp_async_wait<0>();
   if (CL > 1) cluster_sync_all();  // no peer writes here any more
   allow_dependents();
   if (!part) return;
   // the groups hold the same columns: joined in their order
-  float4* join = reinterpret_cast<float4*>(ring);  // [groups][quads * LANES]
+  float4* join = reinterpret_cast<float4*>(ring);  // [groups][Q * LANES]
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     float4* out = reinterpret_cast<float4*>(part + ((int64_t)(blockIdx.x / CL) * 2 + s) * a.d);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < Q; ++k)
-      if (k < r.quads) join[(group * r.quads + k) * LANES + t] = s ? branch_sum[k] : next_sum[k];
+      join[(group * Q + k) * LANES + t] = s ? branch_sum[k] : next_sum[k];
     __syncthreads();
     for (int i = tid; i < q1 - q0; i += NT) {
       float4 v = join[i];
       for (int u = 1; u < GROUPS; ++u) {
-        const float4 x = join[u * r.quads * LANES + i];
+        const float4 x = join[u * Q * LANES + i];
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
       }
       out[q0 + i] = v;
@@ -306,46 +338,52 @@ __global__ void __launch_bounds__(1024)
 }
 
 // How a row of d columns is shared out: threads of a CTA, of a row within it,
-// and CTAs of a row.
+// quads of a thread and CTAs of a row.
 struct BwdShape {
-  int threads, lanes, ctas;
+  int lanes, quads, ctas;
 };
-BwdShape bwd_shape(int d, bool h32) {
-  const int cols = h32 ? 8 : 16;  // of a thread
+BwdShape bwd_shape(int d, bool h32, bool plain) {
+  const int few = h32 ? 2 : 4, most = h32 ? 3 : 4;
+  for (int q = 1; q < few; q *= 2)
+    if (32 * q * 4 >= d) return {32, q, 1};
   int n = 32;
-  while (n < 512 && n * cols < d) n *= 2;
-  if (n * cols >= d) return {512, n, 1};
-  int c = 2;
-  while (c * 256 * cols < d) c *= 2;
-  return {256, 256, c};
+  while (n < kThreads && n * few * 4 < d) n *= 2;
+  // one row at a time where its traffic hides a row's chain: with a second norm
+  // (dy and xout to read) and no dropout (16384 x 4096: 208 us with 512 threads of
+  // two quads, 224 with two groups of 256 of four; with dropout 240 and 219,
+  // without a second norm 174 and 141)
+  if (!h32 && plain && n == 256) return {512, 2, 1};
+  for (int c = 1;; c *= 2)
+    for (int q = c == 1 ? few : 2; q <= most; ++q)
+      if (c * n * q * 4 >= d) return {n, q, c};
 }
 // CTAs (clusters, where ctas > 1) that all SMs hold at a time, at most.
-int bwd_most(const BwdShape& s) { return num_sms() * (512 / s.threads) / s.ctas; }
+int bwd_most(const BwdShape& s) { return num_sms() / s.ctas; }
 int bwd_parts(int64_t rows, const BwdShape& s, int most) {
-  const int groups = s.threads / s.lanes;
+  const int groups = kThreads / s.lanes;
   const int64_t need = (rows + groups - 1) / groups;
   return need < most ? (int)(need > 0 ? need : 1) : most;
 }
 
 BwdRing bwd_ring(const JoinArgs& a, const BwdShape& s, bool h32, bool dres, int parts) {
-  const int n4 = a.d / 4, each = ((n4 + s.ctas - 1) / s.ctas + 1) & ~1;
-  BwdRing r;
-  r.quads = (each + s.lanes - 1) / s.lanes;
-  const int per = r.quads * s.threads;
+  const int per = s.quads * kThreads;
   const bool next = a.g_next != nullptr, gains = a.g_post || a.gate;
+  BwdRing r;
   int at = next ? per * 16 : 0;
-  r.dy = at;
-  at += next ? per * 16 : 0;
-  r.dres = at;
-  at += dres ? per * 16 : 0;
-  r.h = at;
-  at += gains ? per * (h32 ? 16 : 8) : 0;
+  auto place = [&](bool there, int bytes) {
+    const int p = at;
+    at += there ? per * bytes : 0;
+    return there ? p : 0;
+  };
+  r.dy = place(next, 16);
+  r.dres = place(dres, 16);
+  r.h = place(gains, h32 ? 16 : 8);
   r.stats = at;
-  r.stage = at + s.threads / 32 * 8;
-  const int64_t groups = (int64_t)parts * (s.threads / s.lanes), rows = (a.rows + groups - 1) / groups;
-  const int bytes = s.threads == 512 ? kRingBytes<512> : kRingBytes<256>;
+  r.stage = at + kWarps * 8;
+  const int64_t groups = (int64_t)parts * (kThreads / s.lanes), rows = (a.rows + groups - 1) / groups;
   for (int n : {1, 2, 3, 4, 8})
-    if (n == 1 || (n * r.stage <= bytes && n <= rows)) r.stages = n;
+    if (n == 1 || (n * r.stage <= kRingBytes && n <= rows)) r.stages = n;
+  r.last = (r.stages - 1) * r.stage;
   return r;
 }
 
@@ -363,25 +401,25 @@ struct BwdCall {
 };
 
 // Returns the number of partial sums, or 0: no launch.
-template <bool H32, int NT, int LANES, int CL>
+template <bool H32, int LANES, int Q, int CL>
 int launch_bwd(const BwdCall& c) {
-  constexpr auto kern = join_bwd_kernel<H32, NT, LANES, CL>;
-  if (!reserve_smem<kern>(kRingBytes<NT>)) return 0;
-  const BwdShape s = {NT, LANES, CL};
+  constexpr auto kern = join_bwd_kernel<H32, LANES, Q, CL>;
+  if (!reserve_smem<kern>(kRingBytes)) return 0;
+  const BwdShape s = {LANES, Q, CL};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CL;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(NT);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = c.st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int most = bwd_most(s);
   if (CL > 1) {  // clusters that are resident at once: more would take a second turn
     cfg.gridDim = dim3((unsigned)(CL * most));
-    cfg.dynamicSmemBytes = kRingBytes<NT>;
+    cfg.dynamicSmemBytes = kRingBytes;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return 0;
     if (n < most) most = n;
@@ -398,30 +436,42 @@ int launch_bwd(const BwdCall& c) {
 
 template <bool H32>
 int launch_bwd_for(const BwdShape& s, const BwdCall& c) {
-  switch (s.ctas * s.lanes) {
-    case 32: return launch_bwd<H32, 512, 32, 1>(c);
-    case 64: return launch_bwd<H32, 512, 64, 1>(c);
-    case 128: return launch_bwd<H32, 512, 128, 1>(c);
-    case 256: return launch_bwd<H32, 512, 256, 1>(c);
-    case 512: return launch_bwd<H32, 512, 512, 1>(c);
-    case 1024: return launch_bwd<H32, 256, 256, 4>(c);
-    default: return launch_bwd<H32, 256, 256, H32 ? 8 : 4>(c);
+  constexpr int Q = H32 ? 2 : 4;
+  if (s.ctas == 1) {
+    if (s.quads == 1) return launch_bwd<H32, 32, 1, 1>(c);
+    if (!H32 && s.quads == 2) return s.lanes == 32 ? launch_bwd<H32, 32, 2, 1>(c) : launch_bwd<H32, 512, 2, 1>(c);
+    if (H32 && s.quads == 3) return launch_bwd<H32, 512, H32 ? 3 : Q, 1>(c);
+    switch (s.lanes) {
+      case 32: return launch_bwd<H32, 32, Q, 1>(c);
+      case 64: return launch_bwd<H32, 64, Q, 1>(c);
+      case 128: return launch_bwd<H32, 128, Q, 1>(c);
+      case 256: return launch_bwd<H32, 256, Q, 1>(c);
+      default: return launch_bwd<H32, 512, Q, 1>(c);
+    }
   }
+  if (s.ctas == 2) {
+    if (s.quads == 3) return launch_bwd<H32, 512, 3, 2>(c);
+    return launch_bwd<H32, 512, Q, 2>(c);
+  }
+  return launch_bwd<H32, 512, 2, H32 ? 4 : 2>(c);
 }
 
 }  // namespace
 
 int join_bwd_parts(int64_t rows, int d) {
-  const BwdShape s = bwd_shape(d, false), t = bwd_shape(d, true);
-  const int p = bwd_parts(rows, s, bwd_most(s)), q = bwd_parts(rows, t, bwd_most(t));
-  return p > q ? p : q;
+  int most = 0;
+  for (const BwdShape s : {bwd_shape(d, false, false), bwd_shape(d, false, true), bwd_shape(d, true, true)}) {
+    const int p = bwd_parts(rows, s, bwd_most(s));
+    most = p > most ? p : most;
+  }
+  return most;
 }
 
 bool join_bwd(const JoinArgs& a, const float* xout, const void* h, bool h32, const float* rstd_post,
               const float* rstd_next, const float* dy, const float* dres, float* dx, void* dh,
               bf16* dg_post, bf16* dgate, bf16* dg_next, float* part, int* err, cudaStream_t st) {
   if (!dg_post && !dgate && !dg_next) part = nullptr;
-  const BwdShape s = bwd_shape(a.d, h32);
+  const BwdShape s = bwd_shape(a.d, h32, a.g_next && !a.drop.top);
   const BwdCall c = {a, xout, h, rstd_post, rstd_next, dy, dres, dx, dh, part, err, st};
   const int parts = h32 ? launch_bwd_for<true>(s, c) : launch_bwd_for<false>(s, c);
   if (parts && part)
