@@ -680,11 +680,11 @@ int sf_op_logprob_rows_bwd(const void* z, int32_t z_type, int64_t ldz, const int
                            const float* entropy, const float* dlogp, const float* dentropy,
                            uint16_t* dz, int64_t lddz, void* stream);
 
-/* sf_op_logprob_rows of the logits h W^T (fp32, never stored beyond one chunk of
- * chunk_rows rows): h bf16 [n, d], w bf16 [v, d], tokens int32 [n] (device);
- * d and v multiples of 8, v at most 2^24, n >= 1.  workspace:
- * sf_op_lm_logprob_workspace_bytes(n, v, chunk_rows) bytes (4 for each logit of a
- * chunk; -1 for bad sizes), 256-byte aligned.  Errors and the device error word
+/* sf_op_logprob_rows of the logits h W^T (fp32): h bf16 [n, d], w bf16 [v, d],
+ * tokens int32 [n] (device); d and v multiples of 8, v at most 2^24, n >= 1.
+ * With top 0 the logits are never stored; else no more of them than a chunk of
+ * chunk_rows rows.  workspace: sf_op_lm_logprob_workspace_bytes(n, v, chunk_rows)
+ * bytes (4 for each logit of a chunk; -1 for bad sizes), 256-byte aligned.  Errors and the device error word
  * as sf_op_gemm and sf_op_logprob_rows. */
 int sf_op_lm_logprob(const uint16_t* h, const uint16_t* w, const int32_t* tokens, int64_t n,
                      int32_t d, int32_t v, float scale, int64_t chunk_rows, void* workspace,
@@ -692,11 +692,12 @@ int sf_op_lm_logprob(const uint16_t* h, const uint16_t* w, const int32_t* tokens
                      float* top_logp, void* stream);
 int64_t sf_op_lm_logprob_workspace_bytes(int64_t n, int32_t v, int64_t chunk_rows);
 
-/* Backward of sf_op_lm_logprob (logits recomputed chunk by chunk): with dz of
- * sf_op_logprob_rows_bwd, dh bf16 [n, d] = dz W and dw bf16 [v, d] = dz^T h, fp32
- * sums rounded once.  workspace: sf_op_lm_logprob_bwd_workspace_bytes(n, d, v,
- * chunk_rows) bytes (-1 for bad sizes), 256-byte aligned: a chunk's fp32 logits
- * and bf16 dz and, where n > chunk_rows, the fp32 sum of dw over the chunks. */
+/* Backward of sf_op_lm_logprob (the logits are recomputed and not stored): with
+ * dz of sf_op_logprob_rows_bwd, dh bf16 [n, d] = dz W and dw bf16 [v, d] = dz^T h,
+ * fp32 sums rounded once.  workspace: sf_op_lm_logprob_bwd_workspace_bytes(n, d,
+ * v, chunk_rows) bytes (-1 for bad sizes), 256-byte aligned: 6 for each logit of
+ * a chunk, which hold three chunks' dz at a time, and, where n > chunk_rows, the
+ * fp32 sum of dw. */
 int sf_op_lm_logprob_bwd(const uint16_t* h, const uint16_t* w, const int32_t* tokens, int64_t n,
                          int32_t d, int32_t v, float scale, int64_t chunk_rows, const float* lse,
                          const float* entropy, const float* dlogp, const float* dentropy,

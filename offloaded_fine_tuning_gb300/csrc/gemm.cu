@@ -35,6 +35,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "logprob.cuh"
 #include "ptx.cuh"
 #include "sf_internal.h"
 
@@ -57,6 +58,7 @@ struct GemmParams {
   int splitk;                 // K ranges (kEpiF32): split s > 0 writes ws + (s - 1) * ws_stride
   float* ws;
   int64_t ws_stride;
+  LogprobEpi lp;              // kEpiLogprob, kEpiLogprobBwd
 };
 
 // Output columns of one work unit: the gated tile computes a and b for 128
@@ -230,6 +232,15 @@ __device__ __forceinline__ void epi_glu(const GemmParams& p, int row, int j,
     store_f32x32(x, a, n);
     store_f32x32(x + p.N, b, n);
   }
+}
+
+// The gradient of 32 logits of a row (r: their accumulators), as bf16.
+__device__ __forceinline__ void epi_logprob_bwd(const GemmParams& p, const RowGrad& g, int row, int col,
+                                                const uint32_t (&r)[32]) {
+  float y[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) y[j] = g.zero ? 0.f : logit_grad(g, __uint_as_float(r[j]) * p.alpha, col + j);
+  store_bf16x32(reinterpret_cast<__nv_bfloat16*>(p.C) + (int64_t)row * p.ldc + col, y, min(32, p.N - col));
 }
 
 // Store 32 accumulator columns [col, col+32) of one output row.
@@ -619,6 +630,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           if (row < p.M) epi_glu(p, row, col, ra, rb);
         }
+      } else if constexpr (EPI == kEpiLogprob) {
+        // each thread carries its row's sums over the tile's columns; the logits
+        // themselves are not stored
+        Sums sums = {-FLT_MAX, 0.f, 0.f, 0.f};
+        const float c2 = p.lp.scale * kLog2e;
+        const int token = row < p.M ? p.lp.tokens[row] : -1;
+        for (int c = 0; c < BN; c += 32) {
+          const int col = tn * BN + c;
+          if (col >= p.N) break;  // uniform across the warp
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(taddr + c, r);
+          tmem_ld_wait();
+          float z[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            z[j] = col + j < p.N ? __uint_as_float(r[j]) * p.alpha : -__uint_as_float(0x7f800000u);
+            if (col + j == token) p.lp.token_logit[row] = z[j];
+          }
+          add<true>(sums, z, c2);
+        }
+        if (row < p.M) p.lp.parts[(int64_t)tn * p.M + row] = make_float4(sums.m, sums.s, sums.low, sums.t);
+      } else if constexpr (EPI == kEpiLogprobBwd) {
+        RowGrad g = {};
+        if (row < p.M) g = row_grad(p.lp, row, p.N, p.err);
+        for (int c = 0; c < BN; c += 32) {
+          const int col = tn * BN + c;
+          if (col >= p.N) break;  // uniform across the warp
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(taddr + c, r);
+          tmem_ld_wait();
+          if (row < p.M) epi_logprob_bwd(p, g, row, col, r);
+        }
       } else {
         // a K range after the first (kEpiF32) writes into its workspace slice
         GemmParams q = p;
@@ -802,6 +845,12 @@ static int launch_epi(int epi, const CUtensorMap& ta, const CUtensorMap& tb,
     case kEpiF16:  // weight gradients only (dW = dY^T X)
       if constexpr (A_MN && B_MN) return launch_t<A_MN, B_MN, BN, kEpiF16>(ta, tb, tb2, p, st, why);
       break;
+    case kEpiLogprob:  // the LM head's logits, as sums
+      if constexpr (!A_MN && !B_MN) return launch_t<A_MN, B_MN, BN, kEpiLogprob>(ta, tb, tb2, p, st, why);
+      break;
+    case kEpiLogprobBwd:  // the LM head's logits, as their gradient
+      if constexpr (!A_MN && !B_MN) return launch_t<A_MN, B_MN, BN, kEpiLogprobBwd>(ta, tb, tb2, p, st, why);
+      break;
     case kEpiBF16Acc:  // the last chunk of a summed weight gradient
       if constexpr (A_MN && B_MN) return launch_t<A_MN, B_MN, BN, kEpiBF16Acc>(ta, tb, tb2, p, st, why);
       break;
@@ -818,13 +867,13 @@ int gemm_check(const GemmArgs& a, char* why) {
     snprintf(why, 64, "gemm: bad sizes");
     return -1;
   }
-  const int need_layout[] = {-1, -1, -1, -1, kNT, kTN, kNT, kNT, kNN, kTN};
-  if (a.layout < kNT || a.layout > kTN || a.epi < kEpiBF16 || a.epi > kEpiBF16Acc ||
+  const int need_layout[] = {-1, -1, -1, -1, kNT, kTN, kNT, kNT, kNN, kTN, kNT, kNT};
+  if (a.layout < kNT || a.layout > kTN || a.epi < kEpiBF16 || a.epi > kEpiLogprobBwd ||
       (need_layout[a.epi] >= 0 && a.layout != need_layout[a.epi])) {
     snprintf(why, 64, "gemm: bad layout %d or epilogue %d", a.layout, a.epi);
     return -1;
   }
-  if (!a.A || !a.B || !a.C || (a.epi == kEpiF32Add && !a.R) || (a.epi == kEpiBF16Bias && !a.bias) ||
+  if (!a.A || !a.B || (!a.C && a.epi != kEpiLogprob) || (a.epi == kEpiF32Add && !a.R) || (a.epi == kEpiBF16Bias && !a.bias) ||
       (a.epi == kEpiGLUBwd && !a.R) || (a.epi == kEpiQKV && !a.cs)) {
     snprintf(why, 64, "gemm: null operand");
     return -1;
@@ -934,7 +983,7 @@ int gemm(const GemmArgs& a, int* dev_err, cudaStream_t st, char* why) {
   const bool a_mn = (a.layout == kTN);
   const bool b_mn = (a.layout == kNN || a.layout == kTN);
   const bool gated = (a.epi == kEpiGLU);
-  const int BN = (gated || a.N > 128) ? 256 : 128;
+  const int BN = gated ? 256 : gemm_tile_cols(a.N);
   CUtensorMap ta, tb, tb2;
   bool ok = a_mn ? make_map(&ta, a.A, a.M, a.K, a.lda, 64, 64)
                  : make_map(&ta, a.A, a.K, a.M, a.lda, 64, kBM);
@@ -957,7 +1006,8 @@ int gemm(const GemmArgs& a, int* dev_err, cudaStream_t st, char* why) {
   const int splitk = can_split ? choose_splitk(a.M, a.N, a.K, BN, a.splitk_max) : 1;
   GemmParams p{(int)a.M, (int)a.N, (int)a.K, a.C, a.ldc, a.R, a.ldr, a.alpha, dev_err,
                reinterpret_cast<const __nv_bfloat16*>(a.bias), a.cs, a.seq, a.rope_cols, a.hd,
-               a.aux, a.ldaux, unit_order(a.M, a.N, a.K, BN, gated), splitk, a.ws, a.M * a.ldc};
+               a.aux, a.ldaux, unit_order(a.M, a.N, a.K, BN, gated), splitk, a.ws, a.M * a.ldc,
+               a.lp};
   int rc;
   if (BN == 256) {
     if (a.layout == kNT) rc = launch_epi<false, false, 256>(a.epi, ta, tb, tb2, p, st, why);

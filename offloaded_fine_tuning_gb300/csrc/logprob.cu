@@ -21,6 +21,7 @@
 #include <cstdint>
 
 #include "launch.cuh"
+#include "logprob.cuh"
 #include "ptx.cuh"
 #include "sf.h"
 #include "sf_internal.h"
@@ -30,17 +31,6 @@ namespace sf {
 namespace {
 
 typedef __nv_bfloat16 bf16;
-
-constexpr float kLog2e = 1.4426950408889634f;
-// What a difference of logits is cut to where it multiplies a weight: its
-// weight is exp(scale * kFar) = 0 for every scale allowed, and 0 * kFar is 0.
-constexpr float kFar = -1e30f;
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 template <typename T>
 struct alignas(16) Eight {
@@ -62,56 +52,6 @@ __device__ __forceinline__ void load8(const bf16* p, float (&f)[8]) {
 }
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); }
-
-// The maximum, the sum and the weighted sum of a set of logits; the sum's
-// rounding errors are kept beside it, because log S of a peaked row (S near 1)
-// shows them.
-struct Sums {
-  float m, s, low, t;
-};
-__device__ __forceinline__ void raise(Sums& a, float m, float c) {
-  const float dm = fmaxf(a.m - m, kFar), f = exp2_fast(dm * c);
-  a.t = f * fmaf(a.s, dm, a.t);
-  a.s *= f;
-  a.low *= f;
-  a.m = m;
-}
-__device__ __forceinline__ void add_sum(Sums& a, float s) {
-  const float sum = a.s + s, b = sum - a.s;
-  a.low += (a.s - (sum - b)) + (s - b);
-  a.s = sum;
-}
-__device__ __forceinline__ Sums merge(Sums a, Sums b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  raise(a, m, c);
-  raise(b, m, c);
-  add_sum(a, b.s);
-  a.low += b.low;
-  a.t += b.t;
-  return a;
-}
-// N logits at once: one look at the maximum, and a tree of their exponentials.
-// Returns their maximum.
-template <bool ENT, int N>
-__device__ __forceinline__ float add(Sums& a, const float (&z)[N], float c) {
-  float m = z[0];
-#pragma unroll
-  for (int j = 1; j < N; ++j) m = fmaxf(m, z[j]);
-  if (m > a.m) raise(a, m, c);
-  float e[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const float x = z[j] - a.m;
-    e[j] = exp2_fast(x * c);
-    if (ENT) a.t = fmaf(e[j], fmaxf(x, kFar), a.t);
-  }
-#pragma unroll
-  for (int w = N / 2; w > 0; w /= 2)
-#pragma unroll
-    for (int j = 0; j < w; ++j) e[j] += e[j + w];
-  add_sum(a, e[0]);
-  return m;
-}
 
 // The order of the alternatives: larger values first, then lower ids.
 struct Logit {
@@ -294,18 +234,17 @@ __global__ void __launch_bounds__(NT)
       const float2 x = ld_shared_cluster_f32x2(at), y = ld_shared_cluster_f32x2(at + 8);
       all = merge(all, {x.x, x.y, y.x, y.y}, c);
     }
-    const bool none = all.s == 0.f, bad = !(all.s == all.s);
-    const float log_s = logf(all.s) + all.low / all.s;
-    auto value = [&](float v) { return none ? minus_inf : fmaf(v - all.m, scale, -log_s); };
+    const RowStats r = row_stats(all, scale);
+    const bool bad = !(all.s == all.s);
     if (tid == 0) {
       int token = tokens[row];
       if (token >= vocab) {  // outside the vocabulary: reported, and the row ignored
         record_error(err, kDevCeBadLabel);
         token = -1;
       }
-      logp[row] = token < 0 ? 0.f : value(to_float(zr[token]));
-      lse_out[row] = none ? minus_inf : fmaf(all.m, scale, log_s);
-      if (ENT) entropy[row] = none ? 0.f : log_s - scale * (all.t / all.s);
+      logp[row] = token < 0 ? 0.f : r.value(to_float(zr[token]));
+      lse_out[row] = r.lse;
+      if (ENT) entropy[row] = r.entropy;
     }
     if (ncl > 1) {  // the ranges' alternatives in one order
       const int n = (int)ncl * top;
@@ -321,7 +260,7 @@ __global__ void __launch_bounds__(NT)
     }
     if (tid < top) {
       ids[row * top + tid] = bad ? -1 : best[tid].i;
-      top_logp[row * top + tid] = bad ? all.s : value(best[tid].v);
+      top_logp[row * top + tid] = bad ? all.s : r.value(best[tid].v);
     }
   }
   if (ncl > 1) cluster_sync_all();  // the first CTA has read its peers' results
@@ -335,50 +274,73 @@ constexpr int kPiece = kThreads * 8 * 4;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    logprob_rows_bwd_kernel(const T* z, int64_t ld, const int32_t* __restrict__ tokens, int64_t rows, int vocab,
-                            float scale, const float* __restrict__ lse_in, const float* __restrict__ entropy,
-                            const float* __restrict__ dlogp, const float* __restrict__ dentropy, bf16* dz,
-                            int64_t lddz, int* err) {
+    logprob_rows_bwd_kernel(const T* z, int64_t ld, LogprobEpi a, int64_t rows, int vocab, bf16* dz, int64_t lddz,
+                            int* err) {
   const int pieces = (vocab + kPiece - 1) / kPiece;
   for (int64_t item = blockIdx.x; item < rows * pieces; item += gridDim.x) {
     const int64_t row = item / pieces;
     const int first = (int)(item - row * pieces) * kPiece;
-    int token = tokens[row];
-    if (token >= vocab) {
-      if (threadIdx.x == 0) record_error(err, kDevCeBadLabel);
-      token = -1;
-    }
-    const float lse = lse_in[row];
-    const float dl = token < 0 ? 0.f : dlogp[row], de = dentropy ? dentropy[row] : 0.f;
-    const float hh = dentropy ? entropy[row] : 0.f;
-    const bool zero = (dl == 0.f && de == 0.f) || lse == -__uint_as_float(0x7f800000u);
+    const RowGrad g = row_grad(a, row, vocab, err);
     const T* zr = z + row * ld;
     bf16* dr = dz + row * lddz;
-    auto grad = [&](float f, int at) {
-      const float lp = fmaf(f, scale, -lse), p = exp2_fast(lp * kLog2e);
-      const float g = fmaf(de, fmaxf(lp, kFar) + hh, dl);
-      return scale * fmaf(-p, g, at == token ? dl : 0.f);
-    };
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int at = first + (u * kThreads + threadIdx.x) * 8;
       if (at + 8 <= vocab) {
         float f[8];
         Eight<bf16> o;
-        if (zero) {
+        if (g.zero) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) o.v[j] = __float2bfloat16_rn(0.f);
         } else {
           load8(zr + at, f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o.v[j] = __float2bfloat16_rn(grad(f[j], at + j));
+          for (int j = 0; j < 8; ++j) o.v[j] = __float2bfloat16_rn(logit_grad(g, f[j], at + j));
         }
         *reinterpret_cast<Eight<bf16>*>(dr + at) = o;
       } else {
-        for (int j = at; j < vocab; ++j) dr[j] = __float2bfloat16_rn(zero ? 0.f : grad(to_float(zr[j]), j));
+        for (int j = at; j < vocab; ++j)
+          dr[j] = __float2bfloat16_rn(g.zero ? 0.f : logit_grad(g, to_float(zr[j]), j));
       }
     }
   }
+}
+
+// The sums of rows from those of their tiles of columns (the LM head's product
+// leaves them, [tiles][rows]) and the logits of the rows' tokens: a CTA takes 32
+// rows with 32 warps, warp w merges the tiles w, w + 32, ... of its lane's row,
+// then the warps' sums are merged in warp order.
+__global__ void __launch_bounds__(1024)
+    logprob_tiles_kernel(LogprobEpi a, int64_t rows, int tiles, int vocab, float* __restrict__ logp,
+                         float* __restrict__ lse_out, float* __restrict__ entropy, int* err) {
+  __shared__ float4 sh[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  const float c = a.scale * kLog2e;
+  wait_primary();
+  Sums s = {-FLT_MAX, 0.f, 0.f, 0.f};
+  if (row < rows) {
+    for (int t = w; t < tiles; t += 32) {
+      const float4 p = __ldcg(a.parts + (int64_t)t * rows + row);
+      s = merge(s, {p.x, p.y, p.z, p.w}, c);
+    }
+  }
+  sh[w][lane] = make_float4(s.m, s.s, s.low, s.t);
+  __syncthreads();
+  if (w != 0 || row >= rows) return;
+  for (int k = 1; k < 32; ++k) {
+    const float4 p = sh[k][lane];
+    s = merge(s, {p.x, p.y, p.z, p.w}, c);
+  }
+  const RowStats r = row_stats(s, a.scale);
+  int token = a.tokens[row];
+  if (token >= vocab) {  // outside the vocabulary: reported, and the row ignored
+    record_error(err, kDevCeBadLabel);
+    token = -1;
+  }
+  logp[row] = token < 0 ? 0.f : r.value(__ldcg(a.token_logit + row));
+  lse_out[row] = r.lse;
+  if (entropy) entropy[row] = r.entropy;
 }
 
 }  // namespace
@@ -450,17 +412,20 @@ bool logprob_rows(const void* z, bool f32, int64_t ld, const int32_t* tokens, in
 #undef SF_LOGPROB
 }
 
-void logprob_rows_bwd(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows, int vocab,
-                      float scale, const float* lse, const float* entropy, const float* dlogp, const float* dentropy,
-                      bf16* dz, int64_t lddz, int* err, cudaStream_t st) {
+void logprob_rows_bwd(const void* z, bool f32, int64_t ld, const LogprobEpi& a, int64_t rows, int vocab, bf16* dz,
+                      int64_t lddz, int* err, cudaStream_t st) {
   const int64_t items = rows * ((vocab + kPiece - 1) / kPiece);
   const unsigned grid = (unsigned)(items < INT32_MAX ? items : INT32_MAX);
   if (f32)
-    logprob_rows_bwd_kernel<<<grid, kThreads, 0, st>>>(static_cast<const float*>(z), ld, tokens, rows, vocab, scale,
-                                                       lse, entropy, dlogp, dentropy, dz, lddz, err);
+    logprob_rows_bwd_kernel<<<grid, kThreads, 0, st>>>(static_cast<const float*>(z), ld, a, rows, vocab, dz, lddz, err);
   else
-    logprob_rows_bwd_kernel<<<grid, kThreads, 0, st>>>(static_cast<const bf16*>(z), ld, tokens, rows, vocab, scale,
-                                                       lse, entropy, dlogp, dentropy, dz, lddz, err);
+    logprob_rows_bwd_kernel<<<grid, kThreads, 0, st>>>(static_cast<const bf16*>(z), ld, a, rows, vocab, dz, lddz, err);
+}
+
+bool logprob_tiles(const LogprobEpi& a, int64_t rows, int tiles, int vocab, float* logp, float* lse, float* entropy,
+                   int* err, cudaStream_t st) {
+  return launch_dependent(logprob_tiles_kernel, dim3((unsigned)((rows + 31) / 32)), 1024, 0, st, a, rows, tiles, vocab,
+                          logp, lse, entropy, err);
 }
 
 }  // namespace sf

@@ -1,0 +1,123 @@
+// The sums of a row of logits, and their gradient, as the kernels on stored rows
+// (logprob.cu) and the epilogues of the LM head's product (gemm.cu) compute them.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "sf_internal.h"
+
+namespace sf {
+
+constexpr float kLog2e = 1.4426950408889634f;
+// What a difference of logits is cut to where it multiplies a weight: its
+// weight is exp(scale * kFar) = 0 for every scale allowed, and 0 * kFar is 0.
+constexpr float kFar = -1e30f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The maximum, the sum and the weighted sum of a set of logits; the sum's
+// rounding errors are kept beside it, because log S of a peaked row (S near 1)
+// shows them.
+struct Sums {
+  float m, s, low, t;
+};
+__device__ __forceinline__ void raise(Sums& a, float m, float c) {
+  const float dm = fmaxf(a.m - m, kFar), f = exp2_fast(dm * c);
+  a.t = f * fmaf(a.s, dm, a.t);
+  a.s *= f;
+  a.low *= f;
+  a.m = m;
+}
+__device__ __forceinline__ void add_sum(Sums& a, float s) {
+  const float sum = a.s + s, b = sum - a.s;
+  a.low += (a.s - (sum - b)) + (s - b);
+  a.s = sum;
+}
+__device__ __forceinline__ Sums merge(Sums a, Sums b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  raise(a, m, c);
+  raise(b, m, c);
+  add_sum(a, b.s);
+  a.low += b.low;
+  a.t += b.t;
+  return a;
+}
+// N logits at once: one look at the maximum, and a tree of their exponentials.
+// Returns their maximum.
+template <bool ENT, int N>
+__device__ __forceinline__ float add(Sums& a, const float (&z)[N], float c) {
+  float m = z[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) m = fmaxf(m, z[j]);
+  if (m > a.m) raise(a, m, c);
+  float e[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float x = z[j] - a.m;
+    e[j] = exp2_fast(x * c);
+    if (ENT) a.t = fmaf(e[j], fmaxf(x, kFar), a.t);
+  }
+#pragma unroll
+  for (int w = N / 2; w > 0; w /= 2)
+#pragma unroll
+    for (int j = 0; j < w; ++j) e[j] += e[j + w];
+  add_sum(a, e[0]);
+  return m;
+}
+
+// What a row's sums give.
+struct RowStats {
+  float m, scale, log_s, lse, entropy;
+  bool none;  // nothing above -inf
+  // log probability of a logit
+  __device__ __forceinline__ float value(float v) const {
+    return none ? -__uint_as_float(0x7f800000u) : fmaf(v - m, scale, -log_s);
+  }
+};
+__device__ __forceinline__ RowStats row_stats(const Sums& a, float scale) {
+  RowStats r;
+  r.m = a.m;
+  r.scale = scale;
+  r.none = a.s == 0.f;  // it is at least 1 otherwise
+  r.log_s = logf(a.s) + a.low / a.s;
+  r.lse = r.none ? -__uint_as_float(0x7f800000u) : fmaf(a.m, scale, r.log_s);
+  r.entropy = r.none ? 0.f : r.log_s - scale * (a.t / a.s);
+  return r;
+}
+
+// The gradient of a logit f of a row: scale (dlogp [hot] - p (dlogp + dentropy
+// (log p + entropy))).
+struct RowGrad {
+  float lse, entropy, dlogp, dentropy, scale;
+  int token;
+  bool zero;  // both gradients are 0, or the row holds nothing but -inf
+};
+__device__ __forceinline__ RowGrad row_grad(const LogprobEpi& a, int64_t row, int vocab, int* err) {
+  RowGrad g;
+  g.token = a.tokens[row];
+  if (g.token >= vocab) {  // outside the vocabulary: reported, and the row ignored
+    record_error(err, kDevCeBadLabel);
+    g.token = -1;
+  }
+  g.lse = a.lse[row];
+  g.scale = a.scale;
+  g.dlogp = g.token < 0 ? 0.f : a.dlogp[row];
+  g.dentropy = a.dentropy ? a.dentropy[row] : 0.f;
+  g.entropy = a.dentropy ? a.entropy[row] : 0.f;
+  g.zero = (g.dlogp == 0.f && g.dentropy == 0.f) || g.lse == -__uint_as_float(0x7f800000u);
+  return g;
+}
+__device__ __forceinline__ float logit_grad(const RowGrad& g, float f, int at) {
+  const float lp = fmaf(f, g.scale, -g.lse), p = exp2_fast(lp * kLog2e);
+  const float q = fmaf(g.dentropy, fmaxf(lp, kFar) + g.entropy, g.dlogp);
+  return g.scale * fmaf(-p, q, at == g.token ? g.dlogp : 0.f);
+}
+
+}  // namespace sf

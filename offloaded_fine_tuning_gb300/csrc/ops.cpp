@@ -573,6 +573,13 @@ static bool logprob_gradients(const float* lse, const float* entropy, const floa
   return lse && dlogp && al1(lse) && al1(dlogp) && (!dentropy || (entropy && al1(entropy) && al1(dentropy)));
 }
 
+static sf::LogprobEpi logprob_epi(const int32_t* tokens, float scale, const float* lse, const float* entropy,
+                                  const float* dlogp, const float* dentropy) {
+  sf::LogprobEpi a;
+  a.tokens = tokens; a.scale = scale; a.lse = lse; a.entropy = entropy; a.dlogp = dlogp; a.dentropy = dentropy;
+  return a;
+}
+
 int sf_op_logprob_rows(const void* z, int32_t z_type, int64_t ldz, const int32_t* tokens,
                        int64_t rows, int32_t vocab, float scale, float* logp, float* lse,
                        float* entropy, int32_t top, int32_t* ids, float* top_logp, void* stream) {
@@ -602,8 +609,8 @@ int sf_op_logprob_rows_bwd(const void* z, int32_t z_type, int64_t ldz, const int
   if (dz == z && (z_type != SF_BF16 || lddz != ldz)) return SF_EINVAL;
   int* err = dev_err_word();
   if (!err) return SF_ECUDA;
-  sf::logprob_rows_bwd(z, z_type == SF_F32, ldz, tokens, rows, vocab, scale, lse, entropy, dlogp, dentropy,
-                       reinterpret_cast<bf16*>(dz), lddz, err, S(stream));
+  sf::logprob_rows_bwd(z, z_type == SF_F32, ldz, logprob_epi(tokens, scale, lse, entropy, dlogp, dentropy), rows,
+                       vocab, reinterpret_cast<bf16*>(dz), lddz, err, S(stream));
   return launched();
 }
 
@@ -639,15 +646,34 @@ int sf_op_lm_logprob(const uint16_t* h, const uint16_t* w, const int32_t* tokens
   const int64_t c = std::min(n, chunk_rows);
   float* zf = static_cast<float*>(workspace);
   char why[128];
+  cudaStream_t st = S(stream);
+  sf::GemmArgs z;
+  z.layout = sf::kNT; z.N = v; z.K = d; z.lda = d; z.B = w; z.ldb = d; z.ldc = v;
+  if (top == 0) {
+    // The logits leave the product as their sums, 16 bytes for 256 columns of a
+    // row: as many rows at a time as the workspace holds of those.
+    const int tiles = (v + sf::gemm_tile_cols(v) - 1) / sf::gemm_tile_cols(v);
+    const int64_t most = std::min(n, c * v * 4 / (tiles * 16 + 4));
+    for (int64_t r0 = 0; r0 < n; r0 += most) {
+      const int64_t rows = std::min(most, n - r0);
+      sf::LogprobEpi a = logprob_epi(tokens + r0, scale, nullptr, nullptr, nullptr, nullptr);
+      a.parts = reinterpret_cast<float4*>(zf);
+      a.token_logit = zf + rows * tiles * 4;
+      z.epi = sf::kEpiLogprob; z.M = rows; z.A = h + r0 * d; z.lp = a;
+      if (sf::gemm(z, err, st, why) != 0) return SF_ECUDA;
+      if (!sf::logprob_tiles(a, rows, tiles, v, logp + r0, lse + r0, entropy ? entropy + r0 : nullptr, err, st)) {
+        cudaGetLastError();
+        return SF_ECUDA;
+      }
+    }
+    return launched();
+  }
   for (int64_t r0 = 0; r0 < n; r0 += c) {
     const int64_t rows = std::min(c, n - r0);
-    sf::GemmArgs z;
-    z.layout = sf::kNT; z.epi = sf::kEpiF32; z.M = rows; z.N = v; z.K = d;
-    z.A = h + r0 * d; z.lda = d; z.B = w; z.ldb = d; z.C = zf; z.ldc = v;
-    if (sf::gemm(z, err, S(stream), why) != 0) return SF_ECUDA;
+    z.epi = sf::kEpiF32; z.M = rows; z.A = h + r0 * d; z.C = zf;
+    if (sf::gemm(z, err, st, why) != 0) return SF_ECUDA;
     if (!sf::logprob_rows(zf, true, v, tokens + r0, rows, v, scale, logp + r0, lse + r0,
-                          entropy ? entropy + r0 : nullptr, top, top ? ids + r0 * top : nullptr,
-                          top ? top_logp + r0 * top : nullptr, err, S(stream))) {
+                          entropy ? entropy + r0 : nullptr, top, ids + r0 * top, top_logp + r0 * top, err, st)) {
       cudaGetLastError();
       return SF_ECUDA;
     }
@@ -666,22 +692,22 @@ int sf_op_lm_logprob_bwd(const uint16_t* h, const uint16_t* w, const int32_t* to
   if (!logprob_gradients(lse, entropy, dlogp, dentropy)) return SF_EINVAL;
   int* err = dev_err_word();
   if (!err) return SF_ECUDA;
-  const int64_t c = std::min(n, chunk_rows);
+  // the logits leave the product as dz: the room of a chunk's logits holds more rows
+  const int64_t c = std::min(n, chunk_rows), most = std::min(n, 3 * c);
   char* ws = static_cast<char*>(workspace);
-  float* zf = reinterpret_cast<float*>(ws);
-  bf16* dz = reinterpret_cast<bf16*>(ws + up256(c * v * 4));
+  bf16* dz = reinterpret_cast<bf16*>(ws);
   float* sum = reinterpret_cast<float*>(ws + up256(c * v * 4) + up256(c * v * 2));
   char why[128];
   cudaStream_t st = S(stream);
-  for (int64_t r0 = 0; r0 < n; r0 += c) {
-    const int64_t rows = std::min(c, n - r0);
+  for (int64_t r0 = 0; r0 < n; r0 += most) {
+    const int64_t rows = std::min(most, n - r0);
     const bool first = r0 == 0, last = r0 + rows == n;
     sf::GemmArgs z;
-    z.layout = sf::kNT; z.epi = sf::kEpiF32; z.M = rows; z.N = v; z.K = d;
-    z.A = h + r0 * d; z.lda = d; z.B = w; z.ldb = d; z.C = zf; z.ldc = v;
+    z.layout = sf::kNT; z.epi = sf::kEpiLogprobBwd; z.M = rows; z.N = v; z.K = d;
+    z.A = h + r0 * d; z.lda = d; z.B = w; z.ldb = d; z.C = dz; z.ldc = v;
+    z.lp = logprob_epi(tokens + r0, scale, lse + r0, entropy ? entropy + r0 : nullptr, dlogp + r0,
+                       dentropy ? dentropy + r0 : nullptr);
     if (sf::gemm(z, err, st, why) != 0) return SF_ECUDA;
-    sf::logprob_rows_bwd(zf, true, v, tokens + r0, rows, v, scale, lse + r0, entropy ? entropy + r0 : nullptr,
-                         dlogp + r0, dentropy ? dentropy + r0 : nullptr, dz, v, err, st);
     sf::GemmArgs gx;
     gx.layout = sf::kNN; gx.epi = sf::kEpiBF16; gx.M = rows; gx.N = d; gx.K = v;
     gx.A = dz; gx.lda = v; gx.B = w; gx.ldb = d; gx.C = dh + r0 * d; gx.ldc = d;

@@ -40,9 +40,25 @@ enum GemmLayout : int { kNT = 0, kNN = 1, kTN = 2 };
 //   s = sigmoid(a) (the down projection's input gradient through SwiGLU)
 // | kEpiBF16Acc (layout kTN): C bf16 = alpha*acc + R (R fp32, may be null):
 //   the last of a chunked sum of weight gradients, rounded once
+// | kEpiLogprob (layout kNT): no C; for each row and tile of gemm_tile_cols columns
+//   the sums of its logits z = acc as lp.parts[tile * M + row], and the logit of
+//   the row's token (0 <= lp.tokens[row] < N) as lp.token_logit[row]
+// | kEpiLogprobBwd (layout kNT): C bf16 = the gradient of the logits z = acc from
+//   lp's tokens, lse, entropy, dlogp and dentropy
 enum GemmEpi : int {
   kEpiBF16 = 0, kEpiF32 = 1, kEpiF32Add = 2, kEpiF32Acc = 3, kEpiBF16Bias = 4, kEpiF16 = 5,
-  kEpiQKV = 6, kEpiGLU = 7, kEpiGLUBwd = 8, kEpiBF16Acc = 9
+  kEpiQKV = 6, kEpiGLU = 7, kEpiGLUBwd = 8, kEpiBF16Acc = 9, kEpiLogprob = 10, kEpiLogprobBwd = 11
+};
+
+// Rows' tokens and scale for the log probabilities (sf.h); backward: lse,
+// entropy, dlogp, dentropy (may be null, and entropy with it).  parts and
+// token_logit are written by kEpiLogprob and read by logprob_tiles.
+struct LogprobEpi {
+  const int32_t* tokens = nullptr;
+  float scale = 1.f;
+  const float *lse = nullptr, *entropy = nullptr, *dlogp = nullptr, *dentropy = nullptr;
+  float4* parts = nullptr;
+  float* token_logit = nullptr;
 };
 
 struct GemmArgs {
@@ -70,12 +86,15 @@ struct GemmArgs {
   // C (ws: (splitk_max - 1) * M * ldc floats, or null for no split)
   int splitk_max = 1;
   float* ws = nullptr;
+  LogprobEpi lp;  // kEpiLogprob, kEpiLogprobBwd
   // when set, the number of kernels the call launched is added to it
   int* launched = nullptr;
 };
 
 // Returns 0, or a negative status with a message in `why` (64 chars at least).
 int gemm(const GemmArgs& a, int* dev_err, cudaStream_t st, char* why);
+// Columns of a product's tiles.
+constexpr int gemm_tile_cols(int64_t N) { return N > 128 ? 256 : 128; }
 // Host-side argument check only (no CUDA call): 0 or -1.
 int gemm_check(const GemmArgs& a, char* why);
 
@@ -279,11 +298,13 @@ bool join_bwd(const JoinArgs& a, const float* xout, const void* h, bool h32,
 bool logprob_rows(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows,
                   int vocab, float scale, float* logp, float* lse, float* entropy, int top,
                   int32_t* ids, float* top_logp, int* err, cudaStream_t st);
-// dz may be z where z is bf16; dentropy (with entropy) may be null.
-void logprob_rows_bwd(const void* z, bool f32, int64_t ld, const int32_t* tokens, int64_t rows,
-                      int vocab, float scale, const float* lse, const float* entropy,
-                      const float* dlogp, const float* dentropy, __nv_bfloat16* dz, int64_t lddz,
-                      int* err, cudaStream_t st);
+// dz may be z where z is bf16.
+void logprob_rows_bwd(const void* z, bool f32, int64_t ld, const LogprobEpi& a, int64_t rows,
+                      int vocab, __nv_bfloat16* dz, int64_t lddz, int* err, cudaStream_t st);
+// logp, lse and entropy (may be null) from the sums that a kEpiLogprob product
+// left for `tiles` tiles.  Call it right after that launch.  False: no launch.
+bool logprob_tiles(const LogprobEpi& a, int64_t rows, int tiles, int vocab, float* logp,
+                   float* lse, float* entropy, int* err, cudaStream_t st);
 
 int num_sms();
 
