@@ -977,6 +977,10 @@ static int choose_splitk(int64_t M, int64_t N, int64_t K, int BN, int max_split)
   return best;
 }
 
+int gemm_splitk(int64_t M, int64_t N, int64_t K, int max_split) {
+  return choose_splitk(M, N, K, gemm_tile_cols(N), max_split);
+}
+
 int gemm(const GemmArgs& a, int* dev_err, cudaStream_t st, char* why) {
   if (a.M == 0 || a.N == 0) return 0;
   if (int c = gemm_check(a, why)) return c;

@@ -692,15 +692,18 @@ int sf_op_lm_logprob_bwd(const uint16_t* h, const uint16_t* w, const int32_t* to
   if (!logprob_gradients(lse, entropy, dlogp, dentropy)) return SF_EINVAL;
   int* err = dev_err_word();
   if (!err) return SF_ECUDA;
-  // the logits leave the product as dz: the room of a chunk's logits holds more rows
-  const int64_t c = std::min(n, chunk_rows), most = std::min(n, 3 * c);
+  // The logits leave the product as dz, so a chunk's room holds three chunks' rows;
+  // equal passes of whole tiles.
+  const int64_t c = std::min(n, chunk_rows), most = std::min(n, 3 * c), passes = (n + most - 1) / most;
+  const int64_t pass = std::min(most, ((n + passes - 1) / passes + 255) / 256 * 256);
   char* ws = static_cast<char*>(workspace);
   bf16* dz = reinterpret_cast<bf16*>(ws);
-  float* sum = reinterpret_cast<float*>(ws + up256(c * v * 4) + up256(c * v * 2));
+  const int64_t room = up256(c * v * 4) + up256(c * v * 2);
+  float* sum = reinterpret_cast<float*>(ws + room);
   char why[128];
   cudaStream_t st = S(stream);
-  for (int64_t r0 = 0; r0 < n; r0 += most) {
-    const int64_t rows = std::min(most, n - r0);
+  for (int64_t r0 = 0; r0 < n; r0 += pass) {
+    const int64_t rows = std::min(pass, n - r0);
     const bool first = r0 == 0, last = r0 + rows == n;
     sf::GemmArgs z;
     z.layout = sf::kNT; z.epi = sf::kEpiLogprobBwd; z.M = rows; z.N = v; z.K = d;
@@ -708,10 +711,19 @@ int sf_op_lm_logprob_bwd(const uint16_t* h, const uint16_t* w, const int32_t* to
     z.lp = logprob_epi(tokens + r0, scale, lse + r0, entropy ? entropy + r0 : nullptr, dlogp + r0,
                        dentropy ? dentropy + r0 : nullptr);
     if (sf::gemm(z, err, st, why) != 0) return SF_ECUDA;
+    // dH over ranges of the vocabulary where its tiles leave SMs idle and the room
+    // behind dz holds their fp32 sums (1 x 4096 x 128256 in one range: 1.2 ms)
+    const int64_t slice = rows * d, fits = (room - up256(rows * v * 2)) / (slice * 4);
+    const int split = sf::gemm_splitk(rows, d, v, (int)std::min<int64_t>(fits, 64));
+    float* part = reinterpret_cast<float*>(ws + up256(rows * v * 2));
     sf::GemmArgs gx;
     gx.layout = sf::kNN; gx.epi = sf::kEpiBF16; gx.M = rows; gx.N = d; gx.K = v;
     gx.A = dz; gx.lda = v; gx.B = w; gx.ldb = d; gx.C = dh + r0 * d; gx.ldc = d;
+    if (split > 1) {
+      gx.epi = sf::kEpiF32; gx.C = part; gx.splitk_max = split; gx.ws = part + slice;
+    }
     if (sf::gemm(gx, err, st, why) != 0) return SF_ECUDA;
+    if (split > 1) sf::cast_f32_bf16(part, reinterpret_cast<bf16*>(dh) + r0 * d, slice, st);
     // dW: fp32 sums over the chunks; the last chunk's product adds the sum and rounds it once
     sf::GemmArgs gw;
     gw.layout = sf::kTN; gw.epi = last ? sf::kEpiBF16Acc : first ? sf::kEpiF32 : sf::kEpiF32Acc;

@@ -95,6 +95,8 @@ struct GemmArgs {
 int gemm(const GemmArgs& a, int* dev_err, cudaStream_t st, char* why);
 // Columns of a product's tiles.
 constexpr int gemm_tile_cols(int64_t N) { return N > 128 ? 256 : 128; }
+// The K ranges that a kEpiF32 product with splitk_max = max_split takes.
+int gemm_splitk(int64_t M, int64_t N, int64_t K, int max_split);
 // Host-side argument check only (no CUDA call): 0 or -1.
 int gemm_check(const GemmArgs& a, char* why);
 
