@@ -571,7 +571,7 @@ int sf_op_join_fwd(const float* x, const void* h, int32_t h_type, const uint16_t
  * gradient of xout from elsewhere (NULL: none; needed without g_next):
  *   D = dres + rstd_next*(g_next*dy - xhat*mean(g_next*dy*xhat)),
  *   dx = alpha * D, and dh the gradient through beta, dropout, gate and norm.
- * dx fp32 [rows, d] (may be dy or dres); dh of h's type.  dg_post, dgate,
+ * dx fp32 [rows, d] (may be dy or dres, not xout); dh of h's type (not h).  dg_post, dgate,
  * dg_next bf16 [d]: the gradients of the gains that are given (not used for
  * the others), summed over the rows in a fixed order (bit-reproducible).
  * scratch: fp32 of sf_op_join_bwd_scratch(rows, d) elements (-1 for bad sizes),
@@ -660,7 +660,7 @@ int64_t sf_op_lce_launches(void);
  * nothing else has lse, top_logp and its token's logp -inf and entropy 0.  A
  * row with a NaN or +inf has NaN for each of them (but 0 for no token) and ids
  * -1.  Sums in fp32.  top in [0, 32], at most vocab; ids and top_logp are not
- * used with top 0.  ldz a multiple of 8, z 16-byte aligned; vocab in [1, 2^24],
+ * used with top 0.  ldz a multiple of 8, z 16-byte aligned; vocab in [1, 2^20],
  * rows < 2^31 (may be 0). */
 #define SF_LOGPROB_TOP_MAX 32
 int sf_op_logprob_rows(const void* z, int32_t z_type, int64_t ldz, const int32_t* tokens,
@@ -681,7 +681,7 @@ int sf_op_logprob_rows_bwd(const void* z, int32_t z_type, int64_t ldz, const int
                            uint16_t* dz, int64_t lddz, void* stream);
 
 /* sf_op_logprob_rows of the logits h W^T (fp32): h bf16 [n, d], w bf16 [v, d],
- * tokens int32 [n] (device); d and v multiples of 8, v at most 2^24, n >= 1.
+ * tokens int32 [n] (device); d and v multiples of 8, v at most 2^20, n >= 1.
  * With top 0 the logits are never stored; else no more of them than a chunk of
  * chunk_rows rows.  workspace: sf_op_lm_logprob_workspace_bytes(n, v, chunk_rows)
  * bytes (4 for each logit of a chunk; -1 for bad sizes), 256-byte aligned.  Errors and the device error word
@@ -734,8 +734,8 @@ int sf_op_rmsnorm_bwd_noalloc(const float* x, const uint16_t* g, const float* rs
  * sf_op_logprob_rows, sf_op_lm_logprob or their backwards a token, at or beyond
  * the vocabulary; 5: sf_op_qknorm_rope_fwd or _bwd met a position outside the
  * rotation table; 6: an attention backward found its shared memory misaligned
- * and wrote nothing; 7: a bounded wait ran out in sf_op_join_bwd.  The first code a launch writes stays.  Synchronises the
- * device. */
+ * and wrote nothing; 7: a bounded wait ran out in sf_op_join_bwd.  The first
+ * code a launch writes stays.  Synchronises the device. */
 int sf_op_device_error(int32_t* out);
 
 #ifdef __cplusplus

@@ -31,22 +31,43 @@ namespace {
 // ------------------------------------------------------------------ dropout
 constexpr int kDropThreads = 256;
 
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void from_float(float& o, float v) { o = v; }
-__device__ __forceinline__ void from_float(bf16& o, float v) { o = __float2bfloat16_rn(v); }
+// An octet of elements as it is stored, and its kept elements times scale.
+template <bool F32>
+struct Octet;
+template <>
+struct Octet<true> {
+  float4 a, b;
+  __device__ __forceinline__ void drop(const Words& w, const DropArgs& d) {
+    a = pick(mul(a, d.scale), make_uint2(w.a, w.b), d.top);
+    b = pick(mul(b, d.scale), make_uint2(w.c, w.d), d.top);
+  }
+};
+template <>
+struct Octet<false> {
+  uint2 a, b;
+  __device__ __forceinline__ void drop(const Words& w, const DropArgs& d) {
+    const float4 x = pick(mul(unpack4(a), d.scale), make_uint2(w.a, w.b), d.top);
+    const float4 y = pick(mul(unpack4(b), d.scale), make_uint2(w.c, w.d), d.top);
+    a = pack4(x.x, x.y, x.z, x.w);
+    b = pack4(y.x, y.y, y.z, y.w);
+  }
+};
 
 // Two octets of elements a thread, loaded before their bits are drawn.
-template <typename T>
+// Instructions bound it as much as memory: 16384 x 4096 bf16 takes 45.9 us (5,850
+// GB/s, 0.86 of a copy's rate), about 14 instructions an element, half of them the
+// generator's.
+template <bool F32>
 __global__ void __launch_bounds__(kDropThreads)
-    dropout_kernel(const T* x, T* y, int64_t n, DropArgs a) {
-  struct alignas(16) Octet { T v[8]; };
+    dropout_kernel(const void* x, void* y, int64_t n, DropArgs a) {
+  constexpr int SIZE = F32 ? 4 : 2;
+  struct alignas(16) Stored { Octet<F32> v; };
   const int64_t first = (int64_t)blockIdx.x * (2 * kDropThreads) + threadIdx.x;
-  Octet o[2];
+  Stored o[2] = {};
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int64_t at = (first + u * kDropThreads) * 8;
-    if (at + 8 <= n) o[u] = *reinterpret_cast<const Octet*>(x + at);
+    if (at + 8 <= n) o[u] = *reinterpret_cast<const Stored*>(static_cast<const char*>(x) + at * SIZE);
   }
   const uint64_t offset = launch_offset(a);
 #pragma unroll
@@ -54,16 +75,22 @@ __global__ void __launch_bounds__(kDropThreads)
     const int64_t octet = first + u * kDropThreads, at = octet * 8;
     if (at >= n) return;
     const Words w = philox((uint64_t)octet, offset, a.seed);
-    const uint32_t words[4] = {w.a, w.b, w.c, w.d};
-    auto keep = [&](int i) { return i & 1 ? keep_hi(words[i / 2], a.top) : keep_lo(words[i / 2], a.top); };
     if (at + 8 <= n) {
+      o[u].v.drop(w, a);
+      *reinterpret_cast<Stored*>(static_cast<char*>(y) + at * SIZE) = o[u];
+    } else {  // the last few elements, one by one
+      const uint32_t words[4] = {w.a, w.b, w.c, w.d};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) from_float(o[u].v[i], keep(i) ? to_float(o[u].v[i]) * a.scale : 0.f);
-      *reinterpret_cast<Octet*>(y + at) = o[u];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (at + i < n) from_float(y[at + i], keep(i) ? to_float(x[at + i]) * a.scale : 0.f);
+      for (int i = 0; i < 7; ++i) {
+        if (at + i >= n) continue;
+        const bool keep = i & 1 ? keep_hi(words[i / 2], a.top) : keep_lo(words[i / 2], a.top);
+        if (F32) {
+          static_cast<float*>(y)[at + i] = keep ? static_cast<const float*>(x)[at + i] * a.scale : 0.f;
+        } else {
+          const float v = __bfloat162float(static_cast<const bf16*>(x)[at + i]);
+          static_cast<bf16*>(y)[at + i] = __float2bfloat16_rn(keep ? v * a.scale : 0.f);
+        }
+      }
     }
   }
 }
@@ -83,11 +110,12 @@ __device__ __forceinline__ float row_sum(float v, float* sh) {
 }
 
 // Forward: LANES threads take a row and hold it (CH quads each; h as it is stored
-// where there are more than four) in registers from the loads to the stores, with two rows or more on an
-// SM up to 12288 columns, so that one's loads run beside the other's sums and stores.
+// where there are more than four) in registers from the loads to the stores.  1024
+// threads an SM: up to 12288 columns two rows or more, so that one's loads run
+// beside the other's sums and stores.
 // Up to four quads the generator runs while the loads are in flight; for more its
 // words would cost the second row's registers.  16384 x 4096 with both norms, gate
-// and dropout: 120 us (6,690 GB/s, 0.99 of a copy's rate); 144 us with a generator
+// and dropout: 121 us (6,650 GB/s, 0.98 of a copy's rate); 144 us with a generator
 // call for each quad, 128 us with the calls behind the first sum.
 template <bool WIDE>
 struct HQuad {
@@ -101,7 +129,7 @@ __device__ __forceinline__ float4 values(float4 v) { return v; }
 __device__ __forceinline__ float4 values(uint2 v) { return unpack4(v); }
 
 template <int LANES, int CH, bool H32>
-__global__ void __launch_bounds__(LANES > 256 ? LANES : 256, LANES <= 256 ? 4 : CH <= 6 ? 2 : 1)
+__global__ void __launch_bounds__(LANES > 256 ? LANES : 256, 1024 / (LANES > 256 ? LANES : 256))
     join_fwd_kernel(JoinArgs a, const float* x, const void* h, float* xout, bf16* __restrict__ y,
                     float* __restrict__ rstd_post, float* __restrict__ rstd_next, float eps) {
   constexpr bool EARLY = CH <= 4;  // the generator runs while the loads are in flight
@@ -127,16 +155,15 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, LANES <= 256 ? 4 : 
       else hv[k] = v;
     }
   }
-  const uint64_t offset = a.drop.top ? launch_offset(a.drop) : 0;
-  uint2 words[EARLY ? CH : 2] = {};
-  auto draw = [&](int k) {
-    if (a.drop.top)
-      pair_words((at >> 2) + t + k * LANES, LANES, t & 1, offset, a.drop.seed, words[EARLY ? k : 0],
-                 words[EARLY ? k + 1 : 1]);
+  uint2 words[EARLY ? CH : 2];
+  auto draw = [&](int k, uint64_t offset) {
+    pair_words((at >> 2) + t + k * LANES, LANES, t & 1, offset, a.drop.seed, words[EARLY ? k : 0],
+               words[EARLY ? k + 1 : 1]);
   };
-  if (EARLY) {
+  if (EARLY && a.drop.top) {
+    const uint64_t offset = launch_offset(a.drop);
 #pragma unroll
-    for (int k = 0; k < CH; k += 2) draw(k);
+    for (int k = 0; k < CH; k += 2) draw(k, offset);
   }
   const float inv_d = 1.f / a.d;
   float r1 = 1.f;
@@ -152,7 +179,7 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, LANES <= 256 ? 4 : 
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int i = t + k * LANES;
-    if (!EARLY && k % 2 == 0) draw(k);
+    if (!EARLY && k % 2 == 0 && a.drop.top) draw(k, launch_offset(a.drop));
     if (i < n4) {
       float4 u = values(hv[k]);
       if (a.g_post) u = mul(mul(u, r1), gain(a.g_post, i));
@@ -193,22 +220,21 @@ void join_fwd_as(const JoinArgs& a, const float* x, const void* h, bool h32, flo
 
 void dropout(const void* x, void* y, bool f32, int64_t n, const DropArgs& a, cudaStream_t st) {
   const unsigned grid = (unsigned)((n + 16 * kDropThreads - 1) / (16 * kDropThreads));
-  if (f32)
-    dropout_kernel<float><<<grid, kDropThreads, 0, st>>>(static_cast<const float*>(x), static_cast<float*>(y), n, a);
-  else
-    dropout_kernel<bf16><<<grid, kDropThreads, 0, st>>>(static_cast<const bf16*>(x), static_cast<bf16*>(y), n, a);
+  if (f32) dropout_kernel<true><<<grid, kDropThreads, 0, st>>>(x, y, n, a);
+  else dropout_kernel<false><<<grid, kDropThreads, 0, st>>>(x, y, n, a);
 }
 
 void join_fwd(const JoinArgs& a, const float* x, const void* h, bool h32, float* xout, bf16* y,
               float* rstd_post, float* rstd_next, float eps, cudaStream_t st) {
   const int d = a.d;
-  if (d <= 512) join_fwd_as<32, 4>(a, x, h, h32, xout, y, rstd_post, rstd_next, eps, st);
+  if (d <= 256) join_fwd_as<32, 2>(a, x, h, h32, xout, y, rstd_post, rstd_next, eps, st);
+  else if (d <= 512) join_fwd_as<32, 4>(a, x, h, h32, xout, y, rstd_post, rstd_next, eps, st);
   else if (d <= 1024) join_fwd_as<64, 4>(a, x, h, h32, xout, y, rstd_post, rstd_next, eps, st);
   else if (d <= 2048) join_fwd_as<128, 4>(a, x, h, h32, xout, y, rstd_post, rstd_next, eps, st);
   else if (d <= 4096) join_fwd_as<256, 4>(a, x, h, h32, xout, y, rstd_post, rstd_next, eps, st);
   else if (d <= 8192) join_fwd_as<512, 4>(a, x, h, h32, xout, y, rstd_post, rstd_next, eps, st);
   else if (d <= 12288) join_fwd_as<512, 6>(a, x, h, h32, xout, y, rstd_post, rstd_next, eps, st);
-  else join_fwd_as<512, 8>(a, x, h, h32, xout, y, rstd_post, rstd_next, eps, st);  // d <= 16384
+  else join_fwd_as<1024, 4>(a, x, h, h32, xout, y, rstd_post, rstd_next, eps, st);  // d <= 16384
 }
 
 }  // namespace sf

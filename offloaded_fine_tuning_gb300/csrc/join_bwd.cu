@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "join.cuh"
@@ -358,7 +359,7 @@ BwdShape bwd_shape(int d, bool h32, bool plain) {
       if (c * n * q * 4 >= d) return {n, q, c};
 }
 // CTAs (clusters, where ctas > 1) that all SMs hold at a time, at most.
-int bwd_most(const BwdShape& s) { return num_sms() / s.ctas; }
+int bwd_most(const BwdShape& s) { return num_sms() > s.ctas ? num_sms() / s.ctas : 1; }
 int bwd_parts(int64_t rows, const BwdShape& s, int most) {
   const int groups = kThreads / s.lanes;
   const int64_t need = (rows + groups - 1) / groups;
@@ -418,10 +419,16 @@ int launch_bwd(const BwdCall& c) {
   cfg.numAttrs = 1;
   int most = bwd_most(s);
   if (CL > 1) {  // clusters that are resident at once: more would take a second turn
-    cfg.gridDim = dim3((unsigned)(CL * most));
-    cfg.dynamicSmemBytes = kRingBytes;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return 0;
+    static std::atomic<int> resident[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = resident[dev].load(std::memory_order_relaxed);
+    if (n == 0) {  // threads that come here first find the same number
+      cfg.gridDim = dim3((unsigned)(CL * most));
+      cfg.dynamicSmemBytes = kRingBytes;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return 0;
+      resident[dev].store(n, std::memory_order_relaxed);
+    }
     if (n < most) most = n;
   }
   const int parts = bwd_parts(c.a.rows, s, most);

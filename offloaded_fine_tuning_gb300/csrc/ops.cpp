@@ -560,7 +560,7 @@ int64_t sf_op_lce_launches(void) { return lce_launches; }
 
 // What both directions of the log probabilities take.
 static bool logprob_sizes(int32_t z_type, int64_t ldz, int64_t rows, int32_t vocab, float scale) {
-  return a_type(z_type) && rows >= 0 && rows <= INT32_MAX && vocab >= 1 && vocab <= (1 << 24) &&
+  return a_type(z_type) && rows >= 0 && rows <= INT32_MAX && vocab >= 1 && vocab <= (1 << 20) &&
          ldz >= vocab && ldz % 8 == 0 && scale >= 9.5367431640625e-07f && scale <= 1048576.f;
 }
 static bool logprob_outputs(float* logp, float* lse, float* entropy, int32_t vocab, int32_t top, int32_t* ids,
@@ -616,7 +616,7 @@ int sf_op_logprob_rows_bwd(const void* z, int32_t z_type, int64_t ldz, const int
 
 // The head of the log probabilities: sizes, and a chunk's place in the workspace.
 static bool lm_logprob_sizes(int64_t n, int32_t d, int32_t v, int64_t chunk_rows) {
-  return n >= 1 && n <= INT32_MAX && d >= 8 && d % 8 == 0 && v >= 8 && v % 8 == 0 && v <= (1 << 24) &&
+  return n >= 1 && n <= INT32_MAX && d >= 8 && d % 8 == 0 && v >= 8 && v % 8 == 0 && v <= (1 << 20) &&
          chunk_rows >= 1;
 }
 static int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }

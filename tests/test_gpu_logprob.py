@@ -218,6 +218,56 @@ def test_a_token_beyond_the_vocabulary_is_reported():
     assert (dz[1:3, :100] == 0).all() and (dz[[0, 3], :100] != 0).any() and (dz[:, 100:] == 5).all()
 
 
+def test_rows_beyond_2_31_logits():
+    rows, vocab = 17000, 128256
+    z = torch.zeros(rows, vocab, dtype=torch.bfloat16, device="cuda")
+    z[-1] = logits(1, vocab, 0, torch.bfloat16, seed=7)[0]
+    tokens = torch.full((rows,), vocab - 1, **I32)
+    out = Rows(rows, 3)
+    assert out.call(z, vocab, tokens) == 0
+    dl, de = torch.full((rows,), 0.5, **T32), torch.full((rows,), 0.25, **T32)
+    assert sf.op_logprob_rows_bwd(z.data_ptr(), sf.BF16, vocab, tokens.data_ptr(), rows, vocab, 1.0,
+                                  out.lse.data_ptr(), out.entropy.data_ptr(), dl.data_ptr(), de.data_ptr(),
+                                  z.data_ptr(), vocab, stream=stream()) == 0  # in place
+    sync()
+    near(out.lse[:-1], torch.full((rows - 1,), math.log(vocab), dtype=torch.float64, device="cuda"), REL(vocab) + 1e-6)
+    assert (out.ids[:-1] == torch.arange(3, **I32)).all()
+    last = logits(1, vocab, 0, torch.bfloat16, seed=7)
+    lse, _, _, h, _, ids, _ = reference(last, vocab, tokens[-1:], 1.0)
+    near(out.lse[-1:], lse, REL(vocab) + 8 * U * lse.abs())
+    assert torch.equal(out.ids[-1:], ids[:, :3].int())
+    ref, size, lp = gradient(last, vocab, tokens[-1:], 1.0, out.lse[-1:].double(), out.entropy[-1:].double(),
+                             dl[-1:].double(), de[-1:].double())
+    near(z[-1:], ref, BF * ref.abs() + (2.0 ** -20 + 4 * U * lp.abs()) * size + 1e-37)
+
+
+def test_rows_on_two_streams():
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    data = [(logits(400, 5003, 0, torch.float32, seed=s), torch.arange(400, **I32)) for s in (1, 2)]
+    outs = [Rows(400, 7), Rows(400, 7)]
+    sync()
+    for (z, tokens), out, side in zip(data, outs, sides):
+        with torch.cuda.stream(side):
+            assert out.call(z, 5003, tokens) == 0
+    sync()
+    for (z, tokens), out in zip(data, outs):
+        again = Rows(400, 7)
+        assert again.call(z, 5003, tokens) == 0
+        sync()
+        assert all(torch.equal(a, b) for a, b in zip(again.flat, out.flat))
+
+
+def test_rows_of_few_sets_of_large_logits():
+    """Many logits above the bound that the threads' maxima give, rising: the list overflows again and again."""
+    vocab = 128256
+    z = logits(400, vocab, 0, torch.float32)
+    own = torch.zeros(vocab, dtype=torch.bool, device="cuda")
+    own[(torch.arange(vocab, device="cuda") // 8) % 256 < 60] = True  # 15 sets of 4 threads of a row's 256
+    z[:, own] = torch.linspace(10, 20, int(own.sum()), **T32)
+    check(z[::50].contiguous(), vocab, torch.zeros(8, **I32), 32)
+    check(z, vocab, torch.zeros(400, **I32), 32)
+
+
 # ------------------------------------------------------------------ gradients of rows
 def gradient(z, vocab, tokens, scale, lse, h, dl, de):
     t = z[:, :vocab].double() * scale
