@@ -311,25 +311,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The gains' gradients from the partials [parts, 2, d], in a fixed order: a CTA
-// takes 32 columns with 32 warps, warp w adds the partials w, w + 32, ...
-__global__ void __launch_bounds__(1024)
+// takes 64 columns of one sum, a quad for each of 16 lanes, and 32 half warps;
+// half warp w adds the partials w, w + 32, ..., then their sums are added in that
+// order.
+constexpr int kSumGroups = 32;
+
+__global__ void __launch_bounds__(16 * kSumGroups)
     join_sums_kernel(JoinArgs a, const float* __restrict__ part, int parts, bf16* __restrict__ dg_post,
                      bf16* __restrict__ dgate, bf16* __restrict__ dg_next) {
-  __shared__ float sh[32][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int s = blockIdx.y, j = blockIdx.x * 32 + lane;
+  __shared__ float4 sh[kSumGroups][16];
+  const int t = threadIdx.x & 15, w = threadIdx.x >> 4;
+  const int s = blockIdx.y, quad = blockIdx.x * 16 + t;
   wait_primary();
-  float v = 0.f;
-  if (j < a.d) {
-#pragma unroll 8
-    for (int p = w; p < parts; p += 32) v += __ldcg(part + ((int64_t)p * 2 + s) * a.d + j);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (quad < a.d / 4) {
+#pragma unroll 5
+    for (int p = w; p < parts; p += kSumGroups) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(part + ((int64_t)p * 2 + s) * a.d) + quad);
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
   }
-  sh[w][lane] = v;
+  sh[w][t] = v;
   __syncthreads();
-  // warp w joins column w: one value per lane, added pairwise in a fixed tree
-  const float sum = warp_sum(sh[lane][w]);
-  const int c = blockIdx.x * 32 + w;
-  if (lane != 0 || c >= a.d) return;
+  const int c = blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x >= 64 || c >= a.d) return;
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kSumGroups; ++k) sum += reinterpret_cast<const float*>(sh[k])[threadIdx.x];
   if (s == 0) {
     if (dg_next) dg_next[c] = __float2bfloat16_rn(sum);
   } else {
@@ -482,7 +490,7 @@ bool join_bwd(const JoinArgs& a, const float* xout, const void* h, bool h32, con
   const BwdCall c = {a, xout, h, rstd_post, rstd_next, dy, dres, dx, dh, part, err, st};
   const int parts = h32 ? launch_bwd_for<true>(s, c) : launch_bwd_for<false>(s, c);
   if (parts && part)
-    launch_dependent(join_sums_kernel, dim3((unsigned)((a.d + 31) / 32), 2), 1024, 0, st, a, part, parts, dg_post,
+    launch_dependent(join_sums_kernel, dim3((unsigned)((a.d + 63) / 64), 2), 16 * kSumGroups, 0, st, a, part, parts, dg_post,
                      dgate, dg_next);
   return parts > 0;
 }
