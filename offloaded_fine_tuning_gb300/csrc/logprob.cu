@@ -96,7 +96,7 @@ __device__ __forceinline__ void places(const Logit* list, int n, F what) {
 // least kList - top of them, and the low ids come first, so that rows of one
 // value end in two.
 template <typename T, bool ENT, int NT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, NT == 256 || NT == 512 ? 1536 / NT : 1)
     logprob_rows_kernel(const T* __restrict__ z, int64_t ld, const int32_t* __restrict__ tokens, int vocab,
                         float scale, float* __restrict__ logp, float* __restrict__ lse_out,
                         float* __restrict__ entropy, int top, int32_t* __restrict__ ids,
@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(NT)
   if (tid == 0) hot_n = list_n = 0;
   const int octets = (hi - lo + NT - 1) / NT;                        // of a thread
   const int length = ((octets + SPANS - 1) / SPANS + U - 1) / U * U;  // of a span
-  Sums a = {-FLT_MAX, 0.f, 0.f, 0.f};
+  const Sums empty = {-FLT_MAX, 0.f, 0.f, 0.f};
+  Sums a = empty;
 #pragma unroll 1
   for (int s = 0; s < SPANS; ++s) {
     float m = minus_inf;
@@ -152,10 +153,7 @@ __global__ void __launch_bounds__(NT)
     add<ENT>(a, f, c);
   }
   const float mine = a.s == 0.f ? minus_inf : a.m;  // s is at least 1 with any logit above -inf
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    a = merge(a, {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                  __shfl_xor_sync(0xffffffffu, a.low, o), __shfl_xor_sync(0xffffffffu, a.t, o)}, c);
+  a = warp_merge(a, c);
   if (lane == 0) part[warp] = a;
   if (top > 0) {
     float group = mine;
@@ -179,8 +177,7 @@ __global__ void __launch_bounds__(NT)
   }
   __syncthreads();
   if (warp == 0) {
-    a = part[0];
-    for (int w = 1; w < NT / 32; ++w) a = merge(a, part[w], c);
+    a = warp_merge(lane < NT / 32 ? part[lane] : empty, c);
     if (lane == 0) total = a;
   }
   if (top > 0) {
@@ -228,24 +225,6 @@ __global__ void __launch_bounds__(NT)
   if (ncl > 1) cluster_sync_all();
   else __syncthreads();
   if (rank == 0) {
-    Sums all = total;
-    for (uint32_t q = 1; q < ncl; ++q) {
-      const uint32_t at = mapa_shared(smem_u32(&total), q);
-      const float2 x = ld_shared_cluster_f32x2(at), y = ld_shared_cluster_f32x2(at + 8);
-      all = merge(all, {x.x, x.y, y.x, y.y}, c);
-    }
-    const RowStats r = row_stats(all, scale);
-    const bool bad = !(all.s == all.s);
-    if (tid == 0) {
-      int token = tokens[row];
-      if (token >= vocab) {  // outside the vocabulary: reported, and the row ignored
-        record_error(err, kDevCeBadLabel);
-        token = -1;
-      }
-      logp[row] = token < 0 ? 0.f : r.value(to_float(zr[token]));
-      lse_out[row] = r.lse;
-      if (ENT) entropy[row] = r.entropy;
-    }
     if (ncl > 1) {  // the ranges' alternatives in one order
       const int n = (int)ncl * top;
       for (int k = tid; k < n; k += NT) {
@@ -258,9 +237,33 @@ __global__ void __launch_bounds__(NT)
       });
       __syncthreads();
     }
-    if (tid < top) {
-      ids[row * top + tid] = bad ? -1 : best[tid].i;
-      top_logp[row * top + tid] = bad ? all.s : r.value(best[tid].v);
+    if (warp == 0) {  // lane q has CTA q's sums; then one of the alternatives (32 at most)
+      Sums all = total;
+      if (ncl > 1) {
+        all = empty;
+        if (lane < (int)ncl) {
+          const uint32_t at = mapa_shared(smem_u32(&total), lane);
+          const float2 x = ld_shared_cluster_f32x2(at), y = ld_shared_cluster_f32x2(at + 8);
+          all = {x.x, x.y, y.x, y.y};
+        }
+        all = warp_merge(all, c);
+      }
+      const RowStats r = row_stats(all, scale);
+      const bool bad = !(all.s == all.s);
+      if (lane == 0) {
+        int token = tokens[row];
+        if (token >= vocab) {  // outside the vocabulary: reported, and the row ignored
+          record_error(err, kDevCeBadLabel);
+          token = -1;
+        }
+        logp[row] = token < 0 ? 0.f : r.value(to_float(zr[token]));
+        lse_out[row] = r.lse;
+        if (ENT) entropy[row] = r.entropy;
+      }
+      if (lane < top) {
+        ids[row * top + lane] = bad ? -1 : best[lane].i;
+        top_logp[row * top + lane] = bad ? all.s : r.value(best[lane].v);
+      }
     }
   }
   if (ncl > 1) cluster_sync_all();  // the first CTA has read its peers' results
@@ -287,20 +290,19 @@ __global__ void __launch_bounds__(kThreads)
     for (int u = 0; u < 4; ++u) {
       const int at = first + (u * kThreads + threadIdx.x) * 8;
       if (at + 8 <= vocab) {
-        float f[8];
+        float f[8] = {};
         Eight<bf16> o;
-        if (g.zero) {
+        if (!g.zero) load8(zr + at, f);
+        logit_grads(g, f, at);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o.v[j] = __float2bfloat16_rn(0.f);
-        } else {
-          load8(zr + at, f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o.v[j] = __float2bfloat16_rn(logit_grad(g, f[j], at + j));
-        }
+        for (int j = 0; j < 8; ++j) o.v[j] = __float2bfloat16_rn(f[j]);
         *reinterpret_cast<Eight<bf16>*>(dr + at) = o;
       } else {
-        for (int j = at; j < vocab; ++j)
-          dr[j] = __float2bfloat16_rn(g.zero ? 0.f : logit_grad(g, to_float(zr[j]), j));
+        for (int j = at; j < vocab; ++j) {
+          float f[1] = {g.zero ? 0.f : to_float(zr[j])};
+          logit_grads(g, f, j);
+          dr[j] = __float2bfloat16_rn(f[0]);
+        }
       }
     }
   }

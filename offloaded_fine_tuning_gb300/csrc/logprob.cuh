@@ -92,10 +92,20 @@ __device__ __forceinline__ RowStats row_stats(const Sums& a, float scale) {
   return r;
 }
 
-// The gradient of a logit f of a row: scale (dlogp [hot] - p (dlogp + dentropy
-// (log p + entropy))).
+// The sums of the whole warp, in every lane.
+__device__ __forceinline__ Sums warp_merge(Sums a, float c) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    a = merge(a, {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+                  __shfl_xor_sync(0xffffffffu, a.low, o), __shfl_xor_sync(0xffffffffu, a.t, o)}, c);
+  return a;
+}
+
+// The gradient of a logit f of a row, scale (dlogp [hot] - p (dlogp + dentropy
+// (log p + entropy))), with everything but p and log p taken together:
+// p (slope log p + base) [+ hot].
 struct RowGrad {
-  float lse, entropy, dlogp, dentropy, scale;
+  float lse, scale, slope, base, hot;
   int token;
   bool zero;  // both gradients are 0, or the row holds nothing but -inf
 };
@@ -106,18 +116,33 @@ __device__ __forceinline__ RowGrad row_grad(const LogprobEpi& a, int64_t row, in
     record_error(err, kDevCeBadLabel);
     g.token = -1;
   }
+  const float dl = g.token < 0 ? 0.f : a.dlogp[row], de = a.dentropy ? a.dentropy[row] : 0.f;
   g.lse = a.lse[row];
   g.scale = a.scale;
-  g.dlogp = g.token < 0 ? 0.f : a.dlogp[row];
-  g.dentropy = a.dentropy ? a.dentropy[row] : 0.f;
-  g.entropy = a.dentropy ? a.entropy[row] : 0.f;
-  g.zero = (g.dlogp == 0.f && g.dentropy == 0.f) || g.lse == -__uint_as_float(0x7f800000u);
+  g.slope = -a.scale * de;
+  g.base = -a.scale * (a.dentropy ? fmaf(de, a.entropy[row], dl) : dl);
+  g.hot = a.scale * dl;
+  g.zero = (dl == 0.f && de == 0.f) || g.lse == -__uint_as_float(0x7f800000u);
   return g;
 }
-__device__ __forceinline__ float logit_grad(const RowGrad& g, float f, int at) {
-  const float lp = fmaf(f, g.scale, -g.lse), p = exp2_fast(lp * kLog2e);
-  const float q = fmaf(g.dentropy, fmaxf(lp, kFar) + g.entropy, g.dlogp);
-  return g.scale * fmaf(-p, q, at == g.token ? g.dlogp : 0.f);
+// N logits from column `at` on, in place.
+template <int N>
+__device__ __forceinline__ void logit_grads(const RowGrad& g, float (&f)[N], int at) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float lp = fmaf(f[j], g.scale, -g.lse), p = exp2_fast(lp * kLog2e);
+    f[j] = p * fmaf(g.slope, fmaxf(lp, kFar), g.base);
+  }
+  const int hot = g.token - at;
+  if (hot >= 0 && hot < N) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j == hot) f[j] += g.hot;
+  }
+  if (g.zero) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = 0.f;
+  }
 }
 
 }  // namespace sf
