@@ -269,6 +269,129 @@ __global__ void __launch_bounds__(NT, NT == 256 || NT == 512 ? 1536 / NT : 1)
   if (ncl > 1) cluster_sync_all();  // the first CTA has read its peers' results
 }
 
+// Short rows: a warp takes a row, without barriers, and reads it twice where
+// alternatives are wanted (the second time from L1).  Their bound is the top-th of
+// 64 maxima, two a lane: sorted in two runs of 32 by bitonic exchanges, of which
+// the larger of each pair in opposite order are the 32 largest.  16384 x 500 with
+// 20 alternatives: 25 us; 73 us with 64 threads a row, whose barriers and CTA starts
+// outlast the row.
+constexpr int kShortList = 128;  // candidates that a warp holds
+
+// The lanes' values in falling order.
+__device__ __forceinline__ float warp_sort(float v, int from) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2) {
+    if (size < from) continue;
+#pragma unroll
+    for (int o = size / 2; o > 0; o /= 2) {
+      const float w = __shfl_xor_sync(0xffffffffu, v, o);
+      const bool first = (lane & o) == 0, down = size == 32 || (lane & size) == 0;
+      v = first == down ? fmaxf(v, w) : fminf(v, w);
+    }
+  }
+  return v;
+}
+
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kThreads)
+    logprob_short_kernel(const T* __restrict__ z, int64_t ld, const int32_t* __restrict__ tokens, int64_t rows,
+                         int vocab, float scale, float* __restrict__ logp, float* __restrict__ lse_out,
+                         float* __restrict__ entropy, int top, int32_t* __restrict__ ids,
+                         float* __restrict__ top_logp, int* err) {
+  __shared__ Logit lists[kThreads / 32][kShortList];
+  __shared__ int counts[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+  if (row >= rows) return;
+  const T* zr = z + row * ld;
+  const float c = scale * kLog2e, minus_inf = -__uint_as_float(0x7f800000u);
+  const int n8 = vocab >> 3, tail = lane < (vocab & 7) ? 8 * n8 + lane : -1;
+  Sums a = {-FLT_MAX, 0.f, 0.f, 0.f};
+  float max_a = minus_inf, max_b = minus_inf;  // of the first and the last four of each octet
+  for (int i = lane; i < n8; i += 32) {
+    float f[8];
+    load8(zr + 8 * i, f);
+    add<ENT>(a, f, c);
+    max_a = fmaxf(max_a, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
+    max_b = fmaxf(max_b, fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+  }
+  if (tail >= 0) {
+    const float f[1] = {to_float(zr[tail])};
+    add<ENT>(a, f, c);
+    max_a = fmaxf(max_a, f[0]);
+  }
+  a = warp_merge(a, c);
+  const RowStats r = row_stats(a, scale);
+  if (lane == 0) {
+    int token = tokens[row];
+    if (token >= vocab) {  // outside the vocabulary: reported, and the row ignored
+      record_error(err, kDevCeBadLabel);
+      token = -1;
+    }
+    logp[row] = token < 0 ? 0.f : r.value(to_float(zr[token]));
+    lse_out[row] = r.lse;
+    if (ENT) entropy[row] = r.entropy;
+  }
+  if (top == 0) return;
+  if (!(a.s == a.s)) {  // a NaN or +inf
+    if (lane < top) {
+      ids[row * top + lane] = -1;
+      top_logp[row * top + lane] = a.s;
+    }
+    return;
+  }
+  max_b = warp_sort(max_b, 2);
+  const float best = warp_sort(fmaxf(warp_sort(max_a, 2), __shfl_xor_sync(0xffffffffu, max_b, 31)), 32);
+  Logit least = {__shfl_sync(0xffffffffu, best, top - 1), INT_MAX};
+  Logit* list = lists[warp];
+  // the entries' places, were they in order
+  auto places = [&](int n, auto what) {
+    for (int k = lane; k < n; k += 32) {
+      const Logit b = list[k];
+      int place = 0;
+      for (int j = 0; j < n; ++j) place += before(list[j], b);
+      what(b, place);
+    }
+  };
+  while (true) {
+    if (lane == 0) counts[warp] = 0;
+    __syncwarp();
+    auto look = [&](float v, int at) {
+      if (v > least.v || (v == least.v && at <= least.i)) {
+        const int k = atomicAdd(&counts[warp], 1);
+        if (k < kShortList) list[k] = {v, at};
+      }
+    };
+    for (int i = lane; i < n8; i += 32) {
+      float f[8];
+      load8(zr + 8 * i, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) look(f[j], 8 * i + j);
+    }
+    if (tail >= 0) look(to_float(zr[tail]), tail);
+    __syncwarp();
+    const int n = counts[warp];
+    if (n <= kShortList) {
+      places(n, [&](Logit b, int place) {
+        if (place < top) {
+          ids[row * top + place] = b.i;
+          top_logp[row * top + place] = r.value(b.v);
+        }
+      });
+      return;
+    }
+    // more reach the bound than the list holds: the top-th of those that it does is the next one
+    Logit next = {0.f, -1};
+    places(kShortList, [&](Logit b, int place) {
+      if (place == top - 1) next = b;
+    });
+    const int from = __ffs(__ballot_sync(0xffffffffu, next.i >= 0)) - 1;
+    least = {__shfl_sync(0xffffffffu, next.v, from), __shfl_sync(0xffffffffu, next.i, from)};
+    __syncwarp();
+  }
+}
+
 // Backward, element by element from the row's lse and entropy:
 //   dz = scale (dlogp (1[token] - p) - dentropy p (log p + entropy)).
 // A CTA takes kPiece logits of a row.  Rows whose two upstream gradients are
@@ -348,13 +471,17 @@ __global__ void __launch_bounds__(1024)
 }  // namespace
 
 // Threads of a row.  Many rows: as few as still give each a dozen octets, so
-// that one row's reductions hide behind the loads of others.  Few rows: more of
-// them, up to eight CTAs of 1024.
+// that one row's reductions hide behind the loads of others; short rows a warp.
+// Few rows: more of them, up to eight CTAs of 1024.  Measured with 20 alternatives,
+// a warp and 128 threads: 16384 x 2048 47 and 81 us, 16384 x 4096 81 and 96, 16384 x
+// 8192 180 and 133, 1200 x 4096 23 and 22; 256 and 512 threads: 160 x 128256 33 and
+// 25, 304 x 128256 37 and 32, 608 x 128256 54 and 66; 1024 threads in one CTA and in
+// eight: 8 x 128256 20 and 12.
 struct RowShape {
   int threads, ctas;
 };
 static RowShape row_shape(int64_t rows, int vocab) {
-  if (vocab <= 1536) return {64, 1};
+  if (vocab <= 1024 || (vocab <= 4096 && rows > 16 * num_sms())) return {32, 1};
   if (vocab <= 16384) return {128, 1};
   if (rows > 2 * num_sms()) return {256, 1};
   if (rows > num_sms()) return {512, 1};
@@ -394,7 +521,11 @@ static bool logprob_rows_of(const T* z, int64_t ld, const int32_t* tokens, int64
   logprob_rows_as<T, ENT, NT>(z, ld, tokens, rows, vocab, scale, logp, lse, entropy, top, ids, top_logp, err, s.ctas, \
                               st)
   switch (s.threads) {
-    case 64: return SF_LOGPROB(64);
+    case 32:
+      logprob_short_kernel<T, ENT><<<(unsigned)((rows + 7) / 8), kThreads, 0, st>>>(z, ld, tokens, rows, vocab, scale,
+                                                                                   logp, lse, entropy, top, ids,
+                                                                                   top_logp, err);
+      return true;
     case 128: return SF_LOGPROB(128);
     case 256: return SF_LOGPROB(256);
     case 512: return SF_LOGPROB(512);

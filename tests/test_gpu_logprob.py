@@ -112,7 +112,7 @@ def check(z, vocab, tokens, top, scale=1.0):
 
 SIZES = [(1, 1, 0, 1), (3, 7, 8, 7), (5, 50, 0, 20), (4, 255, 8, 32), (2, 2048, 0, 5), (3, 2049, 64, 32),
          (700, 3000, 0, 3), (2, 8197, 0, 20), (5, 32000, 0, 32), (3, 128256, 8, 20), (1, 152064, 0, 32),
-         (2, 300001, 0, 20), (160, 128256, 0, 20), (1, 1 << 20, 0, 32), (1300, 2051, 0, 32)]
+         (2, 300001, 0, 20), (160, 128256, 0, 20), (1, 1 << 20, 0, 32), (1300, 2051, 0, 32), (2500, 2051, 0, 32), (2501, 4096, 8, 20), (12, 1000, 0, 17)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
