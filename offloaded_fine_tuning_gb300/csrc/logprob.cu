@@ -475,8 +475,8 @@ __global__ void __launch_bounds__(1024)
 // Few rows: more of them, up to eight CTAs of 1024.  Measured with 20 alternatives,
 // a warp and 128 threads: 16384 x 2048 47 and 81 us, 16384 x 4096 81 and 96, 16384 x
 // 8192 180 and 133, 1200 x 4096 23 and 22; 256 and 512 threads: 160 x 128256 33 and
-// 25, 304 x 128256 37 and 32, 608 x 128256 54 and 66; 1024 threads in one CTA and in
-// eight: 8 x 128256 20 and 12.
+// 25, 304 x 128256 37 and 32, 608 x 128256 54 and 66; 152 x 128256 38 us with four
+// CTAs of 256, 20 with one of 1024.
 struct RowShape {
   int threads, ctas;
 };
