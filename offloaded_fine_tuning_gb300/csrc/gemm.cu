@@ -339,13 +339,6 @@ __device__ __forceinline__ void epi_store(const GemmParams& p, int row, int col,
     __nv_bfloat16* c = reinterpret_cast<__nv_bfloat16*>(p.C) + (int64_t)row * p.ldc + col;
     store_bf16x32(c, da, n);
     store_bf16x32(c + p.N, db, n);
-  } else if constexpr (EPI == kEpiBF16Acc) {
-    const int n = min(32, p.N - col);
-    float y[32];
-    if (p.R) load_f32x32(p.R + (int64_t)row * p.ldr + col, y, n);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]) * a_ + (p.R ? y[j] : 0.f);
-    store_bf16x32(reinterpret_cast<__nv_bfloat16*>(p.C) + (int64_t)row * p.ldc + col, y, n);
   } else if constexpr (EPI == kEpiF16) {
     __half* c = reinterpret_cast<__half*>(p.C) + (int64_t)row * p.ldc + col;
     if (full && ((reinterpret_cast<uintptr_t>(c) & 15) == 0)) {
@@ -623,7 +616,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 2) {
     // ---------------------------------------------------------------- epilogue
     const int quarter = warp & 3;  // TMEM lanes this warp may read
-    const bool whole_pieces = p.N % 8 == 0 && p.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(p.C) & 15) == 0;
     int iter = 0;
     for (int unit = unit0; unit < num_units; unit += unit_step, ++iter) {
       int tmu, tn, umn, kb0, kb1;
@@ -693,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row < p.M) g = row_grad(p.lp, row, p.N, p.err);
         epi_staged<BN>(p, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
                        [&](float (&y)[32], int col) { logit_grads(g, y, col); });
-      } else if (EPI == kEpiBF16Acc && whole_pieces) {
+      } else if constexpr (EPI == kEpiBF16Acc) {
         epi_staged<BN>(p, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
                        [&](float (&y)[32], int col) {
                          if (!p.R || row >= p.M) return;
@@ -922,8 +914,9 @@ int gemm_check(const GemmArgs& a, char* why) {
     snprintf(why, 64, "gemm: bias must be 64-byte aligned");
     return -1;
   }
-  if (a.epi == kEpiLogprobBwd && (a.N % 8 || a.ldc % 8 || !al(a.C, 16))) {
-    snprintf(why, 64, "gemm: bad gradient rows");
+  // rows stored in pieces of 8 columns
+  if ((a.epi == kEpiLogprobBwd || a.epi == kEpiBF16Acc) && (a.N % 8 || a.ldc % 8 || !al(a.C, 16))) {
+    snprintf(why, 64, "gemm: rows must be whole 16-byte pieces");
     return -1;
   }
   // TMA: 16-byte aligned bases and row strides.

@@ -34,18 +34,21 @@ namespace {
 // One CTA of 512 threads per SM, in groups of LANES threads that take a row each,
 // so that a thread holds Q quads of four columns: up to four, or three with h in
 // fp32.  Wider rows are shared by a cluster of CL CTAs.  A thread copies its
-// quads of the rows ahead (xout, dy, dres and h, 56 or 64 bytes a quad) into its own places of
-// a ring in shared memory with cp.async and reads them back itself.  The ring has
-// as many stages as fit: two of 115 KB for 512 threads, more where rows are narrow or
-// arrays are not there.  dx may be dres or dy: a thread has read its quads of a row
-// before it writes them, and no other touches them.  No barrier but the one for a
-// row's sums stands between rows, and the gains' sums of a thread's columns stay
-// in its registers over all of them.
+// quads of the rows ahead (xout, dy, dres and h, 56 or 64 bytes a quad) into its
+// own places of a ring in shared memory with cp.async and reads them back itself.
+// The ring has as many stages as fit: two of 115 KB, more where rows are narrow or
+// arrays are not there.  dx may be dres or dy: a thread has read its quads of a
+// row before it writes them, and no other touches them.  No barrier but the one
+// for a row's sums stands between rows, and the gains' sums of a thread's columns
+// stay in its registers over all of them.
 // The loops over a thread's quads have no branches, so that the quads' chains
 // run beside one another: quads beyond the row are copied as zeros and not
-// stored, and what an absent array would hold is read from another one and
-// not used.  (With a branch for each quad and array 84 instructions an element
-// were issued, and 16384 x 4096 without a second norm took 171 us.)
+// stored, and what an absent array would hold is read from another one and not
+// used.
+// With both norms, gate and dropout: 16384 x 4096 215 us (6,230 GB/s, 0.92 of a
+// copy's rate; 543 us without the ring), 8192 x 8192 202 us (0.98; 230 us with a
+// barrier for each norm), 16384 x 4096 with fp32 h 246 us (0.96; 272), 4095 x 12288
+// without gate and dropout 171 us (0.87; 214 us with two cluster barriers a row).
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kRingBytes = 230000;
 
@@ -94,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float* dy, const float* dres, float* dx, void* __restrict__ dh,
                     float* __restrict__ part, BwdRing r, int* err) {
   static_assert(CL == 1 || LANES == kThreads, "a cluster's CTAs hold one row");
-  constexpr int NT = kThreads, WARPS = kWarps, GROUPS = NT / LANES, HB = H32 ? 16 : 8;
+  constexpr int NT = kThreads, WARPS = kWarps, GROUPS = NT / LANES;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sums[2][3][CL * WARPS];  // the warps' sums, of two rows in turn; the cluster's
   __shared__ __align__(8) uint64_t bars[2];
@@ -193,9 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // rows below 2^31, and a few strides beyond: 32 bits without a sign
   const uint32_t stride = gridDim.x / CL * GROUPS;
   uint32_t row = blockIdx.x / CL * GROUPS + group;
-  for (int k = 0; k < r.stages; ++k) {
-    issue(row + k * stride, k * r.stage);
-  }
+  for (int k = 0; k < r.stages; ++k) issue(row + k * stride, k * r.stage);
   if (CL > 1) {
     if (tid == 0) {
       for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&bars[k]), 1);
@@ -360,7 +361,7 @@ BwdShape bwd_shape(int d, bool h32, bool plain) {
   // one row at a time where its traffic hides a row's chain: with a second norm
   // (dy and xout to read) and no dropout (16384 x 4096: 208 us with 512 threads of
   // two quads, 224 with two groups of 256 of four; with dropout 240 and 219,
-  // without a second norm 174 and 141)
+  // without a second norm 174 and 154)
   if (!h32 && plain && n == 256) return {512, 2, 1};
   for (int c = 1;; c *= 2)
     for (int q = c == 1 ? few : 2; q <= most; ++q)

@@ -376,7 +376,7 @@ def test_rows_gradient_against_differences():
 
 # ------------------------------------------------------------------ the head
 LM = [(1, 8, 8, 1), (5, 64, 104, 2), (130, 136, 520, 64), (300, 384, 3000, 128), (129, 512, 4096, 1000),
-      (257, 256, 32000, 100)]
+      (257, 256, 32000, 100), (70, 64, 104, 1), (700, 128, 520, 100)]
 
 
 def lm_inputs(n, d, v, seed=4):
