@@ -238,7 +238,7 @@ __device__ __forceinline__ void epi_glu(const GemmParams& p, int row, int j,
 // store instruction writes whole 128-byte lines of four rows: value(y, col) turns
 // 32 accumulators of the lane's row into results.  Stored from the
 // accumulators' rows, 16 bytes of 32 rows at a time, the stores outlast short
-// products (the logits' gradient of 4095 x 2048 x 32000: 388 us, so 300).
+// products (the logits' gradient of 4095 x 2048 x 32000: 388 us, so 305).
 // N and ldc multiples of 8, C 16-byte aligned; stage: 32 rows of kStageRow bytes.
 constexpr int kStageRow = 128 + 16;
 template <int BN, class F>
