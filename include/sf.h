@@ -696,8 +696,9 @@ int64_t sf_op_lm_logprob_workspace_bytes(int64_t n, int32_t v, int64_t chunk_row
  * dz of sf_op_logprob_rows_bwd, dh bf16 [n, d] = dz W and dw bf16 [v, d] = dz^T h,
  * fp32 sums rounded once.  workspace: sf_op_lm_logprob_bwd_workspace_bytes(n, d,
  * v, chunk_rows) bytes (-1 for bad sizes), 256-byte aligned: 6 for each logit of
- * a chunk, which hold three chunks' dz at a time, and, where n > chunk_rows, the
- * fp32 sum of dw. */
+ * a chunk (of 128 rows at least), which hold three chunks' dz at a time, and, where
+ * n is more than a chunk, the fp32 sum of dw; for n up to 128 room for what dz's
+ * rounding left, which then enters both products too, and 12 n d bytes. */
 int sf_op_lm_logprob_bwd(const uint16_t* h, const uint16_t* w, const int32_t* tokens, int64_t n,
                          int32_t d, int32_t v, float scale, int64_t chunk_rows, const float* lse,
                          const float* entropy, const float* dlogp, const float* dentropy,

@@ -242,8 +242,8 @@ __device__ __forceinline__ void epi_glu(const GemmParams& p, int row, int j,
 // N and ldc multiples of 8, C 16-byte aligned; stage: 32 rows of kStageRow bytes.
 constexpr int kStageRow = 128 + 16;
 template <int BN, class F>
-__device__ __forceinline__ void epi_staged(const GemmParams& p, uint32_t taddr, int row0, int col0, uint8_t* stage,
-                                           F value) {
+__device__ __forceinline__ void epi_staged(const GemmParams& p, void* C, uint32_t taddr, int row0, int col0,
+                                           uint8_t* stage, F value) {
   const int lane = threadIdx.x & 31;
   for (int c = 0; c < BN && col0 + c < p.N; c += 64) {
     const int col = col0 + c;
@@ -269,7 +269,7 @@ __device__ __forceinline__ void epi_staged(const GemmParams& p, uint32_t taddr, 
     for (int i = 0; i < 8; ++i) {
       const int r = 4 * i + (lane >> 3);
       if (row0 + r < p.M && col + 8 * piece < p.N)
-        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.C) + (int64_t)(row0 + r) * p.ldc + col +
+        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(C) + (int64_t)(row0 + r) * p.ldc + col +
                                   8 * piece) = *reinterpret_cast<const uint4*>(stage + r * kStageRow + 16 * piece);
     }
     __syncwarp();
@@ -683,10 +683,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         RowGrad g = {};
         g.zero = true;
         if (row < p.M) g = row_grad(p.lp, row, p.N, p.err);
-        epi_staged<BN>(p, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
+        epi_staged<BN>(p, p.C, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
                        [&](float (&y)[32], int col) { logit_grads(g, y, col); });
+        if (p.lp.low)  // what the rounding left
+          epi_staged<BN>(p, p.lp.low, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
+                         [&](float (&y)[32], int col) {
+                           logit_grads(g, y, col);
+#pragma unroll
+                           for (int j = 0; j < 32; ++j) y[j] -= __bfloat162float(__float2bfloat16_rn(y[j]));
+                         });
       } else if constexpr (EPI == kEpiBF16Acc) {
-        epi_staged<BN>(p, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
+        epi_staged<BN>(p, p.C, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
                        [&](float (&y)[32], int col) {
                          if (!p.R || row >= p.M) return;
                          float x[32];

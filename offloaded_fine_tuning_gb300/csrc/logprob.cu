@@ -493,6 +493,23 @@ static RowShape row_shape(int64_t rows, int vocab) {
   return {1024, n};
 }
 
+__global__ void __launch_bounds__(kThreads)
+    add_halves_kernel(const float* __restrict__ x, bf16* __restrict__ y, int64_t n) {
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
+  if (i >= n) return;
+  float a[8], b[8];
+  load8(x + i, a);
+  load8(x + n + i, b);
+  Eight<bf16> o;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o.v[j] = __float2bfloat16_rn(a[j] + b[j]);
+  *reinterpret_cast<Eight<bf16>*>(y + i) = o;
+}
+
+void add_halves_bf16(const float* x, bf16* y, int64_t n, cudaStream_t st) {
+  add_halves_kernel<<<(unsigned)((n + 8 * kThreads - 1) / (8 * kThreads)), kThreads, 0, st>>>(x, y, n);
+}
+
 template <typename T, bool ENT, int NT>
 static bool logprob_rows_as(const T* z, int64_t ld, const int32_t* tokens, int64_t rows, int vocab, float scale,
                             float* logp, float* lse, float* entropy, int top, int32_t* ids, float* top_logp, int* err,

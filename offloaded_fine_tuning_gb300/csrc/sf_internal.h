@@ -52,13 +52,15 @@ enum GemmEpi : int {
 
 // Rows' tokens and scale for the log probabilities (sf.h); backward: lse,
 // entropy, dlogp, dentropy (may be null, and entropy with it).  parts and
-// token_logit are written by kEpiLogprob and read by logprob_tiles.
+// token_logit are written by kEpiLogprob and read by logprob_tiles; low, unless it
+// is null, gets what the rounding of a kEpiLogprobBwd product's C left, as bf16.
 struct LogprobEpi {
   const int32_t* tokens = nullptr;
   float scale = 1.f;
   const float *lse = nullptr, *entropy = nullptr, *dlogp = nullptr, *dentropy = nullptr;
   float4* parts = nullptr;
   float* token_logit = nullptr;
+  __nv_bfloat16* low = nullptr;
 };
 
 struct GemmArgs {
@@ -307,6 +309,9 @@ void logprob_rows_bwd(const void* z, bool f32, int64_t ld, const LogprobEpi& a, 
 // left for `tiles` tiles.  Call it right after that launch.  False: no launch.
 bool logprob_tiles(const LogprobEpi& a, int64_t rows, int tiles, int vocab, float* logp,
                    float* lse, float* entropy, int* err, cudaStream_t st);
+
+// y[i] = bf16(x[i] + x[n + i]), n a multiple of 8.
+void add_halves_bf16(const float* x, __nv_bfloat16* y, int64_t n, cudaStream_t st);
 
 int num_sms();
 

@@ -130,9 +130,10 @@ def test_lm_logprob_backward_refuses(sf, bad):
 def test_lm_logprob_workspaces(sf):
     assert sf.lm_logprob_workspace_bytes(1000, 104, 300) == 300 * 104 * 4 // 256 * 256 + 256
     assert sf.lm_logprob_workspace_bytes(64, 128, 1 << 40) == 64 * 128 * 4
-    whole = sf.lm_logprob_bwd_workspace_bytes(64, 32, 128, 64)
-    assert whole == 64 * 128 * 6  # one chunk: no sum of dw
-    assert sf.lm_logprob_bwd_workspace_bytes(65, 32, 128, 64) == whole + 128 * 32 * 4
+    assert sf.lm_logprob_bwd_workspace_bytes(64, 32, 128, 1) == 64 * 128 * 6 + 64 * 32 * 12  # few rows: one chunk
+    whole = sf.lm_logprob_bwd_workspace_bytes(256, 32, 128, 256)
+    assert whole == 256 * 128 * 6  # one chunk: no sum of dw
+    assert sf.lm_logprob_bwd_workspace_bytes(257, 32, 128, 256) == whole + 128 * 32 * 4
     for bad in ((0, 104, 2), (4, 100, 2), (4, 104, 0), (4, 2 ** 24 + 8, 2), (2 ** 31, 104, 2)):
         assert sf.lm_logprob_workspace_bytes(*bad) == -1
         assert sf.lm_logprob_bwd_workspace_bytes(bad[0], 64, *bad[1:]) == -1

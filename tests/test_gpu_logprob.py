@@ -376,7 +376,7 @@ def test_rows_gradient_against_differences():
 
 # ------------------------------------------------------------------ the head
 LM = [(1, 8, 8, 1), (5, 64, 104, 2), (130, 136, 520, 64), (300, 384, 3000, 128), (129, 512, 4096, 1000),
-      (257, 256, 32000, 100), (70, 64, 104, 1), (700, 128, 520, 100)]
+      (257, 256, 32000, 100), (70, 64, 104, 1), (700, 128, 520, 100), (128, 1024, 512, 7), (128, 64, 20000, 500)]
 
 
 def lm_inputs(n, d, v, seed=4):
@@ -437,9 +437,9 @@ def test_lm_logprob_backward(n, d, v, chunk, entropy):
                                 ws.data_ptr(), dh.data_ptr(), dw.data_ptr(), stream=stream()) == 0
     sync()
     dz, size_z, lp = gradient(z, v, tokens, scale, lse.double(), ent.double(), dl.double(), de.double())
-    # dz's bf16 rounding, the exponential, the logit's error in p and in log p
+    # dz's bf16 rounding (up to 128 rows what it leaves is kept), the exponential, the logit's error in p and in log p
     te = lm_errors(h, w, scale)[:, None]
-    ez = BF * dz.abs() + (2.0 ** -20 + 4 * U * lp.abs() + 2 * te) * size_z + te * (scale * de.abs().double()[:, None] * torch.exp(lp))
+    ez = (BF * BF if n <= 128 else BF) * dz.abs() + (2.0 ** -20 + 4 * U * lp.abs() + 2 * te) * size_z + te * (scale * de.abs().double()[:, None] * torch.exp(lp))
     f32 = 2.0 ** -18
     ref = dz @ w.double()
     near(dh[:n], ref, BF * ref.abs() + ez @ w.double().abs() + f32 * (dz.abs() @ w.double().abs()))
