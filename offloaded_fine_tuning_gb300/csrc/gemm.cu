@@ -238,30 +238,41 @@ __device__ __forceinline__ void epi_glu(const GemmParams& p, int row, int j,
 // store instruction writes whole 128-byte lines of four rows: value(y, col) turns
 // 32 accumulators of the lane's row into results.  Stored from the
 // accumulators' rows, 16 bytes of 32 rows at a time, the stores outlast short
-// products (the logits' gradient of 4095 x 2048 x 32000: 388 us, so 305).
+// products (the logits' gradient of 4095 x 2048 x 32000: 388 us, so 305).  The
+// next columns' accumulators arrive while these are stored.  UNROLL: of the loop
+// over the columns.  Unrolled, the 128256 x 4096 stores of a product over 32 rows
+// take 281 us (a fill of as many bytes 263), 303 us as a loop; the logits'
+// gradient is 32 exponentials a turn, and unrolled its code is too long (16 x 4096
+// x 128256: 195 us, 185 as a loop).
 // N and ldc multiples of 8, C 16-byte aligned; stage: 32 rows of kStageRow bytes.
 constexpr int kStageRow = 128 + 16;
-template <int BN, class F>
+template <int BN, int UNROLL, class F>
 __device__ __forceinline__ void epi_staged(const GemmParams& p, void* C, uint32_t taddr, int row0, int col0,
                                            uint8_t* stage, F value) {
   const int lane = threadIdx.x & 31;
-  for (int c = 0; c < BN && col0 + c < p.N; c += 64) {
+  uint32_t r[2][32];
+  tmem_ld_32x32b_x32(taddr, r[0]);
+  tmem_ld_32x32b_x32(taddr + 32, r[1]);
+#pragma unroll UNROLL
+  for (int c = 0; c < BN; c += 64) {
     const int col = col0 + c;
+    tmem_ld_wait();  // before the way out, too
+    if (col >= p.N) break;  // uniform across the warp
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      if (col + 32 * half >= p.N) break;  // uniform across the warp
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(taddr + c + 32 * half, r);
-      tmem_ld_wait();
       float y[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]) * p.alpha;
-      value(y, col + 32 * half);
+      for (int j = 0; j < 32; ++j) {
+        asm volatile("" : "+r"(r[half][j]));  // not before the wait
+        y[j] = __uint_as_float(r[half][j]) * p.alpha;
+      }
+      if (col + 32 * half < p.N) value(y, col + 32 * half);
       uint4* to = reinterpret_cast<uint4*>(stage + lane * kStageRow + 64 * half);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         to[q] = make_uint4(pack_bf16x2(y[8 * q], y[8 * q + 1]), pack_bf16x2(y[8 * q + 2], y[8 * q + 3]),
                            pack_bf16x2(y[8 * q + 4], y[8 * q + 5]), pack_bf16x2(y[8 * q + 6], y[8 * q + 7]));
+      if (c + 64 < BN) tmem_ld_32x32b_x32(taddr + c + 64 + 32 * half, r[half]);
     }
     __syncwarp();
     const int piece = lane & 7;  // of 8 columns, there or not as a whole
@@ -683,17 +694,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         RowGrad g = {};
         g.zero = true;
         if (row < p.M) g = row_grad(p.lp, row, p.N, p.err);
-        epi_staged<BN>(p, p.C, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
+        epi_staged<BN, 1>(p, p.C, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
                        [&](float (&y)[32], int col) { logit_grads(g, y, col); });
         if (p.lp.low)  // what the rounding left
-          epi_staged<BN>(p, p.lp.low, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
+          epi_staged<BN, 1>(p, p.lp.low, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
                          [&](float (&y)[32], int col) {
                            logit_grads(g, y, col);
 #pragma unroll
                            for (int j = 0; j < 32; ++j) y[j] -= __bfloat162float(__float2bfloat16_rn(y[j]));
                          });
       } else if constexpr (EPI == kEpiBF16Acc) {
-        epi_staged<BN>(p, p.C, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
+        epi_staged<BN, BN / 64>(p, p.C, taddr, row - lane, tn * BN, &stage_rows[quarter * 32 * kStageRow],
                        [&](float (&y)[32], int col) {
                          if (!p.R || row >= p.M) return;
                          float x[32];
