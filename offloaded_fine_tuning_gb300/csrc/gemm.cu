@@ -59,6 +59,7 @@ struct GemmParams {
   float* ws;
   int64_t ws_stride;
   LogprobEpi lp;              // kEpiLogprob, kEpiLogprobBwd
+  bool planes;                // A's map has three dimensions (see few_rows_map)
 };
 
 // Output columns of one work unit: the gated tile computes a and b for 128
@@ -522,7 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kBM / 64; ++j) tma_load_2d_pair(a_dst + j * 8192, &tmA, fb, m0 + 64 * j, k0);
           } else {
-            tma_load_2d_pair(a_dst, &tmA, fb, k0, m0);
+            if (p.planes) tma_load_3d_pair(a_dst, &tmA, fb, k0, m0, 0);
+            else tma_load_2d_pair(a_dst, &tmA, fb, k0, m0);
           }
           constexpr int HB = BN / 2;  // this CTA's half of B
           if constexpr (B_MN) {
@@ -543,7 +545,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kBM / 64; ++j) tma_load_2d(a_dst + j * 8192, &tmA, full_bar(stage), m0 + 64 * j, k0);
         } else {
-          tma_load_2d(a_dst, &tmA, full_bar(stage), k0, m0);
+          if (p.planes) tma_load_3d(a_dst, &tmA, full_bar(stage), k0, m0, 0);
+          else tma_load_2d(a_dst, &tmA, full_bar(stage), k0, m0);
         }
         if constexpr (B_MN) {
 #pragma unroll
@@ -770,17 +773,27 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // 2-D bf16 tensor map over a row-major [rows, cols] matrix with row stride ld
 // (elements), box [box_rows, 64] with the 128-byte swizzle.
 static bool make_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld,
-                     int box_cols, int box_rows) {
+                     int box_cols, int box_rows, int64_t planes = 0) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
-  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+  cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)(rows * ld * 2)};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, const_cast<void*>(base), dims, strides,
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// The planes of the map of a K-major A of few rows, or 0 for a map without them.
+// Tiles of a map over less than 128 KB load slowly (a product of 128256 columns,
+// K = 4096: 15 rows 248 us, 16 rows 173 us; K = 8192: 7 rows 478 us, 8 rows 339 us),
+// so such a matrix gets a third dimension that makes the map larger; only its first
+// plane, the matrix, is ever loaded.
+static int64_t few_rows_map(int64_t rows, int64_t cols) {
+  const int64_t small = 128 << 10, bytes = rows * cols * 2;
+  return bytes < small ? (small + bytes - 1) / bytes : 0;
 }
 
 // CTAs per cluster: the wide tiles run as cta_group::2 pair MMAs.
@@ -1044,8 +1057,9 @@ int gemm(const GemmArgs& a, int* dev_err, cudaStream_t st, char* why) {
   const bool gated = (a.epi == kEpiGLU);
   const int BN = gated ? 256 : gemm_tile_cols(a.N);
   CUtensorMap ta, tb, tb2;
+  const int64_t planes = a_mn ? 0 : few_rows_map(a.M, a.K);
   bool ok = a_mn ? make_map(&ta, a.A, a.M, a.K, a.lda, 64, 64)
-                 : make_map(&ta, a.A, a.K, a.M, a.lda, 64, kBM);
+                 : make_map(&ta, a.A, a.K, a.M, a.lda, 64, kBM, planes);
   // with clusters each CTA loads half of a K-major B tile; the gated tile's
   // halves are the gate rows [0, N) and the up rows [N, 2N) of B
   ok = ok && (b_mn ? make_map(&tb, a.B, a.N, a.K, a.ldb, 64, 64)
@@ -1066,7 +1080,7 @@ int gemm(const GemmArgs& a, int* dev_err, cudaStream_t st, char* why) {
   GemmParams p{(int)a.M, (int)a.N, (int)a.K, a.C, a.ldc, a.R, a.ldr, a.alpha, dev_err,
                reinterpret_cast<const __nv_bfloat16*>(a.bias), a.cs, a.seq, a.rope_cols, a.hd,
                a.aux, a.ldaux, unit_order(a.M, a.N, a.K, BN, gated), splitk, a.ws, a.M * a.ldc,
-               a.lp};
+               a.lp, planes > 0};
   int rc;
   if (BN == 256) {
     if (a.layout == kNT) rc = launch_epi<false, false, 256>(a.epi, ta, tb, tb2, p, st, why);
