@@ -57,7 +57,9 @@ struct Octet<false> {
 // Instructions bound it as much as memory: 16384 x 4096 bf16 takes 45.9 us (5,850
 // GB/s, 0.86 of a copy's rate), about 14 instructions an element, half of them the
 // generator's.
-template <bool F32>
+// DROP false: bf16 with p = 0, a copy without the generator (42.8 us; fp32 with
+// p = 0 gains nothing without it).
+template <bool F32, bool DROP>
 __global__ void __launch_bounds__(kDropThreads)
     dropout_kernel(const void* x, void* y, int64_t n, DropArgs a) {
   constexpr int SIZE = F32 ? 4 : 2;
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(kDropThreads)
   for (int u = 0; u < 2; ++u) {
     const int64_t octet = first + u * kDropThreads, at = octet * 8;
     if (at >= n) return;
-    const Words w = philox((uint64_t)octet, offset, a.seed);
+    const Words w = DROP ? philox((uint64_t)octet, offset, a.seed) : Words{};
     if (at + 8 <= n) {
       o[u].v.drop(w, a);
       *reinterpret_cast<Stored*>(static_cast<char*>(y) + at * SIZE) = o[u];
@@ -220,8 +222,8 @@ void join_fwd_as(const JoinArgs& a, const float* x, const void* h, bool h32, flo
 
 void dropout(const void* x, void* y, bool f32, int64_t n, const DropArgs& a, cudaStream_t st) {
   const unsigned grid = (unsigned)((n + 16 * kDropThreads - 1) / (16 * kDropThreads));
-  if (f32) dropout_kernel<true><<<grid, kDropThreads, 0, st>>>(x, y, n, a);
-  else dropout_kernel<false><<<grid, kDropThreads, 0, st>>>(x, y, n, a);
+  auto* kernel = f32 ? dropout_kernel<true, true> : a.top ? dropout_kernel<false, true> : dropout_kernel<false, false>;
+  kernel<<<grid, kDropThreads, 0, st>>>(x, y, n, a);
 }
 
 void join_fwd(const JoinArgs& a, const float* x, const void* h, bool h32, float* xout, bf16* y,
