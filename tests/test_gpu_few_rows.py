@@ -15,6 +15,7 @@ from tests.gpu_util import stream, sync
 
 pytestmark = pytest.mark.gpu
 sf = pytest.importorskip("offloaded_fine_tuning_gb300")
+F32 = dict(dtype=torch.float32, device="cuda")  # another test module changes the default type
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -27,7 +28,7 @@ def _lib():
 
 def product(layout, a, b, rows, N, K):
     """The fp32 product of a's first rows, and 64 elements behind it."""
-    c = torch.full((rows * N + 64,), 7.0, device="cuda")
+    c = torch.full((rows * N + 64,), 7.0, **F32)
     assert sf.op_gemm(layout, 1, rows, N, K, a.data_ptr(), a.shape[1], b.data_ptr(), b.shape[1], c.data_ptr(), N,
                       stream=stream()) == 0
     sync()
@@ -41,12 +42,12 @@ def product(layout, a, b, rows, N, K):
 def test_products_of_few_rows(layout, rows, N, K):
     g = torch.Generator(device="cuda").manual_seed(rows + N + K)
     many = max(rows + 8, 65536 // K + 1)
-    full = torch.randn(many, K + 8, generator=g, device="cuda").bfloat16()
+    full = torch.randn(many, K + 8, generator=g, **F32).bfloat16()
     full[:, K:] = math.nan  # between the rows
     few = full.clone()
     few[rows:] = math.nan   # behind them
     shape = (N, K) if layout == "NT" else (K, N)
-    b = torch.randn(*shape, generator=g, device="cuda").bfloat16()
+    b = torch.randn(*shape, generator=g, **F32).bfloat16()
     got = product(getattr(sf, layout), few, b, rows, N, K)
     assert torch.equal(got, product(getattr(sf, layout), full, b, many, N, K)[:rows])
     a, b = few[:rows, :K].double(), (b.t() if layout == "NT" else b).double()
@@ -59,17 +60,17 @@ def test_products_of_few_rows(layout, rows, N, K):
 def test_head_of_few_rows(n, top):
     d, v, many = 4096, 2056, 64
     g = torch.Generator(device="cuda").manual_seed(n)
-    w = torch.randn(v, d, generator=g, device="cuda").bfloat16()
-    full = (torch.randn(many, d, generator=g, device="cuda") * 0.02).bfloat16()
+    w = torch.randn(v, d, generator=g, **F32).bfloat16()
+    full = (torch.randn(many, d, generator=g, **F32) * 0.02).bfloat16()
     few = full.clone()
     few[n:] = math.nan
     tokens = torch.randint(0, v, (many,), generator=g, device="cuda", dtype=torch.int32)
 
     def call(h, rows):
         ws = torch.empty(sf.lm_logprob_workspace_bytes(rows, v, rows), dtype=torch.uint8, device="cuda")
-        logp, lse, ent = (torch.empty(rows, device="cuda") for _ in range(3))
+        logp, lse, ent = (torch.empty(rows, **F32) for _ in range(3))
         ids = torch.empty(rows, max(top, 1), dtype=torch.int32, device="cuda")
-        top_logp = torch.empty(rows, max(top, 1), device="cuda")
+        top_logp = torch.empty(rows, max(top, 1), **F32)
         assert sf.op_lm_logprob(h.data_ptr(), w.data_ptr(), tokens.data_ptr(), rows, d, v, 1.0, rows, ws.data_ptr(),
                                 logp.data_ptr(), lse.data_ptr(), ent.data_ptr(), top, ids.data_ptr() if top else 0,
                                 top_logp.data_ptr() if top else 0, stream=stream()) == 0
@@ -93,7 +94,7 @@ def test_head_of_few_rows(n, top):
 @pytest.mark.parametrize("n", [1, 7, 8, 9, 2047, 4096, 4097, 100003])
 def test_dropout_that_drops_nothing(n, kind):
     dtype, code = (torch.bfloat16, sf.BF16) if kind == "bf16" else (torch.float32, sf.F32)
-    x = torch.randn(n, device="cuda").to(dtype)
+    x = torch.randn(n, **F32).to(dtype)
     x[n // 2] = math.inf
     y = torch.full((n + 16,), 7.0, dtype=dtype, device="cuda")
     step = torch.ones(1, dtype=torch.int64, device="cuda")
