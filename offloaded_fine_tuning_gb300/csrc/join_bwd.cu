@@ -232,7 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return unpack4(reinterpret_cast<const uint2*>(st + r.h)[k * NT + tid]);
     };
     const float r2 = stats[0], r1 = post ? stats[1] : 1.f;
-    // dres + r2 g_next dy of quad k; its kept elements of h w (top 0 keeps all)
+    // dres + r2 g_next dy of quad k; the kept elements of a quad (top 0 keeps all).
+    // What comes back to a dropped element counts as 0 in the sums whatever it is
+    // (0 times infinity would not), so it is masked itself
     auto known = [&](int k) {
       float4 o = sdr[k * NT];
       if (!dres) o = zero;
@@ -249,13 +251,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         v[0] += dot(p, unpack4(gn[k]));
         if (post) {
           const float4 hw = keep(k, mul(load_hh(k), w[k]));
-          v[1] += dot(hw, known(k));
+          v[1] += dot(hw, keep(k, known(k)));
           v[2] += dot(hw, x);
         }
       }
     } else if (post) {
 #pragma unroll
-      for (int k = 0; k < Q; ++k) v[1] += dot(keep(k, mul(load_hh(k), w[k])), sdr[k * NT]);
+      for (int k = 0; k < Q; ++k) v[1] += dot(mul(load_hh(k), w[k]), keep(k, sdr[k * NT]));
     }
     if (next || post) row_sums(v);
     const float c1 = next ? v[0] / a.d * r2 * r2 * r2 : 0.f;  // in this order: r2^3 alone may overflow
