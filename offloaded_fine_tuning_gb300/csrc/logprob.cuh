@@ -15,6 +15,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 // What a difference of logits is cut to where it multiplies a weight: its
 // weight is exp(scale * kFar) = 0 for every scale allowed, and 0 * kFar is 0.
 constexpr float kFar = -1e30f;
+// What a log probability is cut to where it multiplies its p in a gradient: p is 0
+// from -88 on (fp32 without denormals), and the product with the entropy's
+// gradient stays finite however large that is (kFar would not: a loss scaled by 2^20
+// and a scale of 2^10 already gave 0 times infinity at masked logits).
+constexpr float kNoWeight = -128.f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -131,7 +136,7 @@ __device__ __forceinline__ void logit_grads(const RowGrad& g, float (&f)[N], int
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     const float lp = fmaf(f[j], g.scale, -g.lse), p = exp2_fast(lp * kLog2e);
-    f[j] = p * fmaf(g.slope, fmaxf(lp, kFar), g.base);
+    f[j] = p * fmaf(g.slope, fmaxf(lp, kNoWeight), g.base);
   }
   const int hot = g.token - at;
   if (hot >= 0 && hot < N) {
