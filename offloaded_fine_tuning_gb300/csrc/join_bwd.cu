@@ -354,17 +354,24 @@ __global__ void __launch_bounds__(16 * kSumGroups)
 struct BwdShape {
   int lanes, quads, ctas;
 };
-BwdShape bwd_shape(int d, bool h32, bool plain) {
+// Whether a row of 2,049 to 4,096 columns of bf16 h has a CTA to itself (two quads for
+// each of 512 threads) rather than half of one (four for 256): where its traffic hides
+// a row's chain, that is with a second norm (dy and xout to read), no dropout and few
+// quads beyond the row.  16384 rows, us alone and in halves: with a norm after the
+// block 2304 columns 186 and 158, 3584 199 and 193, 3648 200 and 197, 3712 200 and 204,
+// 4096 207 and 225; without it 2304 158 and 125, 3200 166 and 165, 3264 167 and 169,
+// 4096 190 and 207.  4096 columns with dropout 240 and 211 (without a norm after the
+// block 215 and 224), without a second norm 190 and 159, 157 and 128 without dropout.
+// Near the borders 3000 rows differ by 8% either way.
+bool row_alone(const JoinArgs& a) { return a.g_next && !a.drop.top && a.d > (a.g_post ? 3648 : 3200); }
+
+BwdShape bwd_shape(int d, bool h32, bool alone) {
   const int few = h32 ? 2 : 4, most = h32 ? 3 : 4;
   for (int q = 1; q < few; q *= 2)
     if (32 * q * 4 >= d) return {32, q, 1};
   int n = 32;
   while (n < kThreads && n * few * 4 < d) n *= 2;
-  // one row at a time where its traffic hides a row's chain: with a second norm
-  // (dy and xout to read) and no dropout (16384 x 4096: 208 us with 512 threads of
-  // two quads, 224 with two groups of 256 of four; with dropout 240 and 219,
-  // without a second norm 174 and 154)
-  if (!h32 && plain && n == 256) return {512, 2, 1};
+  if (!h32 && alone && n == 256) return {512, 2, 1};
   for (int c = 1;; c *= 2)
     for (int q = c == 1 ? few : 2; q <= most; ++q)
       if (c * n * q * 4 >= d) return {n, q, c};
@@ -489,7 +496,7 @@ bool join_bwd(const JoinArgs& a, const float* xout, const void* h, bool h32, con
               const float* rstd_next, const float* dy, const float* dres, float* dx, void* dh,
               bf16* dg_post, bf16* dgate, bf16* dg_next, float* part, int* err, cudaStream_t st) {
   if (!dg_post && !dgate && !dg_next) part = nullptr;
-  const BwdShape s = bwd_shape(a.d, h32, a.g_next && !a.drop.top);
+  const BwdShape s = bwd_shape(a.d, h32, row_alone(a));
   const BwdCall c = {a, xout, h, rstd_post, rstd_next, dy, dres, dx, dh, part, err, st};
   const int parts = h32 ? launch_bwd_for<true>(s, c) : launch_bwd_for<false>(s, c);
   if (parts && part)
