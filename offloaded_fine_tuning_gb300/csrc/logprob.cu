@@ -65,6 +65,27 @@ constexpr int kList = 512;    // candidates that a CTA holds
 constexpr int kGroups = 64;   // sets of threads whose maxima bound the alternatives
 constexpr int kMaxCluster = 8;
 
+// keep_others for the sums of a warp of which lane l has added octets first + l,
+// first + l + STEP, ... below end, with `mine` the largest logit of a lane (perhaps
+// one that belongs to no octet).  The lanes look for the octet among those of the lane
+// that holds the maximum: remembered with each new maximum it costs every row
+// (16384 x 4096 fp32 90 us, 81 so; 4096 x 128256 bf16 210 and 204).
+template <int STEP, typename T>
+__device__ __forceinline__ void keep_others_of_warp(Sums& a, float mine, const T* zr, int first, int end, float c) {
+  const uint32_t owner = __ballot_sync(0xffffffffu, mine == a.m);  // one lane, or S would be 2
+  if (!__any_sync(0xffffffffu, a.s < kAlone) || owner == 0) return;
+  Sums alone = {a.m, 0.f, 0.f, 0.f};
+  for (int i = first + __ffs(owner) - 1 + (threadIdx.x & 31) * STEP; i < end; i += 32 * STEP) {
+    float f[8];
+    load8(zr + 8 * i, f);
+    float m = f[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = fmaxf(m, f[j]);
+    if (m == a.m) keep_others(alone, f, c);
+  }
+  a.low += warp_sum(alone.low);
+}
+
 // The places that the entries of a list would have were it in order: four
 // neighbouring threads count for an entry, and what() gets it with its place.
 template <int NT, class F>
@@ -154,6 +175,7 @@ __global__ void __launch_bounds__(NT, NT == 256 || NT == 512 ? 1536 / NT : 1)
   }
   const float mine = a.s == 0.f ? minus_inf : a.m;  // s is at least 1 with any logit above -inf
   a = warp_merge(a, c);
+  keep_others_of_warp<NT>(a, mine, zr, lo + warp * 32, hi, c);
   if (lane == 0) part[warp] = a;
   if (top > 0) {
     float group = mine;
@@ -270,11 +292,14 @@ __global__ void __launch_bounds__(NT, NT == 256 || NT == 512 ? 1536 / NT : 1)
 }
 
 // Short rows: a warp takes a row, without barriers, and reads it twice where
-// alternatives are wanted (the second time from L1).  Their bound is the top-th of
+// alternatives are wanted (the second time from L1 or L2).  Their bound is the top-th of
 // 64 maxima, two a lane: sorted in two runs of 32 by bitonic exchanges, of which
 // the larger of each pair in opposite order are the 32 largest.  16384 x 500 with
 // 20 alternatives: 25 us; 73 us with 64 threads a row, whose barriers and CTA starts
-// outlast the row.
+// outlast the row.  Five CTAs an SM for fp32, six for bf16: left to itself the compiler
+// has fewer of fp32's loads in flight, and six CTAs' rows do not stay in L2 for the
+// second reading (16384 x 4096, 20 alternatives: 91 us so, 81 with five; bf16 69 with
+// five, 67 with six).
 constexpr int kShortList = 128;  // candidates that a warp holds
 
 // The lanes' values in falling order.
@@ -294,7 +319,7 @@ __device__ __forceinline__ float warp_sort(float v, int from) {
 }
 
 template <typename T, bool ENT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 5 : 6)
     logprob_short_kernel(const T* __restrict__ z, int64_t ld, const int32_t* __restrict__ tokens, int64_t rows,
                          int vocab, float scale, float* __restrict__ logp, float* __restrict__ lse_out,
                          float* __restrict__ entropy, int top, int32_t* __restrict__ ids,
@@ -322,6 +347,7 @@ __global__ void __launch_bounds__(kThreads)
     max_a = fmaxf(max_a, f[0]);
   }
   a = warp_merge(a, c);
+  keep_others_of_warp<32>(a, fmaxf(max_a, max_b), zr, 0, n8, c);
   const RowStats r = row_stats(a, scale);
   if (lane == 0) {
     int token = tokens[row];

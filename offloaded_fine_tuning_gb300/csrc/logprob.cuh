@@ -54,6 +54,15 @@ __device__ __forceinline__ Sums merge(Sums a, Sums b, float c) {
   a.t += b.t;
   return a;
 }
+// The sum of N terms.
+template <int N>
+__device__ __forceinline__ float tree(float (&e)[N]) {
+#pragma unroll
+  for (int w = N / 2; w > 0; w /= 2)
+#pragma unroll
+    for (int j = 0; j < w; ++j) e[j] += e[j + w];
+  return e[0];
+}
 // N logits at once: one look at the maximum, and a tree of their exponentials.
 // Returns their maximum.
 template <bool ENT, int N>
@@ -69,12 +78,23 @@ __device__ __forceinline__ float add(Sums& a, const float (&z)[N], float c) {
     e[j] = exp2_fast(x * c);
     if (ENT) a.t = fmaf(e[j], fmaxf(x, kFar), a.t);
   }
-#pragma unroll
-  for (int w = N / 2; w > 0; w /= 2)
-#pragma unroll
-    for (int j = 0; j < w; ++j) e[j] += e[j + w];
-  add_sum(a, e[0]);
+  add_sum(a, tree(e));
   return m;
+}
+// Where a maximum stands alone (its exponential is 1), the tree of its group has
+// rounded the group's others beside it, and others are all that log S has.  a.low gets
+// the difference, from the logits z of that group, where S is below kAlone; from there
+// on the trees lose at most log2(N) 2^-16 of the others.
+constexpr float kAlone = 1.f + 1.f / 256;
+template <int N>
+__device__ __forceinline__ void keep_others(Sums& a, const float (&z)[N], float c) {
+  float e[N], others = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    e[j] = exp2_fast((z[j] - a.m) * c);
+    others += e[j] == 1.f ? 0.f : e[j];
+  }
+  a.low += others - (tree(e) - 1.f);
 }
 
 // What a row's sums give.
