@@ -474,11 +474,11 @@ int launch_bwd_for(const BwdShape& s, const BwdCall& c) {
       default: return launch_bwd<H32, 512, Q, 1>(c);
     }
   }
-  if (s.ctas == 2) {
-    if (s.quads == 3) return launch_bwd<H32, 512, 3, 2>(c);
-    return launch_bwd<H32, 512, Q, 2>(c);
+  if (s.quads == 3) return launch_bwd<H32, 512, 3, 2>(c);
+  if constexpr (H32) {
+    if (s.ctas == 4) return launch_bwd<H32, 512, 2, 4>(c);
   }
-  return launch_bwd<H32, 512, 2, H32 ? 4 : 2>(c);
+  return launch_bwd<H32, 512, Q, 2>(c);
 }
 
 }  // namespace
