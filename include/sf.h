@@ -694,7 +694,7 @@ int64_t sf_op_lm_logprob_workspace_bytes(int64_t n, int32_t v, int64_t chunk_row
 
 /* Backward of sf_op_lm_logprob (the logits are recomputed and not stored): with
  * dz of sf_op_logprob_rows_bwd, dh bf16 [n, d] = dz W and dw bf16 [v, d] = dz^T h,
- * fp32 sums rounded once.  workspace: sf_op_lm_logprob_bwd_workspace_bytes(n, d,
+ * fp32 sums rounded once; dh may not be h.  workspace: sf_op_lm_logprob_bwd_workspace_bytes(n, d,
  * v, chunk_rows) bytes (-1 for bad sizes), 256-byte aligned: 6 for each logit of
  * a chunk (of 128 rows at least), which hold three chunks' dz at a time, and, where
  * n is more than a chunk, the fp32 sum of dw; for n up to 128 room for what dz's

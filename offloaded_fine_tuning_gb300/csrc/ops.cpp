@@ -701,6 +701,7 @@ int sf_op_lm_logprob_bwd(const uint16_t* h, const uint16_t* w, const int32_t* to
   if (!h || !w || !tokens || !workspace || !dh || !dw || !al16(h) || !al16(w) || !al1(tokens) || !al16(dh) ||
       !al16(dw) || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return SF_EINVAL;
+  if (dh == h) return SF_EINVAL;  // dw's product reads h after dh is written
   if (!logprob_gradients(lse, entropy, dlogp, dentropy)) return SF_EINVAL;
   int* err = dev_err_word();
   if (!err) return SF_ECUDA;
