@@ -55,8 +55,8 @@ struct Octet<false> {
 
 // Two octets of elements a thread, loaded before their bits are drawn.
 // Instructions bound it as much as memory: 16384 x 4096 bf16 takes 45.9 us (5,850
-// GB/s, 0.86 of a copy's rate), about 14 instructions an element, half of them the
-// generator's.
+// GB/s, 0.86 of a copy's rate), about 18 instructions an element, 5 of them the
+// generator's multiplications and logic.
 // DROP false: bf16 with p = 0, a copy without the generator (42.8 us; fp32 with
 // p = 0 gains nothing without it).
 template <bool F32, bool DROP>

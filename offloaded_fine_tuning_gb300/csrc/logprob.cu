@@ -114,8 +114,10 @@ __device__ __forceinline__ void places(const Logit* list, int n, F what) {
 // threads' whole ranges read again, which L2 no longer holds, 314 us so).  Where
 // more reach it than the list holds (equal logits, masked rows), the top-th of
 // those that it does hold is the next bound.  Each such round leaves out at
-// least kList - top of them, and the low ids come first, so that rows of one
-// value end in two.
+// least kList - top of them; which ones the list held follows from the order of the
+// atomics, what is left in the end does not.  A round reads what still reaches the
+// bound again: 4096 x 128256 fp32 with one value, or with 5 logits above a mask, take
+// 1,545 us (random ones 312).
 template <typename T, bool ENT, int NT>
 __global__ void __launch_bounds__(NT, NT == 256 || NT == 512 ? 1536 / NT : 1)
     logprob_rows_kernel(const T* __restrict__ z, int64_t ld, const int32_t* __restrict__ tokens, int vocab,
