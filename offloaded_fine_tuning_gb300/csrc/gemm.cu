@@ -690,8 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             z[j] = col + j < p.N ? __uint_as_float(r[j]) * p.alpha : -__uint_as_float(0x7f800000u);
             if (col + j == token) p.lp.token_logit[row] = z[j];
           }
-          const float most = add<true>(sums, z, c2);
-          if (most == sums.m && sums.s < kAlone) keep_others(sums, z, c2);
+          add<true>(sums, z, c2);
         }
         if (row < p.M) p.lp.parts[(int64_t)tn * p.M + row] = make_float4(sums.m, sums.s, sums.low, sums.t);
       } else if constexpr (EPI == kEpiLogprobBwd) {

@@ -63,24 +63,6 @@ __device__ __forceinline__ float tree(float (&e)[N]) {
     for (int j = 0; j < w; ++j) e[j] += e[j + w];
   return e[0];
 }
-// N logits at once: one look at the maximum, and a tree of their exponentials.
-// Returns their maximum.
-template <bool ENT, int N>
-__device__ __forceinline__ float add(Sums& a, const float (&z)[N], float c) {
-  float m = z[0];
-#pragma unroll
-  for (int j = 1; j < N; ++j) m = fmaxf(m, z[j]);
-  if (m > a.m) raise(a, m, c);
-  float e[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const float x = z[j] - a.m;
-    e[j] = exp2_fast(x * c);
-    if (ENT) a.t = fmaf(e[j], fmaxf(x, kFar), a.t);
-  }
-  add_sum(a, tree(e));
-  return m;
-}
 // Where a maximum stands alone (its exponential is 1), the tree of its group has
 // rounded the group's others beside it, and others are all that log S has.  a.low gets
 // the difference, from the logits z of that group, where S is below kAlone; from there
@@ -95,6 +77,30 @@ __device__ __forceinline__ void keep_others(Sums& a, const float (&z)[N], float 
     others += e[j] == 1.f ? 0.f : e[j];
   }
   a.low += others - (tree(e) - 1.f);
+}
+// N logits at once: one look at the maximum, and a tree of their exponentials.
+// Returns their maximum.  Groups of more than eight are the head's product's, which
+// has them but once: they are looked at for keep_others here.  (Octets of a stored row
+// are looked at when the row is done; in here their logits take registers that spill,
+// 4096 x 128256 bf16 233 us, 204 so.)
+template <bool ENT, int N>
+__device__ __forceinline__ float add(Sums& a, const float (&z)[N], float c) {
+  float m = z[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) m = fmaxf(m, z[j]);
+  if (m > a.m) raise(a, m, c);
+  float e[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float x = z[j] - a.m;
+    e[j] = exp2_fast(x * c);
+    if (ENT) a.t = fmaf(e[j], fmaxf(x, kFar), a.t);
+  }
+  add_sum(a, tree(e));
+  if constexpr (N > 8) {
+    if (m == a.m && a.s < kAlone) keep_others(a, z, c);
+  }
+  return m;
 }
 
 // What a row's sums give.
