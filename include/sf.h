@@ -694,11 +694,13 @@ int64_t sf_op_lm_logprob_workspace_bytes(int64_t n, int32_t v, int64_t chunk_row
 
 /* Backward of sf_op_lm_logprob (the logits are recomputed and not stored): with
  * dz of sf_op_logprob_rows_bwd, dh bf16 [n, d] = dz W and dw bf16 [v, d] = dz^T h,
- * fp32 sums rounded once; dh may not be h.  workspace: sf_op_lm_logprob_bwd_workspace_bytes(n, d,
+ * fp32 sums rounded once.  dz enters both products in bf16 (for n up to 128 with what
+ * that rounding left).  dh may not be h.  A row of h enters dw even where its dz is
+ * 0, so it has to be finite.  workspace: sf_op_lm_logprob_bwd_workspace_bytes(n, d,
  * v, chunk_rows) bytes (-1 for bad sizes), 256-byte aligned: 6 for each logit of
  * a chunk (of 128 rows at least), which hold three chunks' dz at a time, and, where
- * n is more than a chunk, the fp32 sum of dw; for n up to 128 room for what dz's
- * rounding left, which then enters both products too, and 12 n d bytes. */
+ * n is more than a chunk, the fp32 sum of dw (written where n is more than three);
+ * for n up to 128 room for what dz's rounding left and 12 n d bytes. */
 int sf_op_lm_logprob_bwd(const uint16_t* h, const uint16_t* w, const int32_t* tokens, int64_t n,
                          int32_t d, int32_t v, float scale, int64_t chunk_rows, const float* lse,
                          const float* entropy, const float* dlogp, const float* dentropy,
