@@ -45,10 +45,10 @@ namespace {
 // run beside one another: quads beyond the row are copied as zeros and not
 // stored, and what an absent array would hold is read from another one and not
 // used.
-// With both norms, gate and dropout: 16384 x 4096 215 us (6,230 GB/s, 0.92 of a
-// copy's rate; 543 us without the ring), 8192 x 8192 202 us (0.98; 230 us with a
-// barrier for each norm), 16384 x 4096 with fp32 h 246 us (0.96; 272), 4095 x 12288
-// without gate and dropout 171 us (0.87; 214 us with two cluster barriers a row).
+// With both norms, gate and dropout: 16384 x 4096 207 us (6,470 GB/s, 0.95 of a
+// copy's rate; 543 us without the ring), 8192 x 8192 203 us (0.98; 230 us with a
+// barrier for each norm), 16384 x 4096 with fp32 h 249 us (0.95; 272), 4095 x 12288
+// without gate and dropout 170 us (0.87; 214 us with two cluster barriers a row).
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kRingBytes = 230000;
 
